@@ -25,7 +25,9 @@ LIBRARY = os.path.join(_HERE, "libfa_gb300.so")
 EXPORTS = ("fa_fwd", "fa_check_device_status", "fa_status_string", "fa_version", "fa_fwd_debug",
            "fa_splitkv_num_splits", "fa_splitkv_workspace_size", "fa_fwd_splitkv",
            "fa_fwd_splitkv_noalloc", "fa_fwd_ex", "fa_ceiling_ex2_rate", "fa_ceiling_l2_read",
-           "fa_naive_fwd", "fa_naive_workspace_size", "fa_splitkv_num_splits_ex")
+           "fa_naive_fwd", "fa_naive_workspace_size", "fa_splitkv_num_splits_ex",
+           "fa_kv_tables_step", "fa_kv_cache_append", "fa_paged_fwd", "fa_paged_num_splits",
+           "fa_paged_workspace_size", "fa_kv_page_select")
 FA_CEIL_OK, FA_CEIL_ERR_ARG, FA_CEIL_ERR_CUDA = 0, 1, 4
 FA_MASK_NONE, FA_MASK_CAUSAL_TOP_LEFT, FA_MASK_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
 
@@ -58,6 +60,8 @@ class FaError(RuntimeError):
 def library() -> ctypes.CDLL:
     """The loaded C-ABI library (built by ``online_softmax_tiling_gb300.build``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIBRARY):
@@ -100,6 +104,19 @@ def library() -> ctypes.CDLL:
             lib.fa_naive_fwd.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, ctypes.c_float, i, i, vp,
                                          ctypes.c_size_t, vp]
             lib.fa_naive_fwd.restype = i
+            # structures of include/fa_paged.h are passed by address (as bytes)
+            lib.fa_kv_tables_step.argtypes = [vp] * 5 + [i] * 5 + [vp] * 6
+            lib.fa_kv_tables_step.restype = i
+            lib.fa_kv_cache_append.argtypes = [vp, vp, vp, vp, i, vp, vp, i, vp]
+            lib.fa_kv_cache_append.restype = i
+            lib.fa_paged_fwd.argtypes = [vp]
+            lib.fa_paged_fwd.restype = i
+            lib.fa_paged_num_splits.argtypes = [vp]
+            lib.fa_paged_num_splits.restype = i
+            lib.fa_paged_workspace_size.argtypes = [i, i, i, i]
+            lib.fa_paged_workspace_size.restype = ctypes.c_size_t
+            lib.fa_kv_page_select.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp]
+            lib.fa_kv_page_select.restype = i
             _lib = lib
         return _lib
 
@@ -350,3 +367,18 @@ def naive_attention_forward(q, k, v, scale: float | None = None, causal: bool = 
     if st != FA_OK:
         raise FaError(st, "fa_naive_fwd")
     return out, lse
+
+
+_PAGED = ("kv_tables_step", "kv_cache_append", "paged_attention_forward", "kv_page_select",
+          "fa_kv_cache", "fa_paged_args", "FA_ERR_NO_PAGES", "FA_PAGED_MAX_SPLITS")
+
+
+def __getattr__(name):
+    """The paged-cache operators (paged.py) on first use: like the other torch
+    wrappers here they import torch only when called."""
+    if name in _PAGED:
+        from . import paged
+        for n in _PAGED:
+            globals()[n] = getattr(paged, n)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -19,10 +19,13 @@
 
 #include "../../include/fa.h"
 #include "../../include/fa_naive.h"
+#include "../../include/fa_paged.h"
 #include "fa_fwd_kernel.cuh"
 #include "fa_fwd_qtile_kernel.cuh"
 #include "fa_fwd_wide_kernel.cuh"
 #include "naive_attention.cuh"
+
+bool fa_paged_take_status(unsigned int* out);  // paged_api.cu
 
 namespace {
 
@@ -517,7 +520,9 @@ int fa_check_device_status(void* stream) {
     if (cudaMemcpyFromSymbol(&st, fa::g_fa_status, sizeof(st)) != cudaSuccess) return FA_ERR_CUDA;
     if (st != 0 && cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
         return FA_ERR_CUDA;
-    return static_cast<int>(st);
+    unsigned int paged = 0;  // the paged kernels' word (both are cleared)
+    if (!fa_paged_take_status(&paged)) return FA_ERR_CUDA;
+    return static_cast<int>(st != 0 ? st : paged);
 }
 
 const char* fa_status_string(int status) {
@@ -528,6 +533,7 @@ const char* fa_status_string(int status) {
         case FA_ERR_MISALIGNED: return "FA_ERR_MISALIGNED";
         case FA_ERR_CUDA: return "FA_ERR_CUDA";
         case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT";
+        case FA_ERR_NO_PAGES: return "FA_ERR_NO_PAGES";
         default: return "FA_ERR_UNKNOWN";
     }
 }

@@ -1,0 +1,382 @@
+// paged_api.cu - host side of include/fa_paged.h: argument checks, tensor
+// maps, the choice of kernel and of key ranges, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <set>
+#include <utility>
+
+#include "../../include/fa.h"
+#include "../../include/fa_paged.h"
+#include "kv_append.cuh"
+#include "kv_page_select.cuh"
+#include "kv_tables.cuh"
+#include "paged_fwd_kernel.cuh"
+
+namespace {
+
+namespace pg = fa::paged;
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// Codes [rows, d] of a cache (rows = num_pages Hk P) as a 2-D map of bytes;
+// columns >= d read as zeros.
+bool encode_codes(CUtensorMap* map, const void* ptr, int64_t rows, int d, int box_cols, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool misaligned(const void* ptr, uintptr_t al) { return (reinterpret_cast<uintptr_t>(ptr) & (al - 1)) != 0; }
+
+// Opt a kernel into its dynamic shared memory once per device.
+bool ensure_smem(const void* fn, int smem, int device) {
+    static std::mutex mu;
+    static std::set<std::pair<const void*, int>> done;
+    std::lock_guard<std::mutex> lock(mu);
+    if (done.count({fn, device})) return true;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    done.insert({fn, device});
+    return true;
+}
+
+int sm_count() {
+    int device = 0, sms = 152;
+    if (cudaGetDevice(&device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+        sms = 152;
+    return sms;
+}
+
+int shift_of(int page_size) {
+    switch (page_size) {
+        case 16: return 4;
+        case 32: return 5;
+        case 64: return 6;
+        case 128: return 7;
+        default: return -1;
+    }
+}
+
+// The sizes of a cache: FA_OK, or what is wrong with them.
+int check_sizes(const fa_kv_cache& c) {
+    if (c.num_pages < 1 || c.Hk < 1 || shift_of(c.page_size) < 0) return FA_ERR_INVALID_ARG;
+    if (c.d < 16 || c.d > 256 || c.d % 16 != 0) return FA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c.num_pages) * c.page_size > INT32_MAX / c.Hk) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+int check_cache(const fa_kv_cache& c) {
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale) return FA_ERR_INVALID_ARG;
+    const int st = check_sizes(c);
+    if (st != FA_OK) return st;
+    if (misaligned(c.k, 16) || misaligned(c.v, 16) || misaligned(c.k_scale, 4) || misaligned(c.v_scale, 4) ||
+        misaligned(c.k_bounds, 16))
+        return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+// {token, head} strides of a 16-bit tensor: positive multiples of 16 bytes.
+bool bad_strides(const long long* s) {
+    for (int i = 0; i < 2; ++i)
+        if (s[i] <= 0 || s[i] % 8 != 0 || s[i] >= (1ll << 39)) return true;
+    return false;
+}
+
+// Kernel width that serves d.
+int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
+
+// 16-row tiles a CTA holds: two where a request's packed rows fill more than
+// one (each key is then read half as often); one for d > 128, where a second
+// accumulator does not fit the registers.
+int tiles_of(int width, int64_t rows) { return width == 256 || rows <= 16 ? 1 : 2; }
+
+struct Plan {
+    int width, mt, row_blocks;
+    int64_t units;  // row blocks x heads x requests
+};
+
+Plan plan_of(const fa_paged_args& a) {
+    Plan pl;
+    const int64_t rows = static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk);
+    pl.width = width_of(a.cache.d);
+    pl.mt = tiles_of(pl.width, rows);
+    pl.row_blocks = static_cast<int>((rows + 16 * pl.mt - 1) / (16 * pl.mt));
+    pl.units = static_cast<int64_t>(pl.row_blocks) * a.cache.Hk * a.B;
+    return pl;
+}
+
+// Key ranges for num_splits = 0: enough that the CTAs fill the GPU (two per
+// SM), each with at least 256 keys.
+int choose_splits(const fa_paged_args& a, const Plan& pl) {
+    const int64_t keys = static_cast<int64_t>(a.selected ? a.num_selected : a.max_pages) * a.cache.page_size;
+    const int64_t want = (4 * static_cast<int64_t>(sm_count()) + pl.units - 1) / pl.units;
+    const int64_t most = std::max<int64_t>(1, keys / 256);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, FA_PAGED_MAX_SPLITS})));
+}
+
+size_t part_bytes(int64_t rows, int splits, int d) {
+    return (static_cast<size_t>(rows) * splits * d * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+struct KernelEntry {
+    const void* fn;
+    int smem;
+};
+KernelEntry select_kernel(int width, int mt) {
+    if (width == 64)
+        return mt == 1 ? KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<64, 1>), pg::dec_smem<64, 1>()}
+                       : KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<64, 2>), pg::dec_smem<64, 2>()};
+    if (width == 128)
+        return mt == 1 ? KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<128, 1>), pg::dec_smem<128, 1>()}
+                       : KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<128, 2>), pg::dec_smem<128, 2>()};
+    return KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<256, 1>), pg::dec_smem<256, 1>()};
+}
+
+int check_args(const fa_paged_args& a) {
+    if (!a.q || !a.o || !a.lse || !a.block_table || !a.lens) return FA_ERR_INVALID_ARG;
+    if ((a.selected == nullptr) != (a.selected_count == nullptr)) return FA_ERR_INVALID_ARG;
+    if (a.B < 1 || a.T < 0 || a.Hq < 1 || a.max_q < 1 || a.max_pages < 1) return FA_ERR_INVALID_ARG;
+    if (a.dtype != FA_FP16 && a.dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(a.scale) || !(a.scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (a.num_splits < 0 || a.num_splits > FA_PAGED_MAX_SPLITS) return FA_ERR_INVALID_ARG;
+    if (!a.cu_q && (a.T != a.B || a.max_q != 1)) return FA_ERR_INVALID_ARG;
+    if (a.selected && (a.num_selected < 1 || a.max_q != 1)) return FA_ERR_INVALID_ARG;
+    const int st = check_cache(a.cache);
+    if (st != FA_OK) return st;
+    if (a.Hq % a.cache.Hk != 0) return FA_ERR_INVALID_ARG;
+    if (a.max_pages > INT32_MAX / a.cache.page_size) return FA_ERR_INVALID_ARG;
+    if (a.selected && a.num_selected > INT32_MAX / a.cache.page_size) return FA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk) > INT32_MAX / 2) return FA_ERR_INVALID_ARG;
+    if (bad_strides(a.q_stride) || bad_strides(a.o_stride)) return FA_ERR_MISALIGNED;
+    if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
+        misaligned(a.lens, 4) || misaligned(a.cu_q, 4) || misaligned(a.selected, 4) || misaligned(a.selected_count, 4))
+        return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+}  // namespace
+
+// Read and clear the paged kernels' status word (the caller has synchronised).
+__attribute__((visibility("hidden"))) bool fa_paged_take_status(unsigned int* out) {
+    const unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(out, pg::g_paged_status, sizeof(*out)) != cudaSuccess) return false;
+    return *out == 0 || cudaMemcpyToSymbol(pg::g_paged_status, &zero, sizeof(zero)) == cudaSuccess;
+}
+
+extern "C" {
+
+int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, int* free_pages,
+                      const int* free_count, int B, int max_pages, int free_capacity, int page_size,
+                      int max_tokens, int* slots, int* cu_new, int* lens_out, int* free_count_out,
+                      int* status, void* stream) {
+    if (!new_tokens || !lens || !block_table || !free_pages || !free_count || !cu_new || !lens_out ||
+        !free_count_out || !status || (!slots && max_tokens > 0))
+        return FA_ERR_INVALID_ARG;
+    const int shift = shift_of(page_size);
+    if (B < 1 || max_pages < 1 || free_capacity < 1 || max_tokens < 0 || shift < 0) return FA_ERR_INVALID_ARG;
+    if (lens_out == lens || free_count_out == free_count) return FA_ERR_INVALID_ARG;
+    if (max_pages > INT32_MAX / page_size) return FA_ERR_INVALID_ARG;
+    if (B > pg::kTablesMaxB) return FA_ERR_UNSUPPORTED;
+    for (const void* q : {static_cast<const void*>(new_tokens), static_cast<const void*>(lens),
+                          static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(free_count), static_cast<const void*>(slots),
+                          static_cast<const void*>(cu_new), static_cast<const void*>(lens_out),
+                          static_cast<const void*>(free_count_out), static_cast<const void*>(status)})
+        if (misaligned(q, 4)) return FA_ERR_MISALIGNED;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return FA_ERR_CUDA;
+    const void* fn = reinterpret_cast<const void*>(&pg::kv_tables_kernel);
+    const int smem = 3 * (B + 1) * 4;
+    if (!ensure_smem(fn, 3 * (pg::kTablesMaxB + 1) * 4, device)) return FA_ERR_CUDA;
+    pg::TablesParams p{new_tokens, lens, block_table, free_pages, free_count, B, max_pages, free_capacity,
+                       shift, max_tokens, slots, cu_new, lens_out, free_count_out, status};
+    // four tokens (or requests) per thread, at most one CTA per SM
+    const int64_t work = std::max<int64_t>(max_tokens, 2 * static_cast<int64_t>(B));
+    const int64_t ctas = std::min<int64_t>((work + 4 * pg::kTablesThreads - 1) / (4 * pg::kTablesThreads), sm_count());
+    void* args[] = {&p};
+    if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(std::max<int64_t>(1, ctas))), dim3(pg::kTablesThreads), args,
+                         static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, const int* slots, int T,
+                       const long long* k_stride, const long long* v_stride, int dtype, void* stream) {
+    if (!cache || !k || !v || !slots || !k_stride || !v_stride || T < 0) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    const int st = check_cache(*cache);
+    if (st != FA_OK) return st;
+    if (cache->Hk > 32767) return FA_ERR_UNSUPPORTED;
+    if (bad_strides(k_stride) || bad_strides(v_stride) || misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4))
+        return FA_ERR_MISALIGNED;
+    if (T == 0) return FA_OK;
+    pg::AppendParams p;
+    p.x[0] = static_cast<const uint16_t*>(k), p.x[1] = static_cast<const uint16_t*>(v);
+    p.st[0] = k_stride[0], p.sh[0] = k_stride[1], p.st[1] = v_stride[0], p.sh[1] = v_stride[1];
+    p.codes[0] = static_cast<uint8_t*>(cache->k), p.codes[1] = static_cast<uint8_t*>(cache->v);
+    p.scale[0] = cache->k_scale, p.scale[1] = cache->v_scale;
+    p.bounds = reinterpret_cast<int8_t*>(cache->k_bounds);
+    p.slots = slots;
+    p.T = T, p.Hk = cache->Hk, p.d = cache->d, p.num_pages = cache->num_pages, p.page_shift = shift_of(cache->page_size);
+    // slots a CTA looks through: 64, or 8 (one per warp) where that leaves SMs idle
+    p.chunk = static_cast<int64_t>(T) * 2 * p.Hk >= 64ll * 2 * sm_count() ? pg::kAppendMaxChunk : 8;
+    // rows a thread holds of a whole page
+    const int rows = pg::kAppendThreads / (p.d / 8), need = (cache->page_size + rows - 1) / rows;
+    const bool bf = dtype == FA_BF16;
+    const void* fn;
+    if (need <= 4)
+        fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<4, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<4, false>);
+    else if (need <= 8)
+        fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<8, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<8, false>);
+    else
+        fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<16, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<16, false>);
+    void* args[] = {&p};
+    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + p.chunk - 1) / p.chunk), static_cast<unsigned>(2 * p.Hk));
+    if (cudaLaunchKernel(fn, grid, dim3(pg::kAppendThreads), args, 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+int fa_paged_num_splits(const fa_paged_args* a) {
+    if (!a || check_args(*a) != FA_OK) return 1;
+    return choose_splits(*a, plan_of(*a));
+}
+
+size_t fa_paged_workspace_size(int T, int Hq, int d, int num_splits) {
+    if (T < 1 || Hq < 1 || d < 16 || d > 256 || d % 16 != 0 || num_splits < 2) return 0;
+    const int64_t rows = static_cast<int64_t>(T) * Hq;
+    return part_bytes(rows, num_splits, d) + static_cast<size_t>(rows) * num_splits * 4;
+}
+
+int fa_paged_fwd(const fa_paged_args* args) {
+    if (!args) return FA_ERR_INVALID_ARG;
+    const fa_paged_args& a = *args;
+    const int st = check_args(a);
+    if (st != FA_OK) return st;
+    if (a.T == 0) return FA_OK;
+    const Plan pl = plan_of(a);
+    const int splits = a.num_splits == 0 ? choose_splits(a, pl) : a.num_splits;
+    if (splits > 1) {
+        if (!a.workspace) return FA_ERR_INVALID_ARG;
+        if (misaligned(a.workspace, 256)) return FA_ERR_MISALIGNED;
+        if (a.workspace_bytes < fa_paged_workspace_size(a.T, a.Hq, a.cache.d, splits)) return FA_ERR_INVALID_ARG;
+    }
+    const int64_t units = pl.units * splits, rows = static_cast<int64_t>(a.T) * a.Hq;
+    if (units > INT32_MAX || rows > INT32_MAX) return FA_ERR_INVALID_ARG;
+
+    const int keys = pl.width == 256 ? 16 : 32;
+    const int box_rows = std::min(a.cache.page_size, keys), box_cols = std::min(pl.width, 128);
+    const int64_t cache_rows = static_cast<int64_t>(a.cache.num_pages) * a.cache.Hk * a.cache.page_size;
+    CUtensorMap tk, tv;
+    if (!encode_codes(&tk, a.cache.k, cache_rows, a.cache.d, box_cols, box_rows) ||
+        !encode_codes(&tv, a.cache.v, cache_rows, a.cache.d, box_cols, box_rows))
+        return FA_ERR_CUDA;
+    const KernelEntry ke = select_kernel(pl.width, pl.mt);
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || !ensure_smem(ke.fn, ke.smem, device)) return FA_ERR_CUDA;
+
+    pg::PagedParams p;
+    p.q = static_cast<const uint16_t*>(a.q);
+    p.o = static_cast<uint16_t*>(a.o);
+    p.lse = a.lse;
+    p.cu_q = a.cu_q, p.table = a.block_table, p.lens = a.lens;
+    p.sel = a.selected, p.sel_count = a.selected_count;
+    p.k_scale = a.cache.k_scale, p.v_scale = a.cache.v_scale;
+    p.q_st = a.q_stride[0], p.q_sh = a.q_stride[1], p.o_st = a.o_stride[0], p.o_sh = a.o_stride[1];
+    p.T = a.T, p.B = a.B, p.Hq = a.Hq, p.Hk = a.cache.Hk, p.G = a.Hq / a.cache.Hk, p.d = a.cache.d;
+    p.max_q = a.max_q, p.max_pages = a.max_pages, p.num_sel = a.num_selected;
+    p.num_pages = a.cache.num_pages, p.page_shift = shift_of(a.cache.page_size);
+    p.row_blocks = pl.row_blocks, p.splits = splits, p.box_rows = box_rows, p.causal = a.causal != 0;
+    p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    p.o_part = splits > 1 ? static_cast<float*>(a.workspace) : nullptr;
+    p.lse_part = splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + part_bytes(rows, splits, a.cache.d)) : nullptr;
+    bool bf16 = a.dtype == FA_BF16;
+    const cudaStream_t stream = static_cast<cudaStream_t>(a.stream);
+    void* kargs[] = {&tk, &tv, &p, &bf16};
+    if (cudaLaunchKernel(ke.fn, dim3(static_cast<unsigned>(units)), dim3(pg::kDecThreads), kargs,
+                         static_cast<size_t>(ke.smem), stream) != cudaSuccess)
+        return FA_ERR_CUDA;
+    if (splits > 1) {
+        // set up while the attention kernel runs; waits for its end by itself
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>((rows + pg::kMergeWarps - 1) / pg::kMergeWarps));
+        cfg.blockDim = dim3(32 * pg::kMergeWarps);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        void* margs[] = {&p, &bf16};
+        if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&pg::paged_merge_kernel), margs) != cudaSuccess)
+            return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+int fa_kv_page_select(const fa_kv_cache* cache, const void* q, const long long* q_stride, const int* block_table,
+                      const int* lens, int B, int Hq, int max_pages, int num_selected, int dtype, int* selected,
+                      int* selected_count, void* stream) {
+    if (!cache || !cache->k_scale || !cache->k_bounds || !q || !q_stride || !block_table || !lens || !selected ||
+        !selected_count)
+        return FA_ERR_INVALID_ARG;
+    if (B < 1 || Hq < 1 || max_pages < 1 || num_selected < 1) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    const int st = check_sizes(*cache);
+    if (st != FA_OK) return st;
+    if (Hq % cache->Hk != 0 || max_pages > INT32_MAX / cache->page_size ||
+        static_cast<int64_t>(B) * cache->Hk > INT32_MAX)
+        return FA_ERR_INVALID_ARG;
+    if (max_pages > pg::kSelectMaxPages) return FA_ERR_UNSUPPORTED;
+    if (bad_strides(q_stride) || misaligned(q, 16) || misaligned(cache->k_bounds, 16) || misaligned(cache->k_scale, 4) ||
+        misaligned(block_table, 4) || misaligned(lens, 4) || misaligned(selected, 4) || misaligned(selected_count, 4))
+        return FA_ERR_MISALIGNED;
+    pg::SelectParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_st = q_stride[0], p.q_sh = q_stride[1];
+    p.bounds = reinterpret_cast<const int8_t*>(cache->k_bounds);
+    p.k_scale = cache->k_scale;
+    p.table = block_table, p.lens = lens;
+    p.Hk = cache->Hk, p.G = Hq / cache->Hk, p.d = cache->d, p.num_pages = cache->num_pages;
+    p.page_shift = shift_of(cache->page_size), p.max_pages = max_pages, p.keep = num_selected;
+    p.selected = selected, p.count = selected_count;
+    const int64_t smem = 4ll * (2ll * p.G * (p.d / 4) + p.G + max_pages) + 16;
+    if (smem > 200 * 1024) return FA_ERR_UNSUPPORTED;  // a group of very many query heads
+    const void* fn = dtype == FA_BF16 ? reinterpret_cast<const void*>(&pg::kv_page_select_kernel<true>)
+                                      : reinterpret_cast<const void*>(&pg::kv_page_select_kernel<false>);
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess || !ensure_smem(fn, 200 * 1024, device)) return FA_ERR_CUDA;
+    void* args[] = {&p};
+    if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(B * p.Hk)), dim3(pg::kSelectThreads), args,
+                         static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,617 @@
+// paged_fwd_kernel.cuh - attention over the paged 8-bit cache for few query
+// rows per key head (decoding, short drafts, and head widths that the
+// prompt kernel does not serve).
+//
+// Mathematics.  A value is code * 2^ev with ev constant over a page, so with
+// weights w_j = 2^(x_j + ev_j) (x_j the scaled score in the base-2 domain)
+//   O = sum_j w_j v8_j / sum_j w_j 2^-ev_j,   LSE = ln2 log2(sum_j w_j 2^-ev_j):
+// the codes enter the second product as they are, and the running maximum is
+// that of x_j + ev_j, the largest contribution to O.  Weights are scaled by a
+// further 2^14 and rounded to fp16 (their fp32 values are summed): a weight
+// keeps 11 bits down to 2^-28 of the row's largest contribution.  Scores are
+// fp16 products with fp32 sums: e4m3 codes are exact in fp16, and a 16-bit query row is
+// scaled by a power of two (its largest value to [2^14, 2^15)), which leaves
+// out nothing above 2^-38 of that value.
+//
+// Mapping.  The G query heads of a key head (times the request's new tokens)
+// are packed rows; a CTA takes 16 or 32 of them and a range of keys.  Its four
+// warps take 32-key chunks in turn (16-key ones for d > 128), each
+// with a TMA ring, a running softmax and an accumulator of its own; nothing
+// is shared until the end, where the four partial results are joined in
+// shared memory.  Reads are what bounds this kernel (2 d bytes per key and
+// head against 4 G d operations), so mma.sync is the tensor path that fits:
+// tcgen05 would take codes widened in shared memory, 128 rows at a time, for
+// 4 to 16 rows of work.  Codes go from the swizzled tile into registers by
+// 16-byte reads free of bank conflicts (lane (g, t) reads key g, channels
+// 32 t ..; for V keys 2t, 2t+1, 2t+8, 2t+9, channels 16 g ..): channel and key
+// orders inside a product are free as long as both operands agree, so the
+// fragments need no shuffles.
+#pragma once
+
+#include "paged_common.cuh"
+
+namespace fa {
+namespace paged {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr float kWeightShift = 14.f;
+
+struct PagedParams {
+    const uint16_t* q;
+    uint16_t* o;
+    float* lse;
+    const int* cu_q;
+    const int* table;
+    const int* lens;
+    const int* sel;
+    const int* sel_count;
+    const float* k_scale;
+    const float* v_scale;
+    long long q_st, q_sh, o_st, o_sh;
+    int T, B, Hq, Hk, G, d, max_q, max_pages, num_sel, num_pages, page_shift;
+    int row_blocks;   // per request and key head
+    int splits;
+    int box_rows;
+    int causal;
+    float scale_log2;
+    float* o_part;    // [T * Hq][splits][d]
+    float* lse_part;  // [T * Hq][splits], log2 units
+};
+
+template <int D>
+struct DecCfg {
+    static constexpr int kKeys = D == 256 ? 16 : 32;    // keys per chunk
+    static constexpr int kTiles = kKeys / 16;
+    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kHalf = kKeys * D;             // K or V of a chunk
+    static constexpr int kRing = kStages * 2 * kHalf;   // of one warp
+    static constexpr int kSub = D == 256 ? 2 : 1;       // 128-byte column groups
+    static constexpr int kSteps = D / 16;               // k16 steps of q k^T
+    static constexpr int kCols = D / 8;                 // n8 tiles of P V
+    static constexpr int kAccPad = D + 8;
+};
+// Bytes of shared memory: rings (the warps' partial results reuse them), the
+// queries in fragment order, barriers.
+template <int D, int MT>
+constexpr int dec_smem() {
+    const int ring = kDecWarps * DecCfg<D>::kRing;
+    const int join = kDecWarps * (16 * MT * DecCfg<D>::kAccPad + 16 * MT * 2) * 4;
+    return (ring > join ? ring : join) + MT * DecCfg<D>::kSteps * 32 * 16 + kDecWarps * DecCfg<D>::kStages * 8 + 1024;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+    return v;
+}
+
+template <int D, int MT>
+__global__ void __launch_bounds__(kDecThreads, 2)
+    paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                     const PagedParams p, const bool bf16) {
+    using C = DecCfg<D>;
+    constexpr int NST = C::kStages, KEYS = C::kKeys, NT = C::kTiles;
+    extern __shared__ __align__(16) uint8_t dec_raw[];
+    const uint32_t raw = ptx::smem_addr(dec_raw);
+    uint8_t* smem = dec_raw + (((raw + 1023u) & ~1023u) - raw);
+    const uint32_t sbase = ptx::smem_addr(smem);
+    constexpr int kRings = kDecWarps * C::kRing;
+    constexpr int kJoin = kDecWarps * (16 * MT * C::kAccPad + 16 * MT * 2) * 4;
+    constexpr int kOffQ = kRings > kJoin ? kRings : kJoin;
+    constexpr int kOffBar = kOffQ + MT * C::kSteps * 32 * 16;
+    uint4* qfrag = reinterpret_cast<uint4*>(smem + kOffQ);  // [MT][step][lane]
+    __shared__ float row_unit[16 * MT];                     // 2^-e of each row's query scaling
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+
+    // unit: row block fastest (they read the same keys), then range, head, request
+    int u = blockIdx.x;
+    const int rb = u % p.row_blocks;
+    u /= p.row_blocks;
+    const int split = u % p.splits;
+    u /= p.splits;
+    const int h = u % p.Hk, b = u / p.Hk;
+
+    int q0 = b, nq = 1;
+    bool bad = false;
+    if (p.cu_q) {
+        q0 = __ldg(p.cu_q + b);
+        nq = __ldg(p.cu_q + b + 1) - q0;
+        if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
+    }
+    int len = __ldg(p.lens + b);
+    if (len < 0 || (len >> p.page_shift) > p.max_pages || len > (p.max_pages << p.page_shift)) bad = true, len = 0;
+    if (bad && tid == 0) report(kBadData);
+    const int rows = nq * p.G;                 // packed rows of the request: r = i G + g
+    const int r0 = rb * 16 * MT;
+    if (r0 >= rows) return;
+    const int my_rows = min(16 * MT, rows - r0);
+    // keys the last row of the block sees; places the range covers (with a
+    // selection, places in the concatenated selected pages)
+    const int last_i = (r0 + my_rows - 1) / p.G;
+    const int kend = p.causal ? min(len, len - nq + last_i + 1) : len;
+    int places = max(kend, 0);
+    if (p.sel) {
+        int n = __ldg(p.sel_count + b * p.Hk + h);
+        if (n < 0 || n > p.num_sel) {
+            if (tid == 0) report(kBadData);
+            n = 0;
+        }
+        places = n << p.page_shift;
+    }
+    const int chunks = (places + KEYS - 1) / KEYS;
+    const int per = (chunks + p.splits - 1) / p.splits;
+    const int c0 = min(split * per, chunks), c1 = min(c0 + per, chunks);
+    const int mine = c1 > c0 + warp ? (c1 - c0 - warp + kDecWarps - 1) / kDecWarps : 0;  // chunks of this warp
+
+    const uint32_t ring = sbase + warp * C::kRing;
+    const uint32_t bars = sbase + kOffBar + warp * NST * 8;
+    if (lane == 0) {
+        for (int s = 0; s < NST; ++s) ptx::mbar_init(bars + 8 * s, 1);
+        ptx::fence_mbar_init();
+    }
+    if (tid == 0) {
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    __syncwarp();
+
+    // What a warp needs of its next chunks, per 16-key tile: lane i holds that
+    // of chunk 32 n + i (refilled one block ahead).
+    struct Meta {
+        int row[NT];      // first row of the tile in the cache's tensor map, -1: none
+        int pos[NT];      // position of the tile's first key
+        float ks[NT], ev[NT], rv[NT];  // scales: of K; log2 and reciprocal of V's
+    };
+    auto fetch = [&](int k) {  // chunk index of this warp -> its tiles
+        Meta m;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            m.row[i] = -1, m.pos[i] = len, m.ks[i] = 0.f, m.ev[i] = 0.f, m.rv[i] = 1.f;
+            const int place = (c0 + warp + k * kDecWarps) * KEYS + i * 16;
+            if (k < mine && place < places) {
+                int lp = place >> p.page_shift;
+                const int off = place & ((1 << p.page_shift) - 1);
+                if (p.sel) lp = __ldg(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
+                const int pos = (lp << p.page_shift) + off;
+                if (lp < 0 || lp >= p.max_pages) {
+                    report(kBadData);
+                } else if (pos < len) {
+                    const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + lp);
+                    if (page < 0 || page >= p.num_pages) {
+                        report(kBadData);
+                    } else {
+                        const int ph = page * p.Hk + h;
+                        m.row[i] = (ph << p.page_shift) + off;
+                        m.pos[i] = pos;
+                        m.ks[i] = __ldg(p.k_scale + ph);
+                        const float vs = fminf(fmaxf(__ldg(p.v_scale + ph), 0x1p-60f), 0x1p60f);
+                        m.ev[i] = log2f(vs);
+                        m.rv[i] = 1.f / vs;
+                    }
+                }
+            }
+        }
+        return m;
+    };
+    // boxes of a chunk into stage s; every chunk completes its phase (missing
+    // tiles are masked, so their stage may hold anything)
+    auto issue = [&](const int (&row)[NT], int s) {
+        const uint32_t kd = ring + s * 2 * C::kHalf, vd = kd + C::kHalf, bar = bars + 8 * s;
+        if (lane != 0) return;
+        const int tiles_per_box = p.box_rows >> 4;
+        uint32_t bytes = 0;
+        for (int i = 0; i < NT; i += tiles_per_box)
+            if (row[i] >= 0) bytes += 2 * p.box_rows * D;
+        if (bytes == 0) {
+            ptx::mbar_arrive(bar);
+            return;
+        }
+        ptx::mbar_arrive_expect_tx(bar, bytes);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if ((i & (tiles_per_box - 1)) || row[i] < 0) continue;
+#pragma unroll
+            for (int c = 0; c < C::kSub; ++c) {
+                constexpr int W = D > 128 ? 128 : D;  // bytes of a row in one column group
+                tma_load_2d(kd + c * KEYS * 128 + i * 16 * W, &tm_k, bar, 128 * c, row[i]);
+                tma_load_2d(vd + c * KEYS * 128 + i * 16 * W, &tm_v, bar, 128 * c, row[i]);
+            }
+        }
+    };
+    Meta cur = fetch(lane), nxt = cur;
+    if (mine > 32) nxt = fetch(32 + lane);
+    auto row_of = [&](int k, int (&row)[NT]) {  // k in the current or the next block
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int a = __shfl_sync(0xffffffffu, cur.row[i], k & 31);
+            const int c = __shfl_sync(0xffffffffu, nxt.row[i], k & 31);
+            row[i] = (k >> 5) & 1 ? c : a;
+        }
+    };
+    // (blocks alternate between cur and nxt by parity of k / 32)
+#pragma unroll
+    for (int s = 0; s < NST; ++s) {
+        if (s < mine) {
+            int row[NT];
+            row_of(s, row);
+            issue(row, s);
+        }
+    }
+
+    // queries: each warp scales 4 MT of the block's rows and stores them in fragment order
+    {
+        // lane's channels of a row: 8 per step pair ... a row is read as 16-byte pieces
+        constexpr int PIECES = D / 8;
+        for (int r = warp; r < 16 * MT; r += kDecWarps) {
+            uint32_t u4[4] = {0, 0, 0, 0};
+            if (r < my_rows && lane < PIECES && lane * 8 < p.d) {
+                const int pr = r0 + r, i = pr / p.G, hg = pr - i * p.G;
+                const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+                    p.q + static_cast<long long>(q0 + i) * p.q_st + static_cast<long long>(h * p.G + hg) * p.q_sh + lane * 8));
+                u4[0] = v.x, u4[1] = v.y, u4[2] = v.z, u4[3] = v.w;
+            }
+            float f[8], a = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = unpack16(u4[e], bf16);
+                f[2 * e] = x.x, f[2 * e + 1] = x.y;
+                a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
+            }
+#pragma unroll
+            for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            // power of two that takes the largest value to [2^14, 2^15); within
+            // fp32 range for any bf16 value
+            const int e = a > 0.f && a < INFINITY ? max(-120, min(100, 14 - (static_cast<int>(__float_as_uint(a) >> 23) - 127))) : 0;
+            const float s = pow2(e);
+            if (lane == 0) row_unit[r] = pow2(-e);
+            // channel c -> step, word half, lane quarter: within 128 channels
+            // lane quarter t holds 32 t .. 32 t + 31 (d = 64: 16 t .. 16 t + 15)
+            if (lane < PIECES) {
+                constexpr int CPL = D == 64 ? 16 : 32;
+                const int c = lane * 8, cg = c / 128, cc = c % 128, t = cc / CPL, w = (cc % CPL) / 4;
+                const int mt = r / 16, rr = r % 16;
+#pragma unroll
+                for (int e2 = 0; e2 < 2; ++e2) {  // two words of four channels
+                    const int step = cg * 8 + w + e2;
+                    uint32_t* dst = reinterpret_cast<uint32_t*>(qfrag + (mt * C::kSteps + step) * 32 + (rr & 7) * 4 + t);
+                    dst[rr >> 3] = pack_half2(f[4 * e2] * s, f[4 * e2 + 1] * s);
+                    dst[2 + (rr >> 3)] = pack_half2(f[4 * e2 + 2] * s, f[4 * e2 + 3] * s);
+                }
+            }
+        }
+    }
+    __syncthreads();
+
+    constexpr bool kQRegs = MT == 1 && D <= 128;
+    uint4 qr[kQRegs ? C::kSteps : 1];
+    if constexpr (kQRegs) {
+#pragma unroll
+        for (int s = 0; s < C::kSteps; ++s) qr[s] = qfrag[s * 32 + lane];
+    }
+    float mul[MT][2];      // score -> base-2 units, of rows g and g + 8
+    int limit[MT][2];      // keys the row sees
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = 16 * m + 8 * e + g;
+            mul[m][e] = row_unit[r] * p.scale_log2;
+            limit[m][e] = r < my_rows ? (p.causal ? min(len, len - nq + (r0 + r) / p.G + 1) : len) : 0;
+        }
+    int min_limit = len;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (16 * m + 8 * e + g < my_rows) min_limit = min(min_limit, limit[m][e]);
+    min_limit = __reduce_min_sync(0xffffffffu, min_limit);  // every row of the block sees keys below it
+
+    float acc[MT][C::kCols][4];
+    float mx[MT][2], sum[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int c = 0; c < C::kCols; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][c][e] = 0.f;
+        mx[m][0] = mx[m][1] = -INFINITY;
+        sum[m][0] = sum[m][1] = 0.f;
+    }
+
+    bool ok = true;
+    int k = 0;
+    for (; k < mine; ++k) {
+        const int s = k % NST;
+        if (!(ok = wait_warp(bars + 8 * s, (k / NST) & 1))) break;
+        const uint32_t ks_base = ring + s * 2 * C::kHalf, vs_base = ks_base + C::kHalf;
+        int pos[NT], row[NT];
+        float kf[NT], ev[NT], rv[NT];
+        const bool odd = (k >> 5) & 1;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            pos[i] = __shfl_sync(0xffffffffu, odd ? nxt.pos[i] : cur.pos[i], k & 31);
+            row[i] = __shfl_sync(0xffffffffu, odd ? nxt.row[i] : cur.row[i], k & 31);
+            kf[i] = __shfl_sync(0xffffffffu, odd ? nxt.ks[i] : cur.ks[i], k & 31);
+            ev[i] = __shfl_sync(0xffffffffu, odd ? nxt.ev[i] : cur.ev[i], k & 31);
+            rv[i] = __shfl_sync(0xffffffffu, odd ? nxt.rv[i] : cur.rv[i], k & 31);
+        }
+        // ---- scores of 16 MT rows and KEYS keys: n8 tile j holds keys 8 j + ...
+        float sc[MT][2 * NT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 2 * NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[m][j][e] = 0.f;
+#pragma unroll
+        for (int cg = 0; cg < C::kSub; ++cg) {
+#pragma unroll
+            for (int half = 0; half < (D == 64 ? 1 : 2); ++half) {
+                uint4 kw[2 * NT];
+#pragma unroll
+                for (int j = 0; j < 2 * NT; ++j) {
+                    const int key = 8 * j + g;
+                    if constexpr (D == 64)
+                        kw[j] = lds128(ks_base + key * 64 + ((t4 ^ ((key >> 1) & 3)) << 4));
+                    else
+                        kw[j] = lds128(ks_base + cg * KEYS * 128 + key * 128 + (((2 * t4 + half) ^ (key & 7)) << 4));
+                }
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int step = cg * 8 + half * 4 + w;
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        uint4 a;
+                        if constexpr (kQRegs) a = qr[step]; else a = qfrag[(m * C::kSteps + step) * 32 + lane];
+#pragma unroll
+                        for (int j = 0; j < 2 * NT; ++j) {
+                            const uint32_t x = w == 0 ? kw[j].x : w == 1 ? kw[j].y : w == 2 ? kw[j].z : kw[j].w;
+                            mma_f16(sc[m][j], a.x, a.y, a.z, a.w, e4m3x2_to_half2(x & 0xFFFFu), e4m3x2_to_half2(x >> 16));
+                        }
+                    }
+                }
+            }
+        }
+        // ---- weights
+        uint32_t pa[MT][NT][4];
+        bool edge = false;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) edge |= row[i] < 0 || pos[i] + 16 > min_limit;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            float top[2] = {mx[m][0], mx[m][1]};
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 2 * i; j < 2 * i + 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float x = fmaf(sc[m][j][e], mul[m][e >> 1] * kf[i], ev[i]);
+                        if (edge && (row[i] < 0 || pos[i] + 8 * (j & 1) + 2 * t4 + (e & 1) >= limit[m][e >> 1])) x = -INFINITY;
+                        sc[m][j][e] = x;
+                        top[e >> 1] = fmaxf(top[e >> 1], x);
+                    }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
+                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
+            }
+            const float ref[2] = {top[0] == -INFINITY ? 0.f : top[0] - kWeightShift,
+                                  top[1] == -INFINITY ? 0.f : top[1] - kWeightShift};
+            const float al[2] = {ptx::ex2_approx(mx[m][0] - (top[0] == -INFINITY ? 0.f : top[0])),
+                                 ptx::ex2_approx(mx[m][1] - (top[1] == -INFINITY ? 0.f : top[1]))};
+            if (__any_sync(0xffffffffu, top[0] != mx[m][0] || top[1] != mx[m][1])) {
+#pragma unroll
+                for (int c = 0; c < C::kCols; ++c) {
+                    acc[m][c][0] *= al[0], acc[m][c][1] *= al[0];
+                    acc[m][c][2] *= al[1], acc[m][c][3] *= al[1];
+                }
+                sum[m][0] *= al[0], sum[m][1] *= al[1];
+                mx[m][0] = top[0], mx[m][1] = top[1];
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[4 * j + e] = ptx::ex2_approx(sc[m][2 * i + j][e] - ref[e >> 1]);
+                sum[m][0] = fmaf((w[0] + w[1]) + (w[4] + w[5]), rv[i], sum[m][0]);
+                sum[m][1] = fmaf((w[2] + w[3]) + (w[6] + w[7]), rv[i], sum[m][1]);
+                pa[m][i][0] = pack_half2(w[0], w[1]);
+                pa[m][i][1] = pack_half2(w[2], w[3]);
+                pa[m][i][2] = pack_half2(w[4], w[5]);
+                pa[m][i][3] = pack_half2(w[6], w[7]);
+            }
+        }
+        // ---- U += P V, 16 keys at a time
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if (edge && row[i] < 0) continue;
+#pragma unroll
+            for (int cg = 0; cg < C::kSub; ++cg) {
+                constexpr int WORDS = D == 64 ? 2 : 4;   // 4-channel words per key and lane
+                uint32_t vw[4][WORDS];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = 16 * i + 8 * (e >> 1) + 2 * t4 + (e & 1);
+                    if constexpr (D == 64) {
+                        const uint2 v = lds64(vs_base + key * 64 + (((g >> 1) ^ ((key >> 1) & 3)) << 4) + (g & 1) * 8);
+                        vw[e][0] = v.x, vw[e][1] = v.y;
+                    } else {
+                        const uint4 v = lds128(vs_base + cg * KEYS * 128 + key * 128 + ((g ^ (key & 7)) << 4));
+                        vw[e][0] = v.x, vw[e][1] = v.y, vw[e][2] = v.z, vw[e][3] = v.w;
+                    }
+                    // what lies behind the last key carries no weight and may be anything, NaN too
+                    if (edge && pos[i] + key - 16 * i >= len)
+#pragma unroll
+                        for (int w = 0; w < WORDS; ++w) vw[e][w] = 0;
+                }
+#pragma unroll
+                for (int w = 0; w < WORDS; ++w) {
+                    // pairs of keys (2t, 2t+1) and (2t+8, 2t+9) of each of four channels
+                    const uint32_t l0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), l1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+                    const uint32_t h0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), h1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+                    const uint32_t b0[4] = {e4m3x2_to_half2(l0 & 0xFFFFu), e4m3x2_to_half2(l0 >> 16),
+                                            e4m3x2_to_half2(l1 & 0xFFFFu), e4m3x2_to_half2(l1 >> 16)};
+                    const uint32_t b1[4] = {e4m3x2_to_half2(h0 & 0xFFFFu), e4m3x2_to_half2(h0 >> 16),
+                                            e4m3x2_to_half2(h1 & 0xFFFFu), e4m3x2_to_half2(h1 >> 16)};
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            mma_f16(acc[m][cg * 16 + 4 * w + c], pa[m][i][0], pa[m][i][1], pa[m][i][2], pa[m][i][3], b0[c], b1[c]);
+                }
+            }
+        }
+        __syncwarp();
+        // the stage is read: load the chunk NST further on
+        if (k + NST < mine) {
+            int nrow[NT];
+            row_of(k + NST, nrow);
+            issue(nrow, s);
+        }
+        // chunk k was the last of its block: refill that block two further on
+        if ((k & 31) == 31) {
+            if (odd) nxt = fetch(k + 33 + lane); else cur = fetch(k + 33 + lane);
+        }
+    }
+    if (!ok) {  // let copies in flight land before the CTA ends
+        for (const int end = min(k + NST, mine); k < end; ++k) wait_warp(bars + 8 * (k % NST), (k / NST) & 1);
+    }
+
+    // ---- join the four warps' partial results
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 1);
+            sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 2);
+        }
+    __syncthreads();  // every ring is drained: its memory takes the partial results
+    float* part = reinterpret_cast<float*>(smem);
+    constexpr int kPartWarp = 16 * MT * C::kAccPad + 16 * MT * 2;
+    {
+        float* mypart = part + warp * kPartWarp;
+        float* stat = mypart + 16 * MT * C::kAccPad;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int rr = 16 * m + 8 * r + g;
+                if (t4 == 0) stat[2 * rr] = mx[m][r], stat[2 * rr + 1] = sum[m][r];
+#pragma unroll
+                for (int cg = 0; cg < C::kSub; ++cg)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        constexpr int N = D == 64 ? 8 : 16;  // channels in a row of this lane per j
+                        const int ch = cg * 128 + N * (2 * t4 + j);
+#pragma unroll
+                        for (int n = 0; n < N; n += 4)
+                            *reinterpret_cast<float4*>(mypart + rr * C::kAccPad + ch + n) =
+                                make_float4(acc[m][cg * 16 + n][2 * r + j], acc[m][cg * 16 + n + 1][2 * r + j],
+                                            acc[m][cg * 16 + n + 2][2 * r + j], acc[m][cg * 16 + n + 3][2 * r + j]);
+                    }
+            }
+    }
+    __syncthreads();
+    for (int r = warp; r < my_rows; r += kDecWarps) {
+        float m4[kDecWarps], top = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            m4[w] = part[w * kPartWarp + 16 * MT * C::kAccPad + 2 * r];
+            top = fmaxf(top, m4[w]);
+        }
+        const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            m4[w] = ptx::ex2_approx(m4[w] - ref);
+            l = fmaf(part[w * kPartWarp + 16 * MT * C::kAccPad + 2 * r + 1], m4[w], l);
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
+        const float lse2 = l != 0.f ? top - kWeightShift + log2f(l) : -INFINITY;
+        const int pr = r0 + r, i = pr / p.G, hq = h * p.G + pr - i * p.G;
+        const long long tok = q0 + i;
+        const long long grow = tok * p.Hq + hq;
+        for (int c = lane * 4; c < p.d; c += 128) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w) {
+                const float4 x = *reinterpret_cast<const float4*>(part + w * kPartWarp + r * C::kAccPad + c);
+                o.x = fmaf(x.x, m4[w], o.x), o.y = fmaf(x.y, m4[w], o.y);
+                o.z = fmaf(x.z, m4[w], o.z), o.w = fmaf(x.w, m4[w], o.w);
+            }
+            o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+            if (p.splits > 1)
+                *reinterpret_cast<float4*>(p.o_part + (grow * p.splits + split) * p.d + c) = o;
+            else
+                *reinterpret_cast<uint2*>(p.o + tok * p.o_st + static_cast<long long>(hq) * p.o_sh + c) =
+                    make_uint2(pack16(o.x, o.y, bf16), pack16(o.z, o.w, bf16));
+        }
+        if (lane == 0) {
+            if (p.splits > 1)
+                p.lse_part[grow * p.splits + split] = lse2;
+            else
+                p.lse[grow] = lse2 * 0.69314718055994531f;
+        }
+    }
+}
+
+// O = sum_s 2^(lse_s - lse) O_s, LSE = log-sum over the ranges of a row.
+// One warp per row of q.
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedParams p, const bool bf16) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    const long long tok = row / p.Hq;
+    const int hq = static_cast<int>(row - tok * p.Hq);
+    // rows behind the last query were not computed
+    if (tok >= p.T || (p.cu_q && tok >= __ldg(p.cu_q + p.B))) return;
+    const float* ls = p.lse_part + row * p.splits;
+    float a0 = lane < p.splits ? ls[lane] : -INFINITY, a1 = lane + 32 < p.splits ? ls[lane + 32] : -INFINITY;
+    float top = fmaxf(a0, a1);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    a0 = ptx::ex2_approx(a0 - ref), a1 = ptx::ex2_approx(a1 - ref);
+    float l = a0 + a1;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    if (lane == 0) p.lse[row] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const float* op = p.o_part + row * p.splits * p.d;
+    for (int c0 = 0; c0 < p.d; c0 += 128) {
+        const int c = c0 + lane * 4;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < p.splits; ++s) {
+            const float w = __shfl_sync(0xffffffffu, s < 32 ? a0 : a1, s & 31);
+            if (w == 0.f || c >= p.d) continue;
+            const float4 x = *reinterpret_cast<const float4*>(op + s * p.d + c);
+            o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
+        }
+        if (c < p.d)
+            *reinterpret_cast<uint2*>(p.o + tok * p.o_st + static_cast<long long>(hq) * p.o_sh + c) =
+                make_uint2(pack16(o.x * inv, o.y * inv, bf16), pack16(o.z * inv, o.w * inv, bf16));
+    }
+}
+
+}  // namespace paged
+}  // namespace fa
