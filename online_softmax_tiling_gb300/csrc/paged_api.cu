@@ -16,6 +16,7 @@
 #include "kv_page_select.cuh"
 #include "kv_tables.cuh"
 #include "paged_fwd_kernel.cuh"
+#include "paged_prompt_kernel.cuh"
 
 namespace {
 
@@ -117,16 +118,22 @@ int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 int tiles_of(int width, int64_t rows) { return width == 256 || rows <= 16 ? 1 : 2; }
 
 struct Plan {
+    bool prompt;    // tcgen05 kernel (256 packed rows per unit)
     int width, mt, row_blocks;
     int64_t units;  // row blocks x heads x requests
 };
+
+// Packed rows above which the tcgen05 kernel serves a request.
+constexpr int kPromptRows = 64;
 
 Plan plan_of(const fa_paged_args& a) {
     Plan pl;
     const int64_t rows = static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk);
     pl.width = width_of(a.cache.d);
     pl.mt = tiles_of(pl.width, rows);
-    pl.row_blocks = static_cast<int>((rows + 16 * pl.mt - 1) / (16 * pl.mt));
+    pl.prompt = pl.width <= 128 && rows > kPromptRows;
+    const int block = pl.prompt ? pg::kPrRows : 16 * pl.mt;
+    pl.row_blocks = static_cast<int>((rows + block - 1) / block);
     pl.units = static_cast<int64_t>(pl.row_blocks) * a.cache.Hk * a.B;
     return pl;
 }
@@ -135,6 +142,13 @@ Plan plan_of(const fa_paged_args& a) {
 // SM), each with at least 256 keys.
 int choose_splits(const fa_paged_args& a, const Plan& pl) {
     const int64_t keys = static_cast<int64_t>(a.selected ? a.num_selected : a.max_pages) * a.cache.page_size;
+    if (pl.prompt) {
+        // one CTA per SM; ranges only where the units fill less than half of
+        // the SMs, each of at least four key tiles
+        const int64_t sms = sm_count();
+        if (2 * pl.units > sms) return 1;
+        return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.units, keys / 512, FA_PAGED_MAX_SPLITS})));
+    }
     const int64_t want = (4 * static_cast<int64_t>(sm_count()) + pl.units - 1) / pl.units;
     const int64_t most = std::max<int64_t>(1, keys / 256);
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, FA_PAGED_MAX_SPLITS})));
@@ -290,16 +304,15 @@ int fa_paged_fwd(const fa_paged_args* args) {
     const int64_t units = pl.units * splits, rows = static_cast<int64_t>(a.T) * a.Hq;
     if (units > INT32_MAX || rows > INT32_MAX) return FA_ERR_INVALID_ARG;
 
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return FA_ERR_CUDA;
     const int keys = pl.width == 256 ? 16 : 32;
     const int box_rows = std::min(a.cache.page_size, keys), box_cols = std::min(pl.width, 128);
     const int64_t cache_rows = static_cast<int64_t>(a.cache.num_pages) * a.cache.Hk * a.cache.page_size;
     CUtensorMap tk, tv;
-    if (!encode_codes(&tk, a.cache.k, cache_rows, a.cache.d, box_cols, box_rows) ||
-        !encode_codes(&tv, a.cache.v, cache_rows, a.cache.d, box_cols, box_rows))
+    if (!pl.prompt && (!encode_codes(&tk, a.cache.k, cache_rows, a.cache.d, box_cols, box_rows) ||
+                       !encode_codes(&tv, a.cache.v, cache_rows, a.cache.d, box_cols, box_rows)))
         return FA_ERR_CUDA;
-    const KernelEntry ke = select_kernel(pl.width, pl.mt);
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess || !ensure_smem(ke.fn, ke.smem, device)) return FA_ERR_CUDA;
 
     pg::PagedParams p;
     p.q = static_cast<const uint16_t*>(a.q);
@@ -318,10 +331,24 @@ int fa_paged_fwd(const fa_paged_args* args) {
     p.lse_part = splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + part_bytes(rows, splits, a.cache.d)) : nullptr;
     bool bf16 = a.dtype == FA_BF16;
     const cudaStream_t stream = static_cast<cudaStream_t>(a.stream);
-    void* kargs[] = {&tk, &tv, &p, &bf16};
-    if (cudaLaunchKernel(ke.fn, dim3(static_cast<unsigned>(units)), dim3(pg::kDecThreads), kargs,
-                         static_cast<size_t>(ke.smem), stream) != cudaSuccess)
-        return FA_ERR_CUDA;
+    if (pl.prompt) {
+        const uint8_t *kc = static_cast<const uint8_t*>(a.cache.k), *vc = static_cast<const uint8_t*>(a.cache.v);
+        const void* fn = pl.width == 64 ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<64>)
+                                        : reinterpret_cast<const void*>(&pg::paged_prompt_kernel<128>);
+        const int smem = pl.width == 64 ? pg::PrCfg<64>::kSmem : pg::PrCfg<128>::kSmem;
+        void* kargs[] = {&kc, &vc, &p, &bf16};
+        if (!ensure_smem(fn, smem, device) ||
+            cudaLaunchKernel(fn, dim3(static_cast<unsigned>(units)), dim3(pg::kPrThreads), kargs,
+                             static_cast<size_t>(smem), stream) != cudaSuccess)
+            return FA_ERR_CUDA;
+    } else {
+        const KernelEntry ke = select_kernel(pl.width, pl.mt);
+        void* kargs[] = {&tk, &tv, &p, &bf16};
+        if (!ensure_smem(ke.fn, ke.smem, device) ||
+            cudaLaunchKernel(ke.fn, dim3(static_cast<unsigned>(units)), dim3(pg::kDecThreads), kargs,
+                             static_cast<size_t>(ke.smem), stream) != cudaSuccess)
+            return FA_ERR_CUDA;
+    }
     if (splits > 1) {
         // set up while the attention kernel runs; waits for its end by itself
         cudaLaunchAttribute attr[1];

@@ -26,7 +26,7 @@ __device__ __forceinline__ void report(unsigned int code) { atomicCAS(&g_paged_s
 
 // Bounded wait of one thread on an mbarrier phase (it sleeps in the barrier
 // unit).  False after two seconds, with the device status set.
-__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool wait_long(uint32_t bar, uint32_t parity) {
     const uint64_t t0 = ptx::globaltimer();
     for (;;) {
         if (ptx::mbar_try_wait_sleep(bar, parity, 200000)) return true;

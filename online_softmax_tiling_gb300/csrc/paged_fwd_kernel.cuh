@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
                         const int ph = page * p.Hk + h;
                         m.row[i] = (ph << p.page_shift) + off;
                         m.pos[i] = pos;
-                        m.ks[i] = __ldg(p.k_scale + ph);
+                        m.ks[i] = fminf(fmaxf(__ldg(p.k_scale + ph), 0x1p-60f), 0x1p60f);
                         const float vs = fminf(fmaxf(__ldg(p.v_scale + ph), 0x1p-60f), 0x1p60f);
                         m.ev[i] = log2f(vs);
                         m.rv[i] = 1.f / vs;
