@@ -117,8 +117,8 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  *     ascending) are read for the key head; one query per request.
  *   num_splits: key ranges per row, 1 .. FA_PAGED_MAX_SPLITS; 0 = chosen from
  *     the sizes (fa_paged_num_splits).  workspace: device memory of at least
- *     fa_paged_workspace_size bytes, 256-byte aligned, unless num_splits is
- *     1; not to be shared by calls that may run at the same time.
+ *     fa_paged_workspace_size bytes, 256-byte aligned, where that is not 0;
+ *     not to be shared by calls that may run at the same time.
  *   scale: finite and > 0.
  * Rows of o and lse behind the last query (>= cu_q[B]) are left as they were.
  * The softmax runs in 32 bits; its weights enter the second product in fp16,
@@ -154,8 +154,9 @@ int fa_paged_fwd(const fa_paged_args* args);
 /* The count of key ranges fa_paged_fwd uses for num_splits = 0. */
 int fa_paged_num_splits(const fa_paged_args* args);
 
-/* Workspace bytes of fa_paged_fwd for T query rows of Hq heads. */
-size_t fa_paged_workspace_size(int T, int Hq, int d, int num_splits);
+/* Workspace bytes fa_paged_fwd needs with these arguments (0: none; 1, 2, 4, 8
+ * or 16 ranges of few query rows are joined on chip). */
+size_t fa_paged_workspace_size(const fa_paged_args* args);
 
 /*
  * fa_kv_page_select - the pages of each key head that one query per request

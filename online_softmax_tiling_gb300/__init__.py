@@ -113,7 +113,7 @@ def library() -> ctypes.CDLL:
             lib.fa_paged_fwd.restype = i
             lib.fa_paged_num_splits.argtypes = [vp]
             lib.fa_paged_num_splits.restype = i
-            lib.fa_paged_workspace_size.argtypes = [i, i, i, i]
+            lib.fa_paged_workspace_size.argtypes = [vp]
             lib.fa_paged_workspace_size.restype = ctypes.c_size_t
             lib.fa_kv_page_select.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp]
             lib.fa_kv_page_select.restype = i

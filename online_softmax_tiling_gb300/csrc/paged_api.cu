@@ -55,13 +55,15 @@ bool encode_codes(CUtensorMap* map, const void* ptr, int64_t rows, int d, int bo
 
 bool misaligned(const void* ptr, uintptr_t al) { return (reinterpret_cast<uintptr_t>(ptr) & (al - 1)) != 0; }
 
-// Opt a kernel into its dynamic shared memory once per device.
+// Opt a kernel into its dynamic shared memory (and clusters of 16) once per device.
 bool ensure_smem(const void* fn, int smem, int device) {
     static std::mutex mu;
     static std::set<std::pair<const void*, int>> done;
     std::lock_guard<std::mutex> lock(mu);
     if (done.count({fn, device})) return true;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return false;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
     done.insert({fn, device});
     return true;
 }
@@ -138,24 +140,39 @@ Plan plan_of(const fa_paged_args& a) {
     return pl;
 }
 
-// Key ranges for num_splits = 0: enough that the CTAs fill the GPU (two per
-// SM), each with at least 256 keys.
+// Whether the ranges of a row block are joined inside a cluster.
+bool in_cluster(const Plan& pl, int splits) {
+    return !pl.prompt && (splits == 2 || splits == 4 || splits == 8 || splits == 16);
+}
+
+// Key ranges for num_splits = 0.
 int choose_splits(const fa_paged_args& a, const Plan& pl) {
     const int64_t keys = static_cast<int64_t>(a.selected ? a.num_selected : a.max_pages) * a.cache.page_size;
+    const int64_t sms = sm_count();
     if (pl.prompt) {
         // one CTA per SM; ranges only where the units fill less than half of
         // the SMs, each of at least four key tiles
-        const int64_t sms = sm_count();
         if (2 * pl.units > sms) return 1;
         return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.units, keys / 512, FA_PAGED_MAX_SPLITS})));
     }
-    const int64_t want = (4 * static_cast<int64_t>(sm_count()) + pl.units - 1) / pl.units;
+    // two CTAs per SM, and several rounds of them where there are many keys
+    // (requests differ in length); a cluster's count where that fills the GPU
     const int64_t most = std::max<int64_t>(1, keys / 256);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, FA_PAGED_MAX_SPLITS})));
+    const int64_t want = std::min<int64_t>(most, (4 * sms + pl.units - 1) / pl.units);
+    int s = 1;
+    while (s < pg::kDecMaxCluster && s < want) s *= 2;
+    if (s == pg::kDecMaxCluster && want > 4 * s) s = static_cast<int>(std::min<int64_t>(want, FA_PAGED_MAX_SPLITS));
+    return s;
 }
 
 size_t part_bytes(int64_t rows, int splits, int d) {
     return (static_cast<size_t>(rows) * splits * d * 4 + 255) & ~static_cast<size_t>(255);
+}
+
+size_t workspace_bytes(const fa_paged_args& a, const Plan& pl, int splits) {
+    if (splits < 2 || in_cluster(pl, splits)) return 0;
+    const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
+    return part_bytes(rows, splits, a.cache.d) + static_cast<size_t>(rows) * splits * 4;
 }
 
 struct KernelEntry {
@@ -282,10 +299,10 @@ int fa_paged_num_splits(const fa_paged_args* a) {
     return choose_splits(*a, plan_of(*a));
 }
 
-size_t fa_paged_workspace_size(int T, int Hq, int d, int num_splits) {
-    if (T < 1 || Hq < 1 || d < 16 || d > 256 || d % 16 != 0 || num_splits < 2) return 0;
-    const int64_t rows = static_cast<int64_t>(T) * Hq;
-    return part_bytes(rows, num_splits, d) + static_cast<size_t>(rows) * num_splits * 4;
+size_t fa_paged_workspace_size(const fa_paged_args* a) {
+    if (!a || check_args(*a) != FA_OK || a->T == 0) return 0;
+    const Plan pl = plan_of(*a);
+    return workspace_bytes(*a, pl, a->num_splits == 0 ? choose_splits(*a, pl) : a->num_splits);
 }
 
 int fa_paged_fwd(const fa_paged_args* args) {
@@ -296,10 +313,11 @@ int fa_paged_fwd(const fa_paged_args* args) {
     if (a.T == 0) return FA_OK;
     const Plan pl = plan_of(a);
     const int splits = a.num_splits == 0 ? choose_splits(a, pl) : a.num_splits;
-    if (splits > 1) {
+    const size_t need = workspace_bytes(a, pl, splits);
+    if (need > 0) {
         if (!a.workspace) return FA_ERR_INVALID_ARG;
         if (misaligned(a.workspace, 256)) return FA_ERR_MISALIGNED;
-        if (a.workspace_bytes < fa_paged_workspace_size(a.T, a.Hq, a.cache.d, splits)) return FA_ERR_INVALID_ARG;
+        if (a.workspace_bytes < need) return FA_ERR_INVALID_ARG;
     }
     const int64_t units = pl.units * splits, rows = static_cast<int64_t>(a.T) * a.Hq;
     if (units > INT32_MAX || rows > INT32_MAX) return FA_ERR_INVALID_ARG;
@@ -325,10 +343,11 @@ int fa_paged_fwd(const fa_paged_args* args) {
     p.T = a.T, p.B = a.B, p.Hq = a.Hq, p.Hk = a.cache.Hk, p.G = a.Hq / a.cache.Hk, p.d = a.cache.d;
     p.max_q = a.max_q, p.max_pages = a.max_pages, p.num_sel = a.num_selected;
     p.num_pages = a.cache.num_pages, p.page_shift = shift_of(a.cache.page_size);
+    p.in_cluster = in_cluster(pl, splits);
     p.row_blocks = pl.row_blocks, p.splits = splits, p.box_rows = box_rows, p.causal = a.causal != 0;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-    p.o_part = splits > 1 ? static_cast<float*>(a.workspace) : nullptr;
-    p.lse_part = splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + part_bytes(rows, splits, a.cache.d)) : nullptr;
+    p.o_part = need > 0 ? static_cast<float*>(a.workspace) : nullptr;
+    p.lse_part = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + part_bytes(rows, splits, a.cache.d)) : nullptr;
     bool bf16 = a.dtype == FA_BF16;
     const cudaStream_t stream = static_cast<cudaStream_t>(a.stream);
     if (pl.prompt) {
@@ -344,12 +363,21 @@ int fa_paged_fwd(const fa_paged_args* args) {
     } else {
         const KernelEntry ke = select_kernel(pl.width, pl.mt);
         void* kargs[] = {&tk, &tv, &p, &bf16};
-        if (!ensure_smem(ke.fn, ke.smem, device) ||
-            cudaLaunchKernel(ke.fn, dim3(static_cast<unsigned>(units)), dim3(pg::kDecThreads), kargs,
-                             static_cast<size_t>(ke.smem), stream) != cudaSuccess)
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(p.in_cluster ? splits : 1);
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(units));
+        cfg.blockDim = dim3(pg::kDecThreads);
+        cfg.dynamicSmemBytes = static_cast<size_t>(ke.smem);
+        cfg.stream = stream;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (!ensure_smem(ke.fn, ke.smem, device) || cudaLaunchKernelExC(&cfg, ke.fn, kargs) != cudaSuccess)
             return FA_ERR_CUDA;
     }
-    if (splits > 1) {
+    if (need > 0) {
         // set up while the attention kernel runs; waits for its end by itself
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -18,7 +18,9 @@
 // warps take 32-key chunks in turn (16-key ones for d > 128), each
 // with a TMA ring, a running softmax and an accumulator of its own; nothing
 // is shared until the end, where the four partial results are joined in
-// shared memory.  Reads are what bounds this kernel (2 d bytes per key and
+// shared memory.  The CTAs of 2, 4, 8 or 16 key ranges are a cluster and join
+// theirs over distributed shared memory, without a workspace or a second
+// launch; other counts go through a workspace and a merge.  Reads are what bounds this kernel (2 d bytes per key and
 // head against 4 G d operations), so mma.sync is the tensor path that fits:
 // tcgen05 would take codes widened in shared memory, 128 rows at a time, for
 // 4 to 16 rows of work.  Codes go from the swizzled tile into registers by
@@ -36,6 +38,7 @@ namespace paged {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr float kWeightShift = 14.f;
+constexpr int kDecMaxCluster = 16;
 
 struct PagedParams {
     const uint16_t* q;
@@ -51,7 +54,8 @@ struct PagedParams {
     long long q_st, q_sh, o_st, o_sh;
     int T, B, Hq, Hk, G, d, max_q, max_pages, num_sel, num_pages, page_shift;
     int row_blocks;   // per request and key head
-    int splits;
+    int splits;       // key ranges per row block
+    int in_cluster;   // the ranges are the CTAs of a cluster, which join their results themselves
     int box_rows;
     int causal;
     float scale_log2;
@@ -76,7 +80,7 @@ struct DecCfg {
 template <int D, int MT>
 constexpr int dec_smem() {
     const int ring = kDecWarps * DecCfg<D>::kRing;
-    const int join = kDecWarps * (16 * MT * DecCfg<D>::kAccPad + 16 * MT * 2) * 4;
+    const int join = kDecWarps * (16 * MT * DecCfg<D>::kAccPad + 16 * MT * 2) * 4 + 16 * MT * D * 4;
     return (ring > join ? ring : join) + MT * DecCfg<D>::kSteps * 32 * 16 + kDecWarps * DecCfg<D>::kStages * 8 + 1024;
 }
 
@@ -100,6 +104,23 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// What CTA `rank` of the cluster has at the shared address `a` of this one.
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t a, uint32_t rank) {
+    float2 v;
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [r];\n\t}"
+                 : "=f"(v.x), "=f"(v.y) : "r"(a), "r"(rank) : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t a, uint32_t rank) {
+    float4 v;
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %4, %5;\n\tld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [r];\n\t}"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a), "r"(rank) : "memory");
+    return v;
+}
+
 template <int D, int MT>
 __global__ void __launch_bounds__(kDecThreads, 2)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -112,20 +133,22 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     const uint32_t sbase = ptx::smem_addr(smem);
     constexpr int kRings = kDecWarps * C::kRing;
     constexpr int kJoin = kDecWarps * (16 * MT * C::kAccPad + 16 * MT * 2) * 4;
-    constexpr int kOffQ = kRings > kJoin ? kRings : kJoin;
+    constexpr int kJoinAll = kJoin + 16 * MT * D * 4;  // and the CTA's joined result
+    constexpr int kOffQ = kRings > kJoinAll ? kRings : kJoinAll;
     constexpr int kOffBar = kOffQ + MT * C::kSteps * 32 * 16;
     uint4* qfrag = reinterpret_cast<uint4*>(smem + kOffQ);  // [MT][step][lane]
     __shared__ float row_unit[16 * MT];                     // 2^-e of each row's query scaling
+    __shared__ __align__(8) float2 cta_stat[16 * MT];       // this CTA's maximum and sum of each row
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
 
-    // unit: row block fastest (they read the same keys), then range, head, request
+    // unit: range fastest (a cluster's CTAs), then row block (they read the same keys), head, request
     int u = blockIdx.x;
-    const int rb = u % p.row_blocks;
-    u /= p.row_blocks;
     const int split = u % p.splits;
     u /= p.splits;
+    const int rb = u % p.row_blocks;
+    u /= p.row_blocks;
     const int h = u % p.Hk, b = u / p.Hk;
 
     int q0 = b, nq = 1;
@@ -545,7 +568,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
             m4[w] = ptx::ex2_approx(m4[w] - ref);
             l = fmaf(part[w * kPartWarp + 16 * MT * C::kAccPad + 2 * r + 1], m4[w], l);
         }
-        const float inv = l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
+        const float inv = p.in_cluster ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
         const float lse2 = l != 0.f ? top - kWeightShift + log2f(l) : -INFINITY;
         const int pr = r0 + r, i = pr / p.G, hq = h * p.G + pr - i * p.G;
         const long long tok = q0 + i;
@@ -559,19 +582,65 @@ __global__ void __launch_bounds__(kDecThreads, 2)
                 o.z = fmaf(x.z, m4[w], o.z), o.w = fmaf(x.w, m4[w], o.w);
             }
             o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-            if (p.splits > 1)
+            if (p.in_cluster)
+                *reinterpret_cast<float4*>(smem + kJoin + (r * D + c) * 4) = o;
+            else if (p.splits > 1)
                 *reinterpret_cast<float4*>(p.o_part + (grow * p.splits + split) * p.d + c) = o;
             else
                 *reinterpret_cast<uint2*>(p.o + tok * p.o_st + static_cast<long long>(hq) * p.o_sh + c) =
                     make_uint2(pack16(o.x, o.y, bf16), pack16(o.z, o.w, bf16));
         }
         if (lane == 0) {
-            if (p.splits > 1)
+            if (p.in_cluster)
+                cta_stat[r] = make_float2(top, l);
+            else if (p.splits > 1)
                 p.lse_part[grow * p.splits + split] = lse2;
             else
                 p.lse[grow] = lse2 * 0.69314718055994531f;
         }
     }
+    if (!p.in_cluster) return;
+
+    // ---- join the cluster's CTAs: each takes its share of the block's outputs
+    // from all of them
+    cluster_sync();
+    const int n4 = p.d >> 2;
+    for (int i = split * kDecThreads + tid; i < my_rows * n4; i += p.splits * kDecThreads) {
+        const int r = i / n4, c = (i - r * n4) * 4;
+        const uint32_t stat_at = ptx::smem_addr(&cta_stat[r]), o_at = sbase + kJoin + (r * D + c) * 4;
+        float2 st[kDecMaxCluster];
+        float4 x[kDecMaxCluster];
+#pragma unroll
+        for (int s = 0; s < kDecMaxCluster; ++s) {
+            if (s >= p.splits) break;
+            st[s] = ld_cluster_f2(stat_at, s);
+            x[s] = ld_cluster_f4(o_at, s);
+        }
+        float top = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int s = 0; s < kDecMaxCluster; ++s) {
+            if (s >= p.splits) break;
+            top = fmaxf(top, st[s].x);
+        }
+        const float ref = top == -INFINITY ? 0.f : top;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int s = 0; s < kDecMaxCluster; ++s) {
+            if (s >= p.splits) break;
+            const float w = ptx::ex2_approx(st[s].x - ref);
+            l = fmaf(st[s].y, w, l);
+            o.x = fmaf(x[s].x, w, o.x), o.y = fmaf(x[s].y, w, o.y);
+            o.z = fmaf(x[s].z, w, o.z), o.w = fmaf(x[s].w, w, o.w);
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        const int pr = r0 + r, iq = pr / p.G, hq = h * p.G + pr - iq * p.G;
+        const long long tok = q0 + iq;
+        *reinterpret_cast<uint2*>(p.o + tok * p.o_st + static_cast<long long>(hq) * p.o_sh + c) =
+            make_uint2(pack16(o.x * inv, o.y * inv, bf16), pack16(o.z * inv, o.w * inv, bf16));
+        if (c == 0)
+            p.lse[tok * p.Hq + hq] = l != 0.f ? (top - kWeightShift + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+    cluster_sync();  // others may still read this CTA's results
 }
 
 // O = sum_s 2^(lse_s - lse) O_s, LSE = log-sum over the ranges of a row.

@@ -75,23 +75,25 @@ def _fail(name, t, what):
                      f"{'' if t.is_contiguous() else ' (not contiguous)'}")
 
 
-def _need(name, t, dtype, shape, device):
-    """t: contiguous, of this type, shape and device."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        _fail(name, t, f"a contiguous {dtype} tensor {shape} on {device}")
+def _need(name, t, dtype, shape, dev):
+    """Address of t: contiguous, of this type and shape, on CUDA device number `dev`."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _fail(name, t, f"a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}")
     return t.data_ptr()
 
 
-def _rows16(name, t, device, dtype):
-    """t: [rows, heads, d] of a 16-bit type with contiguous d; its strides."""
-    if t.dim() != 3 or t.device != device or t.dtype is not dtype:
-        _fail(name, t, f"a {dtype} tensor [tokens, heads, d] on {device}")
-    s = t.stride()
-    if s[2] != 1:
+def _rows16(name, t, dev, dtype):
+    """Strides of t: [rows, heads, d] of a 16-bit type with contiguous d."""
+    if t.dim() != 3 or t.get_device() != dev or t.dtype is not dtype:
+        _fail(name, t, f"a {dtype} tensor [tokens, heads, d] on cuda:{dev}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and t.shape[2] > 1:
         _fail(name, t, "a tensor with a contiguous last dimension")
-    # the stride of a dimension of one element is never used: any valid one will do
-    n, h, d = t.shape
-    return (s[0] if n > 1 else max(8, s[0] // 8 * 8)), (s[1] if h > 1 else max(8, s[1] // 8 * 8))
+    if s0 < 8 or s1 < 8:
+        # the stride of a dimension of at most one element is never used: any valid one will do
+        n, h, _ = t.shape
+        return (s0 if n > 1 else 8), (s1 if h > 1 else 8)
+    return s0, s1
 
 
 def _dtype_of(t):
@@ -101,25 +103,22 @@ def _dtype_of(t):
     return code
 
 
-def _elsewhere(device, stream):
-    """Contexts that make `device` and `stream` the current ones, or None if they are."""
-    if device.type != "cuda":
+def _device_of(t):
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("tensors must be on a CUDA device")
-    if stream is None and device.index == _current_device():
-        return None
-    stack = torch.cuda.device(device)
-    if stream is None:
-        return (stack,)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    if stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-    return stack, torch.cuda.stream(stream)
+    return dev
 
 
-class _Within:
-    def __init__(self, contexts):
-        self.contexts = contexts
+class _there:
+    """Makes CUDA device `dev` and `stream` (a torch stream, a handle or None) the current ones."""
+
+    def __init__(self, dev, stream):
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=dev)
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
+        self.contexts = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
 
     def __enter__(self):
         for c in self.contexts:
@@ -149,21 +148,21 @@ def kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_s
     FA_ERR_INVALID_ARG on the device; unless it is FA_OK the step changed
     nothing and its slots are all -1.  check=True waits for it and raises.
     """
-    device = new_tokens.device
-    there = _elsewhere(device, stream)
-    if there:
-        with _Within(there):
+    device = _device_of(new_tokens)
+    if stream is not None or device != _current_device():
+        with _there(device, stream):
             return kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size,
                                   max_tokens, check=check)
     if block_table.dim() != 2 or new_tokens.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("new_tokens [B], block_table [B, max_pages], free_pages [capacity]")
     B, M = block_table.shape
-    handle = _raw_stream(device.index)
+    handle = _raw_stream(device)
     max_tokens = int(max_tokens)
-    out = torch.empty(max(max_tokens, 0) + 2 * B + 3, dtype=_I32, device=device)
-    slots, cu, lens_out, count_out, status = out.split((max(max_tokens, 0), B + 1, B, 1, 1))
+    if max_tokens < 0:
+        raise ValueError("max_tokens must not be negative")
+    out = new_tokens.new_empty(max_tokens + 2 * B + 3, dtype=_I32)
     at = out.data_ptr()
-    at_cu = at + 4 * max(max_tokens, 0)
+    at_cu = at + 4 * max_tokens
     at_lens = at_cu + 4 * (B + 1)
     st = library().fa_kv_tables_step(
         _need("new_tokens", new_tokens, _I32, (B,), device), _need("lens", lens, _I32, (B,), device),
@@ -173,12 +172,13 @@ def kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_s
         max_tokens, at, at_cu, at_lens, at_lens + 4 * B, at_lens + 4 * B + 4, handle)
     if st != FA_OK:
         raise FaError(st, "fa_kv_tables_step")
+    parts = out.split_with_sizes((max_tokens, B + 1, B, 1, 1))
     if check:
         _checked(handle, "fa_kv_tables_step")
-        code = int(status.item())
+        code = int(parts[4].item())
         if code != FA_OK:
             raise FaError(code, "fa_kv_tables_step")
-    return slots, cu, lens_out, count_out, status
+    return parts
 
 
 def kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=None, stream=None,
@@ -192,10 +192,9 @@ def kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=No
     [num_pages, Hk, 2, d] int8 for kv_page_select.  The tokens of one page must
     be consecutive rows with ascending slots.
     """
-    device = k.device
-    there = _elsewhere(device, stream)
-    if there:
-        with _Within(there):
+    device = _device_of(k)
+    if stream is not None or device != _current_device():
+        with _there(device, stream):
             return kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds,
                                    check=check)
     shape = _cache_sizes(k_cache)
@@ -212,7 +211,7 @@ def kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=No
     at = _need("slots", slots, _I32, (T,), device)
     if T == 0:
         return
-    handle = _raw_stream(device.index)
+    handle = _raw_stream(device)
     st = library().fa_kv_cache_append(cache, k.data_ptr(), v.data_ptr(), at, T, _PACK_STRIDE.pack(*ks),
                                       _PACK_STRIDE.pack(*vs), dtype, handle)
     if st != FA_OK:
@@ -233,16 +232,15 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     causal: query i of n sees keys j <= i + len - n.  selected [B, Hk, keep]
     with selected_count [B, Hk] (kv_page_select) restricts every key head to
     those pages.  scale defaults to 1/sqrt(d).  num_splits: key ranges per row
-    (0: chosen by the library); more than one needs a workspace, which is
+    (0: chosen by the library); a workspace, where the count needs one, is
     allocated unless given.  Rows of given outputs behind the last query are
     left as they were.  A kernel whose waits run out (2 s) leaves outputs
     unwritten and reports it through fa_check_device_status, as in
     attention_forward.
     """
-    device = q.device
-    there = _elsewhere(device, stream)
-    if there:
-        with _Within(there):
+    device = _device_of(q)
+    if stream is not None or device != _current_device():
+        with _there(device, stream):
             return paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_q,
                                            max_q, scale, causal, selected, selected_count, out, lse,
                                            num_splits, workspace, check=check)
@@ -255,14 +253,14 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
         raise ValueError("q must be [T, Hq, d] with the cache's d, block_table [B, max_pages]")
     B, M = block_table.shape
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         os = (Hq * d, d)
     else:
         os = _rows16("out", out, device, q.dtype)
         if out.shape != q.shape:
             raise ValueError("out must have the shape of q")
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=_F32, device=device)
+        lse = q.new_empty((T, Hq), dtype=_F32)
         at_lse = lse.data_ptr()
     else:
         at_lse = _need("lse", lse, _F32, (T, Hq), device)
@@ -277,25 +275,24 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
         raise ValueError("selected_count comes with selected")
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    handle = _raw_stream(device.index)
-    fields = [q.data_ptr(), out.data_ptr(), at_lse,
+    handle = _raw_stream(device)
+    fields = (q.data_ptr(), out.data_ptr(), at_lse,
               0 if cu_q is None else _need("cu_q", cu_q, _I32, (B + 1,), device),
               _need("block_table", block_table, _I32, (B, M), device), _need("lens", lens, _I32, (B,), device),
               at_sel, at_count,
               _need("k_cache", k_cache, _E4M3, shape, device), _need("v_cache", v_cache, _E4M3, shape, device),
               _need("k_scale", k_scale, _F32, (N, Hk), device), _need("v_scale", v_scale, _F32, (N, Hk), device),
-              0, N, P, Hk, d, *qs, *os, T, B, Hq, max_q, M, keep, scale, causal, dtype, num_splits, 0, 0, handle]
+              0, N, P, Hk, d, *qs, *os, T, B, Hq, max_q, M, keep, scale, causal, dtype, num_splits)
     lib = library()
-    if num_splits == 0:
-        num_splits = fields[-4] = lib.fa_paged_num_splits(_PACK_ARGS.pack(*fields))
-    if num_splits > 1:
-        nbytes = lib.fa_paged_workspace_size(T, Hq, d, num_splits)
+    args = _PACK_ARGS.pack(*fields, 0, 0, handle)
+    nbytes = lib.fa_paged_workspace_size(args)
+    if nbytes:
         if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
-        elif workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        fields[-3], fields[-2] = workspace.data_ptr(), workspace.nbytes
-    st = lib.fa_paged_fwd(_PACK_ARGS.pack(*fields))
+            workspace = q.new_empty(nbytes, dtype=torch.uint8)
+        elif workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+        args = _PACK_ARGS.pack(*fields, workspace.data_ptr(), workspace.nbytes, handle)
+    st = lib.fa_paged_fwd(args)
     if st != FA_OK:
         raise FaError(st, "fa_paged_fwd")
     if check:
@@ -310,10 +307,9 @@ def kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size: int, num_
     exact whole-number score of include/fa_paged.h over k_bounds
     [num_pages, Hk, 2, d]; ascending, -1 behind the last, the last token's page
     always among them."""
-    device = q.device
-    there = _elsewhere(device, stream)
-    if there:
-        with _Within(there):
+    device = _device_of(q)
+    if stream is not None or device != _current_device():
+        with _there(device, stream):
             return kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size, num_selected,
                                   check=check)
     dtype = _dtype_of(q)
@@ -328,9 +324,8 @@ def kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size: int, num_
         raise ValueError("q must be [B, Hq, d], num_selected at least 1")
     cache = _PACK_CACHE.pack(0, 0, _need("k_scale", k_scale, _F32, (N, Hk), device), 0,
                              _need("k_bounds", k_bounds, _I8, (N, Hk, 2, d), device), N, page_size, Hk, d)
-    selected = torch.empty((B, Hk, num_selected), dtype=_I32, device=device)
-    count = torch.empty((B, Hk), dtype=_I32, device=device)
-    handle = _raw_stream(device.index)
+    selected, count = lens.new_empty((B, Hk, num_selected), dtype=_I32), lens.new_empty((B, Hk), dtype=_I32)
+    handle = _raw_stream(device)
     st = library().fa_kv_page_select(
         cache, q.data_ptr(), _PACK_STRIDE.pack(*qs), _need("block_table", block_table, _I32, (B, M), device),
         _need("lens", lens, _I32, (B,), device), B, Hq, M, num_selected, dtype, selected.data_ptr(),

@@ -149,11 +149,11 @@ def tolerances(O, L, A, D, d, n_keys, v_top, dtype):
     two fp32 operations: delta = (d + 4) 2^-23 D, plus the 2^-22 of 2^x and of the subtraction of
     maxima up to |x| = 2^6 (2^-17).  LSE: delta, n 2^-24 from the sum, 2^-22 |L|.
     O: weights off by delta each (2 delta A), rounded to fp16 (2^-11 A), or below its normal range
-    by 2^-25 against a largest weight of 2^14 (n 2^-39 of the largest value), sums in fp32 (n 2^-23 A);
+    by 2^-25 against a largest weight of at least 2^8 (n 2^-33 of the largest value), sums in fp32 (n 2^-23 A);
     then the output's rounding, half a step: eps / 2, or half the type's smallest number."""
     delta = (d + 4) * 2.0 ** -23 * D + 2.0 ** -17
     lse = delta + n_keys * 2.0 ** -24 + 2.0 ** -22 * np.abs(np.where(np.isfinite(L), L, 0))
-    o = (2 * delta[..., None] + 2.0 ** -11 + n_keys * 2.0 ** -23) * A + n_keys * 2.0 ** -39 * v_top
+    o = (2 * delta[..., None] + 2.0 ** -11 + n_keys * 2.0 ** -23) * A + n_keys * 2.0 ** -33 * v_top
     f = torch.finfo(dtype)
     return o + (np.abs(O) + o) * f.eps / 2 + f.smallest_normal * f.eps / 2, lse
 

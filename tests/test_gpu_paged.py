@@ -397,7 +397,7 @@ DECODE = [  # Hk, G, P, d
 
 @pytest.mark.parametrize("Hk,G,P,d", DECODE)
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("splits", [0, 1, 3])
+@pytest.mark.parametrize("splits", [0, 1, 2, 3, 16])
 def test_decode(Hk, G, P, d, dtype, splits):
     """One query per request; lengths 0, 1, around tile and page borders, ragged ones."""
     lens = [0, 1, 15, 16, 17, P - 1, P, P + 1, 127, 300, 777]
@@ -407,7 +407,7 @@ def test_decode(Hk, G, P, d, dtype, splits):
     _check_attend(case, out, lse)
 
 
-@pytest.mark.parametrize("splits", [0, 1, 2, 7, 64])
+@pytest.mark.parametrize("splits", [0, 1, 2, 4, 7, 8, 16, 64])
 def test_decode_long(splits):
     """More than 32 chunks per warp (the lookups are refilled), and splits that stay empty."""
     case = _attend_case([9000, 40], [1, 1], 1, 4, 16, 128, "bf16", 41)
@@ -452,7 +452,7 @@ def test_rows_behind_the_last_query_are_left():
     news = [3, 5]
     cache, table, lens, cu, q = _attend_case([50, 70], news, 2, 2, 16, 128, "bf16", 62)
     pad = torch.cat([q, torch.full((4, 4, 128), float("nan"), dtype=q.dtype)])
-    for splits in (1, 4):
+    for splits in (1, 4, 5):
         out = torch.full_like(pad, 7.0, device="cuda")
         lse = torch.full((12, 4), 7.0, device="cuda")
         _attend(cache, table, lens, cu, pad, news, out=out, lse=lse, num_splits=splits)
@@ -584,7 +584,7 @@ def test_select_and_attend(lens, Hk, G, P, d, keep, dtype):
     want, n = ref.select(cache, q.double().numpy(), table, lens, keep)
     np.testing.assert_array_equal(sel.cpu().numpy(), want)
     np.testing.assert_array_equal(count.cpu().numpy(), n)
-    for splits in (0, 1, 3):
+    for splits in (0, 1, 3, 4):
         out, lse = _fa().paged_attention_forward(q.cuda(), *g[:4], _i32(table), _i32(lens), selected=sel,
                                                  selected_count=count, num_splits=splits)
         _ok()
@@ -745,7 +745,7 @@ def test_wrappers_refuse_wrong_tensors():
              dict(block_table=good["block_table"].long()), dict(lens=good["lens"][:1]), dict(lens=good["lens"].cpu()),
              dict(out=torch.empty_like(good["q"])[:, :2]), dict(lse=torch.empty((2, 4), dtype=torch.float64, device="cuda")),
              dict(cu_q=_i32([0, 1])), dict(selected=_i32(np.zeros((2, 2, 3)))), dict(selected_count=_i32(np.zeros((2, 2)))),
-             dict(scale=-1.0), dict(num_splits=65), dict(max_q=2), dict(num_splits=2, workspace=torch.empty(8, device="cuda"))]
+             dict(scale=-1.0), dict(num_splits=65), dict(max_q=2), dict(num_splits=3, workspace=torch.empty(8, device="cuda"))]
     for w in wrong:
         with pytest.raises((TypeError, ValueError, fa.FaError)):
             fa.paged_attention_forward(**{**good, **w})

@@ -84,14 +84,14 @@ def test_cache_refusals(lib, kw, want):
     (dict(cu_q=A, max_q=0), BAD), (dict(Hq=3), BAD), (dict(Hq=0), BAD), (dict(max_pages=0), BAD),
     (dict(max_pages=1 << 28), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(dtype=2), BAD),
-    (dict(num_splits=-1), BAD), (dict(num_splits=65), BAD), (dict(num_splits=2), BAD),
+    (dict(num_splits=-1), BAD), (dict(num_splits=65), BAD), (dict(num_splits=3), BAD), (dict(num_splits=16), CUDA),
     (dict(selected=A), BAD), (dict(selected_count=A), BAD), (dict(selected=A, selected_count=A), BAD),
     (dict(selected=A, selected_count=A, num_selected=2, cu_q=A, max_q=2), BAD),
     (dict(q=A + 8), MISAL), (dict(o=A + 8), MISAL), (dict(lse=A + 2), MISAL), (dict(cu_q=A + 1, max_q=1), MISAL),
     (dict(q_stride=[0, 64]), MISAL), (dict(q_stride=[256, 60]), MISAL), (dict(o_stride=[-256, 64]), MISAL),
-    (dict(), CUDA), (dict(T=0, cu_q=A), 0), (dict(num_splits=4, workspace=A + 16, workspace_bytes=1 << 30), MISAL),
-    (dict(num_splits=4, workspace=A, workspace_bytes=3 * 4 * 4 * 65 * 4 - 1), BAD),
-    (dict(num_splits=4, workspace=A, workspace_bytes=3 * 4 * 4 * 65 * 4), CUDA)])
+    (dict(), CUDA), (dict(T=0, cu_q=A), 0), (dict(num_splits=5, workspace=A + 16, workspace_bytes=1 << 30), MISAL),
+    (dict(num_splits=5, workspace=A, workspace_bytes=3 * 4 * 5 * 65 * 4 - 1), BAD),
+    (dict(num_splits=5, workspace=A, workspace_bytes=3 * 4 * 5 * 65 * 4), CUDA)])
 def test_attention_refusals(lib, kw, want):
     assert _fwd(lib, _args(**kw)) == want
 
@@ -110,9 +110,13 @@ def test_splits_and_workspace(lib):
     assert 1 < n(max_pages=1000) <= fa.FA_PAGED_MAX_SPLITS        # 6 units, many keys
     assert n(T=4000, B=4000, max_pages=1000) == 1                 # units enough
     assert n(scale=-1.0) == 1
-    assert fa.library().fa_paged_workspace_size(3, 4, 64, 1) == 0
-    assert fa.library().fa_paged_workspace_size(3, 4, 64, 4) == 3 * 4 * 4 * 64 * 4 + 3 * 4 * 4 * 4
-    assert fa.library().fa_paged_workspace_size(3, 4, 24, 4) == 0
+    ws = lambda **kw: lib.fa_paged_workspace_size(ctypes.addressof(_args(**kw)))  # noqa: E731
+    for s in (1, 2, 4, 8, 16):                                    # joined on chip
+        assert ws(num_splits=s) == 0
+    assert ws(num_splits=3) == 3 * 4 * 3 * 64 * 4 + 3 * 4 * 3 * 4
+    assert ws(num_splits=3, scale=-1.0) == 0 and lib.fa_paged_workspace_size(None) == 0
+    rows = dict(cu_q=A, T=100, max_q=90, num_splits=4)            # prompt rows: through a workspace
+    assert ws(**rows) == 100 * 4 * 4 * 64 * 4 + 100 * 4 * 4 * 4
 
 
 @pytest.mark.parametrize("kw,want", [
