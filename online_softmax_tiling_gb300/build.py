@@ -1,9 +1,11 @@
-"""Build the sm_103a shared library in-tree with nvcc (no CMake, three translation units)."""
+"""Build in-tree, without CMake: the sm_103a shared library with nvcc (three translation units)
+and the torch binding of its paged-cache operators with g++ (one)."""
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -16,6 +18,9 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa_fw
                                                      "sm103_ptx.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_ceilings.h", "fa_naive.h", "fa_paged.h")]
 LIBRARY = os.path.join(HERE, "libfa_gb300.so")
+BINDING = os.path.join(HERE, "_paged_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
+BINDING_DEPENDS = [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h"), os.path.join(ROOT, "include", "fa_paged.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -26,24 +31,59 @@ def nvcc() -> str:
     return cand
 
 
-def stale() -> bool:
-    if not os.path.exists(LIBRARY):
+def _stale(target, depends) -> bool:
+    if not os.path.exists(target):
         return True
-    t = os.path.getmtime(LIBRARY)
-    return any(os.path.getmtime(p) > t for p in DEPENDS)
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(p) > t for p in depends)
+
+
+def stale() -> bool:
+    return _stale(LIBRARY, DEPENDS) or _stale(BINDING, BINDING_DEPENDS)
+
+
+def _compile_binding(tmp):
+    """g++ on the binding: the object only, so that it can run beside nvcc."""
+    from torch.utils.cpp_extension import include_paths
+    inc = [f"-I{p}" for p in (*include_paths("cuda"), sysconfig.get_paths()["include"])]
+    return subprocess.Popen(["g++", "-O2", "-std=c++17", "-fPIC", "-c", "-o", tmp, BINDING_SOURCE, *inc])
+
+
+def _link_binding(obj):
+    """The binding finds the library beside itself, torch's libraries are loaded by `import torch`."""
+    from torch.utils.cpp_extension import library_paths
+    tmp = BINDING + f".tmp{os.getpid()}"
+    libs = [f"-L{p}" for p in library_paths("cuda")] + ["-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-ltorch",
+                                                        "-lc10_cuda", "-lc10"]
+    subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libfa_gb300.so", "-Wl,-rpath,$ORIGIN", *libs],
+                   check=True)
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libfa_gb300.so for sm_103a (static cudart, -O3 -lineinfo)."""
+    """Compile libfa_gb300.so for sm_103a (static cudart, -O3 -lineinfo) and the torch binding."""
     if not force and not stale():
         return LIBRARY
-    tmp = LIBRARY + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "--threads", "3", "-o", tmp, *SOURCES]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.run(cmd, check=True)
-    os.replace(tmp, LIBRARY)
+    obj = BINDING + f".tmp{os.getpid()}.o"
+    binding = _compile_binding(obj) if force or _stale(BINDING, BINDING_DEPENDS) else None
+    try:
+        if force or _stale(LIBRARY, DEPENDS):
+            tmp = LIBRARY + f".tmp{os.getpid()}"
+            cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
+                   "-Xlinker", "-soname=libfa_gb300.so", "--threads", "3", "-o", tmp, *SOURCES]
+            if verbose:
+                cmd.insert(1, "-Xptxas=-v")
+            subprocess.run(cmd, check=True)
+            os.replace(tmp, LIBRARY)
+        if binding is not None:
+            if binding.wait() != 0:
+                raise subprocess.CalledProcessError(binding.returncode, "g++ torch_binding.cpp")
+            _link_binding(obj)
+    finally:
+        if binding is not None:
+            binding.wait()
+        if os.path.exists(obj):
+            os.remove(obj)
     return LIBRARY
 
 

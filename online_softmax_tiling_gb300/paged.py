@@ -24,19 +24,17 @@ check=True calls here.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
-import struct
+import os
+import sysconfig
 
 import torch
 
-from . import (FA_BF16, FA_FP16, FA_OK, FaError, _checked, library)
+from . import FA_OK, FaError, _checked, library
 
 FA_ERR_NO_PAGES = 6
 FA_PAGED_MAX_SPLITS = 64
-_E4M3, _F32, _I32, _I8 = torch.float8_e4m3fn, torch.float32, torch.int32, torch.int8
-_CODES = {torch.float16: FA_FP16, torch.bfloat16: FA_BF16}
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
 
 
 class fa_kv_cache(ctypes.Structure):
@@ -61,64 +59,33 @@ class fa_paged_args(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p)]
 
 
-# The same structures packed in one step (a Structure filled field by field
-# costs several times as much on the host).
-_PACK_CACHE = struct.Struct("@5P4i")
-_PACK_ARGS = struct.Struct("@8P5P4i4q6if3iPNP")
-_PACK_STRIDE = struct.Struct("@2q")
+def _load():
+    """The compiled binding (csrc/torch_binding.cpp) beside the library it calls."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    path = os.path.join(here, "_paged_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+    library()  # (raises, saying how to build, if that is missing)
+    if not os.path.exists(path):
+        raise FileNotFoundError(f"{path} is missing: build it with `python -m online_softmax_tiling_gb300.build`")
+    spec = importlib.util.spec_from_file_location("online_softmax_tiling_gb300._paged_binding", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
 
 
-def _fail(name, t, what):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a tensor")
-    raise ValueError(f"{name} must be {what}, got {t.dtype} {tuple(t.shape)} on {t.device}"
-                     f"{'' if t.is_contiguous() else ' (not contiguous)'}")
-
-
-def _need(name, t, dtype, shape, dev):
-    """Address of t: contiguous, of this type and shape, on CUDA device number `dev`."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        _fail(name, t, f"a contiguous {dtype} tensor {tuple(shape)} on cuda:{dev}")
-    return t.data_ptr()
-
-
-def _rows16(name, t, dev, dtype):
-    """Strides of t: [rows, heads, d] of a 16-bit type with contiguous d."""
-    if t.dim() != 3 or t.get_device() != dev or t.dtype is not dtype:
-        _fail(name, t, f"a {dtype} tensor [tokens, heads, d] on cuda:{dev}")
-    s0, s1, s2 = t.stride()
-    if s2 != 1 and t.shape[2] > 1:
-        _fail(name, t, "a tensor with a contiguous last dimension")
-    if s0 < 8 or s1 < 8:
-        # the stride of a dimension of at most one element is never used: any valid one will do
-        n, h, _ = t.shape
-        return (s0 if n > 1 else 8), (s1 if h > 1 else 8)
-    return s0, s1
-
-
-def _dtype_of(t):
-    code = _CODES.get(t.dtype)
-    if code is None:
-        raise TypeError(f"unsupported dtype {t.dtype} (float16 or bfloat16)")
-    return code
-
-
-def _device_of(t):
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("tensors must be on a CUDA device")
-    return dev
+_native = _load()
 
 
 class _there:
-    """Makes CUDA device `dev` and `stream` (a torch stream, a handle or None) the current ones."""
+    """Makes the device of `t` and `stream` (a torch stream or a handle) the current ones."""
 
-    def __init__(self, dev, stream):
+    def __init__(self, t, stream):
+        if not t.is_cuda:
+            raise ValueError("tensors must be on a CUDA device")
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=dev)
-        if stream is not None and stream.device.index != dev:
-            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{dev}")
-        self.contexts = [torch.cuda.device(dev)] + ([torch.cuda.stream(stream)] if stream is not None else [])
+            stream = torch.cuda.ExternalStream(stream, device=t.device)
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        self.contexts = (torch.cuda.device(t.device), torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self.contexts:
@@ -129,10 +96,14 @@ class _there:
             c.__exit__(*a)
 
 
-def _cache_sizes(k_cache):
-    if k_cache.dim() != 4:
-        _fail("k_cache", k_cache, "[num_pages, Hk, page_size, d]")
-    return k_cache.shape
+def _done(result, what, check, t):
+    """The outputs of a call, or its error; check=True also waits for the kernels' status."""
+    if type(result) is int:
+        raise FaError(result, what)
+    if check:
+        with torch.cuda.device(t.device):
+            _checked(torch.cuda.current_stream().cuda_stream, what)
+    return result
 
 
 def kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size: int,
@@ -148,37 +119,15 @@ def kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_s
     FA_ERR_INVALID_ARG on the device; unless it is FA_OK the step changed
     nothing and its slots are all -1.  check=True waits for it and raises.
     """
-    device = _device_of(new_tokens)
-    if stream is not None or device != _current_device():
-        with _there(device, stream):
+    if stream is not None:
+        with _there(new_tokens, stream):
             return kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size,
                                   max_tokens, check=check)
-    if block_table.dim() != 2 or new_tokens.dim() != 1 or free_pages.dim() != 1:
-        raise ValueError("new_tokens [B], block_table [B, max_pages], free_pages [capacity]")
-    B, M = block_table.shape
-    handle = _raw_stream(device)
-    max_tokens = int(max_tokens)
-    if max_tokens < 0:
-        raise ValueError("max_tokens must not be negative")
-    out = new_tokens.new_empty(max_tokens + 2 * B + 3, dtype=_I32)
-    at = out.data_ptr()
-    at_cu = at + 4 * max_tokens
-    at_lens = at_cu + 4 * (B + 1)
-    st = library().fa_kv_tables_step(
-        _need("new_tokens", new_tokens, _I32, (B,), device), _need("lens", lens, _I32, (B,), device),
-        _need("block_table", block_table, _I32, (B, M), device),
-        _need("free_pages", free_pages, _I32, free_pages.shape, device),
-        _need("free_count", free_count, _I32, (1,), device), B, M, free_pages.shape[0], page_size,
-        max_tokens, at, at_cu, at_lens, at_lens + 4 * B, at_lens + 4 * B + 4, handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_kv_tables_step")
-    parts = out.split_with_sizes((max_tokens, B + 1, B, 1, 1))
-    if check:
-        _checked(handle, "fa_kv_tables_step")
-        code = int(parts[4].item())
-        if code != FA_OK:
-            raise FaError(code, "fa_kv_tables_step")
-    return parts
+    out = _done(_native.tables_step(new_tokens, lens, block_table, free_pages, free_count, page_size, max_tokens),
+                "fa_kv_tables_step", check, new_tokens)
+    if check and out[4].item() != FA_OK:
+        raise FaError(out[4].item(), "fa_kv_tables_step")
+    return out
 
 
 def kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=None, stream=None,
@@ -192,32 +141,10 @@ def kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=No
     [num_pages, Hk, 2, d] int8 for kv_page_select.  The tokens of one page must
     be consecutive rows with ascending slots.
     """
-    device = _device_of(k)
-    if stream is not None or device != _current_device():
-        with _there(device, stream):
-            return kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds,
-                                   check=check)
-    shape = _cache_sizes(k_cache)
-    N, Hk, P, d = shape
-    dtype = _dtype_of(k)
-    ks, vs = _rows16("k", k, device, k.dtype), _rows16("v", v, device, k.dtype)
-    T = k.shape[0]
-    if k.shape != (T, Hk, d) or v.shape != (T, Hk, d):
-        raise ValueError(f"k and v must be [T, {Hk}, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    cache = _PACK_CACHE.pack(
-        _need("k_cache", k_cache, _E4M3, shape, device), _need("v_cache", v_cache, _E4M3, shape, device),
-        _need("k_scale", k_scale, _F32, (N, Hk), device), _need("v_scale", v_scale, _F32, (N, Hk), device),
-        0 if k_bounds is None else _need("k_bounds", k_bounds, _I8, (N, Hk, 2, d), device), N, P, Hk, d)
-    at = _need("slots", slots, _I32, (T,), device)
-    if T == 0:
-        return
-    handle = _raw_stream(device)
-    st = library().fa_kv_cache_append(cache, k.data_ptr(), v.data_ptr(), at, T, _PACK_STRIDE.pack(*ks),
-                                      _PACK_STRIDE.pack(*vs), dtype, handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_kv_cache_append")
-    if check:
-        _checked(handle, "fa_kv_cache_append")
+    if stream is not None:
+        with _there(k, stream):
+            return kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds, check=check)
+    _done(_native.append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds), "fa_kv_cache_append", check, k)
 
 
 def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_q=None,
@@ -238,66 +165,16 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     unwritten and reports it through fa_check_device_status, as in
     attention_forward.
     """
-    device = _device_of(q)
-    if stream is not None or device != _current_device():
-        with _there(device, stream):
+    if stream is not None:
+        with _there(q, stream):
             return paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_q,
                                            max_q, scale, causal, selected, selected_count, out, lse,
                                            num_splits, workspace, check=check)
-    shape = _cache_sizes(k_cache)
-    N, Hk, P, d = shape
-    dtype = _dtype_of(q)
-    qs = _rows16("q", q, device, q.dtype)
-    T, Hq, dq = q.shape
-    if dq != d or block_table.dim() != 2:
-        raise ValueError("q must be [T, Hq, d] with the cache's d, block_table [B, max_pages]")
-    B, M = block_table.shape
-    if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        os = (Hq * d, d)
-    else:
-        os = _rows16("out", out, device, q.dtype)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-    if lse is None:
-        lse = q.new_empty((T, Hq), dtype=_F32)
-        at_lse = lse.data_ptr()
-    else:
-        at_lse = _need("lse", lse, _F32, (T, Hq), device)
-    keep = at_sel = at_count = 0
-    if selected is not None:
-        if selected_count is None or selected.dim() != 3:
-            raise ValueError("selected [B, Hk, keep] comes with selected_count [B, Hk]")
-        keep = selected.shape[2]
-        at_sel = _need("selected", selected, _I32, (B, Hk, keep), device)
-        at_count = _need("selected_count", selected_count, _I32, (B, Hk), device)
-    elif selected_count is not None:
-        raise ValueError("selected_count comes with selected")
     if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    handle = _raw_stream(device)
-    fields = (q.data_ptr(), out.data_ptr(), at_lse,
-              0 if cu_q is None else _need("cu_q", cu_q, _I32, (B + 1,), device),
-              _need("block_table", block_table, _I32, (B, M), device), _need("lens", lens, _I32, (B,), device),
-              at_sel, at_count,
-              _need("k_cache", k_cache, _E4M3, shape, device), _need("v_cache", v_cache, _E4M3, shape, device),
-              _need("k_scale", k_scale, _F32, (N, Hk), device), _need("v_scale", v_scale, _F32, (N, Hk), device),
-              0, N, P, Hk, d, *qs, *os, T, B, Hq, max_q, M, keep, scale, causal, dtype, num_splits)
-    lib = library()
-    args = _PACK_ARGS.pack(*fields, 0, 0, handle)
-    nbytes = lib.fa_paged_workspace_size(args)
-    if nbytes:
-        if workspace is None:
-            workspace = q.new_empty(nbytes, dtype=torch.uint8)
-        elif workspace.get_device() != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
-        args = _PACK_ARGS.pack(*fields, workspace.data_ptr(), workspace.nbytes, handle)
-    st = lib.fa_paged_fwd(args)
-    if st != FA_OK:
-        raise FaError(st, "fa_paged_fwd")
-    if check:
-        _checked(handle, "fa_paged_fwd")
-    return out, lse
+        scale = 1.0 / math.sqrt(q.shape[-1])
+    return _done(_native.attend(q, k_cache, v_cache, k_scale, v_scale, block_table, lens, cu_q, max_q, scale, causal,
+                                selected, selected_count, out, lse, num_splits, workspace),
+                 "fa_paged_fwd", check, q)
 
 
 def kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size: int, num_selected: int,
@@ -307,31 +184,8 @@ def kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size: int, num_
     exact whole-number score of include/fa_paged.h over k_bounds
     [num_pages, Hk, 2, d]; ascending, -1 behind the last, the last token's page
     always among them."""
-    device = _device_of(q)
-    if stream is not None or device != _current_device():
-        with _there(device, stream):
-            return kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size, num_selected,
-                                  check=check)
-    dtype = _dtype_of(q)
-    qs = _rows16("q", q, device, q.dtype)
-    if k_bounds.dim() != 4 or block_table.dim() != 2:
-        raise ValueError("k_bounds [num_pages, Hk, 2, d], block_table [B, max_pages]")
-    N, Hk, _, d = k_bounds.shape
-    B, M = block_table.shape
-    Hq = q.shape[1]
-    num_selected = int(num_selected)
-    if q.shape != (B, Hq, d) or num_selected < 1:
-        raise ValueError("q must be [B, Hq, d], num_selected at least 1")
-    cache = _PACK_CACHE.pack(0, 0, _need("k_scale", k_scale, _F32, (N, Hk), device), 0,
-                             _need("k_bounds", k_bounds, _I8, (N, Hk, 2, d), device), N, page_size, Hk, d)
-    selected, count = lens.new_empty((B, Hk, num_selected), dtype=_I32), lens.new_empty((B, Hk), dtype=_I32)
-    handle = _raw_stream(device)
-    st = library().fa_kv_page_select(
-        cache, q.data_ptr(), _PACK_STRIDE.pack(*qs), _need("block_table", block_table, _I32, (B, M), device),
-        _need("lens", lens, _I32, (B,), device), B, Hq, M, num_selected, dtype, selected.data_ptr(),
-        count.data_ptr(), handle)
-    if st != FA_OK:
-        raise FaError(st, "fa_kv_page_select")
-    if check:
-        _checked(handle, "fa_kv_page_select")
-    return selected, count
+    if stream is not None:
+        with _there(q, stream):
+            return kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size, num_selected, check=check)
+    return _done(_native.page_select(q, k_bounds, k_scale, block_table, lens, page_size, num_selected),
+                 "fa_kv_page_select", check, q)

@@ -155,19 +155,6 @@ def test_select_refusals(lib, kw, want):
                                  a["keep"], a["dtype"], a["sel"], a["count"], None) == want
 
 
-def test_packed_structures_match_the_mirrors():
-    from online_softmax_tiling_gb300 import paged
-    assert paged._PACK_CACHE.size == ctypes.sizeof(fa.fa_kv_cache)
-    assert paged._PACK_ARGS.size == ctypes.sizeof(fa.fa_paged_args)
-    f = fa.fa_paged_args
-    raw = paged._PACK_ARGS.pack(*range(1, 9), *range(9, 14), *range(14, 18), *range(18, 22), *range(22, 28), 0.5,
-                                *range(29, 32), *range(32, 35))
-    a = f.from_buffer_copy(raw)
-    assert (a.q, a.selected_count, a.cache.k, a.cache.k_bounds, a.cache.num_pages, a.cache.d) == (1, 8, 9, 13, 14, 17)
-    assert (list(a.q_stride), list(a.o_stride), a.T, a.num_selected, a.scale) == ([18, 19], [20, 21], 22, 27, 0.5)
-    assert (a.causal, a.dtype, a.num_splits, a.workspace, a.workspace_bytes, a.stream) == (29, 30, 31, 32, 33, 34)
-
-
 def test_wrappers_refuse_tensors_on_the_cpu():
     import torch
     i = torch.zeros(4, dtype=torch.int32)
@@ -181,3 +168,5 @@ def test_wrappers_refuse_tensors_on_the_cpu():
                  lambda: fa.kv_page_select(q, b, s, table, i, 16, 2)):
         with pytest.raises(ValueError):
             call()
+    with pytest.raises(TypeError):
+        fa.kv_tables_step(None, i, table, i, i[:1], 16, 8)
