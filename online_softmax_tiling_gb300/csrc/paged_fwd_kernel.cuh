@@ -67,12 +67,14 @@ template <int D>
 struct DecCfg {
     static constexpr int kKeys = D == 256 ? 16 : 32;    // keys per chunk
     static constexpr int kTiles = kKeys / 16;
-    static constexpr int kStages = D == 64 ? 6 : 3;
+    static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 3;
     static constexpr int kHalf = kKeys * D;             // K or V of a chunk
     static constexpr int kRing = kStages * 2 * kHalf;   // of one warp
     static constexpr int kSub = D == 256 ? 2 : 1;       // 128-byte column groups
     static constexpr int kSteps = D / 16;               // k16 steps of q k^T
     static constexpr int kCols = D / 8;                 // n8 tiles of P V
+    static constexpr int kPieces = D / 8;               // 16-byte pieces of a query row
+    static constexpr int kRowsPass = 32 / kPieces;      // query rows a warp reads at once
     static constexpr int kAccPad = D + 8;
 };
 // Bytes of shared memory: rings (the warps' partial results reuse them), the
@@ -122,7 +124,7 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a, uint32_t rank) {
 }
 
 template <int D, int MT>
-__global__ void __launch_bounds__(kDecThreads, 2)
+__global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PagedParams p, const bool bf16) {
     using C = DecCfg<D>;
@@ -159,10 +161,24 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
     }
     int len = __ldg(p.lens + b);
+    // the query rows, on their way while the lengths and pages are looked up
+    constexpr int kQPass = 16 * MT / (kDecWarps * C::kRowsPass);
+    const int piece = lane % C::kPieces, sub_row = lane / C::kPieces;
+    const int r0 = rb * 16 * MT;
+    uint4 qv[kQPass];
+#pragma unroll
+    for (int i = 0; i < kQPass; ++i) {
+        const int pr = r0 + (i * kDecWarps + warp) * C::kRowsPass + sub_row;
+        qv[i] = make_uint4(0, 0, 0, 0);
+        if (pr < nq * p.G && piece * 8 < p.d) {
+            const int tok = pr / p.G, hg = pr - tok * p.G;
+            qv[i] = __ldg(reinterpret_cast<const uint4*>(
+                p.q + static_cast<long long>(q0 + tok) * p.q_st + static_cast<long long>(h * p.G + hg) * p.q_sh + piece * 8));
+        }
+    }
     if (len < 0 || (len >> p.page_shift) > p.max_pages || len > (p.max_pages << p.page_shift)) bad = true, len = 0;
     if (bad && tid == 0) report(kBadData);
     const int rows = nq * p.G;                 // packed rows of the request: r = i G + g
-    const int r0 = rb * 16 * MT;
     if (r0 >= rows) return;
     const int my_rows = min(16 * MT, rows - r0);
     // keys the last row of the block sees; places the range covers (with a
@@ -202,36 +218,41 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         int pos[NT];      // position of the tile's first key
         float ks[NT], ev[NT], rv[NT];  // scales: of K; log2 and reciprocal of V's
     };
-    auto fetch = [&](int k) {  // chunk index of this warp -> its tiles
+    // pages first, so that the boxes can be issued; then the scales
+    auto fetch = [&](int k) {
         Meta m;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            m.row[i] = -1, m.pos[i] = len, m.ks[i] = 0.f, m.ev[i] = 0.f, m.rv[i] = 1.f;
+            m.row[i] = -1, m.pos[i] = len;
             const int place = (c0 + warp + k * kDecWarps) * KEYS + i * 16;
-            if (k < mine && place < places) {
-                int lp = place >> p.page_shift;
-                const int off = place & ((1 << p.page_shift) - 1);
-                if (p.sel) lp = __ldg(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
-                const int pos = (lp << p.page_shift) + off;
-                if (lp < 0 || lp >= p.max_pages) {
+            if (k >= mine || place >= places) continue;
+            int lp = place >> p.page_shift;
+            const int off = place & ((1 << p.page_shift) - 1);
+            if (p.sel) lp = __ldg(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
+            const int pos = (lp << p.page_shift) + off;
+            if (lp < 0 || lp >= p.max_pages) {
+                report(kBadData);
+            } else if (pos < len) {
+                const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + lp);
+                if (page < 0 || page >= p.num_pages) {
                     report(kBadData);
-                } else if (pos < len) {
-                    const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + lp);
-                    if (page < 0 || page >= p.num_pages) {
-                        report(kBadData);
-                    } else {
-                        const int ph = page * p.Hk + h;
-                        m.row[i] = (ph << p.page_shift) + off;
-                        m.pos[i] = pos;
-                        m.ks[i] = fminf(fmaxf(__ldg(p.k_scale + ph), 0x1p-60f), 0x1p60f);
-                        const float vs = fminf(fmaxf(__ldg(p.v_scale + ph), 0x1p-60f), 0x1p60f);
-                        m.ev[i] = log2f(vs);
-                        m.rv[i] = 1.f / vs;
-                    }
+                } else {
+                    m.row[i] = ((page * p.Hk + h) << p.page_shift) + off;
+                    m.pos[i] = pos;
                 }
             }
         }
         return m;
+    };
+    auto fetch_scales = [&](Meta& m) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const int ph = max(m.row[i], 0) >> p.page_shift;
+            m.ks[i] = fminf(fmaxf(__ldg(p.k_scale + ph), 0x1p-60f), 0x1p60f);
+            const float vs = fminf(fmaxf(__ldg(p.v_scale + ph), 0x1p-60f), 0x1p60f);
+            m.ev[i] = log2f(vs);
+            m.rv[i] = 1.f / vs;
+        }
     };
     // boxes of a chunk into stage s; every chunk completes its phase (missing
     // tiles are masked, so their stage may hold anything)
@@ -259,7 +280,6 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         }
     };
     Meta cur = fetch(lane), nxt = cur;
-    if (mine > 32) nxt = fetch(32 + lane);
     auto row_of = [&](int k, int (&row)[NT]) {  // k in the current or the next block
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -277,57 +297,45 @@ __global__ void __launch_bounds__(kDecThreads, 2)
             issue(row, s);
         }
     }
+    fetch_scales(cur);
+    if (mine > 32) {
+        nxt = fetch(32 + lane);
+        fetch_scales(nxt);
+    }
 
-    // queries: each warp scales 4 MT of the block's rows and stores them in fragment order
-    {
-        // lane's channels of a row: 8 per step pair ... a row is read as 16-byte pieces
-        constexpr int PIECES = D / 8;
-        for (int r = warp; r < 16 * MT; r += kDecWarps) {
-            uint32_t u4[4] = {0, 0, 0, 0};
-            if (r < my_rows && lane < PIECES && lane * 8 < p.d) {
-                const int pr = r0 + r, i = pr / p.G, hg = pr - i * p.G;
-                const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                    p.q + static_cast<long long>(q0 + i) * p.q_st + static_cast<long long>(h * p.G + hg) * p.q_sh + lane * 8));
-                u4[0] = v.x, u4[1] = v.y, u4[2] = v.z, u4[3] = v.w;
-            }
-            float f[8], a = 0.f;
+    // queries: rows scaled to fp16 and stored in fragment order
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = unpack16(u4[e], bf16);
-                f[2 * e] = x.x, f[2 * e + 1] = x.y;
-                a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
-            }
+    for (int i = 0; i < kQPass; ++i) {
+        const int r = (i * kDecWarps + warp) * C::kRowsPass + sub_row;
+        const uint32_t u4[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+        float f[8], a = 0.f;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            // power of two that takes the largest value to [2^14, 2^15); within
-            // fp32 range for any bf16 value
-            const int e = a > 0.f && a < INFINITY ? max(-120, min(100, 14 - (static_cast<int>(__float_as_uint(a) >> 23) - 127))) : 0;
-            const float s = pow2(e);
-            if (lane == 0) row_unit[r] = pow2(-e);
-            // channel c -> step, word half, lane quarter: within 128 channels
-            // lane quarter t holds 32 t .. 32 t + 31 (d = 64: 16 t .. 16 t + 15)
-            if (lane < PIECES) {
-                constexpr int CPL = D == 64 ? 16 : 32;
-                const int c = lane * 8, cg = c / 128, cc = c % 128, t = cc / CPL, w = (cc % CPL) / 4;
-                const int mt = r / 16, rr = r % 16;
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = unpack16(u4[e], bf16);
+            f[2 * e] = x.x, f[2 * e + 1] = x.y;
+            a = fmaxf(a, fmaxf(fabsf(x.x), fabsf(x.y)));
+        }
 #pragma unroll
-                for (int e2 = 0; e2 < 2; ++e2) {  // two words of four channels
-                    const int step = cg * 8 + w + e2;
-                    uint32_t* dst = reinterpret_cast<uint32_t*>(qfrag + (mt * C::kSteps + step) * 32 + (rr & 7) * 4 + t);
-                    dst[rr >> 3] = pack_half2(f[4 * e2] * s, f[4 * e2 + 1] * s);
-                    dst[2 + (rr >> 3)] = pack_half2(f[4 * e2 + 2] * s, f[4 * e2 + 3] * s);
-                }
-            }
+        for (int o = C::kPieces / 2; o; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        // power of two that takes the largest value to [2^14, 2^15)
+        const int e = a > 0.f && a < INFINITY ? max(-120, min(100, 14 - (static_cast<int>(__float_as_uint(a) >> 23) - 127))) : 0;
+        const float s = pow2(e);
+        if (piece == 0) row_unit[r] = pow2(-e);
+        // channel c -> step, word half, lane quarter: within 128 channels
+        // lane quarter t holds 32 t .. 32 t + 31 (d = 64: 16 t .. 16 t + 15)
+        constexpr int CPL = D == 64 ? 16 : 32;
+        const int c = piece * 8, cg = c / 128, cc = c % 128, t = cc / CPL, w = (cc % CPL) / 4;
+        const int mt = r / 16, rr = r % 16;
+#pragma unroll
+        for (int e2 = 0; e2 < 2; ++e2) {  // two words of four channels
+            const int step = cg * 8 + w + e2;
+            uint32_t* dst = reinterpret_cast<uint32_t*>(qfrag + (mt * C::kSteps + step) * 32 + (rr & 7) * 4 + t);
+            dst[rr >> 3] = pack_half2(f[4 * e2] * s, f[4 * e2 + 1] * s);
+            dst[2 + (rr >> 3)] = pack_half2(f[4 * e2 + 2] * s, f[4 * e2 + 3] * s);
         }
     }
     __syncthreads();
 
-    constexpr bool kQRegs = MT == 1 && D <= 128;
-    uint4 qr[kQRegs ? C::kSteps : 1];
-    if constexpr (kQRegs) {
-#pragma unroll
-        for (int s = 0; s < C::kSteps; ++s) qr[s] = qfrag[s * 32 + lane];
-    }
     float mul[MT][2];      // score -> base-2 units, of rows g and g + 8
     int limit[MT][2];      // keys the row sees
 #pragma unroll
@@ -401,8 +409,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
                     const int step = cg * 8 + half * 4 + w;
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
-                        uint4 a;
-                        if constexpr (kQRegs) a = qr[step]; else a = qfrag[(m * C::kSteps + step) * 32 + lane];
+                        const uint4 a = qfrag[(m * C::kSteps + step) * 32 + lane];
 #pragma unroll
                         for (int j = 0; j < 2 * NT; ++j) {
                             const uint32_t x = w == 0 ? kw[j].x : w == 1 ? kw[j].y : w == 2 ? kw[j].z : kw[j].w;
@@ -513,7 +520,9 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         }
         // chunk k was the last of its block: refill that block two further on
         if ((k & 31) == 31) {
-            if (odd) nxt = fetch(k + 33 + lane); else cur = fetch(k + 33 + lane);
+            Meta m = fetch(k + 33 + lane);
+            fetch_scales(m);
+            if (odd) nxt = m; else cur = m;
         }
     }
     if (!ok) {  // let copies in flight land before the CTA ends
@@ -605,7 +614,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
     // from all of them
     cluster_sync();
     const int n4 = p.d >> 2;
-    for (int i = split * kDecThreads + tid; i < my_rows * n4; i += p.splits * kDecThreads) {
+    for (int i = tid * p.splits + split; i < my_rows * n4; i += p.splits * kDecThreads) {
         const int r = i / n4, c = (i - r * n4) * 4;
         const uint32_t stat_at = ptx::smem_addr(&cta_stat[r]), o_at = sbase + kJoin + (r * D + c) * 4;
         float2 st[kDecMaxCluster];
@@ -640,7 +649,7 @@ __global__ void __launch_bounds__(kDecThreads, 2)
         if (c == 0)
             p.lse[tok * p.Hq + hq] = l != 0.f ? (top - kWeightShift + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
-    cluster_sync();  // others may still read this CTA's results
+    cluster_sync();  // the others have read this CTA's results
 }
 
 // O = sum_s 2^(lse_s - lse) O_s, LSE = log-sum over the ranges of a row.
