@@ -178,6 +178,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     const int P = 1 << p.page_shift;
     const int t0 = blockIdx.x * p.chunk;
     if (tid == 0) n_short = 0, n_long = 0;
+    dependents_may_start();
+    wait_for_previous();
     // rows t0 .. t0 + 255: the chunk and what runs that begin in it may reach
     const int t = t0 + tid;
     const int slot = t < p.T ? __ldg(p.slots + t) : -1;

@@ -7,12 +7,14 @@
 // 256 * 127 * 112 < 2^24: exact in fp32 too), and the factor is a power of two:
 // scores carry no rounding, and their order does not depend on how the sum is
 // split.
-// A CTA takes one (request, key head): it scores the pages into shared
-// memory (as order-preserving 32-bit keys), finds the key of the
-// num_selected-th best by four passes over histograms of 8 bits, and writes
-// the indices above it, and the first of those equal to it, in ascending order.
+// A cluster takes one (request, key head): its CTAs score shares of the pages
+// into the first one's shared memory (as order-preserving 32-bit keys); that one
+// finds the key of the num_selected-th best by four passes over histograms of
+// 8 bits, and writes the indices above it, and the first of those equal to it,
+// in ascending order.
 // What bounds it: 2 d + 4 bytes per page and head from HBM when there are many
-// requests, the passes' latency for one.
+// requests; for one the dependent reads (table, then bounds), which is why
+// a group of lanes has four pages on their way at a time.
 #pragma once
 
 #include "paged_common.cuh"
@@ -22,6 +24,8 @@ namespace paged {
 
 constexpr int kSelectThreads = 512;
 constexpr int kSelectMaxPages = 32768;
+constexpr int kSelectMaxCluster = 8;
+constexpr int kSelectAhead = 4;    // pages a group of lanes has on their way
 
 struct SelectParams {
     const uint16_t* q;
@@ -31,6 +35,7 @@ struct SelectParams {
     const int* table;
     const int* lens;
     int Hk, G, d, num_pages, page_shift, max_pages, keep;
+    int cluster;      // CTAs that share a row's pages
     int* selected;
     int* count;
 };
@@ -55,17 +60,21 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
     __shared__ int warp_n[2][kSelectThreads / 32];
     constexpr int kWarps = kSelectThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.x % p.Hk, b = blockIdx.x / p.Hk;
+    const int rank = blockIdx.x % p.cluster, unit_at = blockIdx.x / p.cluster;
+    const int h = unit_at % p.Hk, b = unit_at / p.Hk;
+    dependents_may_start();
+    wait_for_previous();
     int len = __ldg(p.lens + b);
     if (len < 0 || len > (p.max_pages << p.page_shift)) {
-        if (tid == 0) report(kBadData);
+        if (tid == 0 && rank == 0) report(kBadData);
         len = min(max(len, 0), p.max_pages << p.page_shift);
     }
     const int n = (len + (1 << p.page_shift) - 1) >> p.page_shift;
-    int* out = p.selected + static_cast<long long>(blockIdx.x) * p.keep;
+    int* out = p.selected + static_cast<long long>(unit_at) * p.keep;
     if (n <= p.keep) {  // all of them
+        if (rank != 0) return;
         for (int i = tid; i < p.keep; i += kSelectThreads) out[i] = i < n ? i : -1;
-        if (tid == 0) p.count[blockIdx.x] = n;
+        if (tid == 0) p.count[unit_at] = n;
         return;
     }
     // queries to whole numbers, one warp per head of the group
@@ -106,45 +115,84 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
     const int LG = p.d <= 128 ? 8 : 16, sub = lane % LG;
     const int per_pass = kSelectThreads / LG;
     const bool on = sub * 16 < p.d;
-    for (int j0 = 0; j0 < n; j0 += per_pass) {
-        const int j = j0 + tid / LG;
-        int4 lo = make_int4(0, 0, 0, 0), hi = lo;
-        float ks = 0.f;
-        if (j < n) {
-            const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + j);
-            if (page < 0 || page >= p.num_pages) {
-                report(kBadData);
-            } else {
-                const long long ph = static_cast<long long>(page) * p.Hk + h;
-                ks = __ldg(p.k_scale + ph);
+    const int share = (n + p.cluster - 1) / p.cluster, j_end = min(n, (rank + 1) * share);
+    const int* trow = p.table + static_cast<long long>(b) * p.max_pages;
+    uint32_t keys_at = ptx::smem_addr(keys);
+    if (p.cluster > 1)  // those of the cluster's first CTA
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(keys_at) : "r"(keys_at));
+    bool bad_page = false;
+    for (int j0 = rank * share; j0 < j_end; j0 += per_pass * kSelectAhead) {
+        int page[kSelectAhead];
+        float ks[kSelectAhead];
+        int4 lo[kSelectAhead], hi[kSelectAhead];
+#pragma unroll
+        for (int i = 0; i < kSelectAhead; ++i) {
+            const int j = j0 + tid / LG + i * per_pass;
+            page[i] = j < j_end ? __ldg(trow + j) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < kSelectAhead; ++i) {
+            const bool there = static_cast<unsigned>(page[i]) < static_cast<unsigned>(p.num_pages);
+            bad_page |= !there;
+            ks[i] = 0.f;
+            lo[i] = hi[i] = make_int4(0, 0, 0, 0);
+            if (there && j0 + tid / LG + i * per_pass < j_end) {
+                const long long ph = static_cast<long long>(page[i]) * p.Hk + h;
+                ks[i] = __ldg(p.k_scale + ph);
                 if (on) {
                     const int4* bd = reinterpret_cast<const int4*>(p.bounds + ph * 2 * p.d) + sub;
-                    lo = __ldg(bd);
-                    hi = __ldg(bd + (p.d >> 4));
+                    lo[i] = __ldg(bd);
+                    hi[i] = __ldg(bd + (p.d >> 4));
                 }
             }
         }
-        float best = -INFINITY;
+        float best[kSelectAhead];
+#pragma unroll
+        for (int i = 0; i < kSelectAhead; ++i) best[i] = -INFINITY;
         for (int g = 0; g < p.G; ++g) {
-            int acc = 0;
+            uint4 a = make_uint4(0, 0, 0, 0), c = a;
             if (on) {
-                const uint4 a = *reinterpret_cast<const uint4*>(qpos + g * dw + sub * 4);
-                const uint4 c = *reinterpret_cast<const uint4*>(qneg + g * dw + sub * 4);
-                acc = __dp4a(hi.x, static_cast<int>(a.x), acc);
-                acc = __dp4a(hi.y, static_cast<int>(a.y), acc);
-                acc = __dp4a(hi.z, static_cast<int>(a.z), acc);
-                acc = __dp4a(hi.w, static_cast<int>(a.w), acc);
-                acc = __dp4a(lo.x, static_cast<int>(c.x), acc);
-                acc = __dp4a(lo.y, static_cast<int>(c.y), acc);
-                acc = __dp4a(lo.z, static_cast<int>(c.z), acc);
-                acc = __dp4a(lo.w, static_cast<int>(c.w), acc);
+                a = *reinterpret_cast<const uint4*>(qpos + g * dw + sub * 4);
+                c = *reinterpret_cast<const uint4*>(qneg + g * dw + sub * 4);
             }
-            for (int o = LG >> 1; o; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-            best = fmaxf(best, static_cast<float>(acc) * (unit[g] * ks));
+            const float u = unit[g];
+#pragma unroll
+            for (int i = 0; i < kSelectAhead; ++i) {
+                int acc = 0;
+                acc = __dp4a(hi[i].x, static_cast<int>(a.x), acc);
+                acc = __dp4a(hi[i].y, static_cast<int>(a.y), acc);
+                acc = __dp4a(hi[i].z, static_cast<int>(a.z), acc);
+                acc = __dp4a(hi[i].w, static_cast<int>(a.w), acc);
+                acc = __dp4a(lo[i].x, static_cast<int>(c.x), acc);
+                acc = __dp4a(lo[i].y, static_cast<int>(c.y), acc);
+                acc = __dp4a(lo[i].z, static_cast<int>(c.z), acc);
+                acc = __dp4a(lo[i].w, static_cast<int>(c.w), acc);
+                acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+                acc += __shfl_xor_sync(0xffffffffu, acc, 2);
+                acc += __shfl_xor_sync(0xffffffffu, acc, 4);
+                if (LG == 16) acc += __shfl_xor_sync(0xffffffffu, acc, 8);
+                best[i] = fmaxf(best[i], static_cast<float>(acc) * (u * ks[i]));
+            }
         }
-        if (sub == 0 && j < n) keys[j] = j == n - 1 ? 0xFFFFFFFFu : ordered(best + 0.f);  // -0 counts as 0
+#pragma unroll
+        for (int i = 0; i < kSelectAhead; ++i) {
+            const int j = j0 + tid / LG + i * per_pass;
+            if (sub == 0 && j < j_end) {
+                const uint32_t key = j == n - 1 ? 0xFFFFFFFFu : ordered(best[i] + 0.f);  // -0 counts as 0
+                if (p.cluster > 1)
+                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys_at + 4 * j), "r"(key) : "memory");
+                else
+                    keys[j] = key;
+            }
+        }
     }
-    __syncthreads();
+    if (bad_page) report(kBadData);
+    if (p.cluster > 1) {
+        cluster_sync();
+        if (rank != 0) return;
+    } else {
+        __syncthreads();
+    }
 
     // the key of the keep-th best: 8 bits at a time from the top
     uint32_t prefix = 0, mask = 0, left = p.keep;
@@ -202,7 +250,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
         base = ab_all, base_eq = eq_all;
         __syncthreads();
     }
-    if (tid == 0) p.count[blockIdx.x] = p.keep;
+    if (tid == 0) p.count[unit_at] = p.keep;
 }
 
 }  // namespace paged

@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P1 = (1 << p.page_shift) - 1;
     if (tid == 0) bad = 0;
+    dependents_may_start();
+    wait_for_previous();
     __syncthreads();
 
     auto request = [&](int b, int& add, int& need, int& back) {

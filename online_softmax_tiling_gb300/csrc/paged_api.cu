@@ -68,6 +68,25 @@ bool ensure_smem(const void* fn, int smem, int device) {
     return true;
 }
 
+// Launch as a programmatic dependent of the kernel before it in the stream,
+// in clusters of `cluster` CTAs.
+bool launch(const void* fn, int64_t ctas, int grid_y, int threads, int smem, int cluster, void* stream, void** args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(grid_y));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess;
+}
+
 int sm_count() {
     int device = 0, sms = 152;
     if (cudaGetDevice(&device) != cudaSuccess ||
@@ -114,14 +133,14 @@ bool bad_strides(const long long* s) {
 // Kernel width that serves d.
 int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 
-// 16-row tiles a CTA holds: two where a request's packed rows fill more than
-// one (each key is then read half as often); one for d > 128, where a second
-// accumulator does not fit the registers.
-int tiles_of(int width, int64_t rows) { return width == 256 || rows <= 16 ? 1 : 2; }
+// Packed rows a CTA holds: 8 or 16 where those of a request fit, else 32 (each
+// key is then read half as often as with 16), but 16 for d > 128, where a
+// second accumulator does not fit the registers.
+int block_rows_of(int width, int64_t rows) { return rows <= 8 ? 8 : width == 256 || rows <= 16 ? 16 : 32; }
 
 struct Plan {
     bool prompt;    // tcgen05 kernel (256 packed rows per unit)
-    int width, mt, row_blocks;
+    int width, block_rows, row_blocks;
     int64_t units;  // row blocks x heads x requests
 };
 
@@ -132,10 +151,9 @@ Plan plan_of(const fa_paged_args& a) {
     Plan pl;
     const int64_t rows = static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk);
     pl.width = width_of(a.cache.d);
-    pl.mt = tiles_of(pl.width, rows);
     pl.prompt = pl.width <= 128 && rows > kPromptRows;
-    const int block = pl.prompt ? pg::kPrRows : 16 * pl.mt;
-    pl.row_blocks = static_cast<int>((rows + block - 1) / block);
+    pl.block_rows = pl.prompt ? pg::kPrRows : block_rows_of(pl.width, rows);
+    pl.row_blocks = static_cast<int>((rows + pl.block_rows - 1) / pl.block_rows);
     pl.units = static_cast<int64_t>(pl.row_blocks) * a.cache.Hk * a.B;
     return pl;
 }
@@ -155,13 +173,18 @@ int choose_splits(const fa_paged_args& a, const Plan& pl) {
         if (2 * pl.units > sms) return 1;
         return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.units, keys / 512, FA_PAGED_MAX_SPLITS})));
     }
-    // two CTAs per SM, and several rounds of them where there are many keys
-    // (requests differ in length); a cluster's count where that fills the GPU
-    const int64_t most = std::max<int64_t>(1, keys / 256);
-    const int64_t want = std::min<int64_t>(most, (4 * sms + pl.units - 1) / pl.units);
+    // One wave of about two CTAs per SM, in a count that a cluster can join;
+    // each range of at least 256 keys.
     int s = 1;
-    while (s < pg::kDecMaxCluster && s < want) s *= 2;
-    if (s == pg::kDecMaxCluster && want > 4 * s) s = static_cast<int>(std::min<int64_t>(want, FA_PAGED_MAX_SPLITS));
+    while (s < pg::kDecMaxCluster && 2 * s * pl.units <= 2 * sms && keys >= 2 * s * 256) s *= 2;
+    // Few heads and a long context: more ranges than a cluster holds, through a
+    // workspace (one request of 8 key heads and 65536 keys: 37 us with 32, 55 with 16).
+    if (s == pg::kDecMaxCluster && s * pl.units < sms)
+        while (s < FA_PAGED_MAX_SPLITS && 2 * s * pl.units <= 2 * sms && keys >= 2 * s * 1024) s *= 2;
+    // Many units of long and probably unequal contexts: several waves of ranges
+    // of at least 4096 keys even them out (64 requests of 5000 to 16384 keys:
+    // 234 us with 4, 251 with 2, 274 with 1).
+    while (s < pg::kDecMaxCluster && s * pl.units >= 2 * sms && s * pl.units < 12 * sms && keys >= 2 * s * 4096) s *= 2;
     return s;
 }
 
@@ -179,14 +202,14 @@ struct KernelEntry {
     const void* fn;
     int smem;
 };
-KernelEntry select_kernel(int width, int mt) {
-    if (width == 64)
-        return mt == 1 ? KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<64, 1>), pg::dec_smem<64, 1>()}
-                       : KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<64, 2>), pg::dec_smem<64, 2>()};
-    if (width == 128)
-        return mt == 1 ? KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<128, 1>), pg::dec_smem<128, 1>()}
-                       : KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<128, 2>), pg::dec_smem<128, 2>()};
-    return KernelEntry{reinterpret_cast<const void*>(&pg::paged_fwd_kernel<256, 1>), pg::dec_smem<256, 1>()};
+template <int D, int R>
+KernelEntry few_rows() {
+    return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R>), pg::dec_smem<D, R>()};
+}
+KernelEntry select_kernel(int width, int rows) {
+    if (width == 64) return rows == 8 ? few_rows<64, 8>() : rows == 16 ? few_rows<64, 16>() : few_rows<64, 32>();
+    if (width == 128) return rows == 8 ? few_rows<128, 8>() : rows == 16 ? few_rows<128, 16>() : few_rows<128, 32>();
+    return rows == 8 ? few_rows<256, 8>() : few_rows<256, 16>();
 }
 
 int check_args(const fa_paged_args& a) {
@@ -251,9 +274,7 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
     const int64_t work = std::max<int64_t>(max_tokens, 2 * static_cast<int64_t>(B));
     const int64_t ctas = std::min<int64_t>((work + 4 * pg::kTablesThreads - 1) / (4 * pg::kTablesThreads), sm_count());
     void* args[] = {&p};
-    if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(std::max<int64_t>(1, ctas))), dim3(pg::kTablesThreads), args,
-                         static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return FA_ERR_CUDA;
+    if (!launch(fn, std::max<int64_t>(1, ctas), 1, pg::kTablesThreads, smem, 1, stream, args)) return FA_ERR_CUDA;
     return FA_OK;
 }
 
@@ -288,8 +309,7 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
     else
         fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<16, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<16, false>);
     void* args[] = {&p};
-    const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(T) + p.chunk - 1) / p.chunk), static_cast<unsigned>(2 * p.Hk));
-    if (cudaLaunchKernel(fn, grid, dim3(pg::kAppendThreads), args, 0, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (!launch(fn, (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk, 2 * p.Hk, pg::kAppendThreads, 0, 1, stream, args))
         return FA_ERR_CUDA;
     return FA_OK;
 }
@@ -349,47 +369,24 @@ int fa_paged_fwd(const fa_paged_args* args) {
     p.o_part = need > 0 ? static_cast<float*>(a.workspace) : nullptr;
     p.lse_part = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + part_bytes(rows, splits, a.cache.d)) : nullptr;
     bool bf16 = a.dtype == FA_BF16;
-    const cudaStream_t stream = static_cast<cudaStream_t>(a.stream);
     if (pl.prompt) {
         const uint8_t *kc = static_cast<const uint8_t*>(a.cache.k), *vc = static_cast<const uint8_t*>(a.cache.v);
         const void* fn = pl.width == 64 ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<64>)
                                         : reinterpret_cast<const void*>(&pg::paged_prompt_kernel<128>);
         const int smem = pl.width == 64 ? pg::PrCfg<64>::kSmem : pg::PrCfg<128>::kSmem;
         void* kargs[] = {&kc, &vc, &p, &bf16};
-        if (!ensure_smem(fn, smem, device) ||
-            cudaLaunchKernel(fn, dim3(static_cast<unsigned>(units)), dim3(pg::kPrThreads), kargs,
-                             static_cast<size_t>(smem), stream) != cudaSuccess)
-            return FA_ERR_CUDA;
+        if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, pg::kPrThreads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
     } else {
-        const KernelEntry ke = select_kernel(pl.width, pl.mt);
+        const KernelEntry ke = select_kernel(pl.width, pl.block_rows);
         void* kargs[] = {&tk, &tv, &p, &bf16};
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(p.in_cluster ? splits : 1);
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(units));
-        cfg.blockDim = dim3(pg::kDecThreads);
-        cfg.dynamicSmemBytes = static_cast<size_t>(ke.smem);
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        if (!ensure_smem(ke.fn, ke.smem, device) || cudaLaunchKernelExC(&cfg, ke.fn, kargs) != cudaSuccess)
+        if (!ensure_smem(ke.fn, ke.smem, device) ||
+            !launch(ke.fn, units, 1, pg::kDecThreads, ke.smem, p.in_cluster ? splits : 1, a.stream, kargs))
             return FA_ERR_CUDA;
     }
     if (need > 0) {
-        // set up while the attention kernel runs; waits for its end by itself
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>((rows + pg::kMergeWarps - 1) / pg::kMergeWarps));
-        cfg.blockDim = dim3(32 * pg::kMergeWarps);
-        cfg.stream = stream;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
         void* margs[] = {&p, &bf16};
-        if (cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(&pg::paged_merge_kernel), margs) != cudaSuccess)
+        if (!launch(reinterpret_cast<const void*>(&pg::paged_merge_kernel), (rows + pg::kMergeWarps - 1) / pg::kMergeWarps, 1,
+                    32 * pg::kMergeWarps, 0, 1, a.stream, margs))
             return FA_ERR_CUDA;
     }
     return FA_OK;
@@ -427,10 +424,13 @@ int fa_kv_page_select(const fa_kv_cache* cache, const void* q, const long long* 
                                       : reinterpret_cast<const void*>(&pg::kv_page_select_kernel<false>);
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess || !ensure_smem(fn, 200 * 1024, device)) return FA_ERR_CUDA;
+    // about 256 pages per CTA, what its groups of lanes have on their way at once
+    p.cluster = 1;
+    while (p.cluster < pg::kSelectMaxCluster && p.cluster * 256 < max_pages) p.cluster *= 2;
+    const int64_t ctas = static_cast<int64_t>(B) * p.Hk * p.cluster;
+    if (ctas > INT32_MAX) return FA_ERR_INVALID_ARG;
     void* args[] = {&p};
-    if (cudaLaunchKernel(fn, dim3(static_cast<unsigned>(B * p.Hk)), dim3(pg::kSelectThreads), args,
-                         static_cast<size_t>(smem), static_cast<cudaStream_t>(stream)) != cudaSuccess)
-        return FA_ERR_CUDA;
+    if (!launch(fn, ctas, 1, pg::kSelectThreads, static_cast<int>(smem), p.cluster, stream, args)) return FA_ERR_CUDA;
     return FA_OK;
 }
 

@@ -44,6 +44,17 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
 }
 
+// Every kernel here is a programmatic dependent launch: it may be set up while
+// the kernel before it in the stream still runs, and reads or writes
+// global memory only behind wait_for_previous (that kernel's end, its writes visible).
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Barrier of a cluster's CTAs; shared memory writes before it are seen behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Exponent of the smallest power of two s in [2^-60, 2^60] with a <= top s,
 // for top = (1 + top_mant / 2^23) 2^top_exp and a finite a >= 0: compares the
 // mantissa and subtracts the exponents (a below 2^-126 gives -60).

@@ -14,7 +14,7 @@
 // out nothing above 2^-38 of that value.
 //
 // Mapping.  The G query heads of a key head (times the request's new tokens)
-// are packed rows; a CTA takes 16 or 32 of them and a range of keys.  Its four
+// are packed rows; a CTA takes 8, 16 or 32 of them and a range of keys.  Its four
 // warps take 32-key chunks in turn (16-key ones for d > 128), each
 // with a TMA ring, a running softmax and an accumulator of its own; nothing
 // is shared until the end, where the four partial results are joined in
@@ -27,7 +27,10 @@
 // 16-byte reads free of bank conflicts (lane (g, t) reads key g, channels
 // 32 t ..; for V keys 2t, 2t+1, 2t+8, 2t+9, channels 16 g ..): channel and key
 // orders inside a product are free as long as both operands agree, so the
-// fragments need no shuffles.
+// fragments need no shuffles.  With 16 or 32 rows the queries are the products'
+// first operand (M = rows); with 8 the codes are (M = keys, then channels, and
+// N = 8 rows), which takes half the mma instructions and accumulators and turns
+// the 8 x 8 blocks of weights with movmatrix in between.
 #pragma once
 
 #include "paged_common.cuh"
@@ -63,9 +66,10 @@ struct PagedParams {
     float* lse_part;  // [T * Hq][splits], log2 units
 };
 
-template <int D>
+template <int D, int R>
 struct DecCfg {
     static constexpr int kKeys = D == 256 ? 16 : 32;    // keys per chunk
+    static constexpr int kMinCtas = D == 256 || R == 32 ? 2 : 3;  // per SM
     static constexpr int kTiles = kKeys / 16;
     static constexpr int kStages = D == 64 ? 4 : D == 128 ? 2 : 3;
     static constexpr int kHalf = kKeys * D;             // K or V of a chunk
@@ -79,11 +83,12 @@ struct DecCfg {
 };
 // Bytes of shared memory: rings (the warps' partial results reuse them), the
 // queries in fragment order, barriers.
-template <int D, int MT>
+template <int D, int R>
 constexpr int dec_smem() {
-    const int ring = kDecWarps * DecCfg<D>::kRing;
-    const int join = kDecWarps * (16 * MT * DecCfg<D>::kAccPad + 16 * MT * 2) * 4 + 16 * MT * D * 4;
-    return (ring > join ? ring : join) + MT * DecCfg<D>::kSteps * 32 * 16 + kDecWarps * DecCfg<D>::kStages * 8 + 1024;
+    using C = DecCfg<D, R>;
+    const int ring = kDecWarps * C::kRing;
+    const int join = kDecWarps * (R * C::kAccPad + R * 2) * 4 + R * D * 4;
+    return (ring > join ? ring : join) + R * C::kSteps * 32 + kDecWarps * C::kStages * 8 + 1024;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -106,9 +111,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t a) {
     return v;
 }
 
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // What CTA `rank` of the cluster has at the shared address `a` of this one.
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t a, uint32_t rank) {
     float2 v;
@@ -123,28 +125,40 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t a, uint32_t rank) {
     return v;
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
+// Transposes an 8 x 8 block of 16-bit values held two per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// R: rows of a CTA's block (8, 16 or 32)
+template <int D, int R>
+__global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PagedParams p, const bool bf16) {
-    using C = DecCfg<D>;
+    using C = DecCfg<D, R>;
+    constexpr bool kTurned = R == 8;    // codes first, rows as N
+    constexpr int MT = R / 16;          // 16-row tiles (not kTurned)
     constexpr int NST = C::kStages, KEYS = C::kKeys, NT = C::kTiles;
     extern __shared__ __align__(16) uint8_t dec_raw[];
     const uint32_t raw = ptx::smem_addr(dec_raw);
     uint8_t* smem = dec_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = ptx::smem_addr(smem);
     constexpr int kRings = kDecWarps * C::kRing;
-    constexpr int kJoin = kDecWarps * (16 * MT * C::kAccPad + 16 * MT * 2) * 4;
-    constexpr int kJoinAll = kJoin + 16 * MT * D * 4;  // and the CTA's joined result
+    constexpr int kJoin = kDecWarps * (R * C::kAccPad + R * 2) * 4;
+    constexpr int kJoinAll = kJoin + R * D * 4;  // and the CTA's joined result
     constexpr int kOffQ = kRings > kJoinAll ? kRings : kJoinAll;
-    constexpr int kOffBar = kOffQ + MT * C::kSteps * 32 * 16;
-    uint4* qfrag = reinterpret_cast<uint4*>(smem + kOffQ);  // [MT][step][lane]
-    __shared__ float row_unit[16 * MT];                     // 2^-e of each row's query scaling
-    __shared__ __align__(8) float2 cta_stat[16 * MT];       // this CTA's maximum and sum of each row
+    constexpr int kOffBar = kOffQ + R * C::kSteps * 32;
+    uint4* qfrag = reinterpret_cast<uint4*>(smem + kOffQ);  // [MT][step][lane], or 8-byte [step][lane]
+    __shared__ float row_unit[R];                           // 2^-e of each row's query scaling
+    __shared__ __align__(8) float2 cta_stat[R];             // this CTA's maximum and sum of each row
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
 
+    dependents_may_start();
+    wait_for_previous();
     // unit: range fastest (a cluster's CTAs), then row block (they read the same keys), head, request
     int u = blockIdx.x;
     const int split = u % p.splits;
@@ -162,15 +176,15 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
     }
     int len = __ldg(p.lens + b);
     // the query rows, on their way while the lengths and pages are looked up
-    constexpr int kQPass = 16 * MT / (kDecWarps * C::kRowsPass);
+    constexpr int kQPass = (R + kDecWarps * C::kRowsPass - 1) / (kDecWarps * C::kRowsPass);
     const int piece = lane % C::kPieces, sub_row = lane / C::kPieces;
-    const int r0 = rb * 16 * MT;
+    const int r0 = rb * R;
     uint4 qv[kQPass];
 #pragma unroll
     for (int i = 0; i < kQPass; ++i) {
-        const int pr = r0 + (i * kDecWarps + warp) * C::kRowsPass + sub_row;
+        const int r = (i * kDecWarps + warp) * C::kRowsPass + sub_row, pr = r0 + r;
         qv[i] = make_uint4(0, 0, 0, 0);
-        if (pr < nq * p.G && piece * 8 < p.d) {
+        if (r < R && pr < nq * p.G && piece * 8 < p.d) {
             const int tok = pr / p.G, hg = pr - tok * p.G;
             qv[i] = __ldg(reinterpret_cast<const uint4*>(
                 p.q + static_cast<long long>(q0 + tok) * p.q_st + static_cast<long long>(h * p.G + hg) * p.q_sh + piece * 8));
@@ -180,7 +194,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
     if (bad && tid == 0) report(kBadData);
     const int rows = nq * p.G;                 // packed rows of the request: r = i G + g
     if (r0 >= rows) return;
-    const int my_rows = min(16 * MT, rows - r0);
+    const int my_rows = min(R, rows - r0);
     // keys the last row of the block sees; places the range covers (with a
     // selection, places in the concatenated selected pages)
     const int last_i = (r0 + my_rows - 1) / p.G;
@@ -320,6 +334,7 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
         // power of two that takes the largest value to [2^14, 2^15)
         const int e = a > 0.f && a < INFINITY ? max(-120, min(100, 14 - (static_cast<int>(__float_as_uint(a) >> 23) - 127))) : 0;
         const float s = pow2(e);
+        if (r >= R) continue;
         if (piece == 0) row_unit[r] = pow2(-e);
         // channel c -> step, word half, lane quarter: within 128 channels
         // lane quarter t holds 32 t .. 32 t + 31 (d = 64: 16 t .. 16 t + 15)
@@ -329,41 +344,52 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
 #pragma unroll
         for (int e2 = 0; e2 < 2; ++e2) {  // two words of four channels
             const int step = cg * 8 + w + e2;
-            uint32_t* dst = reinterpret_cast<uint32_t*>(qfrag + (mt * C::kSteps + step) * 32 + (rr & 7) * 4 + t);
-            dst[rr >> 3] = pack_half2(f[4 * e2] * s, f[4 * e2 + 1] * s);
-            dst[2 + (rr >> 3)] = pack_half2(f[4 * e2 + 2] * s, f[4 * e2 + 3] * s);
+            if constexpr (kTurned) {
+                reinterpret_cast<uint2*>(qfrag)[step * 32 + r * 4 + t] =
+                    make_uint2(pack_half2(f[4 * e2] * s, f[4 * e2 + 1] * s), pack_half2(f[4 * e2 + 2] * s, f[4 * e2 + 3] * s));
+            } else {
+                uint32_t* dst = reinterpret_cast<uint32_t*>(qfrag + (mt * C::kSteps + step) * 32 + (rr & 7) * 4 + t);
+                dst[rr >> 3] = pack_half2(f[4 * e2] * s, f[4 * e2 + 1] * s);
+                dst[2 + (rr >> 3)] = pack_half2(f[4 * e2 + 2] * s, f[4 * e2 + 3] * s);
+            }
         }
     }
     __syncthreads();
 
-    float mul[MT][2];      // score -> base-2 units, of rows g and g + 8
-    int limit[MT][2];      // keys the row sees
-#pragma unroll
-    for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int r = 16 * m + 8 * e + g;
-            mul[m][e] = row_unit[r] * p.scale_log2;
-            limit[m][e] = r < my_rows ? (p.causal ? min(len, len - nq + (r0 + r) / p.G + 1) : len) : 0;
-        }
+    // the rows a lane holds: g and g + 8 of each tile, or 2 t and 2 t + 1
+    constexpr int NR = kTurned ? 1 : MT;
+    auto row_at = [&](int m, int e) { return kTurned ? 2 * t4 + e : 16 * m + 8 * e + g; };
+    float mul[NR][2];      // score -> base-2 units
+    int limit[NR][2];      // keys the row sees
     int min_limit = len;
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NR; ++m)
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (16 * m + 8 * e + g < my_rows) min_limit = min(min_limit, limit[m][e]);
+        for (int e = 0; e < 2; ++e) {
+            const int r = row_at(m, e);
+            mul[m][e] = row_unit[r] * p.scale_log2;
+            limit[m][e] = r < my_rows ? (p.causal ? min(len, len - nq + (r0 + r) / p.G + 1) : len) : 0;
+            if (r < my_rows) min_limit = min(min_limit, limit[m][e]);
+        }
     min_limit = __reduce_min_sync(0xffffffffu, min_limit);  // every row of the block sees keys below it
 
-    float acc[MT][C::kCols][4];
-    float mx[MT][2], sum[MT][2];
+    // accumulators: n8 tiles of channels, or m16 tiles of channels by 8 rows
+    constexpr int NA = kTurned ? D / 16 : C::kCols;
+    float acc[NR][NA][4];
+    float mx[NR][2], sum[NR][2];
 #pragma unroll
-    for (int m = 0; m < MT; ++m) {
+    for (int m = 0; m < NR; ++m) {
 #pragma unroll
-        for (int c = 0; c < C::kCols; ++c)
+        for (int c = 0; c < NA; ++c)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[m][c][e] = 0.f;
         mx[m][0] = mx[m][1] = -INFINITY;
         sum[m][0] = sum[m][1] = 0.f;
+    }
+    uint2 qt[kTurned ? C::kSteps : 1];
+    if constexpr (kTurned) {
+#pragma unroll
+        for (int i = 0; i < C::kSteps; ++i) qt[i] = reinterpret_cast<const uint2*>(qfrag)[i * 32 + lane];
     }
 
     bool ok = true;
@@ -383,12 +409,14 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
             ev[i] = __shfl_sync(0xffffffffu, odd ? nxt.ev[i] : cur.ev[i], k & 31);
             rv[i] = __shfl_sync(0xffffffffu, odd ? nxt.rv[i] : cur.rv[i], k & 31);
         }
-        // ---- scores of 16 MT rows and KEYS keys: n8 tile j holds keys 8 j + ...
-        float sc[MT][2 * NT][4];
+        // ---- scores.  Rows first: n8 tile j holds keys 8 j + ... of rows g, g + 8;
+        // codes first: m16 tile i holds keys 16 i + g and + 8 of rows 2 t, 2 t + 1
+        constexpr int NS = kTurned ? NT : 2 * NT;
+        float sc[NR][NS][4];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NR; ++m)
 #pragma unroll
-            for (int j = 0; j < 2 * NT; ++j)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) sc[m][j][e] = 0.f;
 #pragma unroll
@@ -407,6 +435,16 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const int step = cg * 8 + half * 4 + w;
+                    if constexpr (kTurned) {
+#pragma unroll
+                        for (int i = 0; i < NT; ++i) {
+                            const uint4 &k0 = kw[2 * i], &k1 = kw[2 * i + 1];
+                            const uint32_t x = w == 0 ? k0.x : w == 1 ? k0.y : w == 2 ? k0.z : k0.w;
+                            const uint32_t y = w == 0 ? k1.x : w == 1 ? k1.y : w == 2 ? k1.z : k1.w;
+                            mma_f16(sc[0][i], e4m3x2_to_half2(x & 0xFFFFu), e4m3x2_to_half2(y & 0xFFFFu), e4m3x2_to_half2(x >> 16),
+                                    e4m3x2_to_half2(y >> 16), qt[step].x, qt[step].y);
+                        }
+                    } else {
 #pragma unroll
                     for (int m = 0; m < MT; ++m) {
                         const uint4 a = qfrag[(m * C::kSteps + step) * 32 + lane];
@@ -416,59 +454,70 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
                             mma_f16(sc[m][j], a.x, a.y, a.z, a.w, e4m3x2_to_half2(x & 0xFFFFu), e4m3x2_to_half2(x >> 16));
                         }
                     }
+                    }
                 }
             }
         }
-        // ---- weights
-        uint32_t pa[MT][NT][4];
+        // ---- weights.  Element e of a score tile: row e >> 1 and key e & 1 of the
+        // lane's, or row e & 1 and key e >> 1 where the codes come first
+        uint32_t pa[NR][NT][4];
         bool edge = false;
 #pragma unroll
         for (int i = 0; i < NT; ++i) edge |= row[i] < 0 || pos[i] + 16 > min_limit;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
+        for (int m = 0; m < NR; ++m) {
             float top[2] = {mx[m][0], mx[m][1]};
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-                for (int j = 2 * i; j < 2 * i + 2; ++j)
+                for (int e = 0; e < 4; ++e) {
+                    const int i = kTurned ? j : j / 2, r = kTurned ? e & 1 : e >> 1;
+                    const int key = kTurned ? g + 8 * (e >> 1) : 8 * (j & 1) + 2 * t4 + (e & 1);
+                    float x = fmaf(sc[m][j][e], mul[m][r] * kf[i], ev[i]);
+                    if (edge && (row[i] < 0 || pos[i] + key >= limit[m][r])) x = -INFINITY;
+                    sc[m][j][e] = x;
+                    top[r] = fmaxf(top[r], x);
+                }
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = fmaf(sc[m][j][e], mul[m][e >> 1] * kf[i], ev[i]);
-                        if (edge && (row[i] < 0 || pos[i] + 8 * (j & 1) + 2 * t4 + (e & 1) >= limit[m][e >> 1])) x = -INFINITY;
-                        sc[m][j][e] = x;
-                        top[e >> 1] = fmaxf(top[e >> 1], x);
-                    }
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
-                top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-            }
+                for (int o = kTurned ? 4 : 1; o < (kTurned ? 32 : 4); o *= 2)
+                    top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], o));
             const float ref[2] = {top[0] == -INFINITY ? 0.f : top[0] - kWeightShift,
                                   top[1] == -INFINITY ? 0.f : top[1] - kWeightShift};
-            const float al[2] = {ptx::ex2_approx(mx[m][0] - (top[0] == -INFINITY ? 0.f : top[0])),
-                                 ptx::ex2_approx(mx[m][1] - (top[1] == -INFINITY ? 0.f : top[1]))};
             if (__any_sync(0xffffffffu, top[0] != mx[m][0] || top[1] != mx[m][1])) {
+                const float al[2] = {ptx::ex2_approx(mx[m][0] - (top[0] == -INFINITY ? 0.f : top[0])),
+                                     ptx::ex2_approx(mx[m][1] - (top[1] == -INFINITY ? 0.f : top[1]))};
 #pragma unroll
-                for (int c = 0; c < C::kCols; ++c) {
-                    acc[m][c][0] *= al[0], acc[m][c][1] *= al[0];
-                    acc[m][c][2] *= al[1], acc[m][c][3] *= al[1];
-                }
+                for (int c = 0; c < NA; ++c)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[m][c][e] *= al[kTurned ? e & 1 : e >> 1];
                 sum[m][0] *= al[0], sum[m][1] *= al[1];
                 mx[m][0] = top[0], mx[m][1] = top[1];
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                float w[8];
+                if constexpr (kTurned) {
+                    float w[4];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
+                    for (int e = 0; e < 4; ++e) w[e] = ptx::ex2_approx(sc[m][i][e] - ref[e & 1]);
+                    sum[m][0] = fmaf(w[0] + w[2], rv[i], sum[m][0]);
+                    sum[m][1] = fmaf(w[1] + w[3], rv[i], sum[m][1]);
+                    pa[m][i][0] = transpose8x8(pack_half2(w[0], w[1]));  // keys 2t, 2t + 1 of row g
+                    pa[m][i][1] = transpose8x8(pack_half2(w[2], w[3]));  // keys 2t + 8, 2t + 9
+                } else {
+                    float w[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[4 * j + e] = ptx::ex2_approx(sc[m][2 * i + j][e] - ref[e >> 1]);
-                sum[m][0] = fmaf((w[0] + w[1]) + (w[4] + w[5]), rv[i], sum[m][0]);
-                sum[m][1] = fmaf((w[2] + w[3]) + (w[6] + w[7]), rv[i], sum[m][1]);
-                pa[m][i][0] = pack_half2(w[0], w[1]);
-                pa[m][i][1] = pack_half2(w[2], w[3]);
-                pa[m][i][2] = pack_half2(w[4], w[5]);
-                pa[m][i][3] = pack_half2(w[6], w[7]);
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) w[4 * j + e] = ptx::ex2_approx(sc[m][2 * i + j][e] - ref[e >> 1]);
+                    sum[m][0] = fmaf((w[0] + w[1]) + (w[4] + w[5]), rv[i], sum[m][0]);
+                    sum[m][1] = fmaf((w[2] + w[3]) + (w[6] + w[7]), rv[i], sum[m][1]);
+                    pa[m][i][0] = pack_half2(w[0], w[1]);
+                    pa[m][i][1] = pack_half2(w[2], w[3]);
+                    pa[m][i][2] = pack_half2(w[4], w[5]);
+                    pa[m][i][3] = pack_half2(w[6], w[7]);
+                }
             }
         }
         // ---- U += P V, 16 keys at a time
@@ -503,11 +552,18 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
                                             e4m3x2_to_half2(l1 & 0xFFFFu), e4m3x2_to_half2(l1 >> 16)};
                     const uint32_t b1[4] = {e4m3x2_to_half2(h0 & 0xFFFFu), e4m3x2_to_half2(h0 >> 16),
                                             e4m3x2_to_half2(h1 & 0xFFFFu), e4m3x2_to_half2(h1 >> 16)};
+                    if constexpr (kTurned) {
+                        // rows (channels) 2 c and 2 c + 1 of the lane's, 8 c apart in the tile
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
+                        for (int c = 0; c < 2; ++c)
+                            mma_f16(acc[0][cg * 8 + 2 * w + c], b0[2 * c], b0[2 * c + 1], b1[2 * c], b1[2 * c + 1], pa[0][i][0], pa[0][i][1]);
+                    } else {
 #pragma unroll
-                        for (int m = 0; m < MT; ++m)
-                            mma_f16(acc[m][cg * 16 + 4 * w + c], pa[m][i][0], pa[m][i][1], pa[m][i][2], pa[m][i][3], b0[c], b1[c]);
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+                                mma_f16(acc[m][cg * 16 + 4 * w + c], pa[m][i][0], pa[m][i][1], pa[m][i][2], pa[m][i][3], b0[c], b1[c]);
+                    }
                 }
             }
         }
@@ -531,36 +587,45 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
 
     // ---- join the four warps' partial results
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < NR; ++m)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 1);
-            sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], 2);
-        }
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int o = kTurned ? 4 : 1; o < (kTurned ? 32 : 4); o *= 2)
+                sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], o);
     __syncthreads();  // every ring is drained: its memory takes the partial results
     float* part = reinterpret_cast<float*>(smem);
-    constexpr int kPartWarp = 16 * MT * C::kAccPad + 16 * MT * 2;
+    constexpr int kPartWarp = R * C::kAccPad + R * 2;
     {
         float* mypart = part + warp * kPartWarp;
-        float* stat = mypart + 16 * MT * C::kAccPad;
+        float* stat = mypart + R * C::kAccPad;
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int m = 0; m < NR; ++m)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int rr = 16 * m + 8 * r + g;
-                if (t4 == 0) stat[2 * rr] = mx[m][r], stat[2 * rr + 1] = sum[m][r];
+                const int rr = row_at(m, r);
+                if ((kTurned ? g : t4) == 0) stat[2 * rr] = mx[m][r], stat[2 * rr + 1] = sum[m][r];
+                constexpr int N = D == 64 ? 8 : 16;  // channels in a row of this lane
 #pragma unroll
-                for (int cg = 0; cg < C::kSub; ++cg)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        constexpr int N = D == 64 ? 8 : 16;  // channels in a row of this lane per j
-                        const int ch = cg * 128 + N * (2 * t4 + j);
+                for (int cg = 0; cg < C::kSub; ++cg) {
+                    if constexpr (kTurned) {
 #pragma unroll
                         for (int n = 0; n < N; n += 4)
-                            *reinterpret_cast<float4*>(mypart + rr * C::kAccPad + ch + n) =
-                                make_float4(acc[m][cg * 16 + n][2 * r + j], acc[m][cg * 16 + n + 1][2 * r + j],
-                                            acc[m][cg * 16 + n + 2][2 * r + j], acc[m][cg * 16 + n + 3][2 * r + j]);
+                            *reinterpret_cast<float4*>(mypart + rr * C::kAccPad + cg * 128 + N * g + n) =
+                                make_float4(acc[m][cg * 8 + n / 2][r], acc[m][cg * 8 + n / 2][2 + r],
+                                            acc[m][cg * 8 + n / 2 + 1][r], acc[m][cg * 8 + n / 2 + 1][2 + r]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int ch = cg * 128 + N * (2 * t4 + j);
+#pragma unroll
+                            for (int n = 0; n < N; n += 4)
+                                *reinterpret_cast<float4*>(mypart + rr * C::kAccPad + ch + n) =
+                                    make_float4(acc[m][cg * 16 + n][2 * r + j], acc[m][cg * 16 + n + 1][2 * r + j],
+                                                acc[m][cg * 16 + n + 2][2 * r + j], acc[m][cg * 16 + n + 3][2 * r + j]);
+                        }
                     }
+                }
             }
     }
     __syncthreads();
@@ -568,14 +633,14 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
         float m4[kDecWarps], top = -INFINITY, l = 0.f;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
-            m4[w] = part[w * kPartWarp + 16 * MT * C::kAccPad + 2 * r];
+            m4[w] = part[w * kPartWarp + R * C::kAccPad + 2 * r];
             top = fmaxf(top, m4[w]);
         }
         const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
             m4[w] = ptx::ex2_approx(m4[w] - ref);
-            l = fmaf(part[w * kPartWarp + 16 * MT * C::kAccPad + 2 * r + 1], m4[w], l);
+            l = fmaf(part[w * kPartWarp + R * C::kAccPad + 2 * r + 1], m4[w], l);
         }
         const float inv = p.in_cluster ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
         const float lse2 = l != 0.f ? top - kWeightShift + log2f(l) : -INFINITY;
@@ -656,7 +721,8 @@ __global__ void __launch_bounds__(kDecThreads, MT == 1 && D <= 128 ? 3 : 2)
 // One warp per row of q.
 constexpr int kMergeWarps = 4;
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const PagedParams p, const bool bf16) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    dependents_may_start();
+    wait_for_previous();
     const long long row = static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     const long long tok = row / p.Hq;

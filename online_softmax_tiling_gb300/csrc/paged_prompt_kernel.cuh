@@ -114,6 +114,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     PrCtl* ctl = reinterpret_cast<PrCtl*>(smem + C::kOffCtl);
     const int tid = threadIdx.x, warp = tid >> 5;
 
+    dependents_may_start();
+    wait_for_previous();
     // ---- the unit: row blocks from the last (with the causal mask the one
     // with the most keys) to the first, then request, head, range
     int u = blockIdx.x;
