@@ -9,10 +9,10 @@
 // A run is the tokens of one page that a call brings (consecutive rows, slots
 // ascending by one); an item is one run of one head of K or of V.  A CTA looks
 // through a chunk of slots, finds the runs that begin there and takes them for
-// one (head, K or V); a run of a few tokens (a decode step) is one warp's item,
-// a longer one is the CTA's.  Either way the team holds the item's 16-bit
-// values in registers between the maximum and the rounding, so HBM is read
-// once and written once.
+// one to four pairs of (head, K or V); a run of a few tokens (a decode step) is
+// one warp's item, a longer one is the CTA's.  Either way the team holds the
+// item's 16-bit values in registers between the maximum and the rounding, so HBM
+// is read once and written once, and the CTA reads its next item meanwhile.
 // What bounds it: HBM for prompts (4 d bytes read and 2 d written per token
 // and head), launch and two dependent reads for a decode step.
 #pragma once
@@ -33,7 +33,9 @@ struct AppendParams {
     float* scale[2];            // [num_pages, Hk]
     int8_t* bounds;             // [num_pages, Hk, 2, d] or null (K only)
     const int* slots;
-    int T, Hk, d, num_pages, page_shift, chunk;
+    int T, Hk, d, num_pages, page_shift;
+    int chunk;                  // slots a CTA looks through
+    int pairs;                  // (head, K or V) pairs it takes
 };
 
 // bounds of a code: floor and ceiling of code / 4 (NaN counts as 0)
@@ -43,137 +45,170 @@ __device__ __forceinline__ void code_bounds(float c, int& lo, int& hi) {
     hi = max(hi, __float2int_ru(q));
 }
 
-// One item by a team of TH threads: n tokens from row t into place `place` of
-// `page`.  NL: rows of the run each thread holds.
-template <int TH, int NL, bool BF16>
-__device__ __forceinline__ void append_item(const AppendParams& p, int t, int n, int page, int place,
-                                            int h, int w, int tid, float* red, int* blo, int* bhi) {
-    const int P = 1 << p.page_shift;
-    auto sync = [] { if constexpr (TH == 32) __syncwarp(); else __syncthreads(); };
-    const int LR = p.d >> 3;               // threads per row, 8 channels each
-    const int rows = TH / LR;              // rows per pass
-    const int r0 = tid / LR, c8 = (tid - r0 * LR) * 8;
-    const bool on = r0 < rows;
-    const uint16_t* src = p.x[w] + static_cast<long long>(t) * p.st[w] + static_cast<long long>(h) * p.sh[w] + c8;
-    uint4 v[NL];
-#pragma unroll
-    for (int k = 0; k < NL; ++k) {
-        const int r = r0 + k * rows;
-        v[k] = make_uint4(0, 0, 0, 0);
-        if (on && r < n) v[k] = __ldg(reinterpret_cast<const uint4*>(src + static_cast<long long>(r) * p.st[w]));
+struct AppendItem {
+    int t, n, page, place;  // n tokens from row t into place `place` of `page`
+    int h, w;               // head; K (0) or V (1)
+};
+
+// What a team of TH threads does with one item: load() its rows into registers,
+// then store() them.  NL: rows of the run each thread holds.
+template <int TH, int NL, bool BF16, bool BOUNDS>
+struct AppendTeam {
+    const AppendParams& p;
+    const int tid;
+    const int LR, rows, r0, c8;  // threads per row (8 channels each), rows per pass, this thread's place
+    const bool on;
+    float* red;                  // team's shared memory: a value per warp,
+    uint4* bred;                 //   bounds of a thread's rows,
+    int *blo, *bhi;              //   bounds of a page's older codes
+
+    __device__ AppendTeam(const AppendParams& p_, int tid_, float* red_, uint4* bred_, int* blo_, int* bhi_)
+        : p(p_), tid(tid_), LR(p_.d >> 3), rows(TH / LR), r0(tid / LR), c8((tid - r0 * LR) * 8), on(r0 < rows),
+          red(red_), bred(bred_), blo(blo_), bhi(bhi_) {}
+
+    __device__ static void sync() {
+        if constexpr (TH == 32) __syncwarp(); else __syncthreads();
     }
-    const long long ph = static_cast<long long>(page) * p.Hk + h;
-    const bool fresh = place == 0;
-    const float old = fresh ? 0.f : p.scale[w][ph];
-    float amax = 0.f;
+
+    __device__ void load(const AppendItem& m, uint4 (&v)[NL], float& old) const {
+        // (selected, not indexed: the parameters stay in constant memory)
+        const long long st = m.w ? p.st[1] : p.st[0];
+        const uint16_t* src = (m.w ? p.x[1] : p.x[0]) + m.t * st + m.h * (m.w ? p.sh[1] : p.sh[0]) + c8;
 #pragma unroll
-    for (int k = 0; k < NL; ++k) {
-        const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack16(u[i], BF16);
-            const float a = fabsf(f.x), b = fabsf(f.y);
-            if (a < INFINITY) amax = fmaxf(amax, a);   // an infinity or NaN does not count
-            if (b < INFINITY) amax = fmaxf(amax, b);
+        for (int k = 0; k < NL; ++k) {
+            const int r = r0 + k * rows;
+            v[k] = make_uint4(0, 0, 0, 0);
+            if (on && r < m.n) v[k] = __ldg(reinterpret_cast<const uint4*>(src + r * st));
         }
+        old = m.place == 0 ? 0.f : (m.w ? p.scale[1] : p.scale[0])[static_cast<long long>(m.page) * p.Hk + m.h];
     }
+
+    __device__ void store(const AppendItem& m, const uint4 (&v)[NL], float old) const {
+        float amax = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const bool with_bounds = w == 0 && p.bounds != nullptr;
-    if constexpr (TH > 32) {
-        if ((tid & 31) == 0) red[tid >> 5] = amax;
-    }
-    if (with_bounds)
-        for (int c = tid; c < p.d; c += TH) blo[c] = 127, bhi[c] = -128;
-    sync();
-    if constexpr (TH > 32) {
+        for (int k = 0; k < NL; ++k) {
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-        for (int i = 0; i < TH / 32; ++i) amax = fmaxf(amax, red[i]);
-    }
-    float s = pow2(cache_scale_exp(amax));
-    if (old > s) s = old;                       // never shrinks while a page is in use
-    const bool grown = !fresh && s > old;
-    const float inv = 1.f / s;                  // exact: s is a power of two
-    if (tid == 0) p.scale[w][ph] = s;
-    uint8_t* base = p.codes[w] + (ph << p.page_shift) * p.d;
-    if (grown) {  // the page's older codes, rounded again to the new scale
-        const float ratio = old * inv;
-        const int words = (place * p.d) >> 2;
-        uint32_t* o4 = reinterpret_cast<uint32_t*>(base);
-        for (int i = tid; i < words; i += TH) {
-            const uint32_t c = o4[i];
-            const float2 a = half2_floats(e4m3x2_to_half2(c & 0xFFFFu));
-            const float2 b = half2_floats(e4m3x2_to_half2(c >> 16));
-            const uint32_t lo = e4m3x2(a.x * ratio, a.y * ratio), hi = e4m3x2(b.x * ratio, b.y * ratio);
-            o4[i] = lo | (hi << 16);
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack16(u[i], BF16);
+                const float a = fabsf(f.x), b = fabsf(f.y);
+                if (a < INFINITY) amax = fmaxf(amax, a);  // an infinity or NaN does not count
+                if (b < INFINITY) amax = fmaxf(amax, b);
+            }
+        }
+        amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // (not negative)
+        if constexpr (TH > 32) {
+            if ((tid & 31) == 0) red[tid >> 5] = amax;
+            sync();
+#pragma unroll
+            for (int i = 0; i < TH / 32; ++i) amax = fmaxf(amax, red[i]);
+        }
+        float s = pow2(cache_scale_exp(amax));
+        if (old > s) s = old;                        // never shrinks while a page is in use
+        const bool fresh = m.place == 0, grown = !fresh && s > old;
+        const float inv = 1.f / s;                   // exact: s is a power of two
+        const long long ph = static_cast<long long>(m.page) * p.Hk + m.h;
+        if (tid == 0) (m.w ? p.scale[1] : p.scale[0])[ph] = s;
+        uint8_t* base = (m.w ? p.codes[1] : p.codes[0]) + (ph << p.page_shift) * p.d;
+        const bool with_bounds = BOUNDS && m.w == 0;
+        if (grown) round_older(m, base, old * inv, with_bounds);
+        int lo[8], hi[8];
+        if constexpr (BOUNDS) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) lo[e] = 127, hi[e] = -128;
+        }
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+            const int r = r0 + k * rows;
+            if (!on || r >= m.n) continue;
+            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            uint32_t q[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack16(u[i], BF16);
+                q[i] = e4m3x2(f.x * inv, f.y * inv);
+            }
+            *reinterpret_cast<uint2*>(base + (m.place + r) * p.d + c8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
             if (with_bounds) {
-                const int ch = (i * 4) % p.d;
-                const float2 x = half2_floats(e4m3x2_to_half2(lo)), y = half2_floats(e4m3x2_to_half2(hi));
-                const float f[4] = {x.x, x.y, y.x, y.y};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    int l = 127, m = -128;
-                    code_bounds(f[e], l, m);
-                    atomicMin(&blo[ch + e], l);
-                    atomicMax(&bhi[ch + e], m);
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = half2_floats(e4m3x2_to_half2(q[i]));
+                    code_bounds(f.x, lo[2 * i], hi[2 * i]);
+                    code_bounds(f.y, lo[2 * i + 1], hi[2 * i + 1]);
                 }
             }
         }
-    }
-    int lo[8], hi[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) lo[e] = 127, hi[e] = -128;
-#pragma unroll
-    for (int k = 0; k < NL; ++k) {
-        const int r = r0 + k * rows;
-        if (!on || r >= n) continue;
-        const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-        uint32_t q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack16(u[i], BF16);
-            q[i] = e4m3x2(f.x * inv, f.y * inv);
-        }
-        *reinterpret_cast<uint2*>(base + (place + r) * p.d + c8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
         if (with_bounds) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = half2_floats(e4m3x2_to_half2(q[i]));
-                code_bounds(f.x, lo[2 * i], hi[2 * i]);
-                code_bounds(f.y, lo[2 * i + 1], hi[2 * i + 1]);
+            auto bytes = [](const int* x) {
+                return (x[0] & 255) | ((x[1] & 255) << 8) | ((x[2] & 255) << 16) | (static_cast<uint32_t>(x[3]) << 24);
+            };
+            bred[tid] = make_uint4(bytes(lo), bytes(lo + 4), bytes(hi), bytes(hi + 4));
+            sync();
+            // four channels a thread: words 0, 1 of a column's entries are floors, 2, 3 ceilings
+            int8_t* bd = p.bounds + ph * 2 * p.d;
+            const int have = min(rows, m.n);
+            for (int i = tid; i < p.d / 2; i += TH) {
+                const int c4 = i % (p.d / 4), top = i / (p.d / 4);  // channels 4 c4 .., floor or ceiling
+                const uint32_t* col = reinterpret_cast<const uint32_t*>(bred + (c4 >> 1)) + 2 * top + (c4 & 1);
+                uint32_t x = top ? 0x80808080u : 0x7F7F7F7Fu;
+                for (int r = 0; r < have; ++r) x = top ? __vmaxs4(x, col[r * LR * 4]) : __vmins4(x, col[r * LR * 4]);
+                int8_t* at = bd + top * p.d + 4 * c4;
+                if (!fresh) {
+                    // the older codes': as they stand, or as rounded again
+                    uint32_t y;
+                    if (grown) {
+                        const int* b = (top ? bhi : blo) + 4 * c4;
+                        y = bytes(b);
+                    } else {
+                        y = *reinterpret_cast<const uint32_t*>(at);
+                    }
+                    x = top ? __vmaxs4(x, y) : __vmins4(x, y);
+                }
+                *reinterpret_cast<uint32_t*>(at) = x;
             }
         }
+        sync();  // the team's shared memory is free again
     }
-    if (with_bounds) {
-        if (on && r0 < n) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                atomicMin(&blo[c8 + e], lo[e]);
-                atomicMax(&bhi[c8 + e], hi[e]);
-            }
-        }
-        sync();
-        int8_t* bd = p.bounds + ph * 2 * p.d;
-        const bool keep = !fresh && !grown;     // the older codes stand: so do their bounds
-        for (int c = tid; c < p.d; c += TH) {
-            int l = blo[c], m = bhi[c];
-            if (keep) l = min(l, static_cast<int>(bd[c])), m = max(m, static_cast<int>(bd[p.d + c]));
-            bd[c] = static_cast<int8_t>(l);
-            bd[p.d + c] = static_cast<int8_t>(m);
-        }
-    }
-    sync();  // the team's shared arrays are free again
-    (void)P;
-}
 
-template <int NL, bool BF16>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendParams p) {
+    // The page's older codes (places before the first one written), rounded again.
+    __device__ void round_older(const AppendItem& m, uint8_t* base, float ratio, bool with_bounds) const {
+        if (with_bounds) {
+            for (int c = tid; c < p.d; c += TH) blo[c] = 127, bhi[c] = -128;
+            sync();
+        }
+        uint32_t* o4 = reinterpret_cast<uint32_t*>(base);
+        for (int i = tid; i < (m.place * p.d) >> 2; i += TH) {
+            const uint32_t c = o4[i];
+            const float2 a = half2_floats(e4m3x2_to_half2(c & 0xFFFFu));
+            const float2 b = half2_floats(e4m3x2_to_half2(c >> 16));
+            const uint32_t l = e4m3x2(a.x * ratio, a.y * ratio), h = e4m3x2(b.x * ratio, b.y * ratio);
+            o4[i] = l | (h << 16);
+            if (with_bounds) {
+                const int ch = (i * 4) % p.d;
+                const float2 x = half2_floats(e4m3x2_to_half2(l)), y = half2_floats(e4m3x2_to_half2(h));
+                const float f[4] = {x.x, x.y, y.x, y.y};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    int lo = 127, hi = -128;
+                    code_bounds(f[e], lo, hi);
+                    atomicMin(&blo[ch + e], lo);
+                    atomicMax(&bhi[ch + e], hi);
+                }
+            }
+        }
+        if (with_bounds) sync();
+    }
+};
+
+template <int NL, bool BF16, bool BOUNDS>
+__global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_kernel(const AppendParams p) {
     constexpr int kWarps = kAppendThreads / 32;
     __shared__ uint32_t breaks[8];              // bit i: row t0 + i does not go on from the row before it
     __shared__ int n_short, n_long;
-    __shared__ int short_runs[kAppendMaxChunk], long_runs[kAppendMaxChunk];  // row in the chunk | length << 8
+    __shared__ int2 short_runs[kAppendMaxChunk], long_runs[kAppendMaxChunk];  // row in the chunk | length << 8, slot
     __shared__ float red[kWarps];
-    __shared__ int blo[kWarps][256], bhi[kWarps][256];
+    __shared__ uint4 bred[BOUNDS ? kAppendThreads : 1];
+    __shared__ int blo[BOUNDS ? kWarps : 1][256], bhi[BOUNDS ? kWarps : 1][256];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = 1 << p.page_shift;
     const int t0 = blockIdx.x * p.chunk;
@@ -186,7 +221,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
     int before = __shfl_up_sync(0xffffffffu, slot, 1);
     if (lane == 0) before = (t > 0 && t - 1 < p.T) ? __ldg(p.slots + t - 1) : -1;
     const bool same = slot >= 0 && before >= 0 && (slot >> p.page_shift) == (before >> p.page_shift);
-    bool go_on = same && slot == before + 1;
+    const bool go_on = same && slot == before + 1;
     const uint32_t bits = __ballot_sync(0xffffffffu, !go_on);
     if (lane == 0) breaks[warp] = bits;
     __syncthreads();
@@ -205,22 +240,58 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendP
             const int n = min(e - tid, P - place);
             const int rows = 32 / (p.d >> 3);
             if (n <= kAppendShortRows * rows)
-                short_runs[atomicAdd(&n_short, 1)] = tid | (n << 8);
+                short_runs[atomicAdd(&n_short, 1)] = make_int2(tid | (n << 8), slot);
             else
-                long_runs[atomicAdd(&n_long, 1)] = tid | (n << 8);
+                long_runs[atomicAdd(&n_long, 1)] = make_int2(tid | (n << 8), slot);
         }
     }
     __syncthreads();
-    const int h = blockIdx.y >> 1, w = blockIdx.y & 1;
-    for (int i = 0; i < n_long; ++i) {
-        const int row = long_runs[i] & 255, n = long_runs[i] >> 8;
-        const int s = __ldg(p.slots + t0 + row);
-        append_item<kAppendThreads, NL, BF16>(p, t0 + row, n, s >> p.page_shift, s & (P - 1), h, w, tid, red, blo[0], bhi[0]);
+    // items: (run, pair) of the lists and the CTA's pairs
+    const int pair0 = blockIdx.y * p.pairs, pairs = min(p.pairs, 2 * p.Hk - pair0);
+    auto item = [&](const int2* runs, int i) {
+        const int run = i / pairs, pair = pair0 + i - run * pairs;
+        const int2 r = runs[run];
+        return AppendItem{t0 + (r.x & 255), r.x >> 8, r.y >> p.page_shift, r.y & (P - 1), pair >> 1, pair & 1};
+    };
+    if (n_long > 0) {
+        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS> team(p, tid, red, bred, blo[0], bhi[0]);
+        const int items = n_long * pairs;
+        if constexpr (NL <= 4) {  // the next item is read while this one is stored
+            uint4 v[NL], next[NL];
+            float old, next_old = 0.f;
+            AppendItem m = item(long_runs, 0);
+            team.load(m, v, old);
+            for (int i = 0; i < items; ++i) {
+                AppendItem nm = m;
+                if (i + 1 < items) {
+                    nm = item(long_runs, i + 1);
+                    team.load(nm, next, next_old);
+                }
+                team.store(m, v, old);
+                m = nm, old = next_old;
+#pragma unroll
+                for (int k = 0; k < NL; ++k) v[k] = next[k];
+            }
+        } else {
+            for (int i = 0; i < items; ++i) {
+                const AppendItem m = item(long_runs, i);
+                uint4 v[NL];
+                float old;
+                team.load(m, v, old);
+                team.store(m, v, old);
+            }
+        }
     }
-    for (int i = warp; i < n_short; i += kWarps) {
-        const int row = short_runs[i] & 255, n = short_runs[i] >> 8;
-        const int s = __ldg(p.slots + t0 + row);
-        append_item<32, kAppendShortRows, BF16>(p, t0 + row, n, s >> p.page_shift, s & (P - 1), h, w, lane, red, blo[warp], bhi[warp]);
+    if (n_short > 0) {
+        const int w = BOUNDS ? warp : 0;
+        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS> team(p, lane, red, bred + (BOUNDS ? 32 * warp : 0), blo[w], bhi[w]);
+        for (int i = warp; i < n_short * pairs; i += kWarps) {
+            const AppendItem m = item(short_runs, i);
+            uint4 v[kAppendShortRows];
+            float old;
+            team.load(m, v, old);
+            team.store(m, v, old);
+        }
     }
 }
 

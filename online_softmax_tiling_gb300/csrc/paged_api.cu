@@ -181,10 +181,10 @@ int choose_splits(const fa_paged_args& a, const Plan& pl) {
     // workspace (one request of 8 key heads and 65536 keys: 37 us with 32, 55 with 16).
     if (s == pg::kDecMaxCluster && s * pl.units < sms)
         while (s < FA_PAGED_MAX_SPLITS && 2 * s * pl.units <= 2 * sms && keys >= 2 * s * 1024) s *= 2;
-    // Many units of long and probably unequal contexts: several waves of ranges
-    // of at least 4096 keys even them out (64 requests of 5000 to 16384 keys:
-    // 234 us with 4, 251 with 2, 274 with 1).
-    while (s < pg::kDecMaxCluster && s * pl.units >= 2 * sms && s * pl.units < 12 * sms && keys >= 2 * s * 4096) s *= 2;
+    // Otherwise, as long as a range keeps 1024 keys, enough ranges for four waves of three
+    // CTAs per SM: they even out unequal lengths (64 requests of 5000 to 16384 keys: 234 us
+    // with 4, 251 with 2, 274 with 1) and partly filled waves.
+    while (s < 8 && s * pl.units < 12 * sms && keys >= 2 * s * 1024) s *= 2;
     return s;
 }
 
@@ -210,6 +210,16 @@ KernelEntry select_kernel(int width, int rows) {
     if (width == 64) return rows == 8 ? few_rows<64, 8>() : rows == 16 ? few_rows<64, 16>() : few_rows<64, 32>();
     if (width == 128) return rows == 8 ? few_rows<128, 8>() : rows == 16 ? few_rows<128, 16>() : few_rows<128, 32>();
     return rows == 8 ? few_rows<256, 8>() : few_rows<256, 16>();
+}
+
+template <int NL, bool BF16>
+const void* append_kernel_of(bool bounds) {
+    return bounds ? reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, true>)
+                  : reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, false>);
+}
+const void* append_kernel(bool four_rows, bool bf16, bool bounds) {
+    if (four_rows) return bf16 ? append_kernel_of<4, true>(bounds) : append_kernel_of<4, false>(bounds);
+    return bf16 ? append_kernel_of<16, true>(bounds) : append_kernel_of<16, false>(bounds);
 }
 
 int check_args(const fa_paged_args& a) {
@@ -296,20 +306,18 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
     p.bounds = reinterpret_cast<int8_t*>(cache->k_bounds);
     p.slots = slots;
     p.T = T, p.Hk = cache->Hk, p.d = cache->d, p.num_pages = cache->num_pages, p.page_shift = shift_of(cache->page_size);
-    // slots a CTA looks through: 64, or 8 (one per warp) where that leaves SMs idle
-    p.chunk = static_cast<int64_t>(T) * 2 * p.Hk >= 64ll * 2 * sm_count() ? pg::kAppendMaxChunk : 8;
+    // Slots a CTA looks through (64 down to 8, one per warp) and (head, K or V)
+    // pairs it takes (4 or 1): the most that leaves eight CTAs per SM.
+    const int64_t sms = sm_count();
+    auto ctas = [&] { return (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk * ((2 * p.Hk + p.pairs - 1) / p.pairs); };
+    p.chunk = pg::kAppendMaxChunk, p.pairs = 4;
+    if (ctas() < 8 * sms) p.pairs = 1;
+    while (p.chunk > 8 && ctas() < 8 * sms) p.chunk /= 2;
     // rows a thread holds of a whole page
     const int rows = pg::kAppendThreads / (p.d / 8), need = (cache->page_size + rows - 1) / rows;
-    const bool bf = dtype == FA_BF16;
-    const void* fn;
-    if (need <= 4)
-        fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<4, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<4, false>);
-    else if (need <= 8)
-        fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<8, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<8, false>);
-    else
-        fn = bf ? reinterpret_cast<const void*>(&pg::kv_append_kernel<16, true>) : reinterpret_cast<const void*>(&pg::kv_append_kernel<16, false>);
+    const void* fn = append_kernel(need <= 4, dtype == FA_BF16, p.bounds != nullptr);
     void* args[] = {&p};
-    if (!launch(fn, (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk, 2 * p.Hk, pg::kAppendThreads, 0, 1, stream, args))
+    if (!launch(fn, (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk, (2 * p.Hk + p.pairs - 1) / p.pairs, pg::kAppendThreads, 0, 1, stream, args))
         return FA_ERR_CUDA;
     return FA_OK;
 }
