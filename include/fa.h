@@ -202,7 +202,8 @@ int fa_fwd_splitkv_noalloc(const void* q, const void* k, const void* v, void* o,
 /*
  * fa_check_device_status - synchronise `stream`, then return and clear the
  * device-side status word: FA_OK, FA_ERR_TIMEOUT (some CTA's bounded wait
- * expired and that CTA left its outputs unwritten), or FA_ERR_CUDA if the
+ * expired and that CTA left its outputs unwritten), FA_ERR_INVALID_ARG (an
+ * operator of fa_paged.h met device data that cannot be), or FA_ERR_CUDA if the
  * synchronisation itself failed.  The status word is shared by all launches
  * on the current device.
  */

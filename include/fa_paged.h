@@ -16,7 +16,8 @@
  *                    the page's tokens.
  * Hk: key/value heads; d: a multiple of 16 from 16 to 256.  Token j of
  * request b is at place j % P of page block_table[b][j / P]; a slot is
- * page * P + place.  num_pages * Hk * P must be below 2^31.
+ * page * P + place.  num_pages * Hk * P must be below 2^31, max_pages * P (and
+ * the tokens of one append) at most 2^30.
  *
  * Device data that no entry point can check on the host (lengths, tables,
  * slots) is checked by the kernels: nothing outside the buffers is read or
@@ -122,8 +123,14 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  *   scale: finite and > 0.
  * Rows of o and lse behind the last query (>= cu_q[B]) are left as they were.
  * The softmax runs in 32 bits; its weights enter the second product in fp16,
- * scaled so that the row's largest contribution lies near 2^14, and 16-bit
- * queries are read exactly.
+ * scaled so that a row's largest contribution keeps all of their 11 bits and
+ * one 2^-22 as large still does, and 16-bit queries are read exactly (down
+ * to 2^-38 of a row's largest value).
+ * Places of a page behind a request's last token may hold anything.  As in
+ * fa_fwd, a NaN or infinity in a value that a query does not see because of the causal
+ * mask may still reach it (the product of its weight 0).
+ * A request with bad device data (see above) or a wait that ran out (FA_ERR_TIMEOUT)
+ * has undefined outputs; the others have theirs.
  */
 #define FA_PAGED_MAX_SPLITS 64
 

@@ -22,7 +22,7 @@
 namespace fa {
 namespace paged {
 
-constexpr int kSelectThreads = 512;
+constexpr int kSelectThreads = 256;
 constexpr int kSelectMaxPages = 32768;
 constexpr int kSelectMaxCluster = 8;
 constexpr int kSelectAhead = 4;    // pages a group of lanes has on their way
@@ -77,6 +77,8 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
         if (tid == 0) p.count[unit_at] = n;
         return;
     }
+    // the first CTA's shared memory may be written once all of them have started
+    if (p.cluster > 1) cluster_arrive();
     // queries to whole numbers, one warp per head of the group
     for (int g = warp; g < p.G; g += kWarps) {
         const uint16_t* q = p.q + static_cast<long long>(b) * p.q_st + static_cast<long long>(h * p.G + g) * p.q_sh;
@@ -120,6 +122,7 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
     uint32_t keys_at = ptx::smem_addr(keys);
     if (p.cluster > 1)  // those of the cluster's first CTA
         asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(keys_at) : "r"(keys_at));
+    if (p.cluster > 1) cluster_wait();
     bool bad_page = false;
     for (int j0 = rank * share; j0 < j_end; j0 += per_pass * kSelectAhead) {
         int page[kSelectAhead];

@@ -23,7 +23,7 @@
 namespace fa {
 namespace paged {
 
-constexpr int kTablesThreads = 512;
+constexpr int kTablesThreads = 1024;
 constexpr int kTablesMaxB = 16384;
 
 struct TablesParams {
@@ -80,13 +80,16 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
         back = n < 0 ? static_cast<int>(have) : 0;
     };
 
+    const int count = __ldg(p.free_count);
     // each thread sums a run of consecutive requests, then the block scans the sums
     const int per = (p.B + kTablesThreads - 1) / kTablesThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
     long long s[3] = {0, 0, 0};
+    int add0 = 0, need0 = 0, back0 = 0;  // of the thread's first request, its only one up to 1024
     for (int b = b0; b < b1; ++b) {
         int add, need, back;
         request(b, add, need, back);
+        if (b == b0) add0 = add, need0 = need, back0 = back;
         s[0] += add, s[1] += need, s[2] += back;
     }
     long long incl[3];
@@ -116,7 +119,6 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     }
     __syncthreads();
     const long long T = totals[0], A = totals[1], R = totals[2];
-    const int count = __ldg(p.free_count);
     int status = 0;
     if (bad || count < 0 || count + R > p.free_capacity || T > p.max_tokens)
         status = 1;  // FA_ERR_INVALID_ARG
@@ -127,8 +129,8 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
 #pragma unroll
         for (int k = 0; k < 3; ++k) run[k] = static_cast<int>(warp_sums[k][warp] + incl[k] - s[k]);
         for (int b = b0; b < b1; ++b) {
-            int add, need, back;
-            request(b, add, need, back);
+            int add = add0, need = need0, back = back0;
+            if (b != b0) request(b, add, need, back);
             cu[b] = run[0], pop[b] = run[1], push[b] = run[2];
             run[0] += add, run[1] += need, run[2] += back;
         }

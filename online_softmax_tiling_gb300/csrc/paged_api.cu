@@ -95,6 +95,9 @@ int sm_count() {
     return sms;
 }
 
+// Keys of a request (and tokens of an append) that the kernels' 32-bit positions hold with room to spare.
+constexpr int kMostKeys = 1 << 30;
+
 int shift_of(int page_size) {
     switch (page_size) {
         case 16: return 4;
@@ -234,8 +237,8 @@ int check_args(const fa_paged_args& a) {
     const int st = check_cache(a.cache);
     if (st != FA_OK) return st;
     if (a.Hq % a.cache.Hk != 0) return FA_ERR_INVALID_ARG;
-    if (a.max_pages > INT32_MAX / a.cache.page_size) return FA_ERR_INVALID_ARG;
-    if (a.selected && a.num_selected > INT32_MAX / a.cache.page_size) return FA_ERR_INVALID_ARG;
+    if (a.max_pages > kMostKeys / a.cache.page_size) return FA_ERR_INVALID_ARG;
+    if (a.selected && a.num_selected > kMostKeys / a.cache.page_size) return FA_ERR_INVALID_ARG;
     if (static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk) > INT32_MAX / 2) return FA_ERR_INVALID_ARG;
     if (bad_strides(a.q_stride) || bad_strides(a.o_stride)) return FA_ERR_MISALIGNED;
     if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
@@ -265,7 +268,7 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
     const int shift = shift_of(page_size);
     if (B < 1 || max_pages < 1 || free_capacity < 1 || max_tokens < 0 || shift < 0) return FA_ERR_INVALID_ARG;
     if (lens_out == lens || free_count_out == free_count) return FA_ERR_INVALID_ARG;
-    if (max_pages > INT32_MAX / page_size) return FA_ERR_INVALID_ARG;
+    if (max_pages > kMostKeys / page_size) return FA_ERR_INVALID_ARG;
     if (B > pg::kTablesMaxB) return FA_ERR_UNSUPPORTED;
     for (const void* q : {static_cast<const void*>(new_tokens), static_cast<const void*>(lens),
                           static_cast<const void*>(block_table), static_cast<const void*>(free_pages),
@@ -280,9 +283,9 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
     if (!ensure_smem(fn, 3 * (pg::kTablesMaxB + 1) * 4, device)) return FA_ERR_CUDA;
     pg::TablesParams p{new_tokens, lens, block_table, free_pages, free_count, B, max_pages, free_capacity,
                        shift, max_tokens, slots, cu_new, lens_out, free_count_out, status};
-    // four tokens (or requests) per thread, at most one CTA per SM
-    const int64_t work = std::max<int64_t>(max_tokens, 2 * static_cast<int64_t>(B));
-    const int64_t ctas = std::min<int64_t>((work + 4 * pg::kTablesThreads - 1) / (4 * pg::kTablesThreads), sm_count());
+    // a token (or a request) per thread, at most one CTA per SM: every CTA repeats the prefix sums
+    const int64_t work = std::max<int64_t>(max_tokens, B);
+    const int64_t ctas = std::min<int64_t>((work + pg::kTablesThreads - 1) / pg::kTablesThreads, sm_count());
     void* args[] = {&p};
     if (!launch(fn, std::max<int64_t>(1, ctas), 1, pg::kTablesThreads, smem, 1, stream, args)) return FA_ERR_CUDA;
     return FA_OK;
@@ -295,6 +298,7 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
     const int st = check_cache(*cache);
     if (st != FA_OK) return st;
     if (cache->Hk > 32767) return FA_ERR_UNSUPPORTED;
+    if (T > kMostKeys) return FA_ERR_INVALID_ARG;
     if (bad_strides(k_stride) || bad_strides(v_stride) || misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4))
         return FA_ERR_MISALIGNED;
     if (T == 0) return FA_OK;
@@ -307,12 +311,12 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
     p.slots = slots;
     p.T = T, p.Hk = cache->Hk, p.d = cache->d, p.num_pages = cache->num_pages, p.page_shift = shift_of(cache->page_size);
     // Slots a CTA looks through (64 down to 8, one per warp) and (head, K or V)
-    // pairs it takes (4 or 1): the most that leaves eight CTAs per SM.
+    // pairs it takes (4 or 1): the most that leaves four CTAs per SM.
     const int64_t sms = sm_count();
     auto ctas = [&] { return (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk * ((2 * p.Hk + p.pairs - 1) / p.pairs); };
     p.chunk = pg::kAppendMaxChunk, p.pairs = 4;
-    if (ctas() < 8 * sms) p.pairs = 1;
-    while (p.chunk > 8 && ctas() < 8 * sms) p.chunk /= 2;
+    if (ctas() < 4 * sms) p.pairs = 1;
+    while (p.chunk > 8 && ctas() < 4 * sms) p.chunk /= 2;
     // rows a thread holds of a whole page
     const int rows = pg::kAppendThreads / (p.d / 8), need = (cache->page_size + rows - 1) / rows;
     const void* fn = append_kernel(need <= 4, dtype == FA_BF16, p.bounds != nullptr);
@@ -410,7 +414,7 @@ int fa_kv_page_select(const fa_kv_cache* cache, const void* q, const long long* 
     if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
     const int st = check_sizes(*cache);
     if (st != FA_OK) return st;
-    if (Hq % cache->Hk != 0 || max_pages > INT32_MAX / cache->page_size ||
+    if (Hq % cache->Hk != 0 || max_pages > kMostKeys / cache->page_size ||
         static_cast<int64_t>(B) * cache->Hk > INT32_MAX)
         return FA_ERR_INVALID_ARG;
     if (max_pages > pg::kSelectMaxPages) return FA_ERR_UNSUPPORTED;
@@ -432,9 +436,12 @@ int fa_kv_page_select(const fa_kv_cache* cache, const void* q, const long long* 
                                       : reinterpret_cast<const void*>(&pg::kv_page_select_kernel<false>);
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess || !ensure_smem(fn, 200 * 1024, device)) return FA_ERR_CUDA;
-    // about 256 pages per CTA, what its groups of lanes have on their way at once
+    // 128 pages per CTA, what its groups of lanes have on their way at once, unless
+    // the CTAs would not fit the GPU together (four per SM)
     p.cluster = 1;
-    while (p.cluster < pg::kSelectMaxCluster && p.cluster * 256 < max_pages) p.cluster *= 2;
+    while (p.cluster < pg::kSelectMaxCluster && p.cluster * 128 < max_pages &&
+           2ll * p.cluster * B * p.Hk <= 4ll * sm_count())
+        p.cluster *= 2;
     const int64_t ctas = static_cast<int64_t>(B) * p.Hk * p.cluster;
     if (ctas > INT32_MAX) return FA_ERR_INVALID_ARG;
     void* args[] = {&p};

@@ -162,7 +162,7 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     (0: chosen by the library); a workspace, where the count needs one, is
     allocated unless given.  Rows of given outputs behind the last query are
     left as they were.  A kernel whose waits run out (2 s) leaves outputs
-    unwritten and reports it through fa_check_device_status, as in
+    undefined and reports it through fa_check_device_status, as in
     attention_forward.
     """
     if stream is not None:

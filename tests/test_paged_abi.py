@@ -82,7 +82,7 @@ def test_cache_refusals(lib, kw, want):
     (dict(q=None), BAD), (dict(o=None), BAD), (dict(lse=None), BAD), (dict(block_table=None), BAD),
     (dict(lens=None), BAD), (dict(B=0), BAD), (dict(T=-1), BAD), (dict(T=4), BAD), (dict(max_q=2), BAD),
     (dict(cu_q=A, max_q=0), BAD), (dict(Hq=3), BAD), (dict(Hq=0), BAD), (dict(max_pages=0), BAD),
-    (dict(max_pages=1 << 28), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
+    (dict(max_pages=(1 << 26) + 1), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD),
     (dict(scale=float("nan")), BAD), (dict(scale=float("inf")), BAD), (dict(dtype=2), BAD),
     (dict(num_splits=-1), BAD), (dict(num_splits=65), BAD), (dict(num_splits=3), BAD), (dict(num_splits=16), CUDA),
     (dict(selected=A), BAD), (dict(selected_count=A), BAD), (dict(selected=A, selected_count=A), BAD),
@@ -121,7 +121,7 @@ def test_splits_and_workspace(lib):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(k=None), BAD), (dict(slots=None), BAD), (dict(T=-1), BAD), (dict(dtype=5), BAD), (dict(k=A + 8), MISAL),
-    (dict(ks=(128, 60)), MISAL), (dict(vs=(0, 64)), MISAL), (dict(slots=A + 1), MISAL), (dict(T=0), 0), (dict(), CUDA)])
+    (dict(ks=(128, 60)), MISAL), (dict(vs=(0, 64)), MISAL), (dict(slots=A + 1), MISAL), (dict(T=0), 0), (dict(T=(1 << 30) + 1), BAD), (dict(), CUDA)])
 def test_append_refusals(lib, kw, want):
     a = dict(k=A, v=A, slots=A, T=5, ks=(128, 64), vs=(128, 64), dtype=fa.FA_BF16)
     a.update(kw)
