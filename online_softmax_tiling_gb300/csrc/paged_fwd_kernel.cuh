@@ -157,6 +157,18 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
 
+    // (nothing here touches what the kernel before this one may still write)
+    const uint32_t ring = sbase + warp * C::kRing;
+    const uint32_t bars = sbase + kOffBar + warp * NST * 8;
+    if (lane == 0) {
+        for (int s = 0; s < NST; ++s) ptx::mbar_init(bars + 8 * s, 1);
+        ptx::fence_mbar_init();
+    }
+    if (tid == 0) {
+        ptx::prefetch_tensormap(&tm_k);
+        ptx::prefetch_tensormap(&tm_v);
+    }
+    __syncwarp();
     dependents_may_start();
     wait_for_previous();
     // unit: range fastest (a cluster's CTAs), then row block (they read the same keys), head, request
@@ -212,18 +224,6 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     const int per = (chunks + p.splits - 1) / p.splits;
     const int c0 = min(split * per, chunks), c1 = min(c0 + per, chunks);
     const int mine = c1 > c0 + warp ? (c1 - c0 - warp + kDecWarps - 1) / kDecWarps : 0;  // chunks of this warp
-
-    const uint32_t ring = sbase + warp * C::kRing;
-    const uint32_t bars = sbase + kOffBar + warp * NST * 8;
-    if (lane == 0) {
-        for (int s = 0; s < NST; ++s) ptx::mbar_init(bars + 8 * s, 1);
-        ptx::fence_mbar_init();
-    }
-    if (tid == 0) {
-        ptx::prefetch_tensormap(&tm_k);
-        ptx::prefetch_tensormap(&tm_v);
-    }
-    __syncwarp();
 
     // What a warp needs of its next chunks, per 16-key tile: lane i holds that
     // of chunk 32 n + i (refilled one block ahead).
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             l = fmaf(part[w * kPartWarp + R * C::kAccPad + 2 * r + 1], m4[w], l);
         }
         const float inv = p.in_cluster ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (NaN stays)
-        const float lse2 = l != 0.f ? top - kWeightShift + log2f(l) : -INFINITY;
+        const float lse2 = p.in_cluster ? 0.f : l != 0.f ? top - kWeightShift + log2f(l) : -INFINITY;
         const int pr = r0 + r, i = pr / p.G, hq = h * p.G + pr - i * p.G;
         const long long tok = q0 + i;
         const long long grow = tok * p.Hq + hq;
@@ -678,34 +678,30 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     // ---- join the cluster's CTAs: each takes its share of the block's outputs
     // from all of them
     cluster_sync();
-    const int n4 = p.d >> 2;
-    for (int i = tid * p.splits + split; i < my_rows * n4; i += p.splits * kDecThreads) {
-        const int r = i / n4, c = (i - r * n4) * 4;
-        const uint32_t stat_at = ptx::smem_addr(&cta_stat[r]), o_at = sbase + kJoin + (r * D + c) * 4;
-        float2 st[kDecMaxCluster];
-        float4 x[kDecMaxCluster];
-#pragma unroll
-        for (int s = 0; s < kDecMaxCluster; ++s) {
-            if (s >= p.splits) break;
-            st[s] = ld_cluster_f2(stat_at, s);
-            x[s] = ld_cluster_f4(o_at, s);
-        }
-        float top = -INFINITY, l = 0.f;
-#pragma unroll
-        for (int s = 0; s < kDecMaxCluster; ++s) {
-            if (s >= p.splits) break;
-            top = fmaxf(top, st[s].x);
-        }
-        const float ref = top == -INFINITY ? 0.f : top;
+    // S lanes share four channels of a row, one for each CTA's result
+    const int S = p.splits, n4 = p.d >> 2, n = my_rows * n4, from = tid & (S - 1);
+    for (int i0 = 0; i0 < n; i0 += kDecThreads) {
+        const int i = i0 + (split * kDecThreads + tid) / S;
+        float2 st = make_float2(-INFINITY, 0.f);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int s = 0; s < kDecMaxCluster; ++s) {
-            if (s >= p.splits) break;
-            const float w = ptx::ex2_approx(st[s].x - ref);
-            l = fmaf(st[s].y, w, l);
-            o.x = fmaf(x[s].x, w, o.x), o.y = fmaf(x[s].y, w, o.y);
-            o.z = fmaf(x[s].z, w, o.z), o.w = fmaf(x[s].w, w, o.w);
+        const int r = min(i, n - 1) / n4, c = (min(i, n - 1) - r * n4) * 4;
+        if (i < n) {
+            st = ld_cluster_f2(ptx::smem_addr(&cta_stat[r]), from);
+            o = ld_cluster_f4(sbase + kJoin + (r * D + c) * 4, from);
         }
+        float top = st.x;
+        for (int x = 1; x < S; x *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float w = ptx::ex2_approx(st.x - (top == -INFINITY ? 0.f : top));
+        float l = st.y * w;
+        o.x *= w, o.y *= w, o.z *= w, o.w *= w;
+        for (int x = 1; x < S; x *= 2) {
+            l += __shfl_xor_sync(0xffffffffu, l, x);
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, x);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, x);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, x);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, x);
+        }
+        if (i >= n || from != 0) continue;
         const float inv = l != 0.f ? 1.f / l : 0.f;
         const int pr = r0 + r, iq = pr / p.G, hq = h * p.G + pr - iq * p.G;
         const long long tok = q0 + iq;

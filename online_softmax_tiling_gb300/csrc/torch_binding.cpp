@@ -150,8 +150,17 @@ PyObject* tables_step(PyObject* const* a) {
     const int* count = need<int>(a[4], "free_count", at::kInt, {1}, dev);
     c10::cuda::OptionalCUDAGuard guard;
     guard.set_index(static_cast<c10::DeviceIndex>(dev));
-    at::Tensor slots = empty({T}, at::kInt, dev), cu = empty({B + 1}, at::kInt, dev), lens_out = empty({B}, at::kInt, dev);
-    at::Tensor count_out = empty({1}, at::kInt, dev), status = empty({1}, at::kInt, dev);
+    // one allocation for the five outputs
+    const at::Tensor all = empty({T + 2 * B + 3}, at::kInt, dev);
+    int64_t used = 0;
+    auto part = [&](int64_t n) {
+        auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+        impl->set_storage_offset(used);
+        impl->set_sizes_contiguous({n});
+        used += n;
+        return at::Tensor(std::move(impl));
+    };
+    at::Tensor slots = part(T), cu = part(B + 1), lens_out = part(B), count_out = part(1), status = part(1);
     auto at_int = [](at::Tensor& t) { return static_cast<int*>(t.data_ptr()); };
     const int st = fa_kv_tables_step(new_tokens, lens, table, free_pages, count, dim32(B, "new_tokens"), dim32(M, "block_table"),
                                      dim32(fp.size(0), "free_pages"), P, T, at_int(slots), at_int(cu), at_int(lens_out),
