@@ -8,10 +8,10 @@
 // scores carry no rounding, and their order does not depend on how the sum is
 // split.
 // A cluster takes one (request, key head): its CTAs score shares of the pages
-// into the first one's shared memory (as order-preserving 32-bit keys); that one
-// finds the key of the num_selected-th best by four passes over histograms of
-// 8 bits, and writes the indices above it, and the first of those equal to it,
-// in ascending order.
+// into the first one's shared memory (as order-preserving 32-bit keys, counted
+// by their top 8 bits on the way); that one finds the key of the
+// num_selected-th best by histograms of 8 bits at a time, and writes the indices above
+// it, and the first of those equal to it, in ascending order.
 // What bounds it: 2 d + 4 bytes per page and head from HBM when there are many
 // requests; for one the dependent reads (table, then bounds), which is why
 // a group of lanes has four pages on their way at a time.
@@ -47,7 +47,7 @@ __device__ __forceinline__ uint32_t ordered(float f) {
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const SelectParams p) {
     extern __shared__ __align__(16) uint32_t sel_smem[];
     // [G][d/4] words of max(qi, 0), then of min(qi, 0); [G] units; [pages] keys
     const int dw = p.d >> 2;
@@ -55,13 +55,15 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
     uint32_t* qneg = qpos + p.G * dw;
     float* unit = reinterpret_cast<float*>(qneg + p.G * dw);
     uint32_t* keys = reinterpret_cast<uint32_t*>(unit + p.G);
-    __shared__ uint32_t hist[256];
+    __shared__ uint32_t hist[2][256];
     __shared__ uint32_t pick, need;
     __shared__ int warp_n[2][kSelectThreads / 32];
     constexpr int kWarps = kSelectThreads / 32;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % p.cluster, unit_at = blockIdx.x / p.cluster;
     const int h = unit_at % p.Hk, b = unit_at / p.Hk;
+    static_assert(kSelectThreads == 256, "a thread per bin");
+    hist[0][tid] = 0;
     dependents_may_start();
     wait_for_previous();
     int len = __ldg(p.lens + b);
@@ -79,6 +81,42 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
     }
     // the first CTA's shared memory may be written once all of them have started
     if (p.cluster > 1) cluster_arrive();
+    // LG lanes (16, or 8 for d <= 128) score one page: 16 channels per lane
+    const int LG = p.d <= 128 ? 8 : 16, sub = tid % LG;
+    const int per_pass = kSelectThreads / LG;
+    const bool on = sub * 16 < p.d;
+    const int share = (n + p.cluster - 1) / p.cluster, j_end = min(n, (rank + 1) * share);
+    const int* trow = p.table + static_cast<long long>(b) * p.max_pages;
+    bool bad_page = false;
+    int page[kSelectAhead];
+    float ks[kSelectAhead];
+    int4 lo[kSelectAhead], hi[kSelectAhead];
+    auto load_pages = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < kSelectAhead; ++i) {
+            const int j = j0 + tid / LG + i * per_pass;
+            page[i] = j < j_end ? __ldg(trow + j) : 0;
+        }
+    };
+    auto load_bounds = [&](int j0) {
+#pragma unroll
+        for (int i = 0; i < kSelectAhead; ++i) {
+            const bool there = static_cast<unsigned>(page[i]) < static_cast<unsigned>(p.num_pages);
+            bad_page |= !there;
+            ks[i] = 0.f;
+            lo[i] = hi[i] = make_int4(0, 0, 0, 0);
+            if (there && j0 + tid / LG + i * per_pass < j_end) {
+                const long long ph = static_cast<long long>(page[i]) * p.Hk + h;
+                ks[i] = __ldg(p.k_scale + ph);
+                if (on) {
+                    const int4* bd = reinterpret_cast<const int4*>(p.bounds + ph * 2 * p.d) + sub;
+                    lo[i] = __ldg(bd);
+                    hi[i] = __ldg(bd + (p.d >> 4));
+                }
+            }
+        }
+    };
+    load_pages(rank * share);  // (their latency passes while the queries are rounded)
     // queries to whole numbers, one warp per head of the group
     for (int g = warp; g < p.G; g += kWarps) {
         const uint16_t* q = p.q + static_cast<long long>(b) * p.q_st + static_cast<long long>(h * p.G + g) * p.q_sh;
@@ -111,44 +149,19 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
         }
         if (lane == 0) unit[g] = 4.f * s;
     }
+    load_bounds(rank * share);
     __syncthreads();
 
-    // 16 lanes (8 for d <= 128) score one page: 16 channels per lane
-    const int LG = p.d <= 128 ? 8 : 16, sub = lane % LG;
-    const int per_pass = kSelectThreads / LG;
-    const bool on = sub * 16 < p.d;
-    const int share = (n + p.cluster - 1) / p.cluster, j_end = min(n, (rank + 1) * share);
-    const int* trow = p.table + static_cast<long long>(b) * p.max_pages;
-    uint32_t keys_at = ptx::smem_addr(keys);
-    if (p.cluster > 1)  // those of the cluster's first CTA
+    uint32_t keys_at = ptx::smem_addr(keys), hist_at = ptx::smem_addr(hist[0]);
+    if (p.cluster > 1) {  // those of the cluster's first CTA
         asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(keys_at) : "r"(keys_at));
-    if (p.cluster > 1) cluster_wait();
-    bool bad_page = false;
+        asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(hist_at) : "r"(hist_at));
+        cluster_wait();
+    }
     for (int j0 = rank * share; j0 < j_end; j0 += per_pass * kSelectAhead) {
-        int page[kSelectAhead];
-        float ks[kSelectAhead];
-        int4 lo[kSelectAhead], hi[kSelectAhead];
-#pragma unroll
-        for (int i = 0; i < kSelectAhead; ++i) {
-            const int j = j0 + tid / LG + i * per_pass;
-            page[i] = j < j_end ? __ldg(trow + j) : 0;
-        }
-#pragma unroll
-        for (int i = 0; i < kSelectAhead; ++i) {
-            const bool there = static_cast<unsigned>(page[i]) < static_cast<unsigned>(p.num_pages);
-            bad_page |= !there;
-            ks[i] = 0.f;
-            lo[i] = hi[i] = make_int4(0, 0, 0, 0);
-            if (there && j0 + tid / LG + i * per_pass < j_end) {
-                const long long ph = static_cast<long long>(page[i]) * p.Hk + h;
-                ks[i] = __ldg(p.k_scale + ph);
-                if (on) {
-                    const int4* bd = reinterpret_cast<const int4*>(p.bounds + ph * 2 * p.d) + sub;
-                    lo[i] = __ldg(bd);
-                    hi[i] = __ldg(bd + (p.d >> 4));
-                }
-            }
-        }
+        if (j0 != rank * share) load_bounds(j0);
+        const int j1 = j0 + per_pass * kSelectAhead;
+        if (j1 < j_end) load_pages(j1);
         float best[kSelectAhead];
 #pragma unroll
         for (int i = 0; i < kSelectAhead; ++i) best[i] = -INFINITY;
@@ -182,10 +195,13 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
             const int j = j0 + tid / LG + i * per_pass;
             if (sub == 0 && j < j_end) {
                 const uint32_t key = j == n - 1 ? 0xFFFFFFFFu : ordered(best[i] + 0.f);  // -0 counts as 0
-                if (p.cluster > 1)
+                if (p.cluster > 1) {
                     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(keys_at + 4 * j), "r"(key) : "memory");
-                else
+                    asm volatile("red.shared::cluster.add.u32 [%0], 1;" ::"r"(hist_at + 4 * (key >> 24)) : "memory");
+                } else {
                     keys[j] = key;
+                    atomicAdd(&hist[0][key >> 24], 1);
+                }
             }
         }
     }
@@ -200,16 +216,18 @@ __global__ void __launch_bounds__(kSelectThreads) kv_page_select_kernel(const Se
     // the key of the keep-th best: 8 bits at a time from the top
     uint32_t prefix = 0, mask = 0, left = p.keep;
     for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        for (int j = tid; j < n; j += kSelectThreads)
-            if ((keys[j] & mask) == prefix) atomicAdd(&hist[(keys[j] >> shift) & 255], 1);
-        __syncthreads();
+        const int buf = (shift >> 3) & 1 ^ 1;  // 24: 0, 16: 1, 8: 0, 0: 1
+        if (shift < 24) {
+            for (int j = tid; j < n; j += kSelectThreads)
+                if ((keys[j] & mask) == prefix) atomicAdd(&hist[buf][(keys[j] >> shift) & 255], 1);
+            __syncthreads();
+        }
+        hist[buf ^ 1][tid] = 0;  // the other buffer is for the next 8 bits
         if (warp == 0) {
             // counts of 8 bins per lane, summed from the top
             uint32_t c[8], sum = 0;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) c[e] = hist[255 - (lane * 8 + e)], sum += c[e];
+            for (int e = 0; e < 8; ++e) c[e] = hist[buf][255 - (lane * 8 + e)], sum += c[e];
             uint32_t incl = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
