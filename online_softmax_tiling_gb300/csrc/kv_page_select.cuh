@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const
     hist[0][tid] = 0;
     dependents_may_start();
     wait_for_previous();
-    int len = __ldg(p.lens + b);
+    int len = ld(p.lens + b);
     if (len < 0 || len > (p.max_pages << p.page_shift)) {
         if (tid == 0 && rank == 0) report(kBadData);
         len = min(max(len, 0), p.max_pages << p.page_shift);
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const
 #pragma unroll
         for (int i = 0; i < kSelectAhead; ++i) {
             const int j = j0 + tid / LG + i * per_pass;
-            page[i] = j < j_end ? __ldg(trow + j) : 0;
+            page[i] = j < j_end ? load_page(trow + j) : 0;
         }
     };
     auto load_bounds = [&](int j0) {
@@ -107,11 +107,11 @@ __global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const
             lo[i] = hi[i] = make_int4(0, 0, 0, 0);
             if (there && j0 + tid / LG + i * per_pass < j_end) {
                 const long long ph = static_cast<long long>(page[i]) * p.Hk + h;
-                ks[i] = __ldg(p.k_scale + ph);
+                ks[i] = ld(p.k_scale + ph);
                 if (on) {
                     const int4* bd = reinterpret_cast<const int4*>(p.bounds + ph * 2 * p.d) + sub;
-                    lo[i] = __ldg(bd);
-                    hi[i] = __ldg(bd + (p.d >> 4));
+                    lo[i] = ld(bd);
+                    hi[i] = ld(bd + (p.d >> 4));
                 }
             }
         }
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const
         float f[8];
         const bool on = lane * 8 < p.d;
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (on) v = __ldg(reinterpret_cast<const uint4*>(q + lane * 8));
+        if (on) v = ld(reinterpret_cast<const uint4*>(q + lane * 8));
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         float a = 0.f;
 #pragma unroll

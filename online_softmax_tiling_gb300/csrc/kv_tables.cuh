@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     __syncthreads();
 
     auto request = [&](int b, int& add, int& need, int& back) {
-        const int n = __ldg(p.new_tokens + b), len = __ldg(p.lens + b);
+        const int n = ld(p.new_tokens + b), len = ld(p.lens + b);
         const long long after = static_cast<long long>(max(len, 0)) + max(n, 0);
         const long long have = (static_cast<long long>(max(len, 0)) + P1) >> p.page_shift;
         const long long want = (after + P1) >> p.page_shift;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
         back = n < 0 ? static_cast<int>(have) : 0;
     };
 
-    const int count = __ldg(p.free_count);
+    const int count = ld(p.free_count);
     // each thread sums a run of consecutive requests, then the block scans the sums
     const int per = (p.B + kTablesThreads - 1) / kTablesThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -143,25 +143,25 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     if (status != 0) {
         for (long long i = first; i < p.max_tokens; i += stride) p.slots[i] = -1;
         for (long long b = first; b <= p.B; b += stride) p.cu[b] = 0;
-        for (long long b = first; b < p.B; b += stride) p.lens_out[b] = __ldg(p.lens + b);
+        for (long long b = first; b < p.B; b += stride) p.lens_out[b] = ld(p.lens + b);
         if (first == 0) *p.free_count_out = count, *p.status = status;
         return;
     }
     // the page an entry of the stack holds after the pushes
     auto stack = [&](int i) {
-        if (i < count) return __ldg(p.free_pages + i);
+        if (i < count) return ld(p.free_pages + i);
         const int r = i - count, b = owner_of(push, p.B, r);
-        return p.table[static_cast<long long>(b) * p.max_pages + (r - push[b])];
+        return load_page(p.table + static_cast<long long>(b) * p.max_pages + (r - push[b]));
     };
     const int top = count + static_cast<int>(R) - 1;
     for (long long t = first; t < p.max_tokens; t += stride) {
         int slot = -1;
         if (t < T) {
             const int b = owner_of(cu, p.B, static_cast<int>(t));
-            const int len = __ldg(p.lens + b);
+            const int len = ld(p.lens + b);
             const int pos = len + static_cast<int>(t) - cu[b];
             const int j = pos >> p.page_shift, have = (len + P1) >> p.page_shift;
-            const int page = j < have ? p.table[static_cast<long long>(b) * p.max_pages + j]
+            const int page = j < have ? load_page(p.table + static_cast<long long>(b) * p.max_pages + j)
                                       : stack(top - (pop[b] + j - have));
             slot = (page << p.page_shift) | (pos & P1);
         }
@@ -169,15 +169,15 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     }
     for (long long i = first; i < A; i += stride) {
         const int b = owner_of(pop, p.B, static_cast<int>(i));
-        const int have = (__ldg(p.lens + b) + P1) >> p.page_shift;
+        const int have = (ld(p.lens + b) + P1) >> p.page_shift;
         p.table[static_cast<long long>(b) * p.max_pages + have + (static_cast<int>(i) - pop[b])] =
             stack(top - static_cast<int>(i));
     }
     for (long long i = first; i < R; i += stride) p.free_pages[count + i] = stack(count + static_cast<int>(i));
     for (long long b = first; b < p.B; b += stride) {
-        const int n = __ldg(p.new_tokens + b);
+        const int n = ld(p.new_tokens + b);
         p.cu[b] = cu[b];
-        p.lens_out[b] = n < 0 ? 0 : __ldg(p.lens + b) + n;
+        p.lens_out[b] = n < 0 ? 0 : ld(p.lens + b) + n;
     }
     if (first == 0) {
         p.cu[p.B] = static_cast<int>(T);

@@ -147,14 +147,16 @@ struct Plan {
     int64_t units;  // row blocks x heads x requests
 };
 
-// Packed rows above which the tcgen05 kernel serves a request.
-constexpr int kPromptRows = 64;
+// Packed rows above which the tcgen05 kernel serves a request: 8 requests of 4000
+// keys and 8 heads take 35 us for 32 rows on the few-row kernel and 38 on the other, 52
+// and 40 for 48 rows (which the few-row kernel reads every key twice for).
+constexpr int kPromptRows = 32;
 
 Plan plan_of(const fa_paged_args& a) {
     Plan pl;
     const int64_t rows = static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk);
     pl.width = width_of(a.cache.d);
-    pl.prompt = pl.width <= 128 && rows > kPromptRows;
+    pl.prompt = pl.width <= 128 && rows > kPromptRows && !a.selected;
     pl.block_rows = pl.prompt ? pg::kPrRows : block_rows_of(pl.width, rows);
     pl.row_blocks = static_cast<int>((rows + pl.block_rows - 1) / pl.block_rows);
     pl.units = static_cast<int64_t>(pl.row_blocks) * a.cache.Hk * a.B;
@@ -220,8 +222,10 @@ const void* append_kernel_of(bool bounds) {
     return bounds ? reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, true>)
                   : reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, false>);
 }
-const void* append_kernel(bool four_rows, bool bf16, bool bounds) {
-    if (four_rows) return bf16 ? append_kernel_of<4, true>(bounds) : append_kernel_of<4, false>(bounds);
+const void* append_kernel(int page_size, int d, bool bf16, bool bounds) {
+    // rows of a whole page that a thread of the CTA would hold
+    const int rows = pg::kAppendThreads / (d / 8);
+    if ((page_size + rows - 1) / rows <= 4) return bf16 ? append_kernel_of<4, true>(bounds) : append_kernel_of<4, false>(bounds);
     return bf16 ? append_kernel_of<16, true>(bounds) : append_kernel_of<16, false>(bounds);
 }
 
@@ -317,9 +321,7 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
     p.chunk = pg::kAppendMaxChunk, p.pairs = 4;
     if (ctas() < 4 * sms) p.pairs = 1;
     while (p.chunk > 8 && ctas() < 4 * sms) p.chunk /= 2;
-    // rows a thread holds of a whole page
-    const int rows = pg::kAppendThreads / (p.d / 8), need = (cache->page_size + rows - 1) / rows;
-    const void* fn = append_kernel(need <= 4, dtype == FA_BF16, p.bounds != nullptr);
+    const void* fn = append_kernel(cache->page_size, p.d, dtype == FA_BF16, p.bounds != nullptr);
     void* args[] = {&p};
     if (!launch(fn, (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk, (2 * p.Hk + p.pairs - 1) / p.pairs, pg::kAppendThreads, 0, 1, stream, args))
         return FA_ERR_CUDA;

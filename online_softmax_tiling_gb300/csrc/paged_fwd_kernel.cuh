@@ -182,11 +182,11 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     int q0 = b, nq = 1;
     bool bad = false;
     if (p.cu_q) {
-        q0 = __ldg(p.cu_q + b);
-        nq = __ldg(p.cu_q + b + 1) - q0;
+        q0 = ld(p.cu_q + b);
+        nq = ld(p.cu_q + b + 1) - q0;
         if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
     }
-    int len = __ldg(p.lens + b);
+    int len = ld(p.lens + b);
     // the query rows, on their way while the lengths and pages are looked up
     constexpr int kQPass = (R + kDecWarps * C::kRowsPass - 1) / (kDecWarps * C::kRowsPass);
     const int piece = lane % C::kPieces, sub_row = lane / C::kPieces;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         qv[i] = make_uint4(0, 0, 0, 0);
         if (r < R && pr < nq * p.G && piece * 8 < p.d) {
             const int tok = pr / p.G, hg = pr - tok * p.G;
-            qv[i] = __ldg(reinterpret_cast<const uint4*>(
+            qv[i] = ld(reinterpret_cast<const uint4*>(
                 p.q + static_cast<long long>(q0 + tok) * p.q_st + static_cast<long long>(h * p.G + hg) * p.q_sh + piece * 8));
         }
     }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     const int kend = p.causal ? min(len, len - nq + last_i + 1) : len;
     int places = max(kend, 0);
     if (p.sel) {
-        int n = __ldg(p.sel_count + b * p.Hk + h);
+        int n = ld(p.sel_count + b * p.Hk + h);
         if (n < 0 || n > p.num_sel) {
             if (tid == 0) report(kBadData);
             n = 0;
@@ -242,12 +242,12 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             if (k >= mine || place >= places) continue;
             int lp = place >> p.page_shift;
             const int off = place & ((1 << p.page_shift) - 1);
-            if (p.sel) lp = __ldg(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
+            if (p.sel) lp = ld(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
             const int pos = (lp << p.page_shift) + off;
             if (lp < 0 || lp >= p.max_pages) {
                 report(kBadData);
             } else if (pos < len) {
-                const int page = __ldg(p.table + static_cast<long long>(b) * p.max_pages + lp);
+                const int page = load_page(p.table + static_cast<long long>(b) * p.max_pages + lp);
                 if (page < 0 || page >= p.num_pages) {
                     report(kBadData);
                 } else {
@@ -262,8 +262,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             const int ph = max(m.row[i], 0) >> p.page_shift;
-            m.ks[i] = fminf(fmaxf(__ldg(p.k_scale + ph), 0x1p-60f), 0x1p60f);
-            const float vs = fminf(fmaxf(__ldg(p.v_scale + ph), 0x1p-60f), 0x1p60f);
+            m.ks[i] = fminf(fmaxf(ld(p.k_scale + ph), 0x1p-60f), 0x1p60f);
+            const float vs = fminf(fmaxf(ld(p.v_scale + ph), 0x1p-60f), 0x1p60f);
             m.ev[i] = log2f(vs);
             m.rv[i] = 1.f / vs;
         }
@@ -724,9 +724,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
     const long long tok = row / p.Hq;
     const int hq = static_cast<int>(row - tok * p.Hq);
     // rows behind the last query were not computed
-    if (tok >= p.T || (p.cu_q && tok >= __ldg(p.cu_q + p.B))) return;
+    if (tok >= p.T || (p.cu_q && tok >= ld(p.cu_q + p.B))) return;
     const float* ls = p.lse_part + row * p.splits;
-    float a0 = lane < p.splits ? ls[lane] : -INFINITY, a1 = lane + 32 < p.splits ? ls[lane + 32] : -INFINITY;
+    float a0 = lane < p.splits ? ld(ls + lane) : -INFINITY, a1 = lane + 32 < p.splits ? ld(ls + lane + 32) : -INFINITY;
     float top = fmaxf(a0, a1);
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
         for (int s = 0; s < p.splits; ++s) {
             const float w = __shfl_sync(0xffffffffu, s < 32 ? a0 : a1, s & 31);
             if (w == 0.f || c >= p.d) continue;
-            const float4 x = *reinterpret_cast<const float4*>(op + s * p.d + c);
+            const float4 x = ld(reinterpret_cast<const float4*>(op + s * p.d + c));
             o.x = fmaf(x.x, w, o.x), o.y = fmaf(x.y, w, o.y), o.z = fmaf(x.z, w, o.z), o.w = fmaf(x.w, w, o.w);
         }
         if (c < p.d)

@@ -83,7 +83,7 @@ __host__ __device__ constexpr uint32_t pr_instr(int m, int n, bool b_mn_major) {
 // 16 codes that this SM reads once: not kept in L1, whose memory the tiles take.
 __device__ __forceinline__ uint4 ldg_codes(const uint8_t* a) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a));
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(a) : "memory");
     return v;
 }
 
@@ -127,11 +127,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     int q0 = b, nq = 1;
     bool bad = false;
     if (p.cu_q) {
-        q0 = __ldg(p.cu_q + b);
-        nq = __ldg(p.cu_q + b + 1) - q0;
+        q0 = ld(p.cu_q + b);
+        nq = ld(p.cu_q + b + 1) - q0;
         if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
     }
-    int len = __ldg(p.lens + b);
+    int len = ld(p.lens + b);
     if (len < 0 || len > (p.max_pages << p.page_shift)) bad = true, len = 0;
     if (bad && tid == 0) report(kBadData);
     const int rows = nq * p.G, r0 = rb * kPrRows;
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             if (bf16) {
                 for (int c = 0; c < D / 8; ++c) {
                     uint4 v = make_uint4(0, 0, 0, 0);
-                    if (mine && c * 8 < p.d) v = __ldg(reinterpret_cast<const uint4*>(src + c * 8));
+                    if (mine && c * 8 < p.d) v = ld(reinterpret_cast<const uint4*>(src + c * 8));
                     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 #pragma unroll 4
             for (int c = 0; c < D / 8; ++c) {
                 uint4 v = make_uint4(0, 0, 0, 0);
-                if (mine && c * 8 < p.d) v = __ldg(reinterpret_cast<const uint4*>(src + c * 8));
+                if (mine && c * 8 < p.d) v = ld(reinterpret_cast<const uint4*>(src + c * 8));
                 uint32_t w[4] = {v.x, v.y, v.z, v.w};
                 if (bf16) {
 #pragma unroll
@@ -439,18 +439,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         const bool ch_on = ch * 16 < p.d;
         // Page numbers run two tiles ahead and codes one: all loads of a tile are
         // independent of one another (bad table entries read nothing, reported at the end).
-        int page[NV], gpage = 0;
+        // Lane g of a warp holds the page of the tile's g-th group of 16 keys.
+        int pages = 0;
         bool bad_page = false;
+        const int lane = ct & 31;
         auto load_pages = [&](int j) {
-            const int key0 = (k0 + j) * kPrTile;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) page[k] = __ldg(trow + (min(key0 + row0 + RPP * k, len - 1) >> p.page_shift));
-            if (!is_v && ct < 8) gpage = __ldg(trow + (min(key0 + 16 * ct, len - 1) >> p.page_shift));
+            if (lane < 8) pages = load_page(trow + (min((k0 + j) * kPrTile + 16 * lane, len - 1) >> p.page_shift));
         };
         uint4 v[NV];
         PrGroup mg = {1.f, -INFINITY, 1.f};
         auto load = [&](int j) {
             const int key0 = (k0 + j) * kPrTile;
+            int page[NV];
+#pragma unroll
+            for (int k = 0; k < NV; ++k) page[k] = __shfl_sync(0xffffffffu, pages, (row0 + RPP * k) >> 4);
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int key = key0 + row0 + RPP * k;
@@ -462,10 +464,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             if (!is_v && ct < 8) {  // scales of the tile's eight groups of 16 keys
                 mg = {1.f, -INFINITY, 1.f};
-                if (static_cast<unsigned>(gpage) < static_cast<unsigned>(p.num_pages) && key0 + 16 * ct < len) {
-                    const int ph = gpage * p.Hk + h;
-                    const float vs = fminf(fmaxf(__ldg(p.v_scale + ph), 0x1p-60f), 0x1p60f);
-                    mg = {fminf(fmaxf(__ldg(p.k_scale + ph), 0x1p-60f), 0x1p60f), log2f(vs), 1.f / vs};
+                if (static_cast<unsigned>(pages) < static_cast<unsigned>(p.num_pages) && key0 + 16 * ct < len) {
+                    const int ph = pages * p.Hk + h;
+                    const float vs = fminf(fmaxf(ld(p.v_scale + ph), 0x1p-60f), 0x1p60f);
+                    mg = {fminf(fmaxf(ld(p.k_scale + ph), 0x1p-60f), 0x1p60f), log2f(vs), 1.f / vs};
                 }
             }
         };

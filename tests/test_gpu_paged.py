@@ -392,7 +392,7 @@ def _check_attend(case, out, lse, causal=True, scale=None, selected=None, rows=s
 
 DECODE = [  # Hk, G, P, d
     (1, 1, 16, 64), (2, 4, 64, 128), (1, 8, 32, 256), (3, 2, 128, 96), (2, 5, 16, 80), (1, 16, 64, 128),
-    (1, 24, 32, 64), (2, 3, 64, 16), (1, 2, 16, 192), (1, 40, 16, 128), (1, 17, 128, 256)]
+    (1, 24, 32, 64), (2, 3, 64, 16), (1, 2, 16, 192), (1, 40, 16, 128), (1, 17, 128, 256), (1, 96, 32, 128), (2, 71, 64, 64)]
 
 
 @pytest.mark.parametrize("Hk,G,P,d", DECODE)
@@ -573,7 +573,7 @@ def _select_case(lens, Hk, G, P, d, dtype, seed):
 @pytest.mark.parametrize("lens,Hk,G,P,d,keep", [
     ([0, 1, 16, 17, 400, 2000], 2, 4, 16, 128, 5), ([700, 3000], 3, 1, 32, 64, 1), ([5000], 1, 8, 16, 256, 64),
     ([1000, 999, 64], 2, 5, 64, 96, 3), ([9000, 12], 1, 2, 16, 80, 200), ([640], 1, 4, 128, 16, 4),
-    ([640], 1, 4, 64, 64, 10), ([640], 1, 4, 64, 64, 30)])
+    ([640], 1, 4, 64, 64, 10), ([640], 1, 4, 64, 64, 30), ([900, 70], 1, 70, 16, 128, 6)])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_select_and_attend(lens, Hk, G, P, d, keep, dtype):
     case = _select_case(lens, Hk, G, P, d, dtype, 71 + d)
@@ -760,3 +760,43 @@ def test_wrappers_refuse_wrong_tensors():
             fa.kv_page_select(**{**dict(q=good["q"], k_bounds=g[4], k_scale=g[2], block_table=good["block_table"],
                                         lens=good["lens"], page_size=16, num_selected=2), **w})
     _ok()
+
+
+def test_steps_back_to_back_equal_steps_one_by_one():
+    """The kernels of a step may be set up while the one before still runs: forty steps without a wait
+    give bit for bit what they give with a wait behind every call."""
+    torch, fa = _torch(), _fa()
+    B, Hk, G, P, d, M, steps = 96, 4, 4, 16, 128, 24, 40
+    rng = np.random.default_rng(95)
+    start = rng.integers(1, 300, B)
+    kv = torch.from_numpy(rng.standard_normal((steps, 2, B, Hk, d)).astype(np.float32)).bfloat16().cuda()
+    q = torch.from_numpy(rng.standard_normal((steps, B, Hk * G, d)).astype(np.float32)).bfloat16().cuda()
+    T0 = int(start.sum())
+    kv0 = torch.from_numpy(rng.standard_normal((2, T0, Hk, d)).astype(np.float32)).bfloat16().cuda()
+    perm = rng.permutation(B * M)
+
+    def run(wait):
+        g = ref.Cache(B * M, Hk, P, d, random=False).cuda()
+        table, free, count, lens = _i32(np.zeros((B, M))), _i32(perm), _i32([B * M]), _i32(np.zeros(B))
+        one, got = _i32(np.ones(B)), []
+        slots, cu, lens, count, _ = fa.kv_tables_step(_i32(start), lens, table, free, count, P, T0)
+        fa.kv_cache_append(kv0[0], kv0[1], slots, *g[:4], k_bounds=g[4])
+        torch.cuda.synchronize()
+        for i in range(steps):
+            slots, cu, lens, count, _ = fa.kv_tables_step(one, lens, table, free, count, P, B)
+            wait()
+            fa.kv_cache_append(kv[i, 0], kv[i, 1], slots, *g[:4], k_bounds=g[4])
+            wait()
+            sel, n = fa.kv_page_select(q[i], g[4], g[2], table, lens, P, 6)
+            wait()
+            a = fa.paged_attention_forward(q[i], *g[:4], table, lens)
+            wait()
+            b = fa.paged_attention_forward(q[i], *g[:4], table, lens, selected=sel, selected_count=n)
+            wait()
+            got += [sel, n, *a, *b]
+        torch.cuda.synchronize()
+        _ok()
+        return got + list(g[:4]) + [g[4], table, free, lens, count]
+
+    for x, y in zip(run(lambda: None), run(torch.cuda.synchronize)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
