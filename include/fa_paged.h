@@ -158,11 +158,12 @@ typedef struct fa_paged_args {
 
 int fa_paged_fwd(const fa_paged_args* args);
 
-/* The count of key ranges fa_paged_fwd uses for num_splits = 0. */
+/* The count of key ranges per row that fa_paged_fwd uses for num_splits = 0; 0 where
+ * it shares the keys of all requests out evenly instead. */
 int fa_paged_num_splits(const fa_paged_args* args);
 
-/* Workspace bytes fa_paged_fwd needs with these arguments (0: none; 1, 2, 4, 8
- * or 16 ranges of few query rows are joined on chip). */
+/* Workspace bytes fa_paged_fwd needs with these arguments (0: none; a given count of 1,
+ * 2, 4, 8 or 16 ranges of few query rows is joined on chip). */
 size_t fa_paged_workspace_size(const fa_paged_args* args);
 
 /*

@@ -40,16 +40,6 @@ struct TablesParams {
     int* status;
 };
 
-// Largest b in [0, n) with prefix[b] <= i (prefix ascending, prefix[0] = 0 <= i).
-__device__ __forceinline__ int owner_of(const int* prefix, int n, int i) {
-    int lo = 0, hi = n;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= i) lo = mid; else hi = mid;
-    }
-    return lo;
-}
-
 __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesParams p) {
     extern __shared__ int tab_smem[];
     int* cu = tab_smem;                 // [B + 1] tokens before request b

@@ -145,6 +145,7 @@ struct Plan {
     bool prompt;    // tcgen05 kernel (256 packed rows per unit)
     int width, block_rows, row_blocks;
     int64_t units;  // row blocks x heads x requests
+    int even;       // CTAs of equal shares of all keys (0: key ranges per row block)
 };
 
 // Packed rows above which the tcgen05 kernel serves a request: 8 requests of 4000
@@ -152,20 +153,37 @@ struct Plan {
 // and 40 for 48 rows (which the few-row kernel reads every key twice for).
 constexpr int kPromptRows = 32;
 
+// CTAs that share all keys evenly, one wave of them, or 0 where ranges per row
+// block do better: with few units (a unit's parts are joined one after the other),
+// with so many that they even themselves out, or with few keys (the join is a second launch).
+int even_ctas(const fa_paged_args& a, const Plan& pl) {
+    const int64_t keys = static_cast<int64_t>(a.selected ? a.num_selected : a.max_pages) * a.cache.page_size;
+    const int64_t wave = static_cast<int64_t>(sm_count()) * (pl.width == 256 || pl.block_rows == 32 ? 2 : 3);
+    const int64_t chunk = pl.width == 256 ? 16 : 32;
+    if (pl.prompt || pl.row_blocks != 1 || a.B > pg::kEvenMaxB) return 0;
+    if (16 * pl.units < wave || 4 * pl.units > 5 * wave) return 0;
+    // 64 chunks per CTA at least, by the tables' width (64 requests of 5000 to 16384 keys and 8 heads: 227 us
+    // against 236 with 4 ranges; 32 of 4096 selected keys: 60 against 63; below, the second launch
+    // costs more than it saves: 24 of up to 8000 keys and 4 heads, 41 us against 37)
+    if (pl.units * (keys / chunk) < wave * 64 || pl.units * (keys / chunk) > INT32_MAX / 2) return 0;
+    return static_cast<int>(wave);
+}
+
 Plan plan_of(const fa_paged_args& a) {
-    Plan pl;
+    Plan pl{};
     const int64_t rows = static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk);
     pl.width = width_of(a.cache.d);
     pl.prompt = pl.width <= 128 && rows > kPromptRows && !a.selected;
     pl.block_rows = pl.prompt ? pg::kPrRows : block_rows_of(pl.width, rows);
     pl.row_blocks = static_cast<int>((rows + pl.block_rows - 1) / pl.block_rows);
     pl.units = static_cast<int64_t>(pl.row_blocks) * a.cache.Hk * a.B;
+    pl.even = a.num_splits == 0 ? even_ctas(a, pl) : 0;
     return pl;
 }
 
 // Whether the ranges of a row block are joined inside a cluster.
 bool in_cluster(const Plan& pl, int splits) {
-    return !pl.prompt && (splits == 2 || splits == 4 || splits == 8 || splits == 16);
+    return !pl.prompt && !pl.even && (splits == 2 || splits == 4 || splits == 8 || splits == 16);
 }
 
 // Key ranges for num_splits = 0.
@@ -198,6 +216,10 @@ size_t part_bytes(int64_t rows, int splits, int d) {
 }
 
 size_t workspace_bytes(const fa_paged_args& a, const Plan& pl, int splits) {
+    if (pl.even) {
+        const int64_t rows = 2ll * pl.even * pl.block_rows;
+        return part_bytes(rows, 1, a.cache.d) + part_bytes(rows, 1, 1) + (static_cast<size_t>(pl.even) + 1) * 16;
+    }
     if (splits < 2 || in_cluster(pl, splits)) return 0;
     const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
     return part_bytes(rows, splits, a.cache.d) + static_cast<size_t>(rows) * splits * 4;
@@ -208,13 +230,19 @@ struct KernelEntry {
     int smem;
 };
 template <int D, int R>
-KernelEntry few_rows() {
-    return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R>), pg::dec_smem<D, R>()};
+KernelEntry few_rows(bool even) {
+    if (even) return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, true>), pg::dec_smem<D, R, true>()};
+    return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, false>), pg::dec_smem<D, R, false>()};
 }
-KernelEntry select_kernel(int width, int rows) {
-    if (width == 64) return rows == 8 ? few_rows<64, 8>() : rows == 16 ? few_rows<64, 16>() : few_rows<64, 32>();
-    if (width == 128) return rows == 8 ? few_rows<128, 8>() : rows == 16 ? few_rows<128, 16>() : few_rows<128, 32>();
-    return rows == 8 ? few_rows<256, 8>() : few_rows<256, 16>();
+KernelEntry select_kernel(int width, int rows, bool even) {
+    if (width == 64) return rows == 8 ? few_rows<64, 8>(even) : rows == 16 ? few_rows<64, 16>(even) : few_rows<64, 32>(even);
+    if (width == 128) return rows == 8 ? few_rows<128, 8>(even) : rows == 16 ? few_rows<128, 16>(even) : few_rows<128, 32>(even);
+    return rows == 8 ? few_rows<256, 8>(even) : few_rows<256, 16>(even);
+}
+const void* select_even_join(int rows) {
+    return rows == 8    ? reinterpret_cast<const void*>(&pg::paged_even_join_kernel<8>)
+           : rows == 16 ? reinterpret_cast<const void*>(&pg::paged_even_join_kernel<16>)
+                        : reinterpret_cast<const void*>(&pg::paged_even_join_kernel<32>);
 }
 
 template <int NL, bool BF16>
@@ -330,7 +358,8 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
 
 int fa_paged_num_splits(const fa_paged_args* a) {
     if (!a || check_args(*a) != FA_OK) return 1;
-    return choose_splits(*a, plan_of(*a));
+    const Plan pl = plan_of(*a);
+    return pl.even ? 0 : choose_splits(*a, pl);
 }
 
 size_t fa_paged_workspace_size(const fa_paged_args* a) {
@@ -346,14 +375,14 @@ int fa_paged_fwd(const fa_paged_args* args) {
     if (st != FA_OK) return st;
     if (a.T == 0) return FA_OK;
     const Plan pl = plan_of(a);
-    const int splits = a.num_splits == 0 ? choose_splits(a, pl) : a.num_splits;
+    const int splits = pl.even ? 1 : a.num_splits == 0 ? choose_splits(a, pl) : a.num_splits;
     const size_t need = workspace_bytes(a, pl, splits);
     if (need > 0) {
         if (!a.workspace) return FA_ERR_INVALID_ARG;
         if (misaligned(a.workspace, 256)) return FA_ERR_MISALIGNED;
         if (a.workspace_bytes < need) return FA_ERR_INVALID_ARG;
     }
-    const int64_t units = pl.units * splits, rows = static_cast<int64_t>(a.T) * a.Hq;
+    const int64_t units = pl.even ? pl.even : pl.units * splits, rows = static_cast<int64_t>(a.T) * a.Hq;
     if (units > INT32_MAX || rows > INT32_MAX) return FA_ERR_INVALID_ARG;
 
     int device = 0;
@@ -380,8 +409,12 @@ int fa_paged_fwd(const fa_paged_args* args) {
     p.in_cluster = in_cluster(pl, splits);
     p.row_blocks = pl.row_blocks, p.splits = splits, p.box_rows = box_rows, p.causal = a.causal != 0;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-    p.o_part = need > 0 ? static_cast<float*>(a.workspace) : nullptr;
-    p.lse_part = need > 0 ? reinterpret_cast<float*>(static_cast<char*>(a.workspace) + part_bytes(rows, splits, a.cache.d)) : nullptr;
+    const int64_t part_rows = pl.even ? 2ll * pl.even * pl.block_rows : rows * splits;
+    char* ws = static_cast<char*>(a.workspace);
+    const size_t o_bytes = part_bytes(part_rows, 1, a.cache.d);
+    p.o_part = need > 0 ? reinterpret_cast<float*>(ws) : nullptr;
+    p.lse_part = need > 0 ? reinterpret_cast<float*>(ws + o_bytes) : nullptr;
+    p.shares = pl.even ? reinterpret_cast<int4*>(ws + o_bytes + part_bytes(part_rows, 1, 1)) : nullptr;
     bool bf16 = a.dtype == FA_BF16;
     if (pl.prompt) {
         const uint8_t *kc = static_cast<const uint8_t*>(a.cache.k), *vc = static_cast<const uint8_t*>(a.cache.v);
@@ -391,13 +424,16 @@ int fa_paged_fwd(const fa_paged_args* args) {
         void* kargs[] = {&kc, &vc, &p, &bf16};
         if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, pg::kPrThreads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
     } else {
-        const KernelEntry ke = select_kernel(pl.width, pl.block_rows);
+        const KernelEntry ke = select_kernel(pl.width, pl.block_rows, pl.even != 0);
         void* kargs[] = {&tk, &tv, &p, &bf16};
         if (!ensure_smem(ke.fn, ke.smem, device) ||
             !launch(ke.fn, units, 1, pg::kDecThreads, ke.smem, p.in_cluster ? splits : 1, a.stream, kargs))
             return FA_ERR_CUDA;
     }
-    if (need > 0) {
+    if (pl.even) {
+        void* margs[] = {&p, &bf16};
+        if (!launch(select_even_join(pl.block_rows), pl.even - 1, 1, pg::kJoinThreads, 0, 1, a.stream, margs)) return FA_ERR_CUDA;
+    } else if (need > 0) {
         void* margs[] = {&p, &bf16};
         if (!launch(reinterpret_cast<const void*>(&pg::paged_merge_kernel), (rows + pg::kMergeWarps - 1) / pg::kMergeWarps, 1,
                     32 * pg::kMergeWarps, 0, 1, a.stream, margs))

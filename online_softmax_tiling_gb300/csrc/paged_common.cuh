@@ -57,6 +57,16 @@ template <typename T>
 __device__ __forceinline__ T ld(const T* p) { return *p; }
 __device__ __forceinline__ int load_page(const int* p) { return __ldcg(p); }
 
+// Largest b in [0, n) with prefix[b] <= i (prefix ascending, prefix[0] = 0 <= i).
+__device__ __forceinline__ int owner_of(const int* prefix, int n, int i) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= i) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
 // Barrier of a cluster's CTAs; shared memory writes before it are seen behind it.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }

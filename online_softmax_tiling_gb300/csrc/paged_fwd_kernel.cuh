@@ -20,7 +20,12 @@
 // is shared until the end, where the four partial results are joined in
 // shared memory.  The CTAs of 2, 4, 8 or 16 key ranges are a cluster and join
 // theirs over distributed shared memory, without a workspace or a second
-// launch; other counts go through a workspace and a merge.  Reads are what bounds this kernel (2 d bytes per key and
+// launch; other counts go through a workspace and a merge.  For many keys
+// (EVEN) the chunks of all requests and heads, in order, are dealt out in equal shares
+// to as many CTAs as run at once: lengths as unequal as they like keep every SM
+// busy to the end, and a CTA's fixed time (about 5 us) is paid once or twice instead of per
+// range.  A share's first and last unit may be parts of one; the parts are
+// joined by a second launch.  Reads are what bounds this kernel (2 d bytes per key and
 // head against 4 G d operations), so mma.sync is the tensor path that fits:
 // tcgen05 would take codes widened in shared memory, 128 rows at a time, for
 // 4 to 16 rows of work.  Codes go from the swizzled tile into registers by
@@ -62,9 +67,22 @@ struct PagedParams {
     int box_rows;
     int causal;
     float scale_log2;
-    float* o_part;    // [T * Hq][splits][d]
-    float* lse_part;  // [T * Hq][splits], log2 units
+    float* o_part;    // [T * Hq][splits][d], or [2 CTAs][rows][d] (even shares)
+    float* lse_part;  // [T * Hq][splits], or [2 CTAs][rows]; log2 units
+    int4* shares;     // even shares: each CTA's first unit (first and last + 1 chunk, request, head)
 };
+constexpr int kEvenMaxB = 1024;  // requests whose chunk counts a CTA sums up
+
+// Rows and keys of request b; marks that cannot be leave it without rows.
+__device__ __forceinline__ void request_of(const PagedParams& p, int b, int& q0, int& nq, int& len, bool& bad) {
+    q0 = b, nq = 1;
+    if (p.cu_q) {
+        q0 = ld(p.cu_q + b);
+        nq = ld(p.cu_q + b + 1) - q0;
+        if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
+    }
+    len = ld(p.lens + b);
+}
 
 template <int D, int R>
 struct DecCfg {
@@ -83,12 +101,12 @@ struct DecCfg {
 };
 // Bytes of shared memory: rings (the warps' partial results reuse them), the
 // queries in fragment order, barriers.
-template <int D, int R>
+template <int D, int R, bool EVEN>
 constexpr int dec_smem() {
     using C = DecCfg<D, R>;
     const int ring = kDecWarps * C::kRing;
     const int join = kDecWarps * (R * C::kAccPad + R * 2) * 4 + R * D * 4;
-    return (ring > join ? ring : join) + R * C::kSteps * 32 + kDecWarps * C::kStages * 8 + 1024;
+    return (ring > join ? ring : join) + R * C::kSteps * 32 + kDecWarps * C::kStages * 8 + (EVEN ? (kEvenMaxB + 1) * 4 : 0) + 1024;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -132,8 +150,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-// R: rows of a CTA's block (8, 16 or 32)
-template <int D, int R>
+// R: rows of a CTA's block (8, 16 or 32).  EVEN: equal shares of all chunks
+// (one row block per request).
+template <int D, int R, bool EVEN>
 __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PagedParams p, const bool bf16) {
@@ -153,6 +172,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     uint4* qfrag = reinterpret_cast<uint4*>(smem + kOffQ);  // [MT][step][lane], or 8-byte [step][lane]
     __shared__ float row_unit[R];                           // 2^-e of each row's query scaling
     __shared__ __align__(8) float2 cta_stat[R];             // this CTA's maximum and sum of each row
+    __shared__ int failed;                                  // a wait of this CTA ran out
+    int* tab = reinterpret_cast<int*>(smem + kOffBar + kDecWarps * NST * 8);  // EVEN: chunks before each request
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -165,28 +186,101 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         ptx::fence_mbar_init();
     }
     if (tid == 0) {
+        failed = 0;
         ptx::prefetch_tensormap(&tm_k);
         ptx::prefetch_tensormap(&tm_v);
     }
     __syncwarp();
     dependents_may_start();
     wait_for_previous();
-    // unit: range fastest (a cluster's CTAs), then row block (they read the same keys), head, request
-    int u = blockIdx.x;
-    const int split = u % p.splits;
-    u /= p.splits;
-    const int rb = u % p.row_blocks;
-    u /= p.row_blocks;
-    const int h = u % p.Hk, b = u / p.Hk;
-
-    int q0 = b, nq = 1;
-    bool bad = false;
-    if (p.cu_q) {
-        q0 = ld(p.cu_q + b);
-        nq = ld(p.cu_q + b + 1) - q0;
-        if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
+    // ---- EVEN: this CTA's share [f, f1) of all chunks, in order of request, head, chunk
+    int f = 0, f0 = 0, f1 = 0;
+    if constexpr (EVEN) {
+        __shared__ int warp_sum[kDecWarps];
+        const int per_thread = (p.B + kDecThreads - 1) / kDecThreads;
+        const int b0 = min(tid * per_thread, p.B), b1 = min(b0 + per_thread, p.B);
+        auto chunks_of = [&](int b) {
+            int q, n, l;
+            bool bad = false;
+            request_of(p, b, q, n, l, bad);
+            if (l < 0 || l > (p.max_pages << p.page_shift)) bad = true, l = 0;
+            if (bad) report(kBadData);
+            if (n == 0) return 0;
+            if (p.sel) l = min(p.num_sel, (l + (1 << p.page_shift) - 1) >> p.page_shift) << p.page_shift;
+            return (l + KEYS - 1) / KEYS * p.Hk;
+        };
+        int mine_sum = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int n = chunks_of(b);
+            tab[b] = n;
+            mine_sum += n;
+        }
+        int incl = mine_sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) warp_sum[warp] = incl;
+        __syncthreads();
+        int run = incl - mine_sum;
+        for (int w = 0; w < warp; ++w) run += warp_sum[w];
+        for (int b = b0; b < b1; ++b) {
+            const int n = tab[b];
+            tab[b] = run;
+            run += n;
+        }
+        if (tid == kDecThreads - 1) tab[p.B] = run;
+        __syncthreads();
+        const int all = tab[p.B], G = static_cast<int>(gridDim.x), share = (all + G - 1) / G;
+        f = f0 = static_cast<int>(min(static_cast<long long>(blockIdx.x) * share, static_cast<long long>(all)));
+        f1 = min(f + share, all);
+        if (tid == 0) {
+            if (blockIdx.x == 0) p.shares[G] = make_int4(share, 0, 0, 0);
+            if (f == f1) p.shares[blockIdx.x] = make_int4(f, f, 0, 0);
+        }
+        // rows of requests without a key
+        for (int b = blockIdx.x; b < p.B; b += G) {
+            if (tab[b + 1] != tab[b]) continue;
+            int q, n, l;
+            bool bad = false;
+            request_of(p, b, q, n, l, bad);
+            const int d4 = p.d >> 2;
+            for (int i = tid; i < n * p.Hq * d4; i += kDecThreads) {
+                const int row = i / d4, c = (i - row * d4) * 4, tok = row / p.Hq, hq = row - tok * p.Hq;
+                *reinterpret_cast<uint2*>(p.o + (q + tok) * p.o_st + hq * p.o_sh + c) = make_uint2(0, 0);
+                if (c == 0) p.lse[static_cast<long long>(q + tok) * p.Hq + hq] = -INFINITY;
+            }
+        }
     }
-    int len = ld(p.lens + b);
+    int base = 0;  // chunks this warp has taken before this unit (phases of its ring)
+    do {
+    // unit: range fastest (a cluster's CTAs), then row block (they read the same keys), head, request
+    int split = 0, rb = 0, h, b, first = 0, last = 0;
+    bool whole = !EVEN;
+    if constexpr (EVEN) {
+        if (f >= f1) break;
+        b = owner_of(tab, p.B, f);
+        const int n = (tab[b + 1] - tab[b]) / p.Hk, rel = f - tab[b];
+        h = rel / n;
+        first = rel - h * n;
+        last = min(n, first + f1 - f);
+        whole = first == 0 && last == n;
+        if (tid == 0 && f == f0)
+            p.shares[blockIdx.x] = make_int4(f - first, f - first + n, b, h);
+        f += last - first;
+    } else {
+        int u = blockIdx.x;
+        split = u % p.splits;
+        u /= p.splits;
+        rb = u % p.row_blocks;
+        u /= p.row_blocks;
+        h = u % p.Hk, b = u / p.Hk;
+    }
+
+    int q0, nq, len;
+    bool bad = false;
+    request_of(p, b, q0, nq, len, bad);
     // the query rows, on their way while the lengths and pages are looked up
     constexpr int kQPass = (R + kDecWarps * C::kRowsPass - 1) / (kDecWarps * C::kRowsPass);
     const int piece = lane % C::kPieces, sub_row = lane / C::kPieces;
@@ -205,7 +299,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     if (len < 0 || (len >> p.page_shift) > p.max_pages || len > (p.max_pages << p.page_shift)) bad = true, len = 0;
     if (bad && tid == 0) report(kBadData);
     const int rows = nq * p.G;                 // packed rows of the request: r = i G + g
-    if (r0 >= rows) return;
+    if (!EVEN && r0 >= rows) return;
     const int my_rows = min(R, rows - r0);
     // keys the last row of the block sees; places the range covers (with a
     // selection, places in the concatenated selected pages)
@@ -222,7 +316,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     }
     const int chunks = (places + KEYS - 1) / KEYS;
     const int per = (chunks + p.splits - 1) / p.splits;
-    const int c0 = min(split * per, chunks), c1 = min(c0 + per, chunks);
+    const int c0 = EVEN ? min(first, chunks) : min(split * per, chunks);
+    const int c1 = EVEN ? min(last, chunks) : min(c0 + per, chunks);
     const int mine = c1 > c0 + warp ? (c1 - c0 - warp + kDecWarps - 1) / kDecWarps : 0;  // chunks of this warp
 
     // What a warp needs of its next chunks, per 16-key tile: lane i holds that
@@ -308,7 +403,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         if (s < mine) {
             int row[NT];
             row_of(s, row);
-            issue(row, s);
+            issue(row, (base + s) % NST);
         }
     }
     fetch_scales(cur);
@@ -395,8 +490,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     bool ok = true;
     int k = 0;
     for (; k < mine; ++k) {
-        const int s = k % NST;
-        if (!(ok = wait_warp(bars + 8 * s, (k / NST) & 1))) break;
+        const int s = (base + k) % NST;
+        if (!(ok = wait_warp(bars + 8 * s, ((base + k) / NST) & 1))) break;
         const uint32_t ks_base = ring + s * 2 * C::kHalf, vs_base = ks_base + C::kHalf;
         int pos[NT], row[NT];
         float kf[NT], ev[NT], rv[NT];
@@ -582,7 +677,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         }
     }
     if (!ok) {  // let copies in flight land before the CTA ends
-        for (const int end = min(k + NST, mine); k < end; ++k) wait_warp(bars + 8 * (k % NST), (k / NST) & 1);
+        if (lane == 0) failed = 1;
+        for (const int end = min(k + NST, mine); k < end; ++k) wait_warp(bars + 8 * ((base + k) % NST), ((base + k) / NST) & 1);
     }
 
     // ---- join the four warps' partial results
@@ -594,6 +690,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             for (int o = kTurned ? 4 : 1; o < (kTurned ? 32 : 4); o *= 2)
                 sum[m][r] += __shfl_xor_sync(0xffffffffu, sum[m][r], o);
     __syncthreads();  // every ring is drained: its memory takes the partial results
+    if (EVEN && failed) break;  // (the phases of its ring are lost)
     float* part = reinterpret_cast<float*>(smem);
     constexpr int kPartWarp = R * C::kAccPad + R * 2;
     {
@@ -647,6 +744,9 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         const int pr = r0 + r, i = pr / p.G, hq = h * p.G + pr - i * p.G;
         const long long tok = q0 + i;
         const long long grow = tok * p.Hq + hq;
+        // a part of the row's result: its place in the workspace
+        const long long at = EVEN ? (2ll * blockIdx.x + (first > 0 ? 0 : 1)) * R + r : grow * p.splits + split;
+        const bool partial = EVEN ? !whole : p.splits > 1;
         for (int c = lane * 4; c < p.d; c += 128) {
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -658,8 +758,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
             if (p.in_cluster)
                 *reinterpret_cast<float4*>(smem + kJoin + (r * D + c) * 4) = o;
-            else if (p.splits > 1)
-                *reinterpret_cast<float4*>(p.o_part + (grow * p.splits + split) * p.d + c) = o;
+            else if (partial)
+                *reinterpret_cast<float4*>(p.o_part + at * p.d + c) = o;
             else
                 *reinterpret_cast<uint2*>(p.o + tok * p.o_st + static_cast<long long>(hq) * p.o_sh + c) =
                     make_uint2(pack16(o.x, o.y, bf16), pack16(o.z, o.w, bf16));
@@ -667,11 +767,18 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         if (lane == 0) {
             if (p.in_cluster)
                 cta_stat[r] = make_float2(top, l);
-            else if (p.splits > 1)
-                p.lse_part[grow * p.splits + split] = lse2;
+            else if (partial)
+                p.lse_part[at] = lse2;
             else
                 p.lse[grow] = lse2 * 0.69314718055994531f;
         }
+    }
+    if constexpr (EVEN) {
+        // the next unit's boxes may land where partial results were written and read
+        ptx::fence_proxy_async_smem();
+        __syncthreads();
+        base += mine;
+        continue;
     }
     if (!p.in_cluster) return;
 
@@ -711,6 +818,64 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             p.lse[tok * p.Hq + hq] = l != 0.f ? (top - kWeightShift + log2f(l)) * 0.69314718055994531f : -INFINITY;
     }
     cluster_sync();  // the others have read this CTA's results
+    } while (EVEN);
+}
+
+// Joins the parts of a unit that shares cut: CTA i - 1 of this grid looks at
+// the boundary before share i, and takes the unit if it is the first in it.
+// A warp takes a row at a time: lane j the weight of part j, four channels of every part.
+constexpr int kJoinThreads = 256;
+template <int R>
+__global__ void __launch_bounds__(kJoinThreads) paged_even_join_kernel(const PagedParams p, const bool bf16) {
+    dependents_may_start();
+    wait_for_previous();
+    const int G = static_cast<int>(gridDim.x) + 1, i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int4 unit = ld(p.shares + i);  // first chunk, last + 1, request, head
+    const int share = ld(p.shares + G).x;
+    const long long at = static_cast<long long>(i) * share;
+    if (unit.x >= at || unit.y <= at || at - share > unit.x) return;
+    // share i - 1's last unit, then the first ones of the shares that begin inside
+    const int parts = 1 + static_cast<int>(min(static_cast<long long>(G - i), (unit.y - at + share - 1) / share));
+    auto slot = [&](int j) { return j == 0 ? 2ll * (i - 1) + 1 : 2ll * (i + j - 1); };
+    int q0, nq, len;
+    bool bad = false;
+    request_of(p, unit.z, q0, nq, len, bad);
+    const int my_rows = min(R, nq * p.G);
+    for (int r = threadIdx.x >> 5; r < my_rows; r += kJoinThreads / 32) {
+        const int tok = q0 + r / p.G, hq = unit.w * p.G + r % p.G;
+        for (int c0 = 0; c0 < p.d; c0 += 128) {
+            const int c = c0 + lane * 4;
+            float top = -INFINITY, l = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < parts; j0 += 32) {
+                const float a = j0 + lane < parts ? ld(p.lse_part + slot(j0 + lane) * R + r) : -INFINITY;
+                float next = fmaxf(a, top);
+#pragma unroll
+                for (int x = 16; x; x >>= 1) next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, x));
+                const float ref = next == -INFINITY ? 0.f : next, old = ptx::ex2_approx(top - ref);
+                const float w = ptx::ex2_approx(a - ref);
+                float sum = w;
+#pragma unroll
+                for (int x = 16; x; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+                top = next;
+                l = fmaf(l, old, sum);
+                o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+                const int n = min(32, parts - j0);
+#pragma unroll 4
+                for (int j = 0; j < n; ++j) {
+                    const float wj = __shfl_sync(0xffffffffu, w, j);
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (c < p.d) x = ld(reinterpret_cast<const float4*>(p.o_part + (slot(j0 + j) * R + r) * p.d + c));
+                    o.x = fmaf(x.x, wj, o.x), o.y = fmaf(x.y, wj, o.y), o.z = fmaf(x.z, wj, o.z), o.w = fmaf(x.w, wj, o.w);
+                }
+            }
+            const float inv = l != 0.f ? 1.f / l : 0.f;
+            if (c < p.d)
+                *reinterpret_cast<uint2*>(p.o + tok * p.o_st + hq * p.o_sh + c) =
+                    make_uint2(pack16(o.x * inv, o.y * inv, bf16), pack16(o.z * inv, o.w * inv, bf16));
+            if (c == 0) p.lse[static_cast<long long>(tok) * p.Hq + hq] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+    }
 }
 
 // O = sum_s 2^(lse_s - lse) O_s, LSE = log-sum over the ranges of a row.

@@ -560,6 +560,74 @@ def test_bad_device_data_is_reported():
         assert _torch().equal(out[0], good[0][0])              # the other request is served
 
 
+def _wide_table(table, P, keys):
+    """The same requests with a table that has room for `keys` keys (which decides how the work is split)."""
+    wide = np.full((table.shape[0], -(-keys // P)), -5)
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
+EVEN = [  # lens, news, Hk, G, P, d
+    ([0, 900, 1, 64, 333, 0, 0, 700, 31, 32, 33, 512, 5, 128, 640, 2], 1, 2, 4, 16, 128),
+    ([100 + 37 * i for i in range(20)], 1, 2, 8, 64, 64),
+    ([600 - 30 * i for i in range(20)], 1, 2, 7, 32, 256),
+    ([40 * i for i in range(16)], [2, 0, 1, 2] * 4, 2, 4, 128, 128),
+    ([3000, 1, 2900, 0] * 8, 1, 1, 16, 16, 96),
+    ([250 + i for i in range(30)], [3, 1, 0, 2, 3] * 6, 1, 10, 64, 80),
+    ([777, 3, 500] * 8, 1, 2, 24, 16, 64),
+    ([90, 0, 45] * 10, 1, 1, 12, 16, 192)]
+
+
+@pytest.mark.parametrize("lens,news,Hk,G,P,d", EVEN)
+@pytest.mark.parametrize("causal", [True, False])
+def test_even_shares(lens, news, Hk, G, P, d, causal):
+    """All requests' keys dealt out in equal shares: units cut into many parts, whole ones between them,
+    requests without keys or without queries."""
+    torch, fa = _torch(), _fa()
+    news = [news] * len(lens) if isinstance(news, int) else [min(n, max(m, 1)) for n, m in zip(news, lens)]
+    case = _attend_case(lens, news, Hk, G, P, d, "bf16" if d % 32 else "fp16", 101 + d + G)
+    cache, table, lens, cu, q = case
+    keys = 456 * 66 * 32 // (len(lens) * Hk)
+    wide = _wide_table(table, P, keys)
+    a = fa.fa_paged_args()
+    one = (np.diff(cu) == 1).all()
+    pad = torch.cat([q, q[:2]]) if not one else q
+    out = torch.full_like(pad, 3.0, device="cuda")
+    lse = torch.full(pad.shape[:2], 3.0, device="cuda")
+    a.q, a.o, a.lse, a.block_table, a.lens = out.data_ptr(), out.data_ptr(), lse.data_ptr(), lse.data_ptr(), lse.data_ptr()
+    a.cu_q = None if one else lse.data_ptr()
+    a.cache = fa.fa_kv_cache(out.data_ptr(), out.data_ptr(), lse.data_ptr(), lse.data_ptr(), None, cache.pages, P, Hk, d)
+    a.T, a.B, a.Hq, a.max_q, a.max_pages = pad.shape[0], len(lens), Hk * G, 1 if one else int(max(news)), wide.shape[1]
+    a.q_stride[:] = a.o_stride[:] = [Hk * G * d, d]
+    a.scale, a.causal, a.dtype, a.num_splits = 0.1, causal, fa.FA_BF16, 0
+    import ctypes
+    assert fa.library().fa_paged_num_splits(ctypes.addressof(a)) == 0      # (this is the way that is taken)
+    for _ in range(2):
+        _attend(cache, wide, lens, cu, pad, news, causal=causal, out=out, lse=lse)
+        _ok()
+        _check_attend(case, out[:len(q)], lse[:len(q)], causal)
+        assert (out[len(q):] == 3).all() and (lse[len(q):] == 3).all()
+
+
+def test_even_shares_of_selected_pages():
+    lens = [0, 5000, 64, 3000, 17, 900] * 6
+    case = _select_case(lens, 1, 4, 16, 128, "bf16", 102)
+    cache, table, lens, cu, q = case
+    keep = 64 * 30                                            # (room for them decides how the work is split)
+    g = cache.cuda()
+    rng = np.random.default_rng(102)
+    sel = np.full((len(lens), 1, keep), -1)
+    count = np.zeros((len(lens), 1), np.int64)
+    for b, n in enumerate(lens):
+        pages = -(-n // 16)
+        pick = np.sort(rng.choice(pages, size=min(pages, 40 + b), replace=False)) if pages else []
+        sel[b, 0, :len(pick)], count[b] = pick, len(pick)
+    out, lse = _fa().paged_attention_forward(q.cuda(), *g[:4], _i32(table), _i32(lens), selected=_i32(sel),
+                                             selected_count=_i32(count))
+    _ok()
+    _check_attend(case, out, lse, selected=[[list(r[r >= 0]) for r in rows] for rows in sel])
+
+
 # --------------------------------------------------------- page selection
 def _select_case(lens, Hk, G, P, d, dtype, seed):
     case = _attend_case(lens, [1] * len(lens), Hk, G, P, d, dtype, seed)
