@@ -25,7 +25,7 @@
  * (fa_check_device_status).
  * Every entry point enqueues on `stream`, on the current device, allocates
  * nothing and keeps no pointer; all may be captured in CUDA graphs after a
- * first call outside of a capture (which sets kernel attributes).
+ * call with the same sizes outside of a capture (which sets kernel attributes).
  */
 #ifndef FA_GB300_FA_PAGED_H
 #define FA_GB300_FA_PAGED_H

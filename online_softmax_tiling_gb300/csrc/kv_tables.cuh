@@ -14,8 +14,11 @@
 // requests) are not rows that are written (growing requests), and pushes go
 // to entries >= count while pops read entries < count.
 //
-// What bounds it: 4 bytes written per token, and for a decode step the
-// latency of one launch with two dependent reads.
+// What bounds it: latency.  3.4 us on the GPU for 8 requests, 7.3 us for 1000 that
+// bring 50 thousand tokens with ends and prompts among them, 5.6 us for 128 prompts of
+// 340 thousand tokens (the write of the slots alone would be 0.2 us): two dependent
+// reads, the prefix sums, the search for a token's request, its page, the write.  A
+// token per thread (1024 a CTA) beat four (9.3 us for the second).
 #pragma once
 
 #include "paged_common.cuh"

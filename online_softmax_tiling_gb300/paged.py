@@ -16,7 +16,7 @@ and, for one query per request over the best pages of a long context,
 All work is enqueued on `stream` (default: torch's current stream of the
 tensors' device); outputs and workspaces that are not given are allocated on
 that stream.  Nothing is allocated inside the library, so every call can be
-captured in a CUDA graph (after one call outside of a capture).  Bad device
+captured in a CUDA graph (after one call of the same sizes outside of a capture).  Bad device
 data (a page or slot outside of the cache, lengths beyond the table) is
 skipped by the kernels and reported by fa_check_device_status, which
 check=True calls here.

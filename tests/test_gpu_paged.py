@@ -609,6 +609,32 @@ def test_even_shares(lens, news, Hk, G, P, d, causal):
         assert (out[len(q):] == 3).all() and (lse[len(q):] == 3).all()
 
 
+def test_even_shares_in_a_graph_follow_the_lengths():
+    """A captured call reads lengths, tables and queries when it is replayed."""
+    torch, fa = _torch(), _fa()
+    case = _attend_case([500 + 11 * i for i in range(40)], [1] * 40, 1, 4, 16, 128, "fp16", 103)
+    cache, table, lens, cu, q = case
+    wide, g = _i32(_wide_table(table, 16, 456 * 66 * 32 // 40)), cache.cuda()
+    d_lens, d_q = _i32(lens), q.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        fa.paged_attention_forward(d_q, *g[:4], wide, d_lens)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = fa.paged_attention_forward(d_q, *g[:4], wide, d_lens)
+    rng = np.random.default_rng(103)
+    for _ in range(4):
+        now = np.where(rng.random(40) < 0.2, 0, rng.integers(1, lens + 1))
+        q2 = torch.from_numpy(rng.standard_normal(q.shape)).half()
+        d_lens.copy_(_i32(now))
+        d_q.copy_(q2)
+        graph.replay()
+        _ok()
+        _check_attend((cache, table, now, cu, q2), out, lse)
+
+
 def test_even_shares_of_selected_pages():
     lens = [0, 5000, 64, 3000, 17, 900] * 6
     case = _select_case(lens, 1, 4, 16, 128, "bf16", 102)
