@@ -219,9 +219,9 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     wait_for_previous();
     // rows t0 .. t0 + 255: the chunk and what runs that begin in it may reach
     const int t = t0 + tid;
-    const int slot = t < p.T ? ld(p.slots + t) : -1;
+    const int slot = t < p.T ? ld_meta(p.slots + t) : -1;
     int before = __shfl_up_sync(0xffffffffu, slot, 1);
-    if (lane == 0) before = (t > 0 && t - 1 < p.T) ? ld(p.slots + t - 1) : -1;
+    if (lane == 0) before = (t > 0 && t - 1 < p.T) ? ld_meta(p.slots + t - 1) : -1;
     const bool same = slot >= 0 && before >= 0 && (slot >> p.page_shift) == (before >> p.page_shift);
     const bool go_on = same && slot == before + 1;
     const uint32_t bits = __ballot_sync(0xffffffffu, !go_on);

@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const
     hist[0][tid] = 0;
     dependents_may_start();
     wait_for_previous();
-    int len = ld(p.lens + b);
+    int len = ld_meta(p.lens + b);
     if (len < 0 || len > (p.max_pages << p.page_shift)) {
         if (tid == 0 && rank == 0) report(kBadData);
         len = min(max(len, 0), p.max_pages << p.page_shift);
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kSelectThreads, 4) kv_page_select_kernel(const
 #pragma unroll
         for (int i = 0; i < kSelectAhead; ++i) {
             const int j = j0 + tid / LG + i * per_pass;
-            page[i] = j < j_end ? load_page(trow + j) : 0;
+            page[i] = j < j_end ? ld_meta(trow + j) : 0;
         }
     };
     auto load_bounds = [&](int j0) {

@@ -28,6 +28,7 @@ namespace paged {
 
 constexpr int kTablesThreads = 1024;
 constexpr int kTablesMaxB = 16384;
+constexpr int kTablesKeptLens = 8192;  // requests whose lengths stay in shared memory
 
 struct TablesParams {
     const int* new_tokens;
@@ -48,6 +49,8 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     int* cu = tab_smem;                 // [B + 1] tokens before request b
     int* pop = cu + p.B + 1;            // [B + 1] pages taken before request b
     int* push = pop + p.B + 1;          // [B + 1] pages released before request b
+    int* len_of = push + p.B + 1;       // [B] tokens held, where they fit
+    const bool keep_lens = p.B <= kTablesKeptLens;
     __shared__ long long warp_sums[3][kTablesThreads / 32];
     __shared__ long long totals[3];
     __shared__ int bad;
@@ -59,7 +62,8 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     __syncthreads();
 
     auto request = [&](int b, int& add, int& need, int& back) {
-        const int n = ld(p.new_tokens + b), len = ld(p.lens + b);
+        const int n = ld_meta(p.new_tokens + b), len = ld_meta(p.lens + b);
+        if (keep_lens) len_of[b] = len;
         const long long after = static_cast<long long>(max(len, 0)) + max(n, 0);
         const long long have = (static_cast<long long>(max(len, 0)) + P1) >> p.page_shift;
         const long long want = (after + P1) >> p.page_shift;
@@ -73,7 +77,7 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
         back = n < 0 ? static_cast<int>(have) : 0;
     };
 
-    const int count = ld(p.free_count);
+    const int count = ld_meta(p.free_count);
     // each thread sums a run of consecutive requests, then the block scans the sums
     const int per = (p.B + kTablesThreads - 1) / kTablesThreads;
     const int b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
@@ -131,30 +135,31 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     }
     __syncthreads();
 
+    auto length = [&](int b) { return keep_lens ? len_of[b] : ld_meta(p.lens + b); };
     const long long stride = static_cast<long long>(gridDim.x) * kTablesThreads;
     const long long first = static_cast<long long>(blockIdx.x) * kTablesThreads + tid;
     if (status != 0) {
         for (long long i = first; i < p.max_tokens; i += stride) p.slots[i] = -1;
         for (long long b = first; b <= p.B; b += stride) p.cu[b] = 0;
-        for (long long b = first; b < p.B; b += stride) p.lens_out[b] = ld(p.lens + b);
+        for (long long b = first; b < p.B; b += stride) p.lens_out[b] = length(b);
         if (first == 0) *p.free_count_out = count, *p.status = status;
         return;
     }
     // the page an entry of the stack holds after the pushes
     auto stack = [&](int i) {
-        if (i < count) return ld(p.free_pages + i);
+        if (i < count) return ld_meta(p.free_pages + i);
         const int r = i - count, b = owner_of(push, p.B, r);
-        return load_page(p.table + static_cast<long long>(b) * p.max_pages + (r - push[b]));
+        return ld_meta(p.table + static_cast<long long>(b) * p.max_pages + (r - push[b]));
     };
     const int top = count + static_cast<int>(R) - 1;
     for (long long t = first; t < p.max_tokens; t += stride) {
         int slot = -1;
         if (t < T) {
             const int b = owner_of(cu, p.B, static_cast<int>(t));
-            const int len = ld(p.lens + b);
+            const int len = length(b);
             const int pos = len + static_cast<int>(t) - cu[b];
             const int j = pos >> p.page_shift, have = (len + P1) >> p.page_shift;
-            const int page = j < have ? load_page(p.table + static_cast<long long>(b) * p.max_pages + j)
+            const int page = j < have ? ld_meta(p.table + static_cast<long long>(b) * p.max_pages + j)
                                       : stack(top - (pop[b] + j - have));
             slot = (page << p.page_shift) | (pos & P1);
         }
@@ -162,15 +167,15 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
     }
     for (long long i = first; i < A; i += stride) {
         const int b = owner_of(pop, p.B, static_cast<int>(i));
-        const int have = (ld(p.lens + b) + P1) >> p.page_shift;
+        const int have = (length(b) + P1) >> p.page_shift;
         p.table[static_cast<long long>(b) * p.max_pages + have + (static_cast<int>(i) - pop[b])] =
             stack(top - static_cast<int>(i));
     }
     for (long long i = first; i < R; i += stride) p.free_pages[count + i] = stack(count + static_cast<int>(i));
     for (long long b = first; b < p.B; b += stride) {
-        const int n = ld(p.new_tokens + b);
+        const int n = ld_meta(p.new_tokens + b);
         p.cu[b] = cu[b];
-        p.lens_out[b] = n < 0 ? 0 : ld(p.lens + b) + n;
+        p.lens_out[b] = n < 0 ? 0 : length(b) + n;
     }
     if (first == 0) {
         p.cu[p.B] = static_cast<int>(T);

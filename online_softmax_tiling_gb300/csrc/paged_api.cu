@@ -311,7 +311,7 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess) return FA_ERR_CUDA;
     const void* fn = reinterpret_cast<const void*>(&pg::kv_tables_kernel);
-    const int smem = 3 * (B + 1) * 4;
+    const int smem = (3 * (B + 1) + (B <= pg::kTablesKeptLens ? B : 0)) * 4;
     if (!ensure_smem(fn, 3 * (pg::kTablesMaxB + 1) * 4, device)) return FA_ERR_CUDA;
     pg::TablesParams p{new_tokens, lens, block_table, free_pages, free_count, B, max_pages, free_capacity,
                        shift, max_tokens, slots, cu_new, lens_out, free_count_out, status};

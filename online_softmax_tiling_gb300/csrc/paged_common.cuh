@@ -49,13 +49,13 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
 // global memory only behind wait_for_previous (that kernel's end, its writes visible).
 // So nothing is read on the read-only path, whose data must stand still from the
 // launch on (and whose loads may be moved ahead of the wait): ld() is a plain load.
-// Block tables go past L1 altogether: the kernel that reads one is often the next
-// behind the one that filled it in, from several SMs, line by line.
+// Lengths, tables and slots go past L1 altogether (ld_meta): the kernel that reads them is
+// often the next behind the one that wrote them, from several SMs, line by line.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename T>
 __device__ __forceinline__ T ld(const T* p) { return *p; }
-__device__ __forceinline__ int load_page(const int* p) { return __ldcg(p); }
+__device__ __forceinline__ int ld_meta(const int* p) { return __ldcg(p); }
 
 // Largest b in [0, n) with prefix[b] <= i (prefix ascending, prefix[0] = 0 <= i).
 __device__ __forceinline__ int owner_of(const int* prefix, int n, int i) {

@@ -79,11 +79,11 @@ constexpr int kEvenMaxB = 1024;  // requests whose chunk counts a CTA sums up
 __device__ __forceinline__ void request_of(const PagedParams& p, int b, int& q0, int& nq, int& len, bool& bad) {
     q0 = b, nq = 1;
     if (p.cu_q) {
-        q0 = ld(p.cu_q + b);
-        nq = ld(p.cu_q + b + 1) - q0;
+        q0 = ld_meta(p.cu_q + b);
+        nq = ld_meta(p.cu_q + b + 1) - q0;
         if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
     }
-    len = ld(p.lens + b);
+    len = ld_meta(p.lens + b);
 }
 
 template <int D, int R>
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     const int kend = p.causal ? min(len, len - nq + last_i + 1) : len;
     int places = max(kend, 0);
     if (p.sel) {
-        int n = ld(p.sel_count + b * p.Hk + h);
+        int n = ld_meta(p.sel_count + b * p.Hk + h);
         if (n < 0 || n > p.num_sel) {
             if (tid == 0) report(kBadData);
             n = 0;
@@ -339,12 +339,12 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             if (k >= mine || place >= places) continue;
             int lp = place >> p.page_shift;
             const int off = place & ((1 << p.page_shift) - 1);
-            if (p.sel) lp = ld(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
+            if (p.sel) lp = ld_meta(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
             const int pos = (lp << p.page_shift) + off;
             if (lp < 0 || lp >= p.max_pages) {
                 report(kBadData);
             } else if (pos < len) {
-                const int page = load_page(p.table + static_cast<long long>(b) * p.max_pages + lp);
+                const int page = ld_meta(p.table + static_cast<long long>(b) * p.max_pages + lp);
                 if (page < 0 || page >= p.num_pages) {
                     report(kBadData);
                 } else {
@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
     const long long tok = row / p.Hq;
     const int hq = static_cast<int>(row - tok * p.Hq);
     // rows behind the last query were not computed
-    if (tok >= p.T || (p.cu_q && tok >= ld(p.cu_q + p.B))) return;
+    if (tok >= p.T || (p.cu_q && tok >= ld_meta(p.cu_q + p.B))) return;
     const float* ls = p.lse_part + row * p.splits;
     float a0 = lane < p.splits ? ld(ls + lane) : -INFINITY, a1 = lane + 32 < p.splits ? ld(ls + lane + 32) : -INFINITY;
     float top = fmaxf(a0, a1);

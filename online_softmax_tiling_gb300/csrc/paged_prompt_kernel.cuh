@@ -132,11 +132,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     int q0 = b, nq = 1;
     bool bad = false;
     if (p.cu_q) {
-        q0 = ld(p.cu_q + b);
-        nq = ld(p.cu_q + b + 1) - q0;
+        q0 = ld_meta(p.cu_q + b);
+        nq = ld_meta(p.cu_q + b + 1) - q0;
         if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
     }
-    int len = ld(p.lens + b);
+    int len = ld_meta(p.lens + b);
     if (len < 0 || len > (p.max_pages << p.page_shift)) bad = true, len = 0;
     if (bad && tid == 0) report(kBadData);
     const int rows = nq * p.G, r0 = rb * kPrRows;
@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         bool bad_page = false;
         const int lane = ct & 31;
         auto load_pages = [&](int j) {
-            if (lane < 8) pages = load_page(trow + (min((k0 + j) * kPrTile + 16 * lane, len - 1) >> p.page_shift));
+            if (lane < 8) pages = ld_meta(trow + (min((k0 + j) * kPrTile + 16 * lane, len - 1) >> p.page_shift));
         };
         uint4 v[NV];
         PrGroup mg = {1.f, -INFINITY, 1.f};
