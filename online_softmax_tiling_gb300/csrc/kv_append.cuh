@@ -40,6 +40,8 @@ struct AppendParams {
     int pairs;                  // (head, K or V) pairs it takes
 };
 
+__device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
+__device__ __forceinline__ uint32_t as_bits(__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); }
 // bounds of a code: floor and ceiling of code / 4 (NaN counts as 0)
 __device__ __forceinline__ void code_bounds(float c, int& lo, int& hi) {
     const float q = (c != c) ? 0.f : c * 0.25f;
@@ -61,7 +63,7 @@ struct AppendTeam {
     const int LR, rows, r0, c8;  // threads per row (8 channels each), rows per pass, this thread's place
     const bool on;
     float* red;                  // team's shared memory: a value per warp,
-    uint4* bred;                 //   bounds of a thread's rows,
+    uint4* bred;                 //   least, then largest codes of a thread's rows (fp16 pairs),
     int *blo, *bhi;              //   bounds of a page's older codes
 
     __device__ AppendTeam(const AppendParams& p_, int tid_, float* red_, uint4* bred_, int* blo_, int* bhi_)
@@ -114,10 +116,10 @@ struct AppendTeam {
         uint8_t* base = (m.w ? p.codes[1] : p.codes[0]) + (ph << p.page_shift) * p.d;
         const bool with_bounds = BOUNDS && m.w == 0;
         if (grown) round_older(m, base, old * inv, with_bounds);
-        int lo[8], hi[8];
+        __half2 lo[4], hi[4];  // of the new codes, channels 2 e and 2 e + 1 (NaN as 0)
         if constexpr (BOUNDS) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) lo[e] = 127, hi[e] = -128;
+            for (int e = 0; e < 4; ++e) lo[e] = __float2half2_rn(INFINITY), hi[e] = __float2half2_rn(-INFINITY);
         }
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
@@ -134,39 +136,44 @@ struct AppendTeam {
             if (with_bounds) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = half2_floats(e4m3x2_to_half2(q[i]));
-                    code_bounds(f.x, lo[2 * i], hi[2 * i]);
-                    code_bounds(f.y, lo[2 * i + 1], hi[2 * i + 1]);
+                    uint32_t c = e4m3x2_to_half2(q[i]);
+                    c &= __heq2_mask(as_half2(c), as_half2(c));
+                    lo[i] = __hmin2(lo[i], as_half2(c));
+                    hi[i] = __hmax2(hi[i], as_half2(c));
                 }
             }
         }
         if (with_bounds) {
-            auto bytes = [](const int* x) {
-                return (x[0] & 255) | ((x[1] & 255) << 8) | ((x[2] & 255) << 16) | (static_cast<uint32_t>(x[3]) << 24);
-            };
-            bred[tid] = make_uint4(bytes(lo), bytes(lo + 4), bytes(hi), bytes(hi + 4));
+            bred[2 * tid] = make_uint4(as_bits(lo[0]), as_bits(lo[1]), as_bits(lo[2]), as_bits(lo[3]));
+            bred[2 * tid + 1] = make_uint4(as_bits(hi[0]), as_bits(hi[1]), as_bits(hi[2]), as_bits(hi[3]));
             sync();
-            // four channels a thread: words 0, 1 of a column's entries are floors, 2, 3 ceilings
-            int8_t* bd = p.bounds + ph * 2 * p.d;
+            // a thread takes the floors or the ceilings of two channels
             const int have = min(rows, m.n);
-            for (int i = tid; i < p.d / 2; i += TH) {
-                const int c4 = i % (p.d / 4), top = i / (p.d / 4);  // channels 4 c4 .., floor or ceiling
-                const uint32_t* col = reinterpret_cast<const uint32_t*>(bred + (c4 >> 1)) + 2 * top + (c4 & 1);
-                uint32_t x = top ? 0x80808080u : 0x7F7F7F7Fu;
-                for (int r = 0; r < have; ++r) x = top ? __vmaxs4(x, col[r * LR * 4]) : __vmins4(x, col[r * LR * 4]);
-                int8_t* at = bd + top * p.d + 4 * c4;
+            for (int i = tid; i < p.d; i += TH) {
+                const bool top = i >= p.d / 2;
+                const int c2 = top ? i - p.d / 2 : i;  // channels 2 c2, 2 c2 + 1
+                const uint32_t* col = reinterpret_cast<const uint32_t*>(bred + 2 * (c2 >> 2) + top) + (c2 & 3);
+                __half2 x = as_half2(col[0]);
+                for (int r = 1; r < have; ++r) {
+                    const __half2 y = as_half2(col[r * LR * 8]);
+                    x = top ? __hmax2(x, y) : __hmin2(x, y);
+                }
+                const float2 f = __half22float2(x);
+                int a = top ? __float2int_ru(f.x * 0.25f) : __float2int_rd(f.x * 0.25f);
+                int b = top ? __float2int_ru(f.y * 0.25f) : __float2int_rd(f.y * 0.25f);
+                int8_t* at = p.bounds + ph * 2 * p.d + (top ? p.d : 0) + 2 * c2;
                 if (!fresh) {
                     // the older codes': as they stand, or as rounded again
-                    uint32_t y;
+                    int c, d;
                     if (grown) {
-                        const int* b = (top ? bhi : blo) + 4 * c4;
-                        y = bytes(b);
+                        c = (top ? bhi : blo)[2 * c2], d = (top ? bhi : blo)[2 * c2 + 1];
                     } else {
-                        y = *reinterpret_cast<const uint32_t*>(at);
+                        const char2 o = *reinterpret_cast<const char2*>(at);
+                        c = o.x, d = o.y;
                     }
-                    x = top ? __vmaxs4(x, y) : __vmins4(x, y);
+                    a = top ? max(a, c) : min(a, c), b = top ? max(b, d) : min(b, d);
                 }
-                *reinterpret_cast<uint32_t*>(at) = x;
+                *reinterpret_cast<char2*>(at) = make_char2(static_cast<signed char>(a), static_cast<signed char>(b));
             }
         }
         sync();  // the team's shared memory is free again
@@ -209,7 +216,7 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     __shared__ int n_short, n_long;
     __shared__ int2 short_runs[kAppendMaxChunk], long_runs[kAppendMaxChunk];  // row in the chunk | length << 8, slot
     __shared__ float red[kWarps];
-    __shared__ uint4 bred[BOUNDS ? kAppendThreads : 1];
+    __shared__ uint4 bred[BOUNDS ? 2 * kAppendThreads : 1];
     __shared__ int blo[BOUNDS ? kWarps : 1][256], bhi[BOUNDS ? kWarps : 1][256];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int P = 1 << p.page_shift;
@@ -286,7 +293,7 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     }
     if (n_short > 0) {
         const int w = BOUNDS ? warp : 0;
-        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS> team(p, lane, red, bred + (BOUNDS ? 32 * warp : 0), blo[w], bhi[w]);
+        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS> team(p, lane, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
         for (int i = warp; i < n_short * pairs; i += kWarps) {
             const AppendItem m = item(short_runs, i);
             uint4 v[kAppendShortRows];
