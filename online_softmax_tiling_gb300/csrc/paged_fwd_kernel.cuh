@@ -26,8 +26,8 @@
 // busy to the end, and a CTA's fixed time (about 5 us) is paid once or twice instead of per
 // range.  A share's first and last unit may be parts of one; the parts are
 // joined by a second launch.  64 requests of 5000 to 16384 keys, 32 query and 8 key
-// heads, d 128: 229 us, 6.1 TB/s (250 with two ranges per row); one request of 4096
-// keys: 10.3 us.  Reads are what bounds this kernel (2 d bytes per key and
+// heads, d 128: 226 us, 6.2 TB/s (248 with two ranges per row); one request of 4096
+// keys: 10.1 us.  Reads are what bounds this kernel (2 d bytes per key and
 // head against 4 G d operations), so mma.sync is the tensor path that fits:
 // tcgen05 would take codes widened in shared memory, 128 rows at a time, for
 // 4 to 16 rows of work.  Codes go from the swizzled tile into registers by
@@ -283,6 +283,17 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     int q0, nq, len;
     bool bad = false;
     request_of(p, b, q0, nq, len, bad);
+    // This warp's chunks are chunk0 + k step, whatever the length (ranges are
+    // interleaved, a share is contiguous): the pages of the first 32 are looked up
+    // while the length is still on its way.
+    const int chunk0 = EVEN ? first + warp : split * kDecWarps + warp, step = EVEN ? kDecWarps : p.splits * kDecWarps;
+    int early[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const long long lp = (static_cast<long long>(chunk0 + lane * step) * KEYS + i * 16) >> p.page_shift;
+        early[i] = 0;
+        if (!p.sel && lp < p.max_pages) early[i] = ld_meta(p.table + static_cast<long long>(b) * p.max_pages + lp);
+    }
     // the query rows, on their way while the lengths and pages are looked up
     constexpr int kQPass = (R + kDecWarps * C::kRowsPass - 1) / (kDecWarps * C::kRowsPass);
     const int piece = lane % C::kPieces, sub_row = lane / C::kPieces;
@@ -317,10 +328,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         places = n << p.page_shift;
     }
     const int chunks = (places + KEYS - 1) / KEYS;
-    const int per = (chunks + p.splits - 1) / p.splits;
-    const int c0 = EVEN ? min(first, chunks) : min(split * per, chunks);
-    const int c1 = EVEN ? min(last, chunks) : min(c0 + per, chunks);
-    const int mine = c1 > c0 + warp ? (c1 - c0 - warp + kDecWarps - 1) / kDecWarps : 0;  // chunks of this warp
+    const int end = EVEN ? min(last, chunks) : chunks;
+    const int mine = end > chunk0 ? (end - chunk0 + step - 1) / step : 0;  // chunks of this warp
 
     // What a warp needs of its next chunks, per 16-key tile: lane i holds that
     // of chunk 32 n + i (refilled one block ahead).
@@ -330,13 +339,13 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         float ks[NT], ev[NT], rv[NT];  // scales: of K; log2 and reciprocal of V's
     };
     // pages first, so that the boxes can be issued; then the scales
-    auto fetch = [&](int k) {
+    auto fetch = [&](int k, bool looked_up) {
         Meta m;
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
             m.row[i] = -1, m.pos[i] = len;
-            const int place = (c0 + warp + k * kDecWarps) * KEYS + i * 16;
-            if (k >= mine || place >= places) continue;
+            const int place = k < mine ? (chunk0 + k * step) * KEYS + i * 16 : places;
+            if (place >= places) continue;
             int lp = place >> p.page_shift;
             const int off = place & ((1 << p.page_shift) - 1);
             if (p.sel) lp = ld_meta(p.sel + static_cast<long long>(b * p.Hk + h) * p.num_sel + lp);
@@ -344,7 +353,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             if (lp < 0 || lp >= p.max_pages) {
                 report(kBadData);
             } else if (pos < len) {
-                const int page = ld_meta(p.table + static_cast<long long>(b) * p.max_pages + lp);
+                const int page = looked_up && !p.sel ? early[i] : ld_meta(p.table + static_cast<long long>(b) * p.max_pages + lp);
                 if (page < 0 || page >= p.num_pages) {
                     report(kBadData);
                 } else {
@@ -390,7 +399,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             }
         }
     };
-    Meta cur = fetch(lane), nxt = cur;
+    Meta cur = fetch(lane, true), nxt = cur;
     auto row_of = [&](int k, int (&row)[NT]) {  // k in the current or the next block
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
@@ -410,7 +419,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
     }
     fetch_scales(cur);
     if (mine > 32) {
-        nxt = fetch(32 + lane);
+        nxt = fetch(32 + lane, false);
         fetch_scales(nxt);
     }
 
@@ -673,14 +682,14 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         }
         // chunk k was the last of its block: refill that block two further on
         if ((k & 31) == 31) {
-            Meta m = fetch(k + 33 + lane);
+            Meta m = fetch(k + 33 + lane, false);
             fetch_scales(m);
             if (odd) nxt = m; else cur = m;
         }
     }
     if (!ok) {  // let copies in flight land before the CTA ends
         if (lane == 0) failed = 1;
-        for (const int end = min(k + NST, mine); k < end; ++k) wait_warp(bars + 8 * ((base + k) % NST), ((base + k) / NST) & 1);
+        for (const int until = min(k + NST, mine); k < until; ++k) wait_warp(bars + 8 * ((base + k) % NST), ((base + k) / NST) & 1);
     }
 
     // ---- join the four warps' partial results

@@ -2,9 +2,10 @@
 // query rows per key head (prompts and pieces of them), d <= 128.
 //
 // Three pieces of 1288 to 2048 queries over up to 8192 keys, 32 query and 8 key heads,
-// d 128: 450 us, 1.10 PFLOP/s of visible pairs; the tensor pipe is active 42% of the time and
-// waits for weights otherwise (without the widening 410 us, without widening and
-// softmax 349).
+// d 128: 450 us, 1.10 PFLOP/s of visible pairs.  Of 3,840 cycles per key tile the products
+// take 2,750 (2,048 at their full rate: the widened tiles are written to the shared
+// memory that S = Q K^T reads without a pause), waits for weights 800, for K and V
+// 290 (without the widening 410 us, without widening and softmax 349).
 //
 // The mathematics is that of paged_fwd_kernel.cuh: weights 2^(x_j + ev_j) with
 // ev_j the exponent of the value page's scale, so that both products run on
