@@ -196,9 +196,16 @@ int choose_splits(const fa_paged_args& a, const Plan& pl) {
         if (2 * pl.units > sms) return 1;
         return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({sms / pl.units, keys / 512, FA_PAGED_MAX_SPLITS})));
     }
-    // One wave of about two CTAs per SM, in a count that a cluster can join;
-    // each range of at least 256 keys.
+    // One CTA of eight warps per SM where that fills three quarters of them, or
+    // leaves a warp at most eight chunks (one request of 4096 keys, 8 heads: 8.6 us, 10.1
+    // with CTAs of four warps; 16 of 2048: 16.4 and 20.7; 24 of 8000 and 4 heads, 96 of 152
+    // SMs: 52 and 37).
     int s = 1;
+    while (s < 8 && 2 * s * pl.units <= sms && keys >= 2 * s * 256) s *= 2;
+    if (s * pl.units <= sms && (4 * s * pl.units >= 3 * sms || keys <= s * 2048)) return s;
+    // Else one wave of about two CTAs per SM, in a count that a cluster can join;
+    // each range of at least 256 keys.
+    s = 1;
     while (s < pg::kDecMaxCluster && 2 * s * pl.units <= 2 * sms && keys >= 2 * s * 256) s *= 2;
     // Few heads and a long context: more ranges than a cluster holds, through a
     // workspace (one request of 8 key heads and 65536 keys: 37 us with 32, 55 with 16).
@@ -230,14 +237,18 @@ struct KernelEntry {
     int smem;
 };
 template <int D, int R>
-KernelEntry few_rows(bool even) {
-    if (even) return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, true>), pg::dec_smem<D, R, true>()};
-    return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, false>), pg::dec_smem<D, R, false>()};
+KernelEntry few_rows(bool even, int warps) {
+    static_assert(pg::dec_smem<D, R, true, 4>() <= 232448 && pg::dec_smem<D, R, false, 8>() <= 232448, "shared memory of a CTA");
+    if (even) return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, true, 4>), pg::dec_smem<D, R, true, 4>()};
+    if (warps == 8) return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, false, 8>), pg::dec_smem<D, R, false, 8>()};
+    return {reinterpret_cast<const void*>(&pg::paged_fwd_kernel<D, R, false, 4>), pg::dec_smem<D, R, false, 4>()};
 }
-KernelEntry select_kernel(int width, int rows, bool even) {
-    if (width == 64) return rows == 8 ? few_rows<64, 8>(even) : rows == 16 ? few_rows<64, 16>(even) : few_rows<64, 32>(even);
-    if (width == 128) return rows == 8 ? few_rows<128, 8>(even) : rows == 16 ? few_rows<128, 16>(even) : few_rows<128, 32>(even);
-    return rows == 8 ? few_rows<256, 8>(even) : few_rows<256, 16>(even);
+KernelEntry select_kernel(int width, int rows, bool even, int warps) {
+    if (width == 64)
+        return rows == 8 ? few_rows<64, 8>(even, warps) : rows == 16 ? few_rows<64, 16>(even, warps) : few_rows<64, 32>(even, warps);
+    if (width == 128)
+        return rows == 8 ? few_rows<128, 8>(even, warps) : rows == 16 ? few_rows<128, 16>(even, warps) : few_rows<128, 32>(even, warps);
+    return rows == 8 ? few_rows<256, 8>(even, warps) : few_rows<256, 16>(even, warps);
 }
 const void* select_even_join(int rows) {
     return rows == 8    ? reinterpret_cast<const void*>(&pg::paged_even_join_kernel<8>)
@@ -424,10 +435,13 @@ int fa_paged_fwd(const fa_paged_args* args) {
         void* kargs[] = {&kc, &vc, &p, &bf16};
         if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, pg::kPrThreads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
     } else {
-        const KernelEntry ke = select_kernel(pl.width, pl.block_rows, pl.even != 0);
+        // eight warps where one CTA per SM is all there is (clusters of 16 such CTAs
+        // find no place for many: 13.7 us against 10.1 for one request of 4096 keys)
+        const int warps = !pl.even && units <= sm_count() && splits != pg::kDecMaxCluster ? 8 : 4;
+        const KernelEntry ke = select_kernel(pl.width, pl.block_rows, pl.even != 0, warps);
         void* kargs[] = {&tk, &tv, &p, &bf16};
         if (!ensure_smem(ke.fn, ke.smem, device) ||
-            !launch(ke.fn, units, 1, pg::kDecThreads, ke.smem, p.in_cluster ? splits : 1, a.stream, kargs))
+            !launch(ke.fn, units, 1, 32 * warps, ke.smem, p.in_cluster ? splits : 1, a.stream, kargs))
             return FA_ERR_CUDA;
     }
     if (pl.even) {

@@ -14,10 +14,10 @@
 // out nothing above 2^-38 of that value.
 //
 // Mapping.  The G query heads of a key head (times the request's new tokens)
-// are packed rows; a CTA takes 8, 16 or 32 of them and a range of keys.  Its four
+// are packed rows; a CTA takes 8, 16 or 32 of them and a range of keys.  Its four (or eight)
 // warps take 32-key chunks in turn (16-key ones for d > 128), each
 // with a TMA ring, a running softmax and an accumulator of its own; nothing
-// is shared until the end, where the four partial results are joined in
+// is shared until the end, where their partial results are joined in
 // shared memory.  The CTAs of 2, 4, 8 or 16 key ranges are a cluster and join
 // theirs over distributed shared memory, without a workspace or a second
 // launch; other counts go through a workspace and a merge.  For many keys
@@ -27,7 +27,7 @@
 // range.  A share's first and last unit may be parts of one; the parts are
 // joined by a second launch.  64 requests of 5000 to 16384 keys, 32 query and 8 key
 // heads, d 128: 226 us, 6.2 TB/s (248 with two ranges per row); one request of 4096
-// keys: 10.1 us.  Reads are what bounds this kernel (2 d bytes per key and
+// keys: 8.6 us (10.1 with 16 CTAs of four warps).  Reads are what bounds this kernel (2 d bytes per key and
 // head against 4 G d operations), so mma.sync is the tensor path that fits:
 // tcgen05 would take codes widened in shared memory, 128 rows at a time, for
 // 4 to 16 rows of work.  Codes go from the swizzled tile into registers by
@@ -45,8 +45,6 @@
 namespace fa {
 namespace paged {
 
-constexpr int kDecWarps = 4;
-constexpr int kDecThreads = 32 * kDecWarps;
 constexpr float kWeightShift = 14.f;
 constexpr int kDecMaxCluster = 16;
 
@@ -103,12 +101,12 @@ struct DecCfg {
 };
 // Bytes of shared memory: rings (the warps' partial results reuse them), the
 // queries in fragment order, barriers.
-template <int D, int R, bool EVEN>
+template <int D, int R, bool EVEN, int W>
 constexpr int dec_smem() {
     using C = DecCfg<D, R>;
-    const int ring = kDecWarps * C::kRing;
-    const int join = kDecWarps * (R * C::kAccPad + R * 2) * 4 + R * D * 4;
-    return (ring > join ? ring : join) + R * C::kSteps * 32 + kDecWarps * C::kStages * 8 + (EVEN ? (kEvenMaxB + 1) * 4 : 0) + 1024;
+    const int ring = W * C::kRing;
+    const int join = W * (R * C::kAccPad + R * 2) * 4 + R * D * 4;
+    return (ring > join ? ring : join) + R * C::kSteps * 32 + W * C::kStages * 8 + (EVEN ? (kEvenMaxB + 1) * 4 : 0) + 1024;
 }
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -152,13 +150,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-// R: rows of a CTA's block (8, 16 or 32).  EVEN: equal shares of all chunks
+// R: rows of a CTA's block (8, 16 or 32).  W: warps, 4, or 8 in one CTA per SM where
+// few CTAs have little to do each (one request of 4096 keys: a cluster of 8 such
+// CTAs instead of 16 of four warps).  EVEN: equal shares of all chunks
 // (one row block per request).
-template <int D, int R, bool EVEN>
-__global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
+template <int D, int R, bool EVEN, int W>
+__global__ void __launch_bounds__(32 * W, (W == 4 ? DecCfg<D, R>::kMinCtas : 1))
     paged_fwd_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const PagedParams p, const bool bf16) {
     using C = DecCfg<D, R>;
+    constexpr int kDecWarps = W, kDecThreads = 32 * W;
     constexpr bool kTurned = R == 8;    // codes first, rows as N
     constexpr int MT = R / 16;          // 16-row tiles (not kTurned)
     constexpr int NST = C::kStages, KEYS = C::kKeys, NT = C::kTiles;
@@ -393,9 +394,9 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
             if ((i & (tiles_per_box - 1)) || row[i] < 0) continue;
 #pragma unroll
             for (int c = 0; c < C::kSub; ++c) {
-                constexpr int W = D > 128 ? 128 : D;  // bytes of a row in one column group
-                tma_load_2d(kd + c * KEYS * 128 + i * 16 * W, &tm_k, bar, 128 * c, row[i]);
-                tma_load_2d(vd + c * KEYS * 128 + i * 16 * W, &tm_v, bar, 128 * c, row[i]);
+                constexpr int kRowBytes = D > 128 ? 128 : D;  // of a row in one column group
+                tma_load_2d(kd + c * KEYS * 128 + i * 16 * kRowBytes, &tm_k, bar, 128 * c, row[i]);
+                tma_load_2d(vd + c * KEYS * 128 + i * 16 * kRowBytes, &tm_v, bar, 128 * c, row[i]);
             }
         }
     };
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(kDecThreads, (DecCfg<D, R>::kMinCtas))
         for (const int until = min(k + NST, mine); k < until; ++k) wait_warp(bars + 8 * ((base + k) % NST), ((base + k) / NST) & 1);
     }
 
-    // ---- join the four warps' partial results
+    // ---- join the warps' partial results
 #pragma unroll
     for (int m = 0; m < NR; ++m)
 #pragma unroll

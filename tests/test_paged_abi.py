@@ -105,12 +105,18 @@ def test_null_structures(lib):
 
 def test_splits_and_workspace(lib):
     """With GB300's 152 SMs (counted where no device answers)."""
-    n = lambda **kw: lib.fa_paged_num_splits(ctypes.addressof(_args(**kw)))  # noqa: E731
+    def n(**kw):
+        a = _args(**kw)  # (held until the call is over)
+        return lib.fa_paged_num_splits(ctypes.addressof(a))
+
+    def ws(**kw):
+        a = _args(**kw)
+        return lib.fa_paged_workspace_size(ctypes.addressof(a))
+
     assert n(max_pages=16) == 1                                   # 256 keys: one range
     assert 1 < n(max_pages=1000) <= fa.FA_PAGED_MAX_SPLITS        # 6 units, many keys
     assert n(T=4000, B=4000, max_pages=1000) == 1                 # units enough
     assert n(scale=-1.0) == 1
-    ws = lambda **kw: lib.fa_paged_workspace_size(ctypes.addressof(_args(**kw)))  # noqa: E731
     for s in (1, 2, 4, 8, 16):                                    # joined on chip
         assert ws(num_splits=s) == 0
     assert ws(num_splits=3) == 3 * 4 * 3 * 64 * 4 + 3 * 4 * 3 * 4
