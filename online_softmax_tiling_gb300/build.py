@@ -14,7 +14,7 @@ SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "paged_api.cu", "ceiling
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa_fwd_qtile_kernel.cuh", "fa_fwd_wide_kernel.cuh",
                                                      "naive_attention.cuh", "paged_common.cuh", "kv_tables.cuh",
                                                      "kv_append.cuh", "kv_page_select.cuh", "paged_fwd_kernel.cuh",
-                                                     "paged_prompt_kernel.cuh",
+                                                     "paged_prompt_kernel.cuh", "paged_prompt_wide_kernel.cuh",
                                                      "sm103_ptx.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_ceilings.h", "fa_naive.h", "fa_paged.h")]
 LIBRARY = os.path.join(HERE, "libfa_gb300.so")

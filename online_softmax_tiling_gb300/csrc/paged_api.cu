@@ -17,6 +17,7 @@
 #include "kv_tables.cuh"
 #include "paged_fwd_kernel.cuh"
 #include "paged_prompt_kernel.cuh"
+#include "paged_prompt_wide_kernel.cuh"
 
 namespace {
 
@@ -142,7 +143,7 @@ int width_of(int d) { return d <= 64 ? 64 : d <= 128 ? 128 : 256; }
 int block_rows_of(int width, int64_t rows) { return rows <= 8 ? 8 : width == 256 || rows <= 16 ? 16 : 32; }
 
 struct Plan {
-    bool prompt;    // tcgen05 kernel (256 packed rows per unit)
+    bool prompt;    // a tcgen05 kernel (256 packed rows per unit, 128 for d > 128)
     int width, block_rows, row_blocks;
     int64_t units;  // row blocks x heads x requests
     int even;       // CTAs of equal shares of all keys (0: key ranges per row block)
@@ -150,7 +151,9 @@ struct Plan {
 
 // Packed rows above which the tcgen05 kernel serves a request: 8 requests of 4000
 // keys and 8 heads take 35 us for 32 rows on the few-row kernel and 38 on the other, 52
-// and 40 for 48 rows (which the few-row kernel reads every key twice for).
+// and 40 for 48 rows (which the few-row kernel reads every key twice for).  With d = 256 and
+// 16 requests of up to 6000 keys, 8 heads: 140 and 121 us for 32 rows, 184 and 121 for 48
+// (2 requests, 2 heads: 20 and 30, 21 and 30).
 constexpr int kPromptRows = 32;
 
 // CTAs that share all keys evenly, one wave of them, or 0 where ranges per row
@@ -173,8 +176,8 @@ Plan plan_of(const fa_paged_args& a) {
     Plan pl{};
     const int64_t rows = static_cast<int64_t>(a.max_q) * (a.Hq / a.cache.Hk);
     pl.width = width_of(a.cache.d);
-    pl.prompt = pl.width <= 128 && rows > kPromptRows && !a.selected;
-    pl.block_rows = pl.prompt ? pg::kPrRows : block_rows_of(pl.width, rows);
+    pl.prompt = rows > kPromptRows && !a.selected;
+    pl.block_rows = !pl.prompt ? block_rows_of(pl.width, rows) : pl.width == 256 ? pg::kPwRows : pg::kPrRows;
     pl.row_blocks = static_cast<int>((rows + pl.block_rows - 1) / pl.block_rows);
     pl.units = static_cast<int64_t>(pl.row_blocks) * a.cache.Hk * a.B;
     pl.even = a.num_splits == 0 ? even_ctas(a, pl) : 0;
@@ -429,11 +432,13 @@ int fa_paged_fwd(const fa_paged_args* args) {
     bool bf16 = a.dtype == FA_BF16;
     if (pl.prompt) {
         const uint8_t *kc = static_cast<const uint8_t*>(a.cache.k), *vc = static_cast<const uint8_t*>(a.cache.v);
-        const void* fn = pl.width == 64 ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<64>)
-                                        : reinterpret_cast<const void*>(&pg::paged_prompt_kernel<128>);
-        const int smem = pl.width == 64 ? pg::PrCfg<64>::kSmem : pg::PrCfg<128>::kSmem;
+        const void* fn = pl.width == 64    ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<64>)
+                         : pl.width == 128 ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<128>)
+                                           : reinterpret_cast<const void*>(&pg::paged_prompt_wide_kernel);
+        const int smem = pl.width == 64 ? pg::PrCfg<64>::kSmem : pl.width == 128 ? pg::PrCfg<128>::kSmem : pg::kPwSmem;
+        const int threads = pl.width == 256 ? pg::kPwThreads : pg::kPrThreads;
         void* kargs[] = {&kc, &vc, &p, &bf16};
-        if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, pg::kPrThreads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
+        if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, threads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
     } else {
         // eight warps where one CTA per SM is all there is (clusters of 16 such CTAs
         // find no place for many: 13.7 us against 10.1 for one request of 4096 keys)

@@ -436,6 +436,62 @@ def test_several_queries(lens, news, Hk, G, P, d, causal, dtype, splits):
     _check_attend(case, out, lse, causal)
 
 
+WIDE_PROMPT = [  # lens, news, Hk, G, P, d
+    ([5, 40, 0, 300], [5, 25, 0, 17], 2, 4, 16, 256),
+    ([33, 64, 200], [33, 20, 130], 1, 2, 32, 144),
+    ([1, 63, 64, 65], [1, 63, 64, 65], 1, 1, 16, 192),
+    ([128, 129, 2000], [128, 129, 37], 1, 3, 128, 160),
+    ([700, 500], [260, 300], 1, 8, 64, 256),
+    ([1300, 80], [200, 80], 2, 5, 128, 208),
+]
+
+
+@pytest.mark.parametrize("lens,news,Hk,G,P,d", WIDE_PROMPT)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,splits", [("bf16", 0), ("fp16", 1), ("bf16", 3)])
+def test_several_queries_of_wide_heads(lens, news, Hk, G, P, d, causal, dtype, splits):
+    """Tiles of 64 keys and 128 packed rows: more tiles than stages, odd and even counts, ragged ends."""
+    case = _attend_case(lens, news, Hk, G, P, d, dtype, 151 + d + len(lens))
+    out, lse = _attend(*case, news, causal=causal, num_splits=splits)
+    _ok()
+    _check_attend(case, out, lse, causal)
+
+
+@pytest.mark.parametrize("d", [128, 256])
+def test_several_queries_over_a_wide_range_of_scales(d):
+    """The running reference moves late and by much; rows of very different size; some see no key."""
+    news = [100, 70]
+    case = _attend_case([900, 30], news, 2, 2, 16, d, "bf16", 164 + d)
+    cache, table, lens, cu, q = case
+    rng = np.random.default_rng(64)
+    cache.scale["v"] = 2.0 ** rng.integers(-30, 20, cache.scale["v"].shape)
+    cache.scale["k"] = 2.0 ** rng.integers(-12, -3, cache.scale["k"].shape)
+    q[3, 1] *= 50.0
+    q[4, 0] *= 1e-20
+    q[5, 2] = 0
+    for splits in (1, 3):
+        out, lse = _attend(*case, news, num_splits=splits)
+        _ok()
+        O, L, A, D = ref.attend(cache, q.double().numpy(), table, lens, cu, 1 / math.sqrt(d), True)
+        ref.check(out, lse, (O, L, A, D), d, 900, 448 * cache.scale["v"].max(), q.dtype)
+        assert (lse[100:140].isinf()).all() and (out[100:140] == 0).all()
+
+
+def test_bad_pages_of_wide_heads_are_reported():
+    fa = _fa()
+    news = [40, 30]
+    cache, table, lens, cu, q = _attend_case([100, 100], news, 1, 2, 16, 256, "fp16", 167)
+    good = _attend(cache, table, lens, cu, q, news)
+    _ok()
+    for entry in (cache.pages, -1):
+        t = table.copy()
+        t[1, 3] = entry
+        out, lse = _attend(cache, t, lens, cu, q, news)
+        assert fa.fa_check_device_status(None) == fa.FA_ERR_INVALID_ARG
+        _ok()
+        assert _torch().equal(out[:40], good[0][:40])
+
+
 def test_queries_that_see_no_key():
     """More queries than keys: the first ones see nothing and get 0 and -inf."""
     news = [20, 140, 3]
