@@ -189,6 +189,14 @@ bool in_cluster(const Plan& pl, int splits) {
     return !pl.prompt && !pl.even && (splits == 2 || splits == 4 || splits == 8 || splits == 16);
 }
 
+// Clusters of s CTAs (1, 2, 4, 8 or 16) that the GPU holds at once with one CTA on an SM: a
+// cluster lies within one group of SMs.  One more waits for a whole wave (one
+// request of 2000 keys: 7.6 us for 15 clusters of 8 and 13.4 for 16; 9.1 for 36 of 4 and
+// 16.0 for 37).
+int places(int s) {
+    return s == 1 ? sm_count() : s == 2 ? sm_count() / 2 : s == 4 ? sm_count() * 9 / 38 : s == 8 ? sm_count() / 10 : sm_count() / 20;
+}
+
 // Key ranges for num_splits = 0.
 int choose_splits(const fa_paged_args& a, const Plan& pl) {
     const int64_t keys = static_cast<int64_t>(a.selected ? a.num_selected : a.max_pages) * a.cache.page_size;
@@ -203,13 +211,15 @@ int choose_splits(const fa_paged_args& a, const Plan& pl) {
     // leaves a warp at most eight chunks (one request of 4096 keys, 8 heads: 8.6 us, 10.1
     // with CTAs of four warps; 16 of 2048: 16.4 and 20.7; 24 of 8000 and 4 heads, 96 of 152
     // SMs: 52 and 37).
-    int s = 1;
-    while (s < 8 && 2 * s * pl.units <= sms && keys >= 2 * s * 256) s *= 2;
-    if (s * pl.units <= sms && (4 * s * pl.units >= 3 * sms || keys <= s * 2048)) return s;
+    int s = 8;
+    while (s > 1 && (pl.units > places(s) || keys < s * 256)) s /= 2;
+    if (pl.units <= places(s) && (4 * s * pl.units >= 3 * sms || keys <= s * 2048)) return s;
     // Else one wave of about two CTAs per SM, in a count that a cluster can join;
     // each range of at least 256 keys.
     s = 1;
-    while (s < pg::kDecMaxCluster && 2 * s * pl.units <= 2 * sms && keys >= 2 * s * 256) s *= 2;
+    const int resident = pl.width == 256 || pl.block_rows == 32 ? 2 : 3;
+    while (s < pg::kDecMaxCluster && 2 * s * pl.units <= 2 * sms && pl.units <= resident * places(2 * s) && keys >= 2 * s * 256)
+        s *= 2;
     // Few heads and a long context: more ranges than a cluster holds, through a
     // workspace (one request of 8 key heads and 65536 keys: 37 us with 32, 55 with 16).
     if (s == pg::kDecMaxCluster && s * pl.units < sms)
@@ -440,9 +450,10 @@ int fa_paged_fwd(const fa_paged_args* args) {
         void* kargs[] = {&kc, &vc, &p, &bf16};
         if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, threads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
     } else {
-        // eight warps where one CTA per SM is all there is (clusters of 16 such CTAs
-        // find no place for many: 13.7 us against 10.1 for one request of 4096 keys)
-        const int warps = !pl.even && units <= sm_count() && splits != pg::kDecMaxCluster ? 8 : 4;
+        // eight warps where one CTA per SM is all there is (not for clusters of 16: 13.7
+        // us against 10.1 for one request of 4096 keys and 8 heads)
+        const bool one_each = in_cluster(pl, splits) ? pl.units <= places(splits) : units <= sm_count();
+        const int warps = !pl.even && one_each && splits != pg::kDecMaxCluster ? 8 : 4;
         const KernelEntry ke = select_kernel(pl.width, pl.block_rows, pl.even != 0, warps);
         void* kargs[] = {&tk, &tv, &p, &bf16};
         if (!ensure_smem(ke.fn, ke.smem, device) ||

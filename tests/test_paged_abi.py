@@ -125,6 +125,13 @@ def test_splits_and_workspace(lib):
     assert ws(**rows) == 100 * 4 * 4 * 64 * 4 + 100 * 4 * 4 * 4
 
 
+@pytest.mark.parametrize("requests,want", [(1, 8), (7, 8), (8, 4), (18, 4), (19, 2), (38, 2), (76, 1), (200, 2), (2000, 1)])
+def test_ranges_fill_one_wave_of_clusters(lib, requests, want):
+    """Two heads and 2048 keys: as many key ranges as leave every cluster a place on the 152 SMs."""
+    a = _args(T=requests, B=requests, max_pages=128)
+    assert lib.fa_paged_num_splits(ctypes.addressof(a)) == want
+
+
 @pytest.mark.parametrize("kw,want", [
     (dict(k=None), BAD), (dict(slots=None), BAD), (dict(T=-1), BAD), (dict(dtype=5), BAD), (dict(k=A + 8), MISAL),
     (dict(ks=(128, 60)), MISAL), (dict(vs=(0, 64)), MISAL), (dict(slots=A + 1), MISAL), (dict(T=0), 0), (dict(T=(1 << 30) + 1), BAD), (dict(), CUDA)])
