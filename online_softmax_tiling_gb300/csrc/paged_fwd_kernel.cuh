@@ -26,7 +26,7 @@
 // busy to the end, and a CTA's fixed time (about 5 us) is paid once or twice instead of per
 // range.  A share's first and last unit may be parts of one; the parts are
 // joined by a second launch.  64 requests of 5000 to 16384 keys, 32 query and 8 key
-// heads, d 128: 226 us, 6.2 TB/s (248 with two ranges per row); one request of 4096
+// heads, d 128: 229 us, 6.1 TB/s (248 with two ranges per row); one request of 4096
 // keys: 8.6 us (10.1 with 16 CTAs of four warps).  Reads are what bounds this kernel (2 d bytes per key and
 // head against 4 G d operations), so mma.sync is the tensor path that fits:
 // tcgen05 would take codes widened in shared memory, 128 rows at a time, for
