@@ -184,6 +184,14 @@ Plan plan_of(const fa_paged_args& a) {
     return pl;
 }
 
+// The requests of a mixed call that bring no more than `rows` packed rows.
+Plan single_token_plan(const fa_paged_args& a, int width, int rows) {
+    Plan pl{};
+    pl.width = width, pl.block_rows = rows, pl.row_blocks = 1;
+    pl.units = static_cast<int64_t>(a.cache.Hk) * a.B;
+    return pl;
+}
+
 // Whether the ranges of a row block are joined inside a cluster.
 bool in_cluster(const Plan& pl, int splits) {
     return !pl.prompt && !pl.even && (splits == 2 || splits == 4 || splits == 8 || splits == 16);
@@ -406,7 +414,20 @@ int fa_paged_fwd(const fa_paged_args* args) {
         if (misaligned(a.workspace, 256)) return FA_ERR_MISALIGNED;
         if (a.workspace_bytes < need) return FA_ERR_INVALID_ARG;
     }
-    const int64_t units = pl.even ? pl.even : pl.units * splits, rows = static_cast<int64_t>(a.T) * a.Hq;
+    // Tokens far below B * max_q: prompts beside requests of a few tokens.  Those with no
+    // more rows than a block of the few-row kernel for one token holds are served by it, in a launch
+    // of their own, and the tcgen05 kernel starts a CTA for the others' blocks only (one prompt of
+    // 2000 tokens among 200 requests of 4000 keys, 32 / 8 heads, d 128: 413 us; 884 with
+    // a CTA for every block there could be, 1132 with the tcgen05 kernel alone).
+    const int few = block_rows_of(pl.width, a.Hq / a.cache.Hk);
+    const bool mixed = pl.prompt && a.B > 1 && a.num_splits == 0 && splits == 1 && a.Hq / a.cache.Hk <= few &&
+                       2ll * a.T <= static_cast<int64_t>(a.B) * a.max_q;
+    int64_t units = pl.even ? pl.even : pl.units * splits;
+    if (mixed) {  // (the blocks of all requests with more than `few` rows are no more than this)
+        const int64_t packed = static_cast<int64_t>(a.T) * (a.Hq / a.cache.Hk);
+        units = a.cache.Hk * std::min<int64_t>(units / a.cache.Hk, packed / pl.block_rows + std::min<int64_t>(a.B, packed / (few + 1)));
+    }
+    const int64_t rows = static_cast<int64_t>(a.T) * a.Hq;
     if (units > INT32_MAX || rows > INT32_MAX) return FA_ERR_INVALID_ARG;
 
     int device = 0;
@@ -415,8 +436,8 @@ int fa_paged_fwd(const fa_paged_args* args) {
     const int box_rows = std::min(a.cache.page_size, keys), box_cols = std::min(pl.width, 128);
     const int64_t cache_rows = static_cast<int64_t>(a.cache.num_pages) * a.cache.Hk * a.cache.page_size;
     CUtensorMap tk, tv;
-    if (!pl.prompt && (!encode_codes(&tk, a.cache.k, cache_rows, a.cache.d, box_cols, box_rows) ||
-                       !encode_codes(&tv, a.cache.v, cache_rows, a.cache.d, box_cols, box_rows)))
+    if ((!pl.prompt || mixed) && (!encode_codes(&tk, a.cache.k, cache_rows, a.cache.d, box_cols, box_rows) ||
+                                  !encode_codes(&tv, a.cache.v, cache_rows, a.cache.d, box_cols, box_rows)))
         return FA_ERR_CUDA;
 
     pg::PagedParams p;
@@ -439,8 +460,19 @@ int fa_paged_fwd(const fa_paged_args* args) {
     p.o_part = need > 0 ? reinterpret_cast<float*>(ws) : nullptr;
     p.lse_part = need > 0 ? reinterpret_cast<float*>(ws + o_bytes) : nullptr;
     p.shares = pl.even ? reinterpret_cast<int4*>(ws + o_bytes + part_bytes(part_rows, 1, 1)) : nullptr;
+    p.rows_from = mixed ? few + 1 : 0, p.rows_to = INT32_MAX, p.packed = mixed;
     bool bf16 = a.dtype == FA_BF16;
-    if (pl.prompt) {
+    auto launch_few = [&](const Plan& pl, int splits, int64_t units) {
+        // eight warps where one CTA per SM is all there is (not for clusters of 16: 13.7
+        // us against 10.1 for one request of 4096 keys and 8 heads)
+        const bool one_each = in_cluster(pl, splits) ? pl.units <= places(splits) : units <= sm_count();
+        const int warps = !pl.even && one_each && splits != pg::kDecMaxCluster ? 8 : 4;
+        const KernelEntry ke = select_kernel(pl.width, pl.block_rows, pl.even != 0, warps);
+        void* kargs[] = {&tk, &tv, &p, &bf16};
+        return ensure_smem(ke.fn, ke.smem, device) &&
+               launch(ke.fn, units, 1, 32 * warps, ke.smem, p.in_cluster ? splits : 1, a.stream, kargs);
+    };
+    if (pl.prompt && units > 0) {
         const uint8_t *kc = static_cast<const uint8_t*>(a.cache.k), *vc = static_cast<const uint8_t*>(a.cache.v);
         const void* fn = pl.width == 64    ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<64>)
                          : pl.width == 128 ? reinterpret_cast<const void*>(&pg::paged_prompt_kernel<128>)
@@ -449,16 +481,14 @@ int fa_paged_fwd(const fa_paged_args* args) {
         const int threads = pl.width == 256 ? pg::kPwThreads : pg::kPrThreads;
         void* kargs[] = {&kc, &vc, &p, &bf16};
         if (!ensure_smem(fn, smem, device) || !launch(fn, units, 1, threads, smem, 1, a.stream, kargs)) return FA_ERR_CUDA;
-    } else {
-        // eight warps where one CTA per SM is all there is (not for clusters of 16: 13.7
-        // us against 10.1 for one request of 4096 keys and 8 heads)
-        const bool one_each = in_cluster(pl, splits) ? pl.units <= places(splits) : units <= sm_count();
-        const int warps = !pl.even && one_each && splits != pg::kDecMaxCluster ? 8 : 4;
-        const KernelEntry ke = select_kernel(pl.width, pl.block_rows, pl.even != 0, warps);
-        void* kargs[] = {&tk, &tv, &p, &bf16};
-        if (!ensure_smem(ke.fn, ke.smem, device) ||
-            !launch(ke.fn, units, 1, 32 * warps, ke.smem, p.in_cluster ? splits : 1, a.stream, kargs))
-            return FA_ERR_CUDA;
+    } else if (!pl.prompt && !launch_few(pl, splits, units)) {
+        return FA_ERR_CUDA;
+    }
+    if (mixed) {
+        const Plan one = single_token_plan(a, pl.width, few);
+        const int ranges = std::min(choose_splits(a, one), pg::kDecMaxCluster);  // (joined without a workspace)
+        p.rows_from = 0, p.rows_to = few, p.row_blocks = 1, p.splits = ranges, p.in_cluster = in_cluster(one, ranges);
+        if (!launch_few(one, ranges, one.units * ranges)) return FA_ERR_CUDA;
     }
     if (pl.even) {
         void* margs[] = {&p, &bf16};

@@ -61,7 +61,9 @@ struct PagedParams {
     const float* v_scale;
     long long q_st, q_sh, o_st, o_sh;
     int T, B, Hq, Hk, G, d, max_q, max_pages, num_sel, num_pages, page_shift;
+    int rows_from, rows_to;  // requests of other counts of packed rows are another launch's
     int row_blocks;   // per request and key head
+    int packed;       // only as many row blocks as there are, found by find_block
     int splits;       // key ranges per row block
     int in_cluster;   // the ranges are the CTAs of a cluster, which join their results themselves
     int box_rows;
@@ -73,13 +75,15 @@ struct PagedParams {
 };
 constexpr int kEvenMaxB = 1024;  // requests whose chunk counts a CTA sums up
 
-// Rows and keys of request b; marks that cannot be leave it without rows.
+// Rows and keys of request b; marks that cannot be leave it without rows, and so
+// does a count of rows that another launch serves.
 __device__ __forceinline__ void request_of(const PagedParams& p, int b, int& q0, int& nq, int& len, bool& bad) {
     q0 = b, nq = 1;
     if (p.cu_q) {
         q0 = ld_meta(p.cu_q + b);
         nq = ld_meta(p.cu_q + b + 1) - q0;
         if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
+        if (nq * p.G < p.rows_from || nq * p.G > p.rows_to) nq = 0;
     }
     len = ld_meta(p.lens + b);
 }

@@ -108,6 +108,48 @@ __device__ __forceinline__ void pr_widen16(uint32_t dst0, uint32_t dst1, const u
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(dst1), "r"(h[4]), "r"(h[5]), "r"(h[6]), "r"(h[7]) : "memory");
 }
 
+// The request and row block of the u-th block of `size` rows that the launch serves (false:
+// there are not so many).  A thread counts a run of consecutive requests', the
+// CTA sums up.
+template <int THREADS>
+__device__ __forceinline__ bool find_block(const PagedParams& p, int size, int u, int& b, int& rb) {
+    __shared__ int warp_sums[THREADS / 32], found[2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (p.B + THREADS - 1) / THREADS, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+    auto blocks_of = [&](int i) {
+        int q0, nq, len;
+        bool bad = false;
+        request_of(p, i, q0, nq, len, bad);
+        return (nq * p.G + size - 1) / size;
+    };
+    int own = 0;
+    for (int i = b0; i < b1; ++i) own += blocks_of(i);
+    int sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    if (tid == 0) found[0] = -1;
+    if (lane == 31) warp_sums[warp] = sum;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) sum += warp_sums[w];
+    int at = sum - own;  // blocks before the thread's first request
+    if (at <= u && u < sum) {
+        for (int i = b0; i < b1; ++i) {
+            const int n = blocks_of(i);
+            if (u < at + n) {
+                found[0] = i, found[1] = at + n - 1 - u;  // (with the causal mask the last has the most keys)
+                break;
+            }
+            at += n;
+        }
+    }
+    __syncthreads();
+    b = found[0], rb = found[1];
+    return b >= 0;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kPrThreads, 1)
     paged_prompt_kernel(const uint8_t* __restrict__ k_codes, const uint8_t* __restrict__ v_codes, const PagedParams p,
@@ -129,15 +171,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     u /= p.splits;
     const int h = u % p.Hk;
     u /= p.Hk;
-    const int b = u % p.B, rb = p.row_blocks - 1 - u / p.B;
-    int q0 = b, nq = 1;
+    int b = u % p.B, rb = p.row_blocks - 1 - u / p.B;
+    if (p.packed && !find_block<kPrThreads>(p, kPrRows, u, b, rb)) return;
+    int q0, nq, len;
     bool bad = false;
-    if (p.cu_q) {
-        q0 = ld_meta(p.cu_q + b);
-        nq = ld_meta(p.cu_q + b + 1) - q0;
-        if (q0 < 0 || nq < 0 || nq > p.max_q || q0 > p.T - nq) bad = true, nq = 0;
-    }
-    int len = ld_meta(p.lens + b);
+    request_of(p, b, q0, nq, len, bad);
     if (len < 0 || len > (p.max_pages << p.page_shift)) bad = true, len = 0;
     if (bad && tid == 0) report(kBadData);
     const int rows = nq * p.G, r0 = rb * kPrRows;

@@ -82,7 +82,8 @@ __global__ void __launch_bounds__(kPwThreads, 1)
     u /= p.splits;
     const int h = u % p.Hk;
     u /= p.Hk;
-    const int b = u % p.B, rb = p.row_blocks - 1 - u / p.B;
+    int b = u % p.B, rb = p.row_blocks - 1 - u / p.B;
+    if (p.packed && !find_block<kPwThreads>(p, kPwRows, u, b, rb)) return;
     int q0, nq, len;
     bool bad = false;
     request_of(p, b, q0, nq, len, bad);

@@ -492,6 +492,35 @@ def test_bad_pages_of_wide_heads_are_reported():
         assert _torch().equal(out[:40], good[0][:40])
 
 
+@pytest.mark.parametrize("Hk,G,P,d", [(2, 4, 64, 128), (2, 1, 16, 64), (3, 16, 32, 96), (2, 5, 64, 256), (2, 20, 128, 128)])
+@pytest.mark.parametrize("dtype,causal", [("bf16", True), ("fp16", False)])
+def test_prompts_beside_single_tokens(Hk, G, P, d, dtype, causal):
+    """One call of prompts, drafts, single tokens, requests without queries and without keys."""
+    lens = [1, 300, 33, 700, 1, 64, 0, 500, 17, 40, 900, 128]
+    news = [1, 1, 2, 300, 1, 0, 1, 8, 1, 40, 1, 3]
+    case = _attend_case(lens, news, Hk, G, P, d, dtype, 171 + d + G)
+    out, lse = _attend(*case, news, causal=causal)
+    _ok()
+    _check_attend(case, out, lse, causal)
+    # the same call captured, and rows behind the last query left alone
+    torch = _torch()
+    cache, table, lens_, cu, q = case
+    g, dev = cache.cuda(), (_i32(table), _i32(lens_), _i32(cu))
+    pad = torch.cat([q, q[:4]]).cuda()
+    o, l = torch.full_like(pad, 7.0), torch.full((pad.shape[0], Hk * G), 7.0, device="cuda")
+    call = lambda: _fa().paged_attention_forward(pad, *g[:4], dev[0], dev[1], cu_q=dev[2], max_q=300, causal=causal, out=o, lse=l)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    o.fill_(7.0), l.fill_(7.0)
+    graph.replay()
+    _ok()
+    assert torch.equal(o[:-4], out) and torch.equal(l[:-4], lse)
+    assert (o[-4:] == 7).all() and (l[-4:] == 7).all()
+
+
 def test_queries_that_see_no_key():
     """More queries than keys: the first ones see nothing and get 0 and -inf."""
     news = [20, 140, 3]
