@@ -2,7 +2,7 @@
 // query rows per key head (prompts and pieces of them), d <= 128.
 //
 // Three pieces of 1288 to 2048 queries over up to 8192 keys, 32 query and 8 key heads,
-// d 128: 450 us, 1.10 PFLOP/s of visible pairs.  Of 3,840 cycles per key tile the products
+// d 128: 454 us, 1.09 PFLOP/s of visible pairs.  Of 3,840 cycles per key tile the products
 // take 2,750 (2,048 at their full rate: the widened tiles are written to the shared
 // memory that S = Q K^T reads without a pause), waits for weights 800, for K and V
 // 290 (without the widening 410 us, without widening and softmax 349).

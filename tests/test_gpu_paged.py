@@ -521,6 +521,21 @@ def test_prompts_beside_single_tokens(Hk, G, P, d, dtype, causal):
     assert (o[-4:] == 7).all() and (l[-4:] == 7).all()
 
 
+@pytest.mark.parametrize("d", [64, 256])
+def test_prompts_among_more_requests_than_threads(d):
+    """1500 requests: a thread counts the row blocks of several."""
+    rng = np.random.default_rng(180 + d)
+    news = np.ones(1500, int)
+    news[rng.choice(1500, 200, replace=False)] = 0
+    news[[0, 1, 2, 640, 641, 900, 1498, 1499]] = [70, 3, 200, 9, 64, 130, 33, 65]
+    lens = np.maximum(news, rng.integers(0, 40, 1500))
+    lens[[2, 900]] += 300
+    case = _attend_case(lens, news, 1, 4, 16, d, "bf16", 181)
+    out, lse = _attend(*case, news)
+    _ok()
+    _check_attend(case, out, lse)
+
+
 def test_queries_that_see_no_key():
     """More queries than keys: the first ones see nothing and get 0 and -inf."""
     news = [20, 140, 3]
