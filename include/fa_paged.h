@@ -121,7 +121,8 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  *     fa_paged_workspace_size bytes, 256-byte aligned, where that is not 0;
  *     not to be shared by calls that may run at the same time.
  *   scale: finite and > 0.
- * Rows of o and lse behind the last query (>= cu_q[B]) are left as they were.
+ * Rows of o and lse that are no request's (before cu_q[0], which need not be 0, and
+ * from cu_q[B] on) are left as they were.
  * The softmax runs in 32 bits; its weights enter the second product in fp16,
  * scaled so that a row's largest contribution keeps all of their 11 bits and
  * one 2^-22 as large still does, and 16-bit queries are read exactly (down

@@ -904,8 +904,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_merge_kernel(const Pag
     const int lane = threadIdx.x & 31;
     const long long tok = row / p.Hq;
     const int hq = static_cast<int>(row - tok * p.Hq);
-    // rows behind the last query were not computed
-    if (tok >= p.T || (p.cu_q && tok >= ld_meta(p.cu_q + p.B))) return;
+    // rows before the first query and behind the last were not computed
+    if (tok >= p.T || (p.cu_q && (tok < ld_meta(p.cu_q) || tok >= ld_meta(p.cu_q + p.B)))) return;
     const float* ls = p.lse_part + row * p.splits;
     float a0 = lane < p.splits ? ld(ls + lane) : -INFINITY, a1 = lane + 32 < p.splits ? ld(ls + lane + 32) : -INFINITY;
     float top = fmaxf(a0, a1);

@@ -160,8 +160,8 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     with selected_count [B, Hk] (kv_page_select) restricts every key head to
     those pages.  scale defaults to 1/sqrt(d).  num_splits: key ranges per row
     (0: chosen by the library); a workspace, where the count needs one, is
-    allocated unless given.  Rows of given outputs behind the last query are
-    left as they were.  A kernel whose waits run out (2 s) leaves outputs
+    allocated unless given.  Rows of given outputs before the first query and
+    behind the last are left as they were.  A kernel whose waits run out (2 s) leaves outputs
     undefined and reports it through fa_check_device_status, as in
     attention_forward.
     """
