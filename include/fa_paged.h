@@ -70,7 +70,7 @@ typedef struct fa_kv_cache {
  * or a stack longer than free_capacity).  Where it is not FA_OK nothing is
  * allocated or released: cu_new is 0, slots are -1, lens_out is lens and
  * free_count_out is free_count.
- * B <= 16384; max_tokens >= 0.  One kernel launch.
+ * 1 <= B <= 16384; max_tokens >= 0.  One kernel launch.
  */
 int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, int* free_pages,
                       const int* free_count, int B, int max_pages, int free_capacity,
@@ -121,6 +121,8 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  *     fa_paged_workspace_size bytes, 256-byte aligned, where that is not 0;
  *     not to be shared by calls that may run at the same time.
  *   scale: finite and > 0.
+ * T = 0 (B >= 0): nothing is launched; q, o and lse (for B = 0 the table and lens
+ * too) may be NULL and max_q 0.
  * Rows of o and lse that are no request's (before cu_q[0], which need not be 0, and
  * from cu_q[B] on) are left as they were.
  * The softmax runs in 32 bits; its weights enter the second product in fp16,
@@ -182,7 +184,7 @@ size_t fa_paged_workspace_size(const fa_paged_args* args);
  * selected [B, Hk, num_selected] int32: ascending indices into the request's
  * row of block_table, -1 behind the last; selected_count [B, Hk].
  * Of the cache only k_scale, k_bounds and the sizes are used (k, v and
- * v_scale may be NULL).  1 <= num_selected; max_pages <= 32768.
+ * v_scale may be NULL).  B >= 1; 1 <= num_selected; max_pages <= 32768.
  */
 int fa_kv_page_select(const fa_kv_cache* cache, const void* q, const long long* q_stride,
                       const int* block_table, const int* lens, int B, int Hq, int max_pages,

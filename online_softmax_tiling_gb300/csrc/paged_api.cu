@@ -290,14 +290,17 @@ const void* append_kernel(int page_size, int d, bool bf16, bool bounds) {
 }
 
 int check_args(const fa_paged_args& a) {
-    if (!a.q || !a.o || !a.lse || !a.block_table || !a.lens) return FA_ERR_INVALID_ARG;
-    if ((a.selected == nullptr) != (a.selected_count == nullptr)) return FA_ERR_INVALID_ARG;
-    if (a.B < 1 || a.T < 0 || a.Hq < 1 || a.max_q < 1 || a.max_pages < 1) return FA_ERR_INVALID_ARG;
+    // no query: nothing is read or written, and empty tensors have no address
+    const bool none = a.T == 0;
+    if (!none && (!a.q || !a.o || !a.lse)) return FA_ERR_INVALID_ARG;
+    if (!(none && a.B == 0) && (!a.block_table || !a.lens)) return FA_ERR_INVALID_ARG;
+    if (!none && (a.selected == nullptr) != (a.selected_count == nullptr)) return FA_ERR_INVALID_ARG;
+    if (a.B < (none ? 0 : 1) || a.T < 0 || a.Hq < 1 || a.max_q < (none ? 0 : 1) || a.max_pages < 1) return FA_ERR_INVALID_ARG;
     if (a.dtype != FA_FP16 && a.dtype != FA_BF16) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(a.scale) || !(a.scale > 0.f)) return FA_ERR_INVALID_ARG;
     if (a.num_splits < 0 || a.num_splits > FA_PAGED_MAX_SPLITS) return FA_ERR_INVALID_ARG;
-    if (!a.cu_q && (a.T != a.B || a.max_q != 1)) return FA_ERR_INVALID_ARG;
-    if (a.selected && (a.num_selected < 1 || a.max_q != 1)) return FA_ERR_INVALID_ARG;
+    if (!a.cu_q && (a.T != a.B || (!none && a.max_q != 1))) return FA_ERR_INVALID_ARG;
+    if (a.selected && (a.num_selected < 1 || (!none && a.max_q != 1))) return FA_ERR_INVALID_ARG;
     const int st = check_cache(a.cache);
     if (st != FA_OK) return st;
     if (a.Hq % a.cache.Hk != 0) return FA_ERR_INVALID_ARG;
@@ -389,7 +392,7 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
 }
 
 int fa_paged_num_splits(const fa_paged_args* a) {
-    if (!a || check_args(*a) != FA_OK) return 1;
+    if (!a || check_args(*a) != FA_OK || a->T == 0) return 1;
     const Plan pl = plan_of(*a);
     return pl.even ? 0 : choose_splits(*a, pl);
 }

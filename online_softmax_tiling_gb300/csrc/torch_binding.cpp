@@ -284,6 +284,7 @@ PyObject* page_select(PyObject* const* a) {
     c10::cuda::OptionalCUDAGuard guard;
     guard.set_index(static_cast<c10::DeviceIndex>(dev));
     at::Tensor sel = empty({B, H, keep}, at::kInt, dev), count = empty({B, H}, at::kInt, dev);
+    if (B == 0) return tuple_of({sel, count});
     const int st = fa_kv_page_select(&c, q.data_ptr(), qs.s, table, lens, dim32(B, "block_table"), dim32(Hq, "q"),
                                      dim32(M, "block_table"), keep, dtype, static_cast<int*>(sel.data_ptr()),
                                      static_cast<int*>(count.data_ptr()), stream_of(dev));

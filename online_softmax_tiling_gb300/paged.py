@@ -161,7 +161,8 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     those pages.  scale defaults to 1/sqrt(d).  num_splits: key ranges per row
     (0: chosen by the library); a workspace, where the count needs one, is
     allocated unless given.  Rows of given outputs before the first query and
-    behind the last are left as they were.  A kernel whose waits run out (2 s) leaves outputs
+    behind the last are left as they were.  A step without a query (T = 0, any
+    number of requests) returns empty outputs.  A kernel whose waits run out (2 s) leaves outputs
     undefined and reports it through fa_check_device_status, as in
     attention_forward.
     """
@@ -183,7 +184,7 @@ def kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size: int, num_
     of each key head that one query per request q [B, Hq, d] should read, by the
     exact whole-number score of include/fa_paged.h over k_bounds
     [num_pages, Hk, 2, d]; ascending, -1 behind the last, the last token's page
-    always among them."""
+    always among them.  Empty for B = 0."""
     if stream is not None:
         with _there(q, stream):
             return kv_page_select(q, k_bounds, k_scale, block_table, lens, page_size, num_selected, check=check)

@@ -42,3 +42,33 @@ def test_rows_before_the_first_query_are_left(Hk, G, d, news, splits):
     n = news[0]
     assert (out[:n] == 7).all() and (lse[:n] == 7).all()
     base._check_attend(case, out, lse, rows=slice(n, None))
+
+
+# ------------------------------------------------- steps without a query
+@pytest.mark.parametrize("d", [64, 256])
+def test_attention_of_no_queries(d):
+    """A step that brings no query: empty outputs, given ones left alone, nothing launched."""
+    torch, fa = _torch(), _fa()
+    cache, table, lens, cu, q = base._attend_case([40, 90], [1, 1], 2, 2, 16, d, "bf16", 201)
+    g, dev = cache.cuda(), (_i32(table), _i32(lens))
+    none = q[:0].cuda()
+    for max_q in (0, 1, 100):
+        out, lse = fa.paged_attention_forward(none, *g[:4], *dev, cu_q=_i32([0, 0, 0]), max_q=max_q, check=True)
+        assert out.shape == (0, 4, d) and lse.shape == (0, 4) and out.dtype == q.dtype
+    o, l = torch.empty_like(none), torch.empty((0, 4), device="cuda")
+    got = fa.paged_attention_forward(none, *g[:4], *dev, cu_q=_i32([0, 0, 0]), max_q=4, out=o, lse=l,
+                                     stream=torch.cuda.Stream())
+    assert got[0] is o and got[1] is l
+    # no request at all
+    out, lse = fa.paged_attention_forward(none, *g[:4], dev[0][:0], dev[1][:0])
+    assert out.shape == (0, 4, d) and lse.shape == (0, 4)
+    sel, count = fa.kv_page_select(none, g[4], g[2], dev[0][:0], dev[1][:0], 16, 3)
+    assert sel.shape == (0, 2, 3) and count.shape == (0, 2)
+    out, lse = fa.paged_attention_forward(none, *g[:4], dev[0][:0], dev[1][:0], selected=sel, selected_count=count)
+    assert out.shape == (0, 4, d)
+    # one query per request is still asked for where there are requests, and wrong tensors still refused
+    with pytest.raises(fa.FaError):
+        fa.paged_attention_forward(none, *g[:4], *dev)
+    with pytest.raises(ValueError):
+        fa.paged_attention_forward(none, *g[:4], *dev, cu_q=_i32([0, 0]))
+    _ok()
