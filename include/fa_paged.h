@@ -70,6 +70,10 @@ typedef struct fa_kv_cache {
  * or a stack longer than free_capacity).  Where it is not FA_OK nothing is
  * allocated or released: cu_new is 0, slots are -1, lens_out is lens and
  * free_count_out is free_count.
+ * The step knows no cache, so of a page number it checks that 32 bits hold its
+ * slots (0 <= page < 2^31 / P): new tokens on another one get slot -1, with the
+ * device status FA_ERR_INVALID_ARG and everything else as for a sound page.  A number
+ * beyond the cache's pages is caught by the append and the attention.
  * 1 <= B <= 16384; max_tokens >= 0.  One kernel launch.
  */
 int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, int* free_pages,

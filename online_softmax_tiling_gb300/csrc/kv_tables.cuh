@@ -161,7 +161,11 @@ __global__ void __launch_bounds__(kTablesThreads) kv_tables_kernel(const TablesP
             const int j = pos >> p.page_shift, have = (len + P1) >> p.page_shift;
             const int page = j < have ? ld_meta(p.table + static_cast<long long>(b) * p.max_pages + j)
                                       : stack(top - (pop[b] + j - have));
-            slot = (page << p.page_shift) | (pos & P1);
+            // (a larger number's slot would wrap to another page's)
+            if (page < 0 || page > (0x7FFFFFFF >> p.page_shift))
+                report(kBadData);
+            else
+                slot = (page << p.page_shift) | (pos & P1);
         }
         p.slots[t] = slot;
     }

@@ -117,7 +117,9 @@ def kv_tables_step(new_tokens, lens, block_table, free_pages, free_count, page_s
     free_count_out [1] and status [1] are new int32 tensors: the next step
     takes lens_out and free_count_out.  status is FA_OK, FA_ERR_NO_PAGES or
     FA_ERR_INVALID_ARG on the device; unless it is FA_OK the step changed
-    nothing and its slots are all -1.  check=True waits for it and raises.
+    nothing and its slots are all -1.  A page number that cannot be gives its
+    tokens slot -1 and is reported by fa_check_device_status.  check=True waits
+    for both and raises.
     """
     if stream is not None:
         with _there(new_tokens, stream):

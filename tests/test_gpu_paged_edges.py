@@ -72,3 +72,50 @@ def test_attention_of_no_queries(d):
     with pytest.raises(ValueError):
         fa.paged_attention_forward(none, *g[:4], *dev, cu_q=_i32([0, 0]))
     _ok()
+
+
+# ------------------------------------------------- page numbers that cannot be
+@pytest.mark.parametrize("P", [16, 64, 128])
+@pytest.mark.parametrize("where", ["table", "stack", "given back"])
+def test_tables_bad_page_numbers_give_no_slot(P, where):
+    """A negative page, or one whose slots would pass 32 bits (and wrap to another page's): the tokens on it
+    get no slot and the call is reported; the others have theirs."""
+    fa = _fa()
+    for page in (-1, -(1 << 31), (1 << 31) // P + 3, (1 << 31) - 1):
+        # request 0 goes on inside the page it holds, request 1 needs pages, request 2 ends, request 3 is sound
+        new, lens = np.array([2, 2 * P + 1, -1, 3]), np.array([5, 0, 4, 7])
+        table = np.full((4, 4), -9)
+        table[0, 0], table[2, 0], table[3, 0] = 11, 12, 13
+        free = np.array([21, 22, 0, 0])
+        if where == "table":
+            table[0, 0] = page
+        elif where == "stack":
+            free[1] = page
+        else:
+            table[2, 0] = page
+        T = 2 * P + 10
+        want = ref.tables_step(new, lens, table, free, 2, P, T)
+        assert want["status"] == 0
+        got, g = base._step(new, lens, table, free, 2, P, T)
+        assert fa.fa_check_device_status(None) == fa.FA_ERR_INVALID_ARG
+        _ok()
+        place = want["slots"] % P
+        good = np.array([11, 22, 12, 13, 21])
+        ok = np.isin(want["slots"] // P, good) & (want["slots"] >= 0)
+        slots = got[0].cpu().numpy()
+        np.testing.assert_array_equal(slots, np.where(ok, want["slots"], -1))
+        assert (~ok[:int(want["cu"][-1])]).any() and ok.any() and (place[ok] == slots[ok] % P).all()
+        np.testing.assert_array_equal(got[1].cpu().numpy(), want["cu"])
+        np.testing.assert_array_equal(got[2].cpu().numpy(), want["lens"])
+        with pytest.raises(fa.FaError):
+            base._step(new, lens, table, free, 2, P, T, check=True)
+
+
+def test_tables_largest_page_number():
+    """The last page whose slots 32 bits hold."""
+    for P in (16, 128):
+        page = (1 << 31) // P - 1
+        new, lens, table = np.array([P]), np.array([0]), np.full((1, 2), -1)
+        want = ref.tables_step(new, lens, table, np.array([page]), 1, P, P)
+        got, g = base._step(new, lens, table, np.array([page]), 1, P, P, check=True)
+        base._check_step(got, g, want)
