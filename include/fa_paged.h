@@ -86,8 +86,13 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
  * k, v: [T, Hk, d] 16-bit (dtype), d contiguous; k_stride, v_stride = {token,
  * head} strides in elements, positive multiples of 8; 16-byte aligned.
  * slots [T] int32 as fa_kv_tables_step writes them; negative: not stored.
- * The tokens of one page must be consecutive in the call with ascending
- * slots (a page written from two places in one call is a race).
+ * The tokens of one page must follow one another in the call with slots
+ * ascending by one: a page holds no gaps.  Rows that are not stored may stand
+ * between them, fewer than 128 in a row.  A token whose slot is of the same
+ * page as the token's before it, but not the next one, is reported (device status
+ * FA_ERR_INVALID_ARG) and not stored, nor are those that go on from it.  A page
+ * written from two places of one call (other pages' tokens, or 128 and more rows
+ * that are not stored, between them) is a race.
  * The scale of (page, head) is the smallest power of two s in [2^-60, 2^60]
  * with |x| <= 448 s for every finite x stored there.  A write to place 0
  * starts a page anew.  Otherwise the scale never shrinks; where it grows, the

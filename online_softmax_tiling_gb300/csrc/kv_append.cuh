@@ -6,17 +6,22 @@
 // e4m3, and a page whose scale grows is rounded again only where its codes
 // fall below the normal range.
 //
-// A run is the tokens of one page that a call brings (consecutive rows, slots
-// ascending by one); an item is one run of one head of K or of V.  A CTA looks
-// through a chunk of slots, finds the runs that begin there and takes them for
+// A run is the tokens of one page that a call brings (slots ascending by one; rows
+// left out may stand between them); an item is one run of one head of K or of V.  A
+// CTA looks through a chunk of slots, finds the runs that begin there and takes them for
 // one to four pairs of (head, K or V); a run of a few tokens (a decode step) is
 // one warp's item, a longer one is the CTA's.  Either way the team holds the
 // item's 16-bit values in registers between the maximum and the rounding, so HBM
 // is read once and written once, and the CTA reads its next item meanwhile.
 // What bounds it: HBM for prompts (4 d bytes read and 2 d written per token
 // and head), launch and two dependent reads for a decode step.  45 thousand tokens of 8
-// heads, d 128: 57 us, 5.3 TB/s; without the item read ahead and with 16 CTAs per
-// chunk instead of 4 it was 109.  32 single tokens: 4.3 us.
+// heads, d 128: 58.6 us, 5.2 TB/s; without the item read ahead and with 16 CTAs per
+// chunk instead of 4 it was 109.  32 single tokens: 4.5 us.
+// Rows left out between the tokens of a page must not split it into two runs, which would
+// race on its scale: a CTA that meets such rows counts its tokens out first, and every row is
+// looked up in shared memory.  Calls without them pay 0.2 us for it (57.4 and 4.3 us before),
+// calls with them 2.3 us (32 requests padded to 16 rows: 4.7 before, 7.0); the search or all of
+// the rest in a function of its own costs more (spills: 70 us).
 #pragma once
 
 #include "paged_common.cuh"
@@ -27,6 +32,8 @@ namespace paged {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendMaxChunk = 64;  // slots a CTA looks through for beginnings of runs
 constexpr int kAppendShortRows = 4;  // rows per thread of a one-warp item
+constexpr int kAppendGap = 128;      // rows from a token to the next of its run, at most
+constexpr int kAppendEntries = kAppendThreads + 128;  // stored rows of a window, and of a run that passes it
 
 struct AppendParams {
     const uint16_t* x[2];       // k, v: [T, Hk, d] 16-bit
@@ -50,7 +57,7 @@ __device__ __forceinline__ void code_bounds(float c, int& lo, int& hi) {
 }
 
 struct AppendItem {
-    int t, n, page, place;  // n tokens from row t into place `place` of `page`
+    int e, n, page, place;  // n tokens from the CTA's e-th into place `place` of `page`
     int h, w;               // head; K (0) or V (1)
 };
 
@@ -60,14 +67,15 @@ template <int TH, int NL, bool BF16, bool BOUNDS>
 struct AppendTeam {
     const AppendParams& p;
     const int tid;
+    const int* row_of;           // rows of the CTA's tokens
     const int LR, rows, r0, c8;  // threads per row (8 channels each), rows per pass, this thread's place
     const bool on;
     float* red;                  // team's shared memory: a value per warp,
     uint4* bred;                 //   least, then largest codes of a thread's rows (fp16 pairs),
     int *blo, *bhi;              //   bounds of a page's older codes
 
-    __device__ AppendTeam(const AppendParams& p_, int tid_, float* red_, uint4* bred_, int* blo_, int* bhi_)
-        : p(p_), tid(tid_), LR(p_.d >> 3), rows(TH / LR), r0(tid / LR), c8((tid - r0 * LR) * 8), on(r0 < rows),
+    __device__ AppendTeam(const AppendParams& p_, int tid_, const int* row_of_, float* red_, uint4* bred_, int* blo_, int* bhi_)
+        : p(p_), tid(tid_), row_of(row_of_), LR(p_.d >> 3), rows(TH / LR), r0(tid / LR), c8((tid - r0 * LR) * 8), on(r0 < rows),
           red(red_), bred(bred_), blo(blo_), bhi(bhi_) {}
 
     __device__ static void sync() {
@@ -77,12 +85,12 @@ struct AppendTeam {
     __device__ void load(const AppendItem& m, uint4 (&v)[NL], float& old) const {
         // (selected, not indexed: the parameters stay in constant memory)
         const long long st = m.w ? p.st[1] : p.st[0];
-        const uint16_t* src = (m.w ? p.x[1] : p.x[0]) + m.t * st + m.h * (m.w ? p.sh[1] : p.sh[0]) + c8;
+        const uint16_t* src = (m.w ? p.x[1] : p.x[0]) + m.h * (m.w ? p.sh[1] : p.sh[0]) + c8;
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
             const int r = r0 + k * rows;
             v[k] = make_uint4(0, 0, 0, 0);
-            if (on && r < m.n) v[k] = ld(reinterpret_cast<const uint4*>(src + r * st));
+            if (on && r < m.n) v[k] = ld(reinterpret_cast<const uint4*>(src + row_of[m.e + r] * st));
         }
         old = m.place == 0 ? 0.f : (m.w ? p.scale[1] : p.scale[0])[static_cast<long long>(m.page) * p.Hk + m.h];
     }
@@ -212,9 +220,10 @@ struct AppendTeam {
 template <int NL, bool BF16, bool BOUNDS>
 __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_kernel(const AppendParams p) {
     constexpr int kWarps = kAppendThreads / 32;
-    __shared__ uint32_t breaks[8];              // bit i: row t0 + i does not go on from the row before it
+    __shared__ uint32_t breaks[kAppendEntries / 32];  // bit e: token e does not go on from the one before it
     __shared__ int n_short, n_long;
-    __shared__ int2 short_runs[kAppendMaxChunk], long_runs[kAppendMaxChunk];  // row in the chunk | length << 8, slot
+    __shared__ int2 short_runs[kAppendMaxChunk], long_runs[kAppendMaxChunk];  // first token | length << 8, slot
+    __shared__ int row_of[kAppendEntries];      // rows of the tokens
     __shared__ float red[kWarps];
     __shared__ uint4 bred[BOUNDS ? 2 * kAppendThreads : 1];
     __shared__ int blo[BOUNDS ? kWarps : 1][256], bhi[BOUNDS ? kWarps : 1][256];
@@ -226,27 +235,110 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     wait_for_previous();
     // rows t0 .. t0 + 255: the chunk and what runs that begin in it may reach
     const int t = t0 + tid;
-    const int slot = t < p.T ? ld_meta(p.slots + t) : -1;
+    int slot = t < p.T ? ld_meta(p.slots + t) : -1;
     int before = __shfl_up_sync(0xffffffffu, slot, 1);
     if (lane == 0) before = (t > 0 && t - 1 < p.T) ? ld_meta(p.slots + t - 1) : -1;
-    const bool same = slot >= 0 && before >= 0 && (slot >> p.page_shift) == (before >> p.page_shift);
-    const bool go_on = same && slot == before + 1;
-    const uint32_t bits = __ballot_sync(0xffffffffu, !go_on);
-    if (lane == 0) breaks[warp] = bits;
-    __syncthreads();
-    if (tid < p.chunk && slot >= 0 && !go_on) {
+    bool same = slot >= 0 && before >= 0 && (slot >> p.page_shift) == (before >> p.page_shift);
+    bool go_on = same && slot == before + 1;
+    const uint32_t new_run = __ballot_sync(0xffffffffu, !go_on);
+    if (lane == 0) breaks[warp] = new_run;
+    row_of[tid] = t;
+    // Tokens are numbered from the chunk's start.  Mostly that is their row, and a token goes on
+    // from the row above; where one stands behind rows left out, or a run may pass the end of
+    // the window over such rows, they are counted out.
+    const bool left_out = slot >= 0 ? before < 0 && t > 0 : before >= 0 && tid > kAppendGap && t0 + kAppendThreads < p.T;
+    const bool sparse = __syncthreads_or(left_out);
+    int row = t, limit = kAppendThreads;
+    if (sparse) {
+        __shared__ int slot_of[kAppendEntries];
+        __shared__ uint32_t stored[kWarps], marks[kWarps];
+        __shared__ int back_slot[kAppendGap / 32], back_row[kAppendGap / 32];
+        const uint32_t below = (1u << lane) - 1u;
+        auto rank_of_row = [&] {
+            int n = __popc(stored[warp] & below);
+            for (int w = 0; w < warp; ++w) n += __popc(stored[w]);
+            return n;
+        };
+        auto count = [&] {
+            int n = 0;
+            for (int w = 0; w < kWarps; ++w) n += __popc(stored[w]);
+            return n;
+        };
+        const uint32_t here = __ballot_sync(0xffffffffu, slot >= 0);
+        if (lane == 0) stored[warp] = here;
+        if (warp < kAppendGap / 32) {  // the last token of the rows before the chunk
+            const int at = t0 - kAppendGap + tid, s = at >= 0 ? ld_meta(p.slots + at) : -1;
+            const uint32_t has = __ballot_sync(0xffffffffu, s >= 0);
+            if (lane == 0) back_row[warp] = -1;  // none
+            __syncwarp();
+            if (has && lane == 31 - __clz(has)) back_slot[warp] = s, back_row[warp] = at;
+        }
+        __syncthreads();
+        const int rank = rank_of_row(), tokens = count();
+        if (slot >= 0) slot_of[rank] = slot, row_of[rank] = t;
+        if (tid < kAppendEntries / 32 - kWarps) breaks[kWarps + tid] = 0;
+        __syncthreads();
+        slot = -1, before = -1;
+        if (tid < tokens) {
+            slot = slot_of[tid], row = row_of[tid];
+            int row_before = 0;
+            if (tid > 0) {
+                before = slot_of[tid - 1], row_before = row_of[tid - 1];
+            } else {
+#pragma unroll
+                for (int w = 0; w < kAppendGap / 32; ++w)
+                    if (back_row[w] >= 0) before = back_slot[w], row_before = back_row[w];
+            }
+            if (row - row_before > kAppendGap) before = -1;
+        }
+        same = slot >= 0 && before >= 0 && (slot >> p.page_shift) == (before >> p.page_shift);
+        go_on = same && slot == before + 1;
+        const uint32_t bits = __ballot_sync(0xffffffffu, slot >= 0 && !go_on);
+        if (lane == 0) breaks[warp] = bits;
+        __syncthreads();
+        // the last run's tokens behind the window, if it begins in the chunk
+        limit = tokens;
+        int begin = -1;
+        for (int w = 0; w < kWarps; ++w)
+            if (breaks[w]) begin = 32 * w + 31 - __clz(breaks[w]);
+        if (begin >= 0 && row_of[begin] < t0 + p.chunk) {
+            for (int u = t0 + kAppendThreads; u < p.T; u += kAppendThreads) {
+                const int last = slot_of[limit - 1], left = P - 1 - (last & (P - 1));  // places of the page that are left
+                if (left == 0 || u - row_of[limit - 1] > kAppendGap) break;
+                const int s = u + tid < p.T ? ld_meta(p.slots + u + tid) : -1;
+                const uint32_t has = __ballot_sync(0xffffffffu, s >= 0);
+                __syncthreads();
+                if (lane == 0) stored[warp] = has;
+                __syncthreads();
+                const int at = rank_of_row(), all = count();
+                if (s >= 0 && at < left) slot_of[limit + at] = s, row_of[limit + at] = u + tid;
+                __syncthreads();
+                const int i = limit + tid;
+                const bool goes_on = tid < min(all, left) && slot_of[i] == last + 1 + tid && row_of[i] - row_of[i - 1] <= kAppendGap;
+                const uint32_t ends = __ballot_sync(0xffffffffu, !goes_on);
+                if (lane == 0) marks[warp] = ends;
+                __syncthreads();
+                int more = 0;  // (at most 127 < kAppendThreads go on)
+                while (marks[more >> 5] == 0) more += 32;
+                more += __ffs(marks[more >> 5]) - 1;
+                limit += more;
+                if (more < all) break;
+            }
+        }
+    }
+    if (slot >= 0 && row < t0 + p.chunk && !go_on) {
         const int page = slot >> p.page_shift, place = slot & (P - 1);
         if (same || page >= p.num_pages) {
             // the same page again, not in order, or no page of the cache: not stored
             report(kBadData);
         } else {
-            int e = tid + 1;                    // first row after this one that breaks the run
-            while (e < kAppendThreads) {
+            int e = tid + 1;                    // first token after this one that breaks the run
+            while (e < limit) {
                 const uint32_t m = breaks[e >> 5] >> (e & 31);
                 if (m) { e += __ffs(m) - 1; break; }
                 e = (e | 31) + 1;
             }
-            const int n = min(e - tid, P - place);
+            const int n = min(min(e, limit) - tid, P - place);
             const int rows = 32 / (p.d >> 3);
             if (n <= kAppendShortRows * rows)
                 short_runs[atomicAdd(&n_short, 1)] = make_int2(tid | (n << 8), slot);
@@ -260,10 +352,10 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     auto item = [&](const int2* runs, int i) {
         const int run = i / pairs, pair = pair0 + i - run * pairs;
         const int2 r = runs[run];
-        return AppendItem{t0 + (r.x & 255), r.x >> 8, r.y >> p.page_shift, r.y & (P - 1), pair >> 1, pair & 1};
+        return AppendItem{r.x & 255, r.x >> 8, r.y >> p.page_shift, r.y & (P - 1), pair >> 1, pair & 1};
     };
     if (n_long > 0) {
-        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS> team(p, tid, red, bred, blo[0], bhi[0]);
+        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS> team(p, tid, row_of, red, bred, blo[0], bhi[0]);
         const int items = n_long * pairs;
         if constexpr (NL <= 4) {  // the next item is read while this one is stored
             uint4 v[NL], next[NL];
@@ -293,7 +385,7 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     }
     if (n_short > 0) {
         const int w = BOUNDS ? warp : 0;
-        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS> team(p, lane, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
+        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS> team(p, lane, row_of, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
         for (int i = warp; i < n_short * pairs; i += kWarps) {
             const AppendItem m = item(short_runs, i);
             uint4 v[kAppendShortRows];

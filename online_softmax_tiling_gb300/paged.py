@@ -141,7 +141,9 @@ def kv_cache_append(k, v, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=No
     rows are not stored); k_cache, v_cache [num_pages, Hk, page_size, d]
     float8_e4m3fn; k_scale, v_scale [num_pages, Hk] float32; k_bounds
     [num_pages, Hk, 2, d] int8 for kv_page_select.  The tokens of one page must
-    be consecutive rows with ascending slots.
+    follow one another with slots ascending by one; rows that are not stored may
+    stand between them, fewer than 128 in a row.  Any other order within a page is
+    reported by fa_check_device_status and not stored.
     """
     if stream is not None:
         with _there(k, stream):

@@ -119,3 +119,85 @@ def test_tables_largest_page_number():
         want = ref.tables_step(new, lens, table, np.array([page]), 1, P, P)
         got, g = base._step(new, lens, table, np.array([page]), 1, P, P, check=True)
         base._check_step(got, g, want)
+
+
+# ------------------------------------------------- slots left out of an append
+def _append_sparse(cache, kv, slots, rows, dtype, bounds=True):
+    """The tokens (kv, slots) at the given rows of a call whose other rows hold NaN and negative slots."""
+    torch = _torch()
+    T = int(rows[-1]) + 1 + 40
+    x = torch.full((2, T, *kv.shape[2:]), float("nan"), dtype=kv.dtype)
+    s = np.random.default_rng(len(rows)).choice([-1, -7, -(1 << 31)], size=T)
+    x[:, rows], s[rows] = kv, slots
+    g = base._append(cache, x, s, bounds=bounds)
+    _ok()
+    cache.append(*(y.double().numpy() for y in kv), slots, bounds=bounds)
+    base._same_cache(g, cache, bounds)
+
+
+@pytest.mark.parametrize("Hk,P,d,dtype", [(1, 16, 64, "bf16"), (3, 32, 96, "fp16"), (2, 128, 128, "bf16"), (1, 64, 256, "fp16")])
+@pytest.mark.parametrize("drop", [0.05, 0.5, 0.9])
+def test_append_with_rows_left_out_between_tokens(Hk, P, d, dtype, drop):
+    """Rejected drafts, padded batches: rows without a slot anywhere, also between the tokens of one page."""
+    pieces = [(0, 1), (P - 1, 1), (P - 1, 2), (3, 1), (0, P), (0, 3 * P + 5), (P, 7), (P + 5, P), (2 * P - 1, P + 2),
+              (7, 3), (1, 5), (0, 9)]
+    cache, kv, slots = base._append_case(Hk, P, d, pieces, dtype, 261 + d)
+    rng = np.random.default_rng(261 + P)
+    gaps = np.minimum(rng.geometric(1 - drop, size=len(slots)), 128)         # rows to the next token
+    far = rng.random(len(slots)) < 0.03
+    gaps[far] = rng.choice([127, 128], size=int(far.sum()))                  # the most there may be
+    _append_sparse(cache, kv, slots, np.cumsum(gaps) - 1 + 5, dtype)
+
+
+@pytest.mark.parametrize("T", [20, 700, 40000])
+def test_append_rows_left_out_and_windows(T):
+    """Runs of whole pages of 128 whose rows pass the 256 that a CTA looks at, beginnings behind rows left out,
+    values that grow (a scale taken from part of a run would be too small), with few and many tokens."""
+    rng = np.random.default_rng(T)
+    P, pieces, n = 128, [], 0
+    while n < T:
+        k = int(rng.choice([1, 5, 127, 128, 129, 300]))
+        pieces.append((int(rng.integers(0, P)) if rng.random() < 0.7 else 0, k))
+        n += k
+    cache, kv, slots = base._append_case(1, P, 16, pieces, "bf16", 271 + T)
+    kv *= _torch().from_numpy(2.0 ** (np.arange(len(slots)) % 97 / 8.0))[None, :, None, None].to(kv.dtype)
+    style = rng.random(len(slots))
+    gaps = np.where(style < 0.8, 1, np.where(style < 0.95, rng.integers(2, 12, len(slots)), rng.integers(60, 129, len(slots))))
+    _append_sparse(cache, kv, slots, np.cumsum(gaps) - 1, "bf16", bounds=T < 1000)
+
+
+@pytest.mark.parametrize("L", [8, 64, 500])
+def test_append_of_a_padded_batch(L):
+    """[requests, L] rows, each request's tokens first (and once: last) in its L rows."""
+    rng = np.random.default_rng(L)
+    for first in (True, False):
+        n = rng.integers(0, min(L, 150) + 1, 30)
+        pieces = [(int(rng.integers(0, 200)), int(k)) for k in n if k]
+        cache, kv, slots = base._append_case(2, 64, 64, pieces, "fp16", 281 + L)
+        rows = np.concatenate([b * L + (0 if first else L - k) + np.arange(k) for b, k in enumerate(n)])
+        _append_sparse(cache, kv, slots, rows, "fp16")
+
+
+def test_append_slots_with_a_gap_are_reported_and_not_stored():
+    """A page holds no gaps: tokens behind one are left out, those before it and other pages' are stored; with rows
+    left out at the gap as well."""
+    fa = _fa()
+    for between in (0, 1, 127):
+        for jump in (2, 5, 0, -1):
+            cache, kv, slots = base._append_case(2, 32, 64, [(0, 20), (3, 1), (0, 9), (33, 4)], "bf16", 291)
+            s, at = slots.copy(), 5
+            s[at:20] += jump - 1                                             # row 5 is not the next place
+            keep = np.ones(len(s), bool)
+            keep[at:20] = False
+            gap = np.ones(len(s), np.int64)
+            gap[at] += between
+            rows = np.cumsum(gap) - 1
+            torch = _torch()
+            x = torch.full((2, int(rows[-1]) + 1, *kv.shape[2:]), float("nan"), dtype=kv.dtype)
+            y = np.full(int(rows[-1]) + 1, -1)
+            x[:, rows], y[rows] = kv, s
+            g = base._append(cache, x, y)
+            assert fa.fa_check_device_status(None) == fa.FA_ERR_INVALID_ARG, (between, jump)
+            _ok()
+            cache.append(*(z.double().numpy() for z in kv[:, keep]), slots[keep])
+            base._same_cache(g, cache)
