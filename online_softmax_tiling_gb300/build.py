@@ -1,10 +1,13 @@
 """Build in-tree, without CMake: the sm_103a shared library with nvcc (three translation units)
-and the torch binding of its paged-cache operators with g++ (one)."""
+and, where torch is installed, the torch binding of its paged-cache operators with g++ (one).
+The library needs nvcc alone."""
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +22,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa_fw
     os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_ceilings.h", "fa_naive.h", "fa_paged.h")]
 LIBRARY = os.path.join(HERE, "libfa_gb300.so")
 BINDING = os.path.join(HERE, "_paged_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_TORCH = BINDING + ".torch"  # the version of torch that BINDING was built for
 BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 BINDING_DEPENDS = [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h"), os.path.join(ROOT, "include", "fa_paged.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,13 +42,44 @@ def _stale(target, depends) -> bool:
     return any(os.path.getmtime(p) > t for p in depends)
 
 
+def _torch_version():
+    """The torch's version, None where there is none (imported only if it is not an installed package)."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        pass
+    try:
+        import torch
+        return torch.__version__
+    except (ImportError, OSError):
+        return None
+
+
+def _binding_stale() -> bool:
+    """Whether there is a torch that the binding does not fit: missing, older than its sources, or built for
+    another version (its C++ interface differs from one to the next)."""
+    version = _torch_version()
+    if version is None:
+        return False
+    if _stale(BINDING, BINDING_DEPENDS) or not os.path.exists(BINDING_TORCH):
+        return True
+    with open(BINDING_TORCH, encoding="utf-8") as f:
+        return f.read() != version
+
+
 def stale() -> bool:
-    return _stale(LIBRARY, DEPENDS) or _stale(BINDING, BINDING_DEPENDS)
+    return _stale(LIBRARY, DEPENDS) or _binding_stale()
 
 
 def _compile_binding(tmp):
-    """g++ on the binding: the object only, so that it can run beside nvcc."""
-    from torch.utils.cpp_extension import include_paths
+    """g++ on the binding: the object only, so that it can run beside nvcc.  None where torch cannot be
+    imported: then only callers of the C ABI are served."""
+    try:
+        from torch.utils.cpp_extension import include_paths
+    except (ImportError, OSError) as e:
+        print(f"torch cannot be imported ({e}): the torch binding of the paged-cache operators is not built",
+              file=sys.stderr)
+        return None
     inc = [f"-I{p}" for p in (*include_paths("cuda"), sysconfig.get_paths()["include"])]
     return subprocess.Popen(["g++", "-O2", "-std=c++17", "-fPIC", "-c", "-o", tmp, BINDING_SOURCE, *inc])
 
@@ -57,15 +92,19 @@ def _link_binding(obj):
                                                         "-lc10_cuda", "-lc10"]
     subprocess.run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:libfa_gb300.so", "-Wl,-rpath,$ORIGIN", *libs],
                    check=True)
+    if os.path.exists(BINDING_TORCH):
+        os.remove(BINDING_TORCH)
     os.replace(tmp, BINDING)
+    with open(BINDING_TORCH, "w", encoding="utf-8") as f:
+        f.write(_torch_version() or "")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libfa_gb300.so for sm_103a (static cudart, -O3 -lineinfo) and the torch binding."""
+    """Compile libfa_gb300.so for sm_103a (static cudart, -O3 -lineinfo) and, where there is a torch, its binding."""
     if not force and not stale():
         return LIBRARY
     obj = BINDING + f".tmp{os.getpid()}.o"
-    binding = _compile_binding(obj) if force or _stale(BINDING, BINDING_DEPENDS) else None
+    binding = _compile_binding(obj) if _binding_stale() or (force and _torch_version() is not None) else None
     try:
         if force or _stale(LIBRARY, DEPENDS):
             tmp = LIBRARY + f".tmp{os.getpid()}"
