@@ -204,8 +204,9 @@ int fa_fwd_splitkv_noalloc(const void* q, const void* k, const void* v, void* o,
  * device-side status word: FA_OK, FA_ERR_TIMEOUT (some CTA's bounded wait
  * expired and that CTA left its outputs unwritten), FA_ERR_INVALID_ARG (an
  * operator of fa_paged.h met device data that cannot be), or FA_ERR_CUDA if the
- * synchronisation itself failed.  The status word is shared by all launches
- * on the current device.
+ * synchronisation itself failed.  The status is shared by all launches on the
+ * current device.  One of fa_fwd's kernels and one of fa_paged.h's can both be
+ * pending: fa_fwd's is returned first, the other one by the next call.
  */
 int fa_check_device_status(void* stream);
 

@@ -520,9 +520,10 @@ int fa_check_device_status(void* stream) {
     if (cudaMemcpyFromSymbol(&st, fa::g_fa_status, sizeof(st)) != cudaSuccess) return FA_ERR_CUDA;
     if (st != 0 && cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(zero)) != cudaSuccess)
         return FA_ERR_CUDA;
-    unsigned int paged = 0;  // the paged kernels' word (both are cleared)
+    if (st != 0) return static_cast<int>(st);
+    unsigned int paged = 0;  // the paged kernels' word: the next call's answer where this one has another
     if (!fa_paged_take_status(&paged)) return FA_ERR_CUDA;
-    return static_cast<int>(st != 0 ? st : paged);
+    return static_cast<int>(paged);
 }
 
 const char* fa_status_string(int status) {

@@ -201,3 +201,26 @@ def test_append_slots_with_a_gap_are_reported_and_not_stored():
             _ok()
             cache.append(*(z.double().numpy() for z in kv[:, keep]), slots[keep])
             base._same_cache(g, cache)
+
+
+# ------------------------------------------------- pending statuses
+def test_a_status_of_each_kind_is_reported():
+    """A wait that ran out in fa_fwd and bad data of a paged call, both pending: one answer after the other."""
+    torch, fa = _torch(), _fa()
+    B, H, N, d = 1, 1, 256, 64
+    x = torch.randn((B, H, N, d), device="cuda").half()
+    o, lse = torch.empty_like(x), torch.empty((B, H, N), device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    case = base._attend_case([40, 40], [1, 1], 1, 2, 16, 64, "fp16", 221)
+    bad = case[1].copy()
+    bad[1, 0] = -1
+    for first in (0, 1):
+        for step in (first, 1 - first):
+            if step:
+                assert fa.fa_fwd_debug(x.data_ptr(), x.data_ptr(), x.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, N, d,
+                                       0.125, 0, fa.FA_FP16, s, 1, 0.05) == fa.FA_OK
+            else:
+                base._attend(case[0], bad, *case[2:], [1, 1])
+        got = [fa.fa_check_device_status(s) for _ in range(3)]
+        assert sorted(got[:2]) == sorted([fa.FA_ERR_TIMEOUT, fa.FA_ERR_INVALID_ARG]), got
+        assert got[2] == fa.FA_OK
