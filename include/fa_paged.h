@@ -138,6 +138,9 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  * scaled so that a row's largest contribution keeps all of their 11 bits and
  * one 2^-22 as large still does, and 16-bit queries are read exactly (down
  * to 2^-38 of a row's largest value).
+ * That holds as long as the value scales that a row reads lie within 2^96 of each
+ * other (a page of zeros has the scale 2^-60); beyond that keys of the smallest scales may be
+ * missing from the sum, and so from the LSE.
  * Places of a page behind a request's last token may hold anything.  As in
  * fa_fwd, a NaN or infinity in a value that a query does not see because of the causal
  * mask may still reach it (the product of its weight 0).
