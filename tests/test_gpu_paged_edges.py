@@ -224,3 +224,92 @@ def test_a_status_of_each_kind_is_reported():
         got = [fa.fa_check_device_status(s) for _ in range(3)]
         assert sorted(got[:2]) == sorted([fa.FA_ERR_TIMEOUT, fa.FA_ERR_INVALID_ARG]), got
         assert got[2] == fa.FA_OK
+
+
+# ------------------------------------------------- bad device data on every kernel
+@pytest.mark.parametrize("d", [64, 96, 128, 160, 256])
+@pytest.mark.parametrize("splits", [1, 2])
+def test_bad_pages_of_prompts_are_reported(d, splits):
+    fa = _fa()
+    news = [40, 30]
+    cache, table, lens, cu, q = base._attend_case([100, 300], news, 1, 2, 16, d, "fp16", 231 + d)
+    good = base._attend(cache, table, lens, cu, q, news, num_splits=splits)
+    _ok()
+    for at, entry in ((3, cache.pages), (0, -1), (18, 1 << 30), (7, -(1 << 31))):
+        t = table.copy()
+        t[1, at] = entry
+        out, lse = base._attend(cache, t, lens, cu, q, news, num_splits=splits)
+        assert fa.fa_check_device_status(None) == fa.FA_ERR_INVALID_ARG, (at, entry)
+        _ok()
+        assert _torch().equal(out[:40], good[0][:40]) and _torch().equal(lse[:40], good[1][:40])
+
+
+@pytest.mark.parametrize("splits", [1, 2, 3])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_bad_selections_are_reported(d, splits):
+    """Counts outside [0, keep] and indices outside the table: reported, the other request is served."""
+    fa = _fa()
+    case = base._select_case([900, 900], 2, 2, 16, d, "bf16", 241 + d)
+    cache, table, lens, cu, q = case
+    g, keep = cache.cuda(), 5
+    sel = np.tile(np.array([1, 4, 9, 30, 56]), (2, 2, 1))
+    count = np.full((2, 2), keep)
+
+    def call(s, n):
+        return fa.paged_attention_forward(q.cuda(), *g[:4], _i32(table), _i32(lens), selected=_i32(s),
+                                          selected_count=_i32(n), num_splits=splits)
+
+    good = call(sel, count)
+    _ok()
+    base._check_attend(case, *good, selected=[[list(r) for r in rows] for rows in sel])
+    for what, value in (("count", keep + 1), ("count", -1), ("index", table.shape[1]), ("index", -1),
+                        ("index", (1 << 31) - 1), ("index", -(1 << 31))):
+        s, n = sel.copy(), count.copy()
+        if what == "count":
+            n[1, 1] = value
+        else:
+            s[1, 1, 2] = value
+        out, lse = call(s, n)
+        assert fa.fa_check_device_status(None) == fa.FA_ERR_INVALID_ARG, (what, value)
+        _ok()
+        assert _torch().equal(out[0], good[0][0]) and _torch().equal(lse[0], good[1][0])
+
+
+def test_bad_selections_of_equal_shares_are_reported():
+    import ctypes
+    torch, fa = _torch(), _fa()
+    B, Hk, G, P, d = 36, 1, 4, 16, 128
+    case = base._select_case([900] * B, Hk, G, P, d, "bf16", 251)
+    cache, table, lens, cu, q = case
+    g, keep = cache.cuda(), 64 * 30
+    rng = np.random.default_rng(251)
+    sel, count = np.full((B, Hk, keep), -1), np.full((B, Hk), 20)
+    for b in range(B):
+        sel[b, 0, :20] = np.sort(rng.choice(57, size=20, replace=False))
+
+    def call(s, n):
+        return fa.paged_attention_forward(q.cuda(), *g[:4], _i32(table), _i32(lens), selected=_i32(s), selected_count=_i32(n))
+
+    a = fa.fa_paged_args()
+    p = g[0].data_ptr()
+    a.q = a.o = a.lse = a.block_table = a.lens = a.selected = a.selected_count = p
+    a.cache = fa.fa_kv_cache(p, p, p, p, None, cache.pages, P, Hk, d)
+    a.T, a.B, a.Hq, a.max_q, a.max_pages, a.num_selected = B, B, Hk * G, 1, table.shape[1], keep
+    a.q_stride[:] = a.o_stride[:] = [Hk * G * d, d]
+    a.scale, a.causal, a.dtype, a.num_splits = 0.1, 1, fa.FA_BF16, 0
+    assert fa.library().fa_paged_num_splits(ctypes.addressof(a)) == 0      # (this is the way that is taken)
+    good = call(sel, count)
+    _ok()
+    base._check_attend(case, *good, selected=[[list(r[r >= 0]) for r in rows] for rows in sel])
+    others = np.arange(B) != 17
+    for what, value in (("count", keep + 1), ("count", -1), ("index", table.shape[1]), ("index", -7)):
+        s, n = sel.copy(), count.copy()
+        if what == "count":
+            n[17, 0] = value
+        else:
+            s[17, 0, 3] = value
+        out, lse = call(s, n)
+        assert fa.fa_check_device_status(None) == fa.FA_ERR_INVALID_ARG, (what, value)
+        _ok()
+        keep_rows = torch.from_numpy(others).cuda()
+        assert torch.equal(out[keep_rows], good[0][keep_rows]) and torch.equal(lse[keep_rows], good[1][keep_rows])
