@@ -102,7 +102,7 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
  * given, follows the codes (NaN counts as 0): the bounds that stand for the
  * page's older codes are widened by the new ones, or taken anew from all codes
  * up to the last one written where the page is new or its key scale grows.
- * T >= 0 (0: nothing is launched).
+ * T >= 0 (0: nothing is launched); Hk <= 32767.
  */
 int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, const int* slots,
                        int T, const long long* k_stride, const long long* v_stride, int dtype,
@@ -126,8 +126,9 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  *     NULL: only these pages (indices into the request's row of block_table,
  *     ascending) are read for the key head; one query per request.
  *   num_splits: key ranges per row, 1 .. FA_PAGED_MAX_SPLITS; 0 = chosen from
- *     the sizes (fa_paged_num_splits).  workspace: device memory of at least
- *     fa_paged_workspace_size bytes, 256-byte aligned, where that is not 0;
+ *     the sizes (fa_paged_num_splits), for requests about as long as the table is
+ *     wide: where they are known to be much shorter, a smaller count is faster.
+ *     workspace: device memory of at least fa_paged_workspace_size bytes, 256-byte aligned, where that is not 0;
  *     not to be shared by calls that may run at the same time.
  *   scale: finite and > 0.
  * T = 0 (B >= 0): nothing is launched; q, o and lse (for B = 0 the table and lens
@@ -144,8 +145,8 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  * Places of a page behind a request's last token may hold anything.  As in
  * fa_fwd, a NaN or infinity in a value that a query does not see because of the causal
  * mask may still reach it (the product of its weight 0).
- * A request with bad device data (see above) or a wait that ran out (FA_ERR_TIMEOUT)
- * has undefined outputs; the others have theirs.
+ * A request with bad device data (see above) has undefined outputs; the others have theirs.
+ * Where a wait ran out (FA_ERR_TIMEOUT) all outputs of the call are undefined.
  */
 #define FA_PAGED_MAX_SPLITS 64
 
@@ -190,8 +191,8 @@ size_t fa_paged_workspace_size(const fa_paged_args* args);
  *   max over the heads of a group of
  *     u * 4 k_scale * sum_c max(qi_c lo_c, qi_c hi_c)
  * with (lo, hi) = k_bounds: up to rounding of q an upper bound of q . k over
- * the page's keys, computed exactly.  Kept are the page of the last token and
- * the num_selected - 1 others with the largest scores (equal ones: the lower
+ * the page's keys, computed exactly (from 2^128 on: infinite).  Kept are the page of the
+ * last token and the num_selected - 1 others with the largest scores (equal ones: the lower
  * index); all of them where a request has no more.
  * selected [B, Hk, num_selected] int32: ascending indices into the request's
  * row of block_table, -1 behind the last; selected_count [B, Hk].

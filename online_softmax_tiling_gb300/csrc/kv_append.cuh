@@ -15,7 +15,7 @@
 // is read once and written once, and the CTA reads its next item meanwhile.
 // What bounds it: HBM for prompts (4 d bytes read and 2 d written per token
 // and head), launch and two dependent reads for a decode step.  45 thousand tokens of 8
-// heads, d 128: 58.6 us, 5.2 TB/s; without the item read ahead and with 16 CTAs per
+// heads, d 128: 58.7 us, 5.2 TB/s; without the item read ahead and with 16 CTAs per
 // chunk instead of 4 it was 109.  32 single tokens: 4.5 us.
 // Rows left out between the tokens of a page must not split it into two runs, which would
 // race on its scale: a CTA that meets such rows counts its tokens out first, and every row is

@@ -1,9 +1,9 @@
 // paged_prompt_wide_kernel.cuh - attention over the paged 8-bit cache for many
 // query rows per key head, 128 < d <= 256.
 //
-// Two pieces of 2000 queries over 6000 keys, 16 query and 2 key heads, d 256: 268 us, 0.83
-// PFLOP/s of visible pairs (the few-row kernel 1085; with the scales read by
-// the widening warps 300, page numbers looked up one by one 324).
+// Two pieces of 1258 and 2000 queries over 3404 and 6000 keys, 16 query and 2 key heads, d 256:
+// 268 us, 0.83 PFLOP/s of visible pairs (the few-row kernel 1085; with the scales read by
+// the widening warps 300, page numbers looked up one by one 324).  Both of 2000 over 6000: 369.
 //
 // The mathematics is that of paged_prompt_kernel.cuh.  An accumulator of 128 rows
 // takes half of TMEM here, so a unit is one tile of 128 packed rows, and the

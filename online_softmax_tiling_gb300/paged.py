@@ -163,7 +163,7 @@ def paged_attention_forward(q, k_cache, v_cache, k_scale, v_scale, block_table, 
     causal: query i of n sees keys j <= i + len - n.  selected [B, Hk, keep]
     with selected_count [B, Hk] (kv_page_select) restricts every key head to
     those pages.  scale defaults to 1/sqrt(d).  num_splits: key ranges per row
-    (0: chosen by the library); a workspace, where the count needs one, is
+    (0: chosen by the library from the table's width); a workspace, where the count needs one, is
     allocated unless given.  Rows of given outputs before the first query and
     behind the last are left as they were.  A step without a query (T = 0, any
     number of requests) returns empty outputs.  A kernel whose waits run out (2 s) leaves outputs
