@@ -128,8 +128,9 @@ int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, c
  *   num_splits: key ranges per row, 1 .. FA_PAGED_MAX_SPLITS; 0 = chosen from
  *     the sizes (fa_paged_num_splits), for requests about as long as the table is
  *     wide: where they are known to be much shorter, a smaller count is faster.
- *     workspace: device memory of at least fa_paged_workspace_size bytes, 256-byte aligned, where that is not 0;
- *     not to be shared by calls that may run at the same time.
+ *     workspace: device memory of at least fa_paged_workspace_size bytes,
+ *     256-byte aligned, where that is not 0; not to be shared by calls that may
+ *     run at the same time.
  *   scale: finite and > 0.
  * T = 0 (B >= 0): nothing is launched; q, o and lse (for B = 0 the table and lens
  * too) may be NULL and max_q 0.
