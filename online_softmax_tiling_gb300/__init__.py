@@ -12,6 +12,7 @@ tensors; torch is used only to allocate device memory and to name the stream.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import math
 import os
 import threading
@@ -27,7 +28,8 @@ EXPORTS = ("fa_fwd", "fa_check_device_status", "fa_status_string", "fa_version",
            "fa_fwd_splitkv_noalloc", "fa_fwd_ex", "fa_ceiling_ex2_rate", "fa_ceiling_l2_read",
            "fa_naive_fwd", "fa_naive_workspace_size", "fa_splitkv_num_splits_ex",
            "fa_kv_tables_step", "fa_kv_cache_append", "fa_paged_fwd", "fa_paged_num_splits",
-           "fa_paged_workspace_size", "fa_kv_page_select")
+           "fa_paged_workspace_size", "fa_kv_page_select", "fa_rotary_embed", "fa_kv_cache_append_rotary",
+           "fa_latent_cache_append", "fa_latent_paged_fwd", "fa_latent_paged_workspace_size", "fa_latent_fwd")
 FA_CEIL_OK, FA_CEIL_ERR_ARG, FA_CEIL_ERR_CUDA = 0, 1, 4
 FA_MASK_NONE, FA_MASK_CAUSAL_TOP_LEFT, FA_MASK_CAUSAL_BOTTOM_RIGHT = 0, 1, 2
 
@@ -117,6 +119,19 @@ def library() -> ctypes.CDLL:
             lib.fa_paged_workspace_size.restype = ctypes.c_size_t
             lib.fa_kv_page_select.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, i, vp, vp, vp]
             lib.fa_kv_page_select.restype = i
+            # those of include/fa_rotary.h and fa_latent.h too
+            lib.fa_rotary_embed.argtypes = [vp, vp, vp, i, i, i, vp]
+            lib.fa_rotary_embed.restype = i
+            lib.fa_kv_cache_append_rotary.argtypes = [vp, vp, vp, vp, i, vp, vp, vp, vp, i, vp]
+            lib.fa_kv_cache_append_rotary.restype = i
+            lib.fa_latent_cache_append.argtypes = [vp, vp, ctypes.c_longlong, vp, ctypes.c_longlong, vp, i, vp, vp, i, vp]
+            lib.fa_latent_cache_append.restype = i
+            lib.fa_latent_paged_fwd.argtypes = [vp]
+            lib.fa_latent_paged_fwd.restype = i
+            lib.fa_latent_paged_workspace_size.argtypes = [vp]
+            lib.fa_latent_paged_workspace_size.restype = ctypes.c_size_t
+            lib.fa_latent_fwd.argtypes = [vp]
+            lib.fa_latent_fwd.restype = i
             _lib = lib
         return _lib
 
@@ -371,14 +386,18 @@ def naive_attention_forward(q, k, v, scale: float | None = None, causal: bool = 
 
 _PAGED = ("kv_tables_step", "kv_cache_append", "paged_attention_forward", "kv_page_select",
           "fa_kv_cache", "fa_paged_args", "FA_ERR_NO_PAGES", "FA_PAGED_MAX_SPLITS")
+_ROTARY = ("rotary_frequencies", "rotary_table", "rotary_embed", "kv_cache_append_rotary", "fa_rotary", "fa_rotary_part")
+_LATENT = ("latent_cache_append", "latent_paged_attention_forward", "latent_attention_forward", "fa_latent_cache",
+           "fa_latent_paged_args", "fa_latent_args")
 
 
 def __getattr__(name):
-    """The paged-cache operators (paged.py) on first use: like the other torch
+    """The serving operators (paged.py, rotary.py, latent.py) on first use: like the other torch
     wrappers here they import torch only when called."""
-    if name in _PAGED:
-        from . import paged
-        for n in _PAGED:
-            globals()[n] = getattr(paged, n)
-        return globals()[name]
+    for module, names in (("paged", _PAGED), ("rotary", _ROTARY), ("latent", _LATENT)):
+        if name in names:
+            m = importlib.import_module("." + module, __name__)
+            for n in names:
+                globals()[n] = getattr(m, n)
+            return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

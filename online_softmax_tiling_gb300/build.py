@@ -1,4 +1,4 @@
-"""Build in-tree, without CMake: the sm_103a shared library with nvcc (three translation units)
+"""Build in-tree, without CMake: the sm_103a shared library with nvcc (four translation units)
 and, where torch is installed, the torch binding of its paged-cache operators with g++ (one).
 The library needs nvcc alone."""
 from __future__ import annotations
@@ -13,18 +13,19 @@ import sysconfig
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
-SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "paged_api.cu", "ceilings.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "paged_api.cu", "latent_api.cu", "ceilings.cu")]
 DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa_fwd_qtile_kernel.cuh", "fa_fwd_wide_kernel.cuh",
                                                      "naive_attention.cuh", "paged_common.cuh", "kv_tables.cuh",
                                                      "kv_append.cuh", "kv_page_select.cuh", "paged_fwd_kernel.cuh",
                                                      "paged_prompt_kernel.cuh", "paged_prompt_wide_kernel.cuh",
-                                                     "sm103_ptx.cuh")] + [
-    os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_ceilings.h", "fa_naive.h", "fa_paged.h")]
+                                                     "rotary.cuh", "rotary_host.h", "host_common.h", "latent_append.cuh",
+                                                     "latent_paged_kernel.cuh", "latent_fwd_kernel.cuh", "sm103_ptx.cuh")] + [
+    os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_ceilings.h", "fa_naive.h", "fa_paged.h", "fa_rotary.h", "fa_latent.h")]
 LIBRARY = os.path.join(HERE, "libfa_gb300.so")
 BINDING = os.path.join(HERE, "_paged_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BINDING_TORCH = BINDING + ".torch"  # the version of torch that BINDING was built for
 BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
-BINDING_DEPENDS = [BINDING_SOURCE, os.path.join(ROOT, "include", "fa.h"), os.path.join(ROOT, "include", "fa_paged.h")]
+BINDING_DEPENDS = [BINDING_SOURCE, *(os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_paged.h", "fa_rotary.h", "fa_latent.h"))]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -109,7 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if force or _stale(LIBRARY, DEPENDS):
             tmp = LIBRARY + f".tmp{os.getpid()}"
             cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-                   "-Xlinker", "-soname=libfa_gb300.so", "--threads", "3", "-o", tmp, *SOURCES]
+                   "-Xlinker", "-soname=libfa_gb300.so", "--threads", "4", "-o", tmp, *SOURCES]
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")
             subprocess.run(cmd, check=True)

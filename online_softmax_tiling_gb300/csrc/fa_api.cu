@@ -25,7 +25,8 @@
 #include "fa_fwd_wide_kernel.cuh"
 #include "naive_attention.cuh"
 
-bool fa_paged_take_status(unsigned int* out);  // paged_api.cu
+bool fa_paged_take_status(unsigned int* out);   // paged_api.cu
+bool fa_latent_take_status(unsigned int* out);  // latent_api.cu
 
 namespace {
 
@@ -523,6 +524,7 @@ int fa_check_device_status(void* stream) {
     if (st != 0) return static_cast<int>(st);
     unsigned int paged = 0;  // the paged kernels' word: the next call's answer where this one has another
     if (!fa_paged_take_status(&paged)) return FA_ERR_CUDA;
+    if (paged == 0 && !fa_latent_take_status(&paged)) return FA_ERR_CUDA;  // (and theirs)
     return static_cast<int>(paged);
 }
 

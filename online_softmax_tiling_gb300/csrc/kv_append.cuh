@@ -24,7 +24,7 @@
 // the rest in a function of its own costs more (spills: 70 us).
 #pragma once
 
-#include "paged_common.cuh"
+#include "rotary.cuh"
 
 namespace fa {
 namespace paged {
@@ -45,6 +45,11 @@ struct AppendParams {
     int T, Hk, d, num_pages, page_shift;
     int chunk;                  // slots a CTA looks through
     int pairs;                  // (head, K or V) pairs it takes
+    // keys turned on their way (the ROT kernels): the table, the queries that are turned beside
+    // them (T = 0: none) by the grid's rows from `pair_rows` on
+    RotaryTable turn;
+    RotaryWork q;
+    int pair_rows;
 };
 
 __device__ __forceinline__ __half2 as_half2(uint32_t v) { return *reinterpret_cast<const __half2*>(&v); }
@@ -61,10 +66,23 @@ struct AppendItem {
     int h, w;               // head; K (0) or V (1)
 };
 
+// A thread's rows of an item: 16-bit values; with keys turned the fp32 values (so that they are rounded
+// once, to e4m3), or, for more rows than the registers hold of these, none: they are read twice.
+template <int NL, bool ROT>
+struct AppendRows {
+    uint4 v[NL];
+};
+template <int NL>
+struct AppendRows<NL, true> {
+    float f[NL <= 4 ? NL : 1][8];
+};
+
 // What a team of TH threads does with one item: load() its rows into registers,
 // then store() them.  NL: rows of the run each thread holds.
-template <int TH, int NL, bool BF16, bool BOUNDS>
+template <int TH, int NL, bool BF16, bool BOUNDS, bool ROT>
 struct AppendTeam {
+    using Rows = AppendRows<NL, ROT>;
+    static constexpr bool kReadTwice = ROT && NL > 4;
     const AppendParams& p;
     const int tid;
     const int* row_of;           // rows of the CTA's tokens
@@ -82,7 +100,76 @@ struct AppendTeam {
         if constexpr (TH == 32) __syncwarp(); else __syncthreads();
     }
 
-    __device__ void load(const AppendItem& m, uint4 (&v)[NL], float& old) const {
+    // Channels c8 .. c8 + 7 of the item's row r in fp32, keys turned.
+    __device__ void fetch(const AppendItem& m, int r, float (&f)[8]) const {
+        const int row = row_of[m.e + r];
+        const uint16_t* src = (m.w ? p.x[1] : p.x[0]) + m.h * (m.w ? p.sh[1] : p.sh[0]) + row * (m.w ? p.st[1] : p.st[0]);
+        const uint4 own = ld(reinterpret_cast<const uint4*>(src + c8));
+        const int half = p.turn.half;
+        const bool first = c8 < half, pairs_here = p.turn.interleaved != 0;
+        const float* turn = m.w == 0 && c8 < 2 * half ? rotary_row(p.turn, row) : nullptr;
+        uint4 other = own;
+        if (turn && !pairs_here) other = ld(reinterpret_cast<const uint4*>(src + (first ? c8 + half : c8 - half)));
+        const uint32_t a[4] = {own.x, own.y, own.z, own.w}, b[4] = {other.x, other.y, other.z, other.w};
+        if (turn && pairs_here) {
+            const float4 c = ld(reinterpret_cast<const float4*>(turn + c8 / 2)), s = ld(reinterpret_cast<const float4*>(turn + half + c8 / 2));
+            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack16(a[i], BF16);
+                f[2 * i] = turn_first(x.x, x.y, cs[i], sn[i]);
+                f[2 * i + 1] = turn_second(x.x, x.y, cs[i], sn[i]);
+            }
+        } else if (turn) {
+            float cs[8], sn[8];
+            load_floats8(turn + (first ? c8 : c8 - half), cs);
+            load_floats8(turn + (first ? c8 + half : c8), sn);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack16(a[i], BF16), y = unpack16(b[i], BF16);
+                f[2 * i] = first ? turn_first(x.x, y.x, cs[2 * i], sn[2 * i]) : turn_second(y.x, x.x, cs[2 * i], sn[2 * i]);
+                f[2 * i + 1] = first ? turn_first(x.y, y.y, cs[2 * i + 1], sn[2 * i + 1]) : turn_second(y.y, x.y, cs[2 * i + 1], sn[2 * i + 1]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack16(a[i], BF16);
+                f[2 * i] = x.x, f[2 * i + 1] = x.y;
+            }
+        }
+    }
+
+    // The k-th of this thread's rows in fp32.
+    __device__ void values(const AppendItem& m, const Rows& v, int k, float (&f)[8]) const {
+        if constexpr (kReadTwice) {
+            fetch(m, r0 + k * rows, f);
+        } else if constexpr (ROT) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = v.f[k][i];
+        } else {
+            const uint32_t u[4] = {v.v[k].x, v.v[k].y, v.v[k].z, v.v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 x = unpack16(u[i], BF16);
+                f[2 * i] = x.x, f[2 * i + 1] = x.y;
+            }
+        }
+    }
+
+    __device__ void load(const AppendItem& m, Rows& held, float& old) const {
+        old = m.place == 0 ? 0.f : (m.w ? p.scale[1] : p.scale[0])[static_cast<long long>(m.page) * p.Hk + m.h];
+        if constexpr (ROT) {
+            if constexpr (!kReadTwice) {
+#pragma unroll
+                for (int k = 0; k < NL; ++k)
+                    if (on && r0 + k * rows < m.n) fetch(m, r0 + k * rows, held.f[k]);
+            }
+        } else {
+            load16(m, held.v);
+        }
+    }
+
+    __device__ void load16(const AppendItem& m, uint4 (&v)[NL]) const {
         // (selected, not indexed: the parameters stay in constant memory)
         const long long st = m.w ? p.st[1] : p.st[0];
         const uint16_t* src = (m.w ? p.x[1] : p.x[0]) + m.h * (m.w ? p.sh[1] : p.sh[0]) + c8;
@@ -105,21 +192,18 @@ struct AppendTeam {
                 if (on && r < m.n) v[k] = ld(reinterpret_cast<const uint4*>(src + row_of[m.e + r] * st));
             }
         }
-        old = m.place == 0 ? 0.f : (m.w ? p.scale[1] : p.scale[0])[static_cast<long long>(m.page) * p.Hk + m.h];
     }
 
-    __device__ void store(const AppendItem& m, const uint4 (&v)[NL], float old) const {
+    __device__ void store(const AppendItem& m, const Rows& v, float old) const {
         float amax = 0.f;
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
-            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            if (ROT && !(on && r0 + k * rows < m.n)) continue;  // (else rows of zeros)
+            float f[8];
+            values(m, v, k, f);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack16(u[i], BF16);
-                const float a = fabsf(f.x), b = fabsf(f.y);
-                if (a < INFINITY) amax = fmaxf(amax, a);  // an infinity or NaN does not count
-                if (b < INFINITY) amax = fmaxf(amax, b);
-            }
+            for (int i = 0; i < 8; ++i)
+                if (fabsf(f[i]) < INFINITY) amax = fmaxf(amax, fabsf(f[i]));  // an infinity or NaN does not count
         }
         amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));  // (not negative)
         if constexpr (TH > 32) {
@@ -146,13 +230,11 @@ struct AppendTeam {
         for (int k = 0; k < NL; ++k) {
             const int r = r0 + k * rows;
             if (!on || r >= m.n) continue;
-            const uint32_t u[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            float f[8];
+            values(m, v, k, f);
             uint32_t q[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack16(u[i], BF16);
-                q[i] = e4m3x2(f.x * inv, f.y * inv);
-            }
+            for (int i = 0; i < 4; ++i) q[i] = e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
             *reinterpret_cast<uint2*>(base + (m.place + r) * p.d + c8) = make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
             if (with_bounds) {
 #pragma unroll
@@ -230,8 +312,8 @@ struct AppendTeam {
     }
 };
 
-template <int NL, bool BF16, bool BOUNDS>
-__global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_kernel(const AppendParams p) {
+template <int NL, bool BF16, bool BOUNDS, bool ROT>
+__global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_append_kernel(const AppendParams p) {
     constexpr int kWarps = kAppendThreads / 32;
     __shared__ uint32_t breaks[kAppendEntries / 32];  // bit e: token e does not go on from the one before it
     __shared__ int n_short, n_long;
@@ -246,6 +328,15 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     if (tid == 0) n_short = 0, n_long = 0;
     dependents_may_start();
     wait_for_previous();
+    if constexpr (ROT) {
+        if (static_cast<int>(blockIdx.y) >= p.pair_rows) {  // queries
+            const unsigned items = static_cast<unsigned>(p.q.T) * static_cast<unsigned>(p.q.groups * (p.q.cols + p.q.tail));
+            const unsigned long long step = 1ull * gridDim.x * (gridDim.y - p.pair_rows) * kAppendThreads;
+            for (unsigned long long i = (1ull * (blockIdx.y - p.pair_rows) * gridDim.x + blockIdx.x) * kAppendThreads + tid; i < items; i += step)
+                rotary_item<1, BF16>(p.q, static_cast<unsigned>(i));
+            return;
+        }
+    }
     // rows t0 .. t0 + 255: the chunk and what runs that begin in it may reach
     const int t = t0 + tid;
     int slot = t < p.T ? ld_meta(p.slots + t) : -1;
@@ -368,10 +459,10 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
         return AppendItem{r.x & 255, r.x >> 8, r.y >> p.page_shift, r.y & (P - 1), pair >> 1, pair & 1};
     };
     if (n_long > 0) {
-        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS> team(p, tid, row_of, red, bred, blo[0], bhi[0]);
+        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS, ROT> team(p, tid, row_of, red, bred, blo[0], bhi[0]);
         const int items = n_long * pairs;
-        if constexpr (NL <= 4) {  // the next item is read while this one is stored
-            uint4 v[NL], next[NL];
+        if constexpr (NL <= 4 && !ROT) {  // the next item is read while this one is stored
+            AppendRows<NL, ROT> v, next;
             float old, next_old = 0.f;
             AppendItem m = item(long_runs, 0);
             team.load(m, v, old);
@@ -383,13 +474,12 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
                 }
                 team.store(m, v, old);
                 m = nm, old = next_old;
-#pragma unroll
-                for (int k = 0; k < NL; ++k) v[k] = next[k];
+                v = next;
             }
         } else {
             for (int i = 0; i < items; ++i) {
                 const AppendItem m = item(long_runs, i);
-                uint4 v[NL];
+                AppendRows<NL, ROT> v;
                 float old;
                 team.load(m, v, old);
                 team.store(m, v, old);
@@ -398,10 +488,10 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 ? 4 : 2) kv_append_ker
     }
     if (n_short > 0) {
         const int w = BOUNDS ? warp : 0;
-        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS> team(p, lane, row_of, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
+        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS, ROT> team(p, lane, row_of, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
         for (int i = warp; i < n_short * pairs; i += kWarps) {
             const AppendItem m = item(short_runs, i);
-            uint4 v[kAppendShortRows];
+            AppendRows<kAppendShortRows, ROT> v;
             float old;
             team.load(m, v, old);
             team.store(m, v, old);

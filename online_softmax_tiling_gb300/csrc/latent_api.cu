@@ -1,0 +1,293 @@
+// latent_api.cu - host side of include/fa_latent.h and of fa_rotary_embed: argument checks, tensor maps, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/fa.h"
+#include "../../include/fa_latent.h"
+#include "host_common.h"
+#include "latent_append.cuh"
+#include "latent_fwd_kernel.cuh"
+#include "latent_paged_kernel.cuh"
+#include "rotary_host.h"
+
+namespace {
+
+// 16-bit [rows, cols] (or [heads, rows, cols]) with element strides as a 4-D map; columns >= cols and rows >= rows read as zeros.
+bool encode_rows(CUtensorMap* map, const void* ptr, bool bf16, int64_t cols, int64_t rows, int64_t heads, int64_t row_stride,
+                 int64_t head_stride, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(heads), 1};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(row_stride) * 2, static_cast<cuuint64_t>(head_stride) * 2,
+                                   static_cast<cuuint64_t>(head_stride) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows), 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(ptr), dims, strides,
+              box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_cache(CUtensorMap* map, const fa_latent_cache& c, bool bf16, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t W = static_cast<cuuint64_t>(c.value_dim + c.rope_dim);
+    const cuuint64_t dims[2] = {W, static_cast<cuuint64_t>(c.num_pages) * c.page_size};
+    const cuuint64_t strides[1] = {W * 2};
+    const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, c.rows, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int check_latent_cache(const fa_latent_cache& c) {
+    if (!c.rows || c.num_pages < 1 || shift_of(c.page_size) < 0) return FA_ERR_INVALID_ARG;
+    if (c.value_dim < 8 || c.value_dim > 512 || c.value_dim % 8 != 0 || c.rope_dim < 0 || c.rope_dim % 8 != 0 ||
+        c.value_dim + c.rope_dim > 576)
+        return FA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(c.num_pages) * c.page_size > INT32_MAX) return FA_ERR_INVALID_ARG;
+    return misaligned(c.rows, 16) ? FA_ERR_MISALIGNED : FA_OK;
+}
+bool bad_stride(long long s) { return s <= 0 || s % 8 != 0 || s >= (1ll << 39); }
+
+// ---- absorbed form
+struct LatentPlan {
+    int members, groups, min_share;
+};
+// Two CTAs share keys where a request may have more rows than one holds.  Shares of at least kMinShare tiles, so that a
+// short context is not cut into more parts than the join reads quickly.
+constexpr int kMinShare = 4;
+int64_t most_tiles(const fa_latent_paged_args& a, int members) {
+    const int64_t rows = static_cast<int64_t>(a.max_q) * a.H, pairs = (rows + members * pg::kLatRows - 1) / (members * pg::kLatRows);
+    const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(a.max_pages) * a.cache.page_size + pg::kLatKeys - 1) / pg::kLatKeys);
+    return a.B * std::min<int64_t>(pairs, INT32_MAX) * tiles;
+}
+LatentPlan latent_plan(const fa_latent_paged_args& a) {
+    LatentPlan pl;
+    pl.members = static_cast<int64_t>(a.max_q) * a.H > pg::kLatRows ? 2 : 1;
+    pl.min_share = kMinShare;
+    const int64_t most = most_tiles(a, pl.members);
+    pl.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count() / pl.members, (most + pl.min_share - 1) / pl.min_share)));
+    return pl;
+}
+size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+size_t latent_workspace(const fa_latent_paged_args& a, const LatentPlan& pl) {
+    if (pl.groups < 2) return 0;
+    const size_t rows = 2ull * pl.groups * pl.members * pg::kLatRows;
+    return round256(rows * a.cache.value_dim * 4) + round256(rows * 8) + (static_cast<size_t>(pl.groups) + 1) * 16;
+}
+
+int check_latent_paged(const fa_latent_paged_args& a) {
+    const bool none = a.T == 0;
+    if (!none && (!a.q || !a.o || !a.lse)) return FA_ERR_INVALID_ARG;
+    if (!(none && a.B == 0) && (!a.block_table || !a.lens)) return FA_ERR_INVALID_ARG;
+    if (a.B < (none ? 0 : 1) || a.T < 0 || a.H < 1 || a.max_q < (none ? 0 : 1) || a.max_pages < 1) return FA_ERR_INVALID_ARG;
+    if (a.dtype != FA_FP16 && a.dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(a.scale) || !(a.scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (!a.cu_q && (a.T != a.B || (!none && a.max_q != 1))) return FA_ERR_INVALID_ARG;
+    const int st = check_latent_cache(a.cache);
+    if (st != FA_OK) return st;
+    if (a.max_pages > kMostKeys / a.cache.page_size) return FA_ERR_INVALID_ARG;
+    if (a.B > pg::kLatMaxB) return FA_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(a.max_q) * a.H > INT32_MAX / 2 || static_cast<int64_t>(a.T) * a.H > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if (most_tiles(a, 1) > INT32_MAX) return FA_ERR_INVALID_ARG;  // (tiles of all units are counted in 32 bits)
+    if (bad_strides(a.q_stride) || bad_strides(a.o_stride) || misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) ||
+        misaligned(a.block_table, 4) || misaligned(a.lens, 4) || misaligned(a.cu_q, 4))
+        return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+int check_latent(const fa_latent_args& a) {
+    const bool none = a.T == 0;
+    if (!none && (!a.q || !a.k || !a.k_rope || !a.v || !a.o || !a.lse)) return FA_ERR_INVALID_ARG;
+    if (!(none && a.B == 0) && (!a.cu_q || !a.cu_k)) return FA_ERR_INVALID_ARG;
+    if (a.B < (none ? 0 : 1) || a.T < 0 || a.Tk < 0 || a.H < 1 || a.max_q < (none ? 0 : 1) || a.max_k < (none ? 0 : 1)) return FA_ERR_INVALID_ARG;
+    if (a.dtype != FA_FP16 && a.dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(a.scale) || !(a.scale > 0.f)) return FA_ERR_INVALID_ARG;
+    if (a.Dn < 8 || a.Dn > 128 || a.Dn % 8 != 0 || a.Dv < 8 || a.Dv > 128 || a.Dv % 8 != 0 || a.R < 8 || a.R > 64 || a.R % 8 != 0)
+        return FA_ERR_UNSUPPORTED;
+    if (a.max_q > kMostKeys || a.T > kMostKeys || a.Tk > kMostKeys || static_cast<int64_t>(a.T) * a.H > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(a.B) * a.H * ((a.max_q + 255) / 256) > INT32_MAX / 2) return FA_ERR_INVALID_ARG;
+    if (bad_strides(a.q_stride) || bad_strides(a.k_stride) || bad_strides(a.v_stride) || bad_strides(a.o_stride) || bad_stride(a.k_rope_stride))
+        return FA_ERR_MISALIGNED;
+    for (const void* t : {a.q, a.k, a.k_rope, a.v, static_cast<const void*>(a.o)})
+        if (misaligned(t, 16)) return FA_ERR_MISALIGNED;
+    if (misaligned(a.lse, 4) || misaligned(a.cu_q, 4) || misaligned(a.cu_k, 4)) return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+}  // namespace
+
+// Read and clear the status word of this file's kernels (the caller has synchronised).
+__attribute__((visibility("hidden"))) bool fa_latent_take_status(unsigned int* out) {
+    const unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(out, pg::g_paged_status, sizeof(*out)) != cudaSuccess) return false;
+    return *out == 0 || cudaMemcpyToSymbol(pg::g_paged_status, &zero, sizeof(zero)) == cudaSuccess;
+}
+
+extern "C" {
+
+int fa_rotary_embed(const fa_rotary* rotary, const fa_rotary_part* q, const fa_rotary_part* k, int T, int d, int dtype, void* stream) {
+    if (!q || T < 0) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    if (d < 16 || d > 512 || d % 8 != 0) return FA_ERR_UNSUPPORTED;
+    int st = check_rotary(rotary, d, T);
+    if (st == FA_OK) st = check_part(q, T);
+    if (st == FA_OK && k) st = check_part(k, T);
+    if (st != FA_OK) return st;
+    if (T == 0) return FA_OK;
+    pg::RotaryWork w = rotary_work(*rotary, q, k, T, d);
+    const int heads = w.part[0].heads + w.part[1].heads;
+    // Items of four heads read the table a quarter as often; of one, where there are too few items to fill the SMs.
+    const int64_t width = w.cols + w.tail, one = static_cast<int64_t>(T) * heads * width;
+    const bool single = one < 4ll * 2048 * sm_count();
+    w.groups = single ? heads : (heads + pg::kRotaryHeads - 1) / pg::kRotaryHeads;
+    if (static_cast<int64_t>(T) * w.groups * width > INT32_MAX) return FA_ERR_INVALID_ARG;
+    const bool bf16 = dtype == FA_BF16;
+    const void* fn = single ? (bf16 ? reinterpret_cast<const void*>(&pg::rotary_kernel<1, true>) : reinterpret_cast<const void*>(&pg::rotary_kernel<1, false>))
+                            : (bf16 ? reinterpret_cast<const void*>(&pg::rotary_kernel<pg::kRotaryHeads, true>)
+                                    : reinterpret_cast<const void*>(&pg::rotary_kernel<pg::kRotaryHeads, false>));
+    void* args[] = {&w};
+    const int64_t ctas = (static_cast<int64_t>(T) * w.groups * width + pg::kRotaryThreads - 1) / pg::kRotaryThreads;
+    return launch(fn, ctas, 1, pg::kRotaryThreads, 0, 1, stream, args) ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_latent_cache_append(const fa_latent_cache* cache, const void* latent, long long latent_stride, const void* rope,
+                           long long rope_stride, const int* slots, int T, const fa_rotary* rotary, const fa_rotary_part* q, int dtype,
+                           void* stream) {
+    if (!cache || T < 0 || (q && !rotary)) return FA_ERR_INVALID_ARG;
+    if (T > 0 && (!latent || !slots || (!rope && cache->rope_dim > 0))) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    int st = check_latent_cache(*cache);
+    const int C = cache->value_dim, R = cache->rope_dim;
+    if (st == FA_OK && rotary) {
+        if (rotary->inverse || rotary->dim != R) return FA_ERR_INVALID_ARG;
+        st = check_rotary(rotary, R, T);
+        if (st == FA_OK && q) st = check_part(q, T);
+    }
+    if (st != FA_OK) return st;
+    if (T > kMostKeys) return FA_ERR_INVALID_ARG;
+    if (bad_stride(latent_stride) || (R > 0 && bad_stride(rope_stride)) || misaligned(latent, 16) || misaligned(rope, 16) || misaligned(slots, 4))
+        return FA_ERR_MISALIGNED;
+    if (T == 0) return FA_OK;
+    pg::LatentAppendParams p = {};
+    p.latent = static_cast<const uint16_t*>(latent), p.rope = static_cast<const uint16_t*>(rope);
+    p.latent_st = latent_stride, p.rope_st = rope_stride;
+    p.cache = static_cast<uint16_t*>(cache->rows);
+    p.slots = slots;
+    p.T = T, p.C = C, p.R = R, p.num_slots = cache->num_pages * cache->page_size;
+    if (rotary) p.r = rotary_table(*rotary);
+    int64_t q_ctas = 0;
+    if (q) {
+        p.q = rotary_work(*rotary, q, nullptr, T, R);
+        p.q.groups = q->heads;
+        const int64_t items = static_cast<int64_t>(T) * q->heads * (p.q.cols + p.q.tail);
+        if (items > INT32_MAX) return FA_ERR_INVALID_ARG;
+        q_ctas = (items + pg::kRotaryThreads - 1) / pg::kRotaryThreads;
+    }
+    const int64_t items = static_cast<int64_t>(T) * (C / 8 + (rotary ? R / 16 : R / 8));
+    const int64_t ctas = (items + pg::kRotaryThreads - 1) / pg::kRotaryThreads;
+    if (items > INT32_MAX || ctas + q_ctas > INT32_MAX) return FA_ERR_INVALID_ARG;
+    p.latent_ctas = static_cast<int>(ctas);
+    const void* fn = dtype == FA_BF16 ? reinterpret_cast<const void*>(&pg::latent_append_kernel<true>)
+                                      : reinterpret_cast<const void*>(&pg::latent_append_kernel<false>);
+    void* args[] = {&p};
+    return launch(fn, ctas + q_ctas, 1, pg::kRotaryThreads, 0, 1, stream, args) ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_latent_paged_workspace_size(const fa_latent_paged_args* a) {
+    if (!a || check_latent_paged(*a) != FA_OK || a->T == 0) return 0;
+    return latent_workspace(*a, latent_plan(*a));
+}
+
+int fa_latent_paged_fwd(const fa_latent_paged_args* args) {
+    if (!args) return FA_ERR_INVALID_ARG;
+    const fa_latent_paged_args& a = *args;
+    const int st = check_latent_paged(a);
+    if (st != FA_OK) return st;
+    if (a.T == 0) return FA_OK;
+    const LatentPlan pl = latent_plan(a);
+    const size_t need = latent_workspace(a, pl);
+    if (need > 0) {
+        if (!a.workspace) return FA_ERR_INVALID_ARG;
+        if (misaligned(a.workspace, 256)) return FA_ERR_MISALIGNED;
+        if (a.workspace_bytes < need) return FA_ERR_INVALID_ARG;
+    }
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return FA_ERR_CUDA;
+    const bool bf16 = a.dtype == FA_BF16;
+    pg::LatentParams p = {};
+    p.q = static_cast<const uint16_t*>(a.q), p.o = static_cast<uint16_t*>(a.o), p.lse = a.lse;
+    p.cu_q = a.cu_q, p.table = a.block_table, p.lens = a.lens;
+    p.q_st = a.q_stride[0], p.q_sh = a.q_stride[1], p.o_st = a.o_stride[0], p.o_sh = a.o_stride[1];
+    p.T = a.T, p.B = a.B, p.H = a.H, p.C = a.cache.value_dim, p.W = a.cache.value_dim + a.cache.rope_dim;
+    p.max_q = a.max_q, p.max_pages = a.max_pages, p.num_pages = a.cache.num_pages, p.page_shift = shift_of(a.cache.page_size);
+    p.members = pl.members, p.min_share = pl.min_share;
+    p.box_rows = std::min(a.cache.page_size, pg::kLatKeys);
+    p.causal = a.causal != 0;
+    p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    if (need > 0) {
+        char* ws = static_cast<char*>(a.workspace);
+        const size_t rows = 2ull * pl.groups * pl.members * pg::kLatRows;
+        p.o_part = reinterpret_cast<float*>(ws);
+        ws += round256(rows * p.C * 4);
+        p.stats = reinterpret_cast<float2*>(ws);
+        p.shares = reinterpret_cast<int4*>(ws + round256(rows * 8));
+    } else {
+        p.min_share = INT32_MAX;  // one group: all of it
+    }
+    CUtensorMap tm;
+    if (!encode_cache(&tm, a.cache, bf16, p.box_rows)) return FA_ERR_CUDA;
+    const void* fn = bf16 ? reinterpret_cast<const void*>(&pg::latent_paged_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_paged_kernel<false>);
+    void* kargs[] = {&tm, &p};
+    if (!ensure_smem(fn, pg::kLatSmem, device) || !launch(fn, static_cast<int64_t>(pl.groups) * pl.members, 1, pg::kLatThreads, pg::kLatSmem, 1, a.stream, kargs))
+        return FA_ERR_CUDA;
+    if (need > 0) {
+        const void* join = bf16 ? reinterpret_cast<const void*>(&pg::latent_join_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_join_kernel<false>);
+        void* jargs[] = {&p};
+        if (!launch(join, pl.groups - 1, pl.members * (pg::kLatRows / (pg::kLatJoinThreads / 32)), pg::kLatJoinThreads, 0, 1, a.stream, jargs))
+            return FA_ERR_CUDA;
+    }
+    return FA_OK;
+}
+
+int fa_latent_fwd(const fa_latent_args* args) {
+    if (!args) return FA_ERR_INVALID_ARG;
+    const fa_latent_args& a = *args;
+    const int st = check_latent(a);
+    if (st != FA_OK) return st;
+    if (a.T == 0) return FA_OK;
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return FA_ERR_CUDA;
+    const bool bf16 = a.dtype == FA_BF16;
+    pg::LatentFwdParams p = {};
+    p.o = static_cast<uint16_t*>(a.o), p.lse = a.lse, p.cu_q = a.cu_q, p.cu_k = a.cu_k;
+    p.o_st = a.o_stride[0], p.o_sh = a.o_stride[1];
+    p.T = a.T, p.Tk = a.Tk, p.B = a.B, p.H = a.H, p.Dn = a.Dn, p.Dv = a.Dv, p.max_q = a.max_q;
+    p.pieces = (a.Dn + 63) / 64 + 1, p.wide_v = a.Dv > 64;
+    p.q_blocks = (a.max_q + 255) / 256;
+    p.units = a.B * a.H * p.q_blocks;
+    p.causal = a.causal != 0;
+    p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
+    // (request, head) pairs whose keys and values fill about half of L2
+    const int64_t pair = static_cast<int64_t>(std::max(a.max_k, 1)) * (a.Dn + a.Dv) * 2;
+    p.group = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({static_cast<int64_t>(a.B) * a.H, (48ll << 20) / pair, INT32_MAX / p.q_blocks})));
+    CUtensorMap tq, tk, ts, tv;
+    const int keys = std::max(a.Tk, 1);  // (no key at all: nothing is read)
+    if (!encode_rows(&tq, a.q, bf16, a.Dn + a.R, a.T, a.H, a.q_stride[0], a.q_stride[1], 128) ||
+        !encode_rows(&tk, a.k, bf16, a.Dn, keys, a.H, a.k_stride[0], a.k_stride[1], 128) ||
+        !encode_rows(&ts, a.k_rope, bf16, a.R, keys, 1, a.k_rope_stride, a.k_rope_stride, 128) ||
+        !encode_rows(&tv, a.v, bf16, a.Dv, keys, a.H, a.v_stride[0], a.v_stride[1], 64))
+        return FA_ERR_CUDA;
+    const void* fn = bf16 ? reinterpret_cast<const void*>(&pg::latent_fwd_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_fwd_kernel<false>);
+    void* kargs[] = {&tq, &tk, &ts, &tv, &p};
+    if (!ensure_smem(fn, pg::kLfSmem, device) ||
+        !launch(fn, std::min(p.units, sm_count()), 1, pg::kLfThreads, pg::kLfSmem, 1, a.stream, kargs))
+        return FA_ERR_CUDA;
+    return FA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,67 @@
+// latent_append.cuh - a token's latent vector and its turned key part into a row of the paged
+// latent cache [pages, P, C + R], and the queries' R channels turned beside it.
+//
+// What bounds it: HBM for prompts (4 (C + R) bytes per token, 4 H R for the queries), one launch and two
+// dependent reads (slot and position, then the row) for a decode step.  CTAs of the first grid row
+// block take 8-channel pieces of the cache's rows, the others the queries.
+#pragma once
+
+#include "rotary.cuh"
+
+namespace fa {
+namespace paged {
+
+struct LatentAppendParams {
+    const uint16_t* latent;
+    const uint16_t* rope;
+    long long latent_st, rope_st;  // token strides, elements
+    uint16_t* cache;
+    const int* slots;
+    RotaryTable r;                 // rows null: the key part is stored as it is
+    RotaryWork q;                  // T = 0: none
+    int T, C, R, num_slots;
+    int latent_ctas;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(kRotaryThreads) latent_append_kernel(const LatentAppendParams p) {
+    dependents_may_start();
+    wait_for_previous();
+    if (static_cast<int>(blockIdx.x) >= p.latent_ctas) {
+        const unsigned item = (blockIdx.x - p.latent_ctas) * static_cast<unsigned>(kRotaryThreads) + threadIdx.x;
+        if (item < static_cast<unsigned>(p.q.T) * static_cast<unsigned>(p.q.groups * (p.q.cols + p.q.tail))) rotary_item<1, BF16>(p.q, item);
+        return;
+    }
+    // pieces of a row: C / 8 copied, then R / 16 turned (two of 8 channels each) or R / 8 copied
+    const unsigned copied = p.C >> 3, width = copied + (p.r.rows ? p.R >> 4 : p.R >> 3);
+    const unsigned item = blockIdx.x * static_cast<unsigned>(kRotaryThreads) + threadIdx.x, token = item / width, col = item - token * width;
+    if (token >= static_cast<unsigned>(p.T)) return;
+    const int slot = ld_meta(p.slots + token);
+    if (slot >= p.num_slots) report(kBadData);
+    if (slot < 0 || slot >= p.num_slots) return;
+    uint16_t* dst = p.cache + static_cast<long long>(slot) * (p.C + p.R);
+    if (col < copied) {
+        *reinterpret_cast<uint4*>(dst + col * 8) = ld(reinterpret_cast<const uint4*>(p.latent + token * p.latent_st + col * 8));
+        return;
+    }
+    const int at = col - copied;
+    const uint16_t* src = p.rope + token * p.rope_st;
+    dst += p.C;
+    if (!p.r.rows) {
+        *reinterpret_cast<uint4*>(dst + at * 8) = ld(reinterpret_cast<const uint4*>(src + at * 8));
+        return;
+    }
+    const int c0 = p.r.interleaved ? at * 16 : at * 8, c1 = p.r.interleaved ? c0 + 8 : c0 + p.r.half;
+    uint4 u = ld(reinterpret_cast<const uint4*>(src + c0)), v = ld(reinterpret_cast<const uint4*>(src + c1));
+    if (const float* row = rotary_row(p.r, token)) {
+        float c[8], s[8];
+        load_floats8(row + at * 8, c);
+        load_floats8(row + p.r.half + at * 8, s);
+        turn16(u, v, c, s, p.r.interleaved != 0, BF16);
+    }
+    *reinterpret_cast<uint4*>(dst + c0) = u;
+    *reinterpret_cast<uint4*>(dst + c1) = v;
+}
+
+}  // namespace paged
+}  // namespace fa

@@ -1,4 +1,4 @@
-// paged_api.cu - host side of include/fa_paged.h: argument checks, tensor
+// paged_api.cu - host side of include/fa_paged.h and of fa_kv_cache_append_rotary: argument checks, tensor
 // maps, the choice of kernel and of key ranges, launches.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -6,39 +6,22 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
-#include <set>
-#include <utility>
 
 #include "../../include/fa.h"
 #include "../../include/fa_paged.h"
+#include "../../include/fa_rotary.h"
+#include "host_common.h"
 #include "kv_append.cuh"
 #include "kv_page_select.cuh"
 #include "kv_tables.cuh"
 #include "paged_fwd_kernel.cuh"
 #include "paged_prompt_kernel.cuh"
 #include "paged_prompt_wide_kernel.cuh"
+#include "rotary_host.h"
 
 namespace {
 
 namespace pg = fa::paged;
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
 
 // Codes [rows, d] of a cache (rows = num_pages Hk P) as a 2-D map of bytes;
 // columns >= d read as zeros.
@@ -52,61 +35,6 @@ bool encode_codes(CUtensorMap* map, const void* ptr, int64_t rows, int d, int bo
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(ptr), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool misaligned(const void* ptr, uintptr_t al) { return (reinterpret_cast<uintptr_t>(ptr) & (al - 1)) != 0; }
-
-// Opt a kernel into its dynamic shared memory (and clusters of 16) once per device.
-bool ensure_smem(const void* fn, int smem, int device) {
-    static std::mutex mu;
-    static std::set<std::pair<const void*, int>> done;
-    std::lock_guard<std::mutex> lock(mu);
-    if (done.count({fn, device})) return true;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-        return false;
-    done.insert({fn, device});
-    return true;
-}
-
-// Launch as a programmatic dependent of the kernel before it in the stream,
-// in clusters of `cluster` CTAs.
-bool launch(const void* fn, int64_t ctas, int grid_y, int threads, int smem, int cluster, void* stream, void** args) {
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(ctas), static_cast<unsigned>(grid_y));
-    cfg.blockDim = dim3(static_cast<unsigned>(threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
-    cfg.stream = static_cast<cudaStream_t>(stream);
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelExC(&cfg, fn, args) == cudaSuccess;
-}
-
-int sm_count() {
-    int device = 0, sms = 152;
-    if (cudaGetDevice(&device) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
-        sms = 152;
-    return sms;
-}
-
-// Keys of a request (and tokens of an append) that the kernels' 32-bit positions hold with room to spare.
-constexpr int kMostKeys = 1 << 30;
-
-int shift_of(int page_size) {
-    switch (page_size) {
-        case 16: return 4;
-        case 32: return 5;
-        case 64: return 6;
-        case 128: return 7;
-        default: return -1;
-    }
 }
 
 // The sizes of a cache: FA_OK, or what is wrong with them.
@@ -125,13 +53,6 @@ int check_cache(const fa_kv_cache& c) {
         misaligned(c.k_bounds, 16))
         return FA_ERR_MISALIGNED;
     return FA_OK;
-}
-
-// {token, head} strides of a 16-bit tensor: positive multiples of 16 bytes.
-bool bad_strides(const long long* s) {
-    for (int i = 0; i < 2; ++i)
-        if (s[i] <= 0 || s[i] % 8 != 0 || s[i] >= (1ll << 39)) return true;
-    return false;
 }
 
 // Kernel width that serves d.
@@ -277,16 +198,17 @@ const void* select_even_join(int rows) {
                         : reinterpret_cast<const void*>(&pg::paged_even_join_kernel<32>);
 }
 
-template <int NL, bool BF16>
+template <int NL, bool BF16, bool ROT>
 const void* append_kernel_of(bool bounds) {
-    return bounds ? reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, true>)
-                  : reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, false>);
+    return bounds ? reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, true, ROT>)
+                  : reinterpret_cast<const void*>(&pg::kv_append_kernel<NL, BF16, false, ROT>);
 }
+template <bool ROT>
 const void* append_kernel(int page_size, int d, bool bf16, bool bounds) {
     // rows of a whole page that a thread of the CTA would hold
     const int rows = pg::kAppendThreads / (d / 8);
-    if ((page_size + rows - 1) / rows <= 4) return bf16 ? append_kernel_of<4, true>(bounds) : append_kernel_of<4, false>(bounds);
-    return bf16 ? append_kernel_of<16, true>(bounds) : append_kernel_of<16, false>(bounds);
+    if ((page_size + rows - 1) / rows <= 4) return bf16 ? append_kernel_of<4, true, ROT>(bounds) : append_kernel_of<4, false, ROT>(bounds);
+    return bf16 ? append_kernel_of<16, true, ROT>(bounds) : append_kernel_of<16, false, ROT>(bounds);
 }
 
 int check_args(const fa_paged_args& a) {
@@ -311,6 +233,60 @@ int check_args(const fa_paged_args& a) {
     if (misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) || misaligned(a.block_table, 4) ||
         misaligned(a.lens, 4) || misaligned(a.cu_q, 4) || misaligned(a.selected, 4) || misaligned(a.selected_count, 4))
         return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+
+// Keys and values into their slots; with `rotary` the keys are turned first, and the queries beside them.
+int append(const fa_kv_cache* cache, const void* k, const void* v, const int* slots, int T, const long long* k_stride,
+           const long long* v_stride, const fa_rotary* rotary, const fa_rotary_part* q, int dtype, void* stream) {
+    if (!cache || !k || !v || !slots || !k_stride || !v_stride || T < 0) return FA_ERR_INVALID_ARG;
+    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
+    const int st = check_cache(*cache);
+    if (st != FA_OK) return st;
+    if (cache->Hk > 32767) return FA_ERR_UNSUPPORTED;
+    if (T > kMostKeys) return FA_ERR_INVALID_ARG;
+    if (bad_strides(k_stride) || bad_strides(v_stride) || misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4))
+        return FA_ERR_MISALIGNED;
+    if (rotary) {
+        int bad = check_rotary(rotary, cache->d, T);
+        if (bad == FA_OK && q) bad = check_part(q, T);
+        if (bad != FA_OK) return bad;
+    }
+    if (T == 0) return FA_OK;
+    pg::AppendParams p = {};
+    p.x[0] = static_cast<const uint16_t*>(k), p.x[1] = static_cast<const uint16_t*>(v);
+    p.st[0] = k_stride[0], p.sh[0] = k_stride[1], p.st[1] = v_stride[0], p.sh[1] = v_stride[1];
+    p.codes[0] = static_cast<uint8_t*>(cache->k), p.codes[1] = static_cast<uint8_t*>(cache->v);
+    p.scale[0] = cache->k_scale, p.scale[1] = cache->v_scale;
+    p.bounds = reinterpret_cast<int8_t*>(cache->k_bounds);
+    p.slots = slots;
+    p.T = T, p.Hk = cache->Hk, p.d = cache->d, p.num_pages = cache->num_pages, p.page_shift = shift_of(cache->page_size);
+    // Slots a CTA looks through (64 down to 8, one per warp) and (head, K or V)
+    // pairs it takes (4 or 1): the most that leaves four CTAs per SM.
+    const int64_t sms = sm_count();
+    auto ctas = [&] { return (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk * ((2 * p.Hk + p.pairs - 1) / p.pairs); };
+    p.chunk = pg::kAppendMaxChunk, p.pairs = 4;
+    if (ctas() < 4 * sms) p.pairs = 1;
+    while (p.chunk > 8 && ctas() < 4 * sms) p.chunk /= 2;
+    const bool bf16 = dtype == FA_BF16;
+    const int64_t columns = (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk;
+    p.pair_rows = (2 * p.Hk + p.pairs - 1) / p.pairs;
+    int64_t rows = p.pair_rows;
+    const void* fn = rotary ? append_kernel<true>(cache->page_size, p.d, bf16, p.bounds != nullptr)
+                            : append_kernel<false>(cache->page_size, p.d, bf16, p.bounds != nullptr);
+    if (rotary) {
+        p.turn = rotary_table(*rotary);
+        if (q) {
+            p.q = rotary_work(*rotary, q, nullptr, T, p.d);
+            p.q.groups = q->heads;
+            const int64_t items = static_cast<int64_t>(T) * q->heads * (p.q.cols + p.q.tail);
+            if (items > INT32_MAX) return FA_ERR_INVALID_ARG;
+            // an item per thread; the grid's rows end at 65535, what is beyond goes round
+            rows = std::min<int64_t>(65535, rows + (items + columns * pg::kAppendThreads - 1) / (columns * pg::kAppendThreads));
+        }
+    }
+    void* args[] = {&p};
+    if (!launch(fn, columns, static_cast<int>(rows), pg::kAppendThreads, 0, 1, stream, args)) return FA_ERR_CUDA;
     return FA_OK;
 }
 
@@ -360,35 +336,14 @@ int fa_kv_tables_step(const int* new_tokens, const int* lens, int* block_table, 
 
 int fa_kv_cache_append(const fa_kv_cache* cache, const void* k, const void* v, const int* slots, int T,
                        const long long* k_stride, const long long* v_stride, int dtype, void* stream) {
-    if (!cache || !k || !v || !slots || !k_stride || !v_stride || T < 0) return FA_ERR_INVALID_ARG;
-    if (dtype != FA_FP16 && dtype != FA_BF16) return FA_ERR_INVALID_ARG;
-    const int st = check_cache(*cache);
-    if (st != FA_OK) return st;
-    if (cache->Hk > 32767) return FA_ERR_UNSUPPORTED;
-    if (T > kMostKeys) return FA_ERR_INVALID_ARG;
-    if (bad_strides(k_stride) || bad_strides(v_stride) || misaligned(k, 16) || misaligned(v, 16) || misaligned(slots, 4))
-        return FA_ERR_MISALIGNED;
-    if (T == 0) return FA_OK;
-    pg::AppendParams p;
-    p.x[0] = static_cast<const uint16_t*>(k), p.x[1] = static_cast<const uint16_t*>(v);
-    p.st[0] = k_stride[0], p.sh[0] = k_stride[1], p.st[1] = v_stride[0], p.sh[1] = v_stride[1];
-    p.codes[0] = static_cast<uint8_t*>(cache->k), p.codes[1] = static_cast<uint8_t*>(cache->v);
-    p.scale[0] = cache->k_scale, p.scale[1] = cache->v_scale;
-    p.bounds = reinterpret_cast<int8_t*>(cache->k_bounds);
-    p.slots = slots;
-    p.T = T, p.Hk = cache->Hk, p.d = cache->d, p.num_pages = cache->num_pages, p.page_shift = shift_of(cache->page_size);
-    // Slots a CTA looks through (64 down to 8, one per warp) and (head, K or V)
-    // pairs it takes (4 or 1): the most that leaves four CTAs per SM.
-    const int64_t sms = sm_count();
-    auto ctas = [&] { return (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk * ((2 * p.Hk + p.pairs - 1) / p.pairs); };
-    p.chunk = pg::kAppendMaxChunk, p.pairs = 4;
-    if (ctas() < 4 * sms) p.pairs = 1;
-    while (p.chunk > 8 && ctas() < 4 * sms) p.chunk /= 2;
-    const void* fn = append_kernel(cache->page_size, p.d, dtype == FA_BF16, p.bounds != nullptr);
-    void* args[] = {&p};
-    if (!launch(fn, (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk, (2 * p.Hk + p.pairs - 1) / p.pairs, pg::kAppendThreads, 0, 1, stream, args))
-        return FA_ERR_CUDA;
-    return FA_OK;
+    return append(cache, k, v, slots, T, k_stride, v_stride, nullptr, nullptr, dtype, stream);
+}
+
+int fa_kv_cache_append_rotary(const fa_kv_cache* cache, const void* k, const void* v, const int* slots, int T,
+                              const long long* k_stride, const long long* v_stride, const fa_rotary* rotary,
+                              const fa_rotary_part* q, int dtype, void* stream) {
+    if (!rotary || rotary->inverse) return FA_ERR_INVALID_ARG;
+    return append(cache, k, v, slots, T, k_stride, v_stride, rotary, q, dtype, stream);
 }
 
 int fa_paged_num_splits(const fa_paged_args* a) {

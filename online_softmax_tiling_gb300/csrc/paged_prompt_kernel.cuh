@@ -74,18 +74,6 @@ struct PrCtl {
     PrGroup meta[kPrMeta][8];
 };
 
-// Shared-memory matrix descriptor for tcgen05.mma: 128-byte swizzle, start
-// address, leading and stride byte offsets in 16-byte units, version 1.
-__device__ __forceinline__ uint64_t pr_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
-           (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46) | (2ull << 61);
-}
-// Instruction descriptor, kind::f16: fp16 operands, fp32 sums.
-__host__ __device__ constexpr uint32_t pr_instr(int m, int n, bool b_mn_major) {
-    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((static_cast<uint32_t>(n) >> 3) << 17) |
-           ((static_cast<uint32_t>(m) >> 4) << 24);
-}
-
 // 16 codes that this SM reads once: not kept in L1, whose memory the tiles take.
 __device__ __forceinline__ uint4 ldg_codes(const uint8_t* a) {
     uint4 v;

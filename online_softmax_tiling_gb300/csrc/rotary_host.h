@@ -1,0 +1,46 @@
+// rotary_host.h - checks and kernel parameters of the structures of include/fa_rotary.h.
+#pragma once
+
+#include "../../include/fa.h"
+#include "../../include/fa_rotary.h"
+#include "host_common.h"
+#include "rotary.cuh"
+
+namespace {
+
+namespace pg = fa::paged;
+
+// d: head width that the turned channels are of; T: tokens.
+int check_rotary(const fa_rotary* r, int d, int T) {
+    if (!r || r->num_positions < 1 || (T > 0 && (!r->table || !r->positions))) return FA_ERR_INVALID_ARG;
+    if (r->dim < 16 || r->dim > 512 || r->dim % 16 != 0 || r->dim > d) return FA_ERR_UNSUPPORTED;
+    return misaligned(r->table, 16) || misaligned(r->positions, 4) ? FA_ERR_MISALIGNED : FA_OK;
+}
+int check_part(const fa_rotary_part* p, int T) {
+    if ((T > 0 && (!p->x || !p->y)) || p->heads < 1) return FA_ERR_INVALID_ARG;
+    if (bad_strides(p->x_stride) || bad_strides(p->y_stride) || misaligned(p->x, 16) || misaligned(p->y, 16)) return FA_ERR_MISALIGNED;
+    return FA_OK;
+}
+pg::RotaryTable rotary_table(const fa_rotary& r) {
+    return {r.table, r.positions, r.num_positions, r.dim / 2, r.interleaved != 0, r.inverse != 0};
+}
+// Work of one part or two (groups is left to the caller).
+pg::RotaryWork rotary_work(const fa_rotary& r, const fa_rotary_part* q, const fa_rotary_part* k, int T, int d) {
+    pg::RotaryWork w = {};
+    w.r = rotary_table(r);
+    bool in_place = true;
+    const fa_rotary_part* parts[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        const fa_rotary_part* p = parts[i];
+        if (!p) continue;
+        w.part[i] = {static_cast<const uint16_t*>(p->x), static_cast<uint16_t*>(p->y), p->x_stride[0], p->x_stride[1],
+                     p->y_stride[0], p->y_stride[1], p->heads};
+        in_place = in_place && p->x == p->y;
+    }
+    w.T = T;
+    w.cols = r.dim / 16;
+    w.tail = in_place ? 0 : (d - r.dim) / 8;
+    return w;
+}
+
+}  // namespace
