@@ -43,6 +43,18 @@ bool encode_cache(CUtensorMap* map, const fa_latent_cache& c, bool bf16, int box
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Queries [T, H, W] in boxes of 64 channels x `box` heads of one token.
+bool encode_queries(CUtensorMap* map, const fa_latent_paged_args& a, bool bf16, int box_heads) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(a.cache.value_dim + a.cache.rope_dim), static_cast<cuuint64_t>(a.H), static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.q_stride[1]) * 2, static_cast<cuuint64_t>(a.q_stride[0]) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 int check_latent_cache(const fa_latent_cache& c) {
     if (!c.rows || c.num_pages < 1 || shift_of(c.page_size) < 0) return FA_ERR_INVALID_ARG;
     if (c.value_dim < 8 || c.value_dim > 512 || c.value_dim % 8 != 0 || c.rope_dim < 0 || c.rope_dim % 8 != 0 ||
@@ -55,29 +67,26 @@ bool bad_stride(long long s) { return s <= 0 || s % 8 != 0 || s >= (1ll << 39); 
 
 // ---- absorbed form
 struct LatentPlan {
-    int members, groups, min_share;
+    int pairs, min_share;
 };
-// Two CTAs share keys where a request may have more rows than one holds.  Shares of at least kMinShare tiles, so that a
-// short context is not cut into more parts than the join reads quickly.
-constexpr int kMinShare = 4;
-int64_t most_tiles(const fa_latent_paged_args& a, int members) {
-    const int64_t rows = static_cast<int64_t>(a.max_q) * a.H, pairs = (rows + members * pg::kLatRows - 1) / (members * pg::kLatRows);
+// Shares of at least kMinShare tiles, so that a short context is not cut into more parts than the join reads quickly.
+constexpr int kMinShare = 2;
+int64_t most_tiles(const fa_latent_paged_args& a) {
+    const int64_t blocks = (static_cast<int64_t>(a.max_q) * a.H + pg::kLatRows - 1) / pg::kLatRows;
     const int64_t tiles = std::max<int64_t>(1, (static_cast<int64_t>(a.max_pages) * a.cache.page_size + pg::kLatKeys - 1) / pg::kLatKeys);
-    return a.B * std::min<int64_t>(pairs, INT32_MAX) * tiles;
+    return a.B * blocks * tiles;
 }
 LatentPlan latent_plan(const fa_latent_paged_args& a) {
     LatentPlan pl;
-    pl.members = static_cast<int64_t>(a.max_q) * a.H > pg::kLatRows ? 2 : 1;
     pl.min_share = kMinShare;
-    const int64_t most = most_tiles(a, pl.members);
-    pl.groups = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count() / pl.members, (most + pl.min_share - 1) / pl.min_share)));
+    pl.pairs = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(sm_count() / 2, (most_tiles(a) + pl.min_share - 1) / pl.min_share)));
     return pl;
 }
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 size_t latent_workspace(const fa_latent_paged_args& a, const LatentPlan& pl) {
-    if (pl.groups < 2) return 0;
-    const size_t rows = 2ull * pl.groups * pl.members * pg::kLatRows;
-    return round256(rows * a.cache.value_dim * 4) + round256(rows * 8) + (static_cast<size_t>(pl.groups) + 1) * 16;
+    if (pl.pairs < 2) return 0;
+    const size_t rows = 2ull * pl.pairs * pg::kLatRows;
+    return round256(rows * a.cache.value_dim * 4) + round256(rows * 8) + (static_cast<size_t>(pl.pairs) + 1) * 16;
 }
 
 int check_latent_paged(const fa_latent_paged_args& a) {
@@ -93,7 +102,7 @@ int check_latent_paged(const fa_latent_paged_args& a) {
     if (a.max_pages > kMostKeys / a.cache.page_size) return FA_ERR_INVALID_ARG;
     if (a.B > pg::kLatMaxB) return FA_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(a.max_q) * a.H > INT32_MAX / 2 || static_cast<int64_t>(a.T) * a.H > INT32_MAX) return FA_ERR_INVALID_ARG;
-    if (most_tiles(a, 1) > INT32_MAX) return FA_ERR_INVALID_ARG;  // (tiles of all units are counted in 32 bits)
+    if (most_tiles(a) > INT32_MAX) return FA_ERR_INVALID_ARG;  // (tiles of all units are counted in 32 bits)
     if (bad_strides(a.q_stride) || bad_strides(a.o_stride) || misaligned(a.q, 16) || misaligned(a.o, 16) || misaligned(a.lse, 4) ||
         misaligned(a.block_table, 4) || misaligned(a.lens, 4) || misaligned(a.cu_q, 4))
         return FA_ERR_MISALIGNED;
@@ -225,30 +234,35 @@ int fa_latent_paged_fwd(const fa_latent_paged_args* args) {
     p.q_st = a.q_stride[0], p.q_sh = a.q_stride[1], p.o_st = a.o_stride[0], p.o_sh = a.o_stride[1];
     p.T = a.T, p.B = a.B, p.H = a.H, p.C = a.cache.value_dim, p.W = a.cache.value_dim + a.cache.rope_dim;
     p.max_q = a.max_q, p.max_pages = a.max_pages, p.num_pages = a.cache.num_pages, p.page_shift = shift_of(a.cache.page_size);
-    p.members = pl.members, p.min_share = pl.min_share;
-    p.box_rows = std::min(a.cache.page_size, pg::kLatKeys);
+    p.min_share = pl.min_share;
+    p.box_rows = std::min(a.cache.page_size, 64);
     p.causal = a.causal != 0;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     if (need > 0) {
         char* ws = static_cast<char*>(a.workspace);
-        const size_t rows = 2ull * pl.groups * pl.members * pg::kLatRows;
+        const size_t rows = 2ull * pl.pairs * pg::kLatRows;
         p.o_part = reinterpret_cast<float*>(ws);
         ws += round256(rows * p.C * 4);
         p.stats = reinterpret_cast<float2*>(ws);
         p.shares = reinterpret_cast<int4*>(ws + round256(rows * 8));
     } else {
-        p.min_share = INT32_MAX;  // one group: all of it
+        p.min_share = INT32_MAX;  // one pair: all of it
     }
-    CUtensorMap tm;
+    CUtensorMap tm, tm_q = {};
     if (!encode_cache(&tm, a.cache, bf16, p.box_rows)) return FA_ERR_CUDA;
+    // boxes of queries: as many heads as divide both H and a CTA's 64 rows, a whole swizzle pattern (eight rows) at least
+    int box = 64;
+    while (a.H % box != 0) box /= 2;
+    p.q_box = box >= 8 ? box : 0;
+    if (p.q_box && !encode_queries(&tm_q, a, bf16, p.q_box)) return FA_ERR_CUDA;
     const void* fn = bf16 ? reinterpret_cast<const void*>(&pg::latent_paged_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_paged_kernel<false>);
-    void* kargs[] = {&tm, &p};
-    if (!ensure_smem(fn, pg::kLatSmem, device) || !launch(fn, static_cast<int64_t>(pl.groups) * pl.members, 1, pg::kLatThreads, pg::kLatSmem, 1, a.stream, kargs))
+    void* kargs[] = {&tm, &tm_q, &p};
+    if (!ensure_smem(fn, pg::kLatSmem, device) || !launch(fn, 2ll * pl.pairs, 1, pg::kLatThreads, pg::kLatSmem, 2, a.stream, kargs))
         return FA_ERR_CUDA;
     if (need > 0) {
         const void* join = bf16 ? reinterpret_cast<const void*>(&pg::latent_join_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_join_kernel<false>);
         void* jargs[] = {&p};
-        if (!launch(join, pl.groups - 1, pl.members * (pg::kLatRows / (pg::kLatJoinThreads / 32)), pg::kLatJoinThreads, 0, 1, a.stream, jargs))
+        if (!launch(join, pl.pairs - 1, pg::kLatRows / pg::kLatJoinRows * ((p.C + 127) / 128), pg::kLatJoinThreads, 0, 1, a.stream, jargs))
             return FA_ERR_CUDA;
     }
     return FA_OK;

@@ -5,29 +5,38 @@
 //   O = softmax(scale q c^T) c[:, :C],   W <= 576, C <= 512.
 // A key brings 2 W bytes and 2 (W + C) operations per head: with 128 heads and one token 241 per byte,
 // below the 286 at which the tensor cores and HBM take the same time, so HBM bounds decoding as
-// long as each key is read from it once and enters both products from shared memory.
+// long as each key is read from it once, enters both products from shared memory, and the tensor cores run at their full rate.
 //
-// Mapping.  Packed rows r = i H + g (query i, head g) of a request; a CTA takes 64 of them, and one CTA fills
-// an SM: 64 rows of queries (72 KB), two tiles of 64 keys (144 KB), the tile's weights (8 KB).  128 rows would
-// leave room for neither the accumulator (512 fp32 columns) beside the scores, nor a second key tile.
-// tcgen05.mma.ws with M = 64 spreads 64 rows by N columns over all 128 lanes of tensor memory (lanes 0-63
-// hold the first N / 2 columns, lanes 64-127 the others), so 64 x 512 fp32 take 256 columns.
-//   * warps 0-3: softmax and epilogue.  Warp w has rows 32 (w & 1) .. and keys 32 (w >> 1) .. of a tile;
-//     the two warps of a row exchange its maximum through shared memory;
-//   * warp 4: TMA of the key tiles, pages looked up three tiles ahead;
-//   * warp 5: tcgen05.mma: S(j + 1) = Q K(j + 1)^T before U += P(j) V(j), so that the tensor core works
-//     while the weights of tile j + 1 are computed;
-//   * warps 6-7: query rows by cp.async (any strides), for the next unit as soon as the last S of this one is done.
-// TMEM: U 0-255, S 256-287 and 288-319.
+// Mapping.  Packed rows r = i H + g (query i, head g) of a request; a unit is 128 of them over some tiles of 128 keys,
+// and a pair of CTAs (a cluster, one CTA per SM) works on it with tcgen05.mma of both (cta_group::2, M = 128):
+// each CTA holds 64 rows of queries, weights and U, and one half of every B operand.  64 x 512 fp32 of U
+// take 256 columns of tensor memory (lanes 0-63 hold the first half of a product's columns, lanes 64-127 the other), which
+// leaves room for two tiles of scores; 128 rows in one CTA would leave none.  (One CTA per 64 rows with M = 64 runs the
+// tensor core at half this rate and reads every key twice for 128 heads.)
+//   S = Q K^T, N = 128 keys: CTA r loads keys 64 r .. 64 r + 63 of the tile, all channels.
+//   U += P V, N = 256 channels twice: CTA r brings channels 128 r .. of each 256, of all 128 keys.  Half of that it has
+//     loaded as keys.  The other half, the peer's keys, is loaded once S is done into the places of its own
+//     keys' other channels, which nothing needs any more: slots 4 b + 2 h and 4 b + 2 h + 1 of both CTAs hold the CTA's
+//     channels of block b for the tile's half h.
+// So two stages of a tile fit beside the queries: 72 KB of queries, 2 x 64 KB of latents, 8 KB of channels from 512 on (one
+// stage: they are read by S alone), 16 KB through which warps exchange weights.
+// Roles:
+//   * warps 0-3: softmax and epilogue.  Warp w has rows 32 (w & 1) .. and keys 64 (w >> 1) .. of a tile;
+//     the two warps of a row exchange its maximum and their weights through shared memory;
+//   * warp 4: TMA of the CTA's keys, pages looked up three tiles ahead, in two halves of four pieces with barriers of
+//     their own: S begins with the first half while the second is on its way, and U += P V frees them one by one;
+//   * warp 5 (of the first CTA): tcgen05.mma, S(j + 1) and U += P(j) V(j) in whichever order they become ready;
+//   * warp 6: TMA of the peer's keys as values, half by half behind S, and of channels from 512 on;
+//   * warps 7-8: queries, for the next unit as soon as the last S of this one is done: TMA boxes of gcd(H, 64) heads, or
+//     where these are below eight cp.async.
+// TMEM: U 0-255, S 256-319 and 320-383, weights 384-447 and 448-511.
 //
 // Weights are 2^(x - ref + 7) in the operands' 16-bit type; ref is the row's maximum when it last moved, and moves only
 // where the maximum has grown by more than 2^8 (fp16 holds 2^15), with U rescaled then.  O is divided by the sum of
 // the rounded weights, the LSE takes the sum of the fp32 ones.
 //
-// Sharing out.  All (request, row blocks, tile) of a call, in that order, are dealt out in equal shares to as many
-// CTAs as run at once, whatever the lengths.  With more than 64 rows two CTAs (a group) go over the same
-// share, one for each row block of a pair, so that a key comes from HBM once.  Parts of a unit go
-// through a workspace and are joined by a second launch.
+// Sharing out.  All (request, 128 rows, tile) of a call, in that order, are dealt out in equal shares to as many
+// pairs as run at once, whatever the lengths.  Parts of a unit go through a workspace and are joined by a second launch.
 #pragma once
 
 #include "paged_common.cuh"
@@ -35,14 +44,15 @@
 namespace fa {
 namespace paged {
 
-constexpr int kLatRows = 64, kLatKeys = 64;
-constexpr int kLatThreads = 256;
+constexpr int kLatRows = 128, kLatKeys = 128; // of a unit and a tile; half of each per CTA
+constexpr int kLatThreads = 288;
 constexpr int kLatPieces = 9;                 // 64-channel pieces of a row: W <= 576
 constexpr int kLatPiece = 64 * 128;           // 64 rows x 64 16-bit channels, 128-byte swizzle
-constexpr int kLatStages = 2;
+constexpr int kLatStages = 2, kLatSlots = 8;  // pieces of a stage
 constexpr int kLatOffK = kLatPieces * kLatPiece;
-constexpr int kLatOffP = kLatOffK + kLatStages * kLatPieces * kLatPiece;
-constexpr int kLatOffCtl = kLatOffP + kLatPiece;
+constexpr int kLatOffTail = kLatOffK + kLatStages * kLatSlots * kLatPiece;  // the ninth piece
+constexpr int kLatOffP = kLatOffTail + kLatPiece;
+constexpr int kLatOffCtl = kLatOffP + 2 * kLatPiece;
 constexpr int kLatMaxB = 16384;
 constexpr float kLatShift = 7.f, kLatLag = 8.f;
 
@@ -55,21 +65,23 @@ struct LatentParams {
     const int* lens;
     long long q_st, q_sh, o_st, o_sh;
     int T, B, H, C, W, max_q, max_pages, num_pages, page_shift;
-    int members;      // CTAs of a group: 1, or 2 (row blocks 2 i and 2 i + 1)
     int min_share;    // tiles
+    int q_box;        // heads of a box of queries (0: read by cp.async)
     int box_rows;
     int causal;
     float scale_log2;
-    float* o_part;    // [2 CTAs][64][C]: the parts of a share's first and last unit
-    float2* stats;    // [2 CTAs][64]: log2 of the sums of the fp32 and of the rounded weights
-    int4* shares;     // [groups + 1]: first unit's begin, end, request, pair; behind the last: the share
+    float* o_part;    // [2 pairs][128][C]: the parts of a share's first and last unit
+    float2* stats;    // [2 pairs][128]: log2 of the sums of the fp32 and of the rounded weights
+    int4* shares;     // [pairs + 1]: first unit's begin, end, request, row block; behind the last: the share
 };
 
 struct LatCtl {
-    uint64_t q_full, q_empty, k_full[kLatStages], k_empty[kLatStages], s_full[2], p_full, pv_done, o_empty, drain;
+    // signalled in the first CTA by both: queries, keys, weights, U read; in both by the tensor core, or by the CTA's own loads
+    uint64_t q_full, k_full[4], p_full[2], o_empty;                            // k: by stage and half of its pieces
+    uint64_t q_empty, k_empty[4], s_half[2], s_full[2], pv_done[2], v_full[2], drain;
     uint32_t tmem_base;
-    int start[4];                 // request, pair, tile of the share's first unit; tiles of all units
-    float top[2][2][kLatRows];    // by tile parity, key half, row
+    int start[4];                // request, row block, tile of the share's first unit; tiles of that unit
+    float top[2][2][64];         // by tile parity, key half, row
 };
 static_assert(kLatOffCtl + sizeof(LatCtl) + 1024 <= 232448, "shared memory of a CTA");
 constexpr int kLatSmem = kLatOffCtl + static_cast<int>(sizeof(LatCtl)) + 1024;
@@ -80,22 +92,111 @@ __device__ __forceinline__ uint64_t lat_desc(uint32_t saddr, uint32_t lbo) {
 }
 __device__ __forceinline__ uint32_t lat_instr(bool bf16, int n, bool b_mn_major) {
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-           ((static_cast<uint32_t>(n) >> 3) << 17) | ((64u >> 4) << 24);
-}
-// D (tmem) (+)= A (smem) B (smem)^T, 64 rows over all lanes.
-__device__ __forceinline__ void mma_ws(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.ws.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
+           ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
 
-// Rows and keys of request b, and its units: pairs of row blocks times tiles of keys (at least one).
+// ---- a pair of CTAs
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The shared address `a` in the first CTA of the cluster.
+__device__ __forceinline__ uint32_t in_first_cta(uint32_t a) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
+    return r;
+}
+// An arrival in either CTA.  What it orders is tensor memory (behind the tcgen05 fences) and the execution of what waits for
+// it; a release to the cluster would first wait for all of the SM's memory traffic, the next tile's loads too (1.3 us).
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// The same behind writes to shared memory that the tensor cores of the pair are to read.
+__device__ __forceinline__ void arrive_remote_release(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void arrive_remote_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Whether the phase is complete, with what both CTAs did before it visible (does not wait).
+__device__ __forceinline__ bool test_cluster(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// A TMA load into this CTA that signals a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+// D (tmem of both) (+)= A (smem, 64 rows of each) B (smem, half of the columns of each)^T over four steps of 16 along
+// K, 32 bytes of swizzled rows each.  One elected lane of the (converged) warp issues.
+__device__ __forceinline__ void mma_pair_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\t"
+        "setp.eq.b32 p1, %4, %4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+        "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t"
+        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t"
+        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// The same with A in tensor memory (16 elements in 8 columns), B's steps 16 rows of 128 bytes.
+__device__ __forceinline__ void mma_pair_ts_k64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %4, 0;\n\t"
+        "setp.eq.b32 p1, %4, %4;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
+        "add.u32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [x], y, %3, p1;\n\t"
+        "add.u32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [x], y, %3, p1;\n\t"
+        "add.u32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [x], y, %3, p1;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrives on `bar` in both CTAs when what the elected lane issued before is done.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"(static_cast<unsigned short>(3))
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+        : "memory");
+}
+
+// Rows and keys of request b, and its units: blocks of 128 rows times tiles of keys (at least one).
 struct LatRequest {
-    int q0, nq, len, pairs, tiles;
+    int q0, nq, len, blocks, tiles;
 };
 __device__ __forceinline__ LatRequest lat_request(const LatentParams& p, int b, bool& bad) {
     LatRequest r;
@@ -107,23 +208,23 @@ __device__ __forceinline__ LatRequest lat_request(const LatentParams& p, int b, 
     }
     r.len = ld_meta(p.lens + b);
     if (r.len < 0 || r.len > (p.max_pages << p.page_shift)) bad = true, r.len = 0;
-    r.pairs = (r.nq * p.H + p.members * kLatRows - 1) / (p.members * kLatRows);
+    r.blocks = (r.nq * p.H + kLatRows - 1) / kLatRows;
     r.tiles = max(1, (r.len + kLatKeys - 1) / kLatKeys);
     return r;
 }
 
-// Walks the parts of a CTA's share: for every unit some tiles of its keys.
+// Walks the parts of a pair's share: for every unit some tiles of its keys.
 struct LatWalk {
     const LatentParams& p;
-    const int member, f0, f1;
-    int f, b, pair, first;
+    const int f0, f1;
+    int f, b, block, first;
     LatRequest rq;
     // of the current part
-    int r0, rows, lo, hi, kend;   // this CTA's rows, and their tiles [lo, hi)
+    int r0, rows, lo, hi, load_end;   // first row, rows; tiles [lo, hi); keys that are loaded (whole boxes up to the last seen)
     bool whole, at_start;
 
-    __device__ LatWalk(const LatentParams& p_, const LatCtl* ctl, int member_, int f0_, int f1_)
-        : p(p_), member(member_), f0(f0_), f1(f1_), f(f0_), b(ctl->start[0]), pair(ctl->start[1]), first(ctl->start[2]) {
+    __device__ LatWalk(const LatentParams& p_, const LatCtl* ctl, int f0_, int f1_)
+        : p(p_), f0(f0_), f1(f1_), f(f0_), b(ctl->start[0]), block(ctl->start[1]), first(ctl->start[2]) {
         bool bad = false;
         if (f < f1) rq = lat_request(p, b, bad);
     }
@@ -131,75 +232,108 @@ struct LatWalk {
     // the next part; false behind the last
     __device__ bool next() {
         if (f >= f1) return false;
-        while (pair >= rq.pairs) {  // (units are left, so there is a request that has some)
+        while (block >= rq.blocks) {  // (units are left, so there is a request that has some)
             if (b + 1 >= p.B) return false;
             bool bad = false;
-            ++b, pair = 0;
+            ++b, block = 0;
             rq = lat_request(p, b, bad);
         }
         const int n = min(rq.tiles - first, f1 - f);
-        r0 = (pair * p.members + member) * kLatRows;
-        rows = max(0, min(kLatRows, rq.nq * p.H - r0));
-        kend = rows > 0 ? max(0, limit(r0 + rows - 1)) : 0;
-        const int kt = (kend + kLatKeys - 1) / kLatKeys;
+        r0 = block * kLatRows;
+        rows = min(kLatRows, rq.nq * p.H - r0);
+        const int kend = max(0, limit(r0 + rows - 1)), kt = (kend + kLatKeys - 1) / kLatKeys;
+        load_end = min(rq.len, (kend + p.box_rows - 1) / p.box_rows * p.box_rows);
         lo = min(first, kt), hi = min(first + n, kt);
         whole = first == 0 && n == rq.tiles;
         at_start = f == f0;
         f += n;
         first = 0;
-        ++pair;
+        ++block;
         return true;
+    }
+};
+
+// The pages of one half of the tiles of a part, looked up three tiles ahead: lane i has box i of the half.
+struct LatPages {
+    const LatentParams& p;
+    const LatWalk& w;
+    const int* trow;
+    const int half;
+    int page, page1, page2;
+    __device__ LatPages(const LatentParams& p_, const LatWalk& w_, int half_, int lane) : p(p_), w(w_), half(half_) {
+        trow = p.table + static_cast<long long>(w.b) * p.max_pages;
+        page = at(w.lo, lane), page1 = at(w.lo + 1, lane), page2 = at(w.lo + 2, lane);
+    }
+    __device__ int key(int j, int lane) const { return j * kLatKeys + half * 64 + lane * p.box_rows; }
+    __device__ bool wanted(int j, int lane) const { return j < w.hi && lane * p.box_rows < 64 && key(j, lane) < w.load_end; }
+    __device__ int at(int j, int lane) const { return wanted(j, lane) ? ld_meta(trow + (key(j, lane) >> p.page_shift)) : -1; }
+    // First row of the lane's box of tile j in the cache (-1: not read); moves on to tile j + 1.
+    __device__ int take(int j, int lane) {
+        const int ahead = at(j + 3, lane);
+        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+        if (wanted(j, lane) && !there) report(kBadData);
+        const int row = there ? (page << p.page_shift) + (key(j, lane) & ((1 << p.page_shift) - 1)) : -1;
+        page = page1, page1 = page2, page2 = ahead;
+        return row;
     }
 };
 
 template <bool BF16>
 __global__ void __launch_bounds__(kLatThreads, 1)
-    latent_paged_kernel(const __grid_constant__ CUtensorMap tm, const LatentParams p) {
+    latent_paged_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q, const LatentParams p) {
     extern __shared__ __align__(16) uint8_t lat_raw[];
     const uint32_t raw = ptx::smem_addr(lat_raw);
     uint8_t* smem = lat_raw + (((raw + 1023u) & ~1023u) - raw);
     const uint32_t sbase = ptx::smem_addr(smem);
     LatCtl* ctl = reinterpret_cast<LatCtl*>(smem + kLatOffCtl);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int rank = static_cast<int>(cluster_rank());
+    const int kp = (p.W + 63) >> 6;
+    const bool tail = kp > kLatSlots;
 
     const uint32_t b_qf = ptx::smem_addr(&ctl->q_full), b_qe = ptx::smem_addr(&ctl->q_empty);
     const uint32_t b_kf = ptx::smem_addr(&ctl->k_full[0]), b_ke = ptx::smem_addr(&ctl->k_empty[0]);
-    const uint32_t b_sf = ptx::smem_addr(&ctl->s_full[0]), b_pf = ptx::smem_addr(&ctl->p_full);
-    const uint32_t b_pv = ptx::smem_addr(&ctl->pv_done), b_oe = ptx::smem_addr(&ctl->o_empty);
+    const uint32_t b_sh = ptx::smem_addr(&ctl->s_half[0]), b_sf = ptx::smem_addr(&ctl->s_full[0]), b_vf = ptx::smem_addr(&ctl->v_full[0]);
+    const uint32_t b_pf = ptx::smem_addr(&ctl->p_full[0]), b_pv = ptx::smem_addr(&ctl->pv_done[0]), b_oe = ptx::smem_addr(&ctl->o_empty);
     const uint32_t b_drain = ptx::smem_addr(&ctl->drain);
     if (tid == 0) {
-        ptx::mbar_init(b_qf, 64);
+        ptx::mbar_init(b_qf, 2 * (p.q_box ? 1 : 64));
         ptx::mbar_init(b_qe, 1);
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(b_kf + 8 * s, 1);
-            ptx::mbar_init(b_ke + 8 * s, 1);
+            ptx::mbar_init(b_kf + 16 * s, 2);
+            ptx::mbar_init(b_kf + 16 * s + 8, tail ? 4 : 2);
+            ptx::mbar_init(b_ke + 16 * s, 1);
+            ptx::mbar_init(b_ke + 16 * s + 8, 1);
+            ptx::mbar_init(b_sh + 8 * s, 1);
             ptx::mbar_init(b_sf + 8 * s, 1);
+            ptx::mbar_init(b_pv + 8 * s, 1);
+            ptx::mbar_init(b_pf + 8 * s, 2 * 4);  // (a warp may be a tile ahead of another)
+            ptx::mbar_init(b_vf + 8 * s, 1);
         }
-        ptx::mbar_init(b_pf, 128);
-        ptx::mbar_init(b_pv, 1);
-        ptx::mbar_init(b_oe, 128);
+        ptx::mbar_init(b_oe, 2 * 4);
         ptx::mbar_init(b_drain, 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tm);
+        if (p.q_box) ptx::prefetch_tensormap(&tm_q);
     }
     if (warp == 5) {
-        ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), 512);
-        ptx::tmem_relinquish();
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(&ctl->tmem_base)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     dependents_may_start();
     wait_for_previous();
 
-    // ---- this group's share [f0, f1) of all tiles, in order of request, pair of row blocks, tile
-    const int groups = gridDim.x / p.members, group = blockIdx.x / p.members, member = blockIdx.x - group * p.members;
+    // ---- this pair's share [f0, f1) of all tiles, in order of request, row block, tile
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
     int f0, f1;
     {
-        int* before = reinterpret_cast<int*>(smem);  // (the tiles' memory) tiles before each of a thread's runs of requests
+        int* before = reinterpret_cast<int*>(smem);  // (the queries' memory)
         const int per = (p.B + kLatThreads - 1) / kLatThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
         bool bad = false;
         int own = 0;
         for (int b = b0; b < b1; ++b) {
             const LatRequest r = lat_request(p, b, bad);
-            own += r.pairs * r.tiles;
+            own += r.blocks * r.tiles;
         }
         if (bad) report(kBadData);
         int incl = own;
@@ -209,21 +343,19 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             if (lane >= o) incl += y;
         }
         if (lane == 31) before[warp] = incl;
-        ptx::tc_fence_before_sync();
         __syncthreads();
-        ptx::tc_fence_after_sync();
         int run = incl - own, all = 0;
         for (int w = 0; w < kLatThreads / 32; ++w) {
             if (w < warp) run += before[w];
             all += before[w];
         }
-        const int share = max((all + groups - 1) / groups, p.min_share);
-        f0 = static_cast<int>(min(static_cast<long long>(group) * share, static_cast<long long>(all)));
+        const int share = max((all + pairs - 1) / pairs, p.min_share);
+        f0 = static_cast<int>(min(static_cast<long long>(pair) * share, static_cast<long long>(all)));
         f1 = static_cast<int>(min(static_cast<long long>(f0) + share, static_cast<long long>(all)));
         if (f0 < f1 && run <= f0 && f0 < run + own) {
             for (int b = b0; b < b1; ++b) {
                 const LatRequest r = lat_request(p, b, bad);
-                const int n = r.pairs * r.tiles;
+                const int n = r.blocks * r.tiles;
                 if (f0 < run + n) {
                     const int rel = f0 - run;
                     ctl->start[0] = b, ctl->start[1] = rel / r.tiles, ctl->start[2] = rel % r.tiles, ctl->start[3] = r.tiles;
@@ -232,61 +364,67 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 run += n;
             }
         }
-        ptx::fence_proxy_async_smem();  // (what was read and written here is the key tiles' and queries' memory)
+        ptx::fence_proxy_async_smem();  // (what was read and written here is the queries' memory)
+        ptx::tc_fence_before_sync();
         __syncthreads();
-        if (p.shares && member == 0 && tid == 0) {
+        cluster_sync();  // barriers and tensor memory of both CTAs are there
+        ptx::tc_fence_after_sync();
+        if (p.shares && rank == 0 && tid == 0) {
             int4 u = make_int4(f0, f0, 0, 0);
             if (f0 < f1) u = make_int4(f0 - ctl->start[2], f0 - ctl->start[2] + ctl->start[3], ctl->start[0], ctl->start[1]);
-            p.shares[group] = u;
-            if (group == 0) p.shares[groups] = make_int4(share, 0, 0, 0);
+            p.shares[pair] = u;
+            if (pair == 0) p.shares[pairs] = make_int4(share, 0, 0, 0);
         }
     }
     const uint32_t tmem = ctl->tmem_base;
-    const int kp = (p.W + 63) >> 6;
-    LatWalk walk(p, ctl, member, f0, f1);
+    LatWalk walk(p, ctl, f0, f1);
 
     if (warp < 4) {
         // ================================================ softmax and epilogue
         const int half = warp >> 1, row = (warp & 1) * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
-        const uint32_t p_row = sbase + kLatOffP + row * 128;
+        // the warp's 32 rows x 128 bytes of exchange memory, and those of the warp with the same rows
+        const uint32_t box = sbase + kLatOffP + warp * 4096, own = box + lane * 128, other = sbase + kLatOffP + (warp ^ 2) * 4096 + lane * 128;
+        const uint32_t r_pf = in_first_cta(b_pf), r_oe = in_first_cta(b_oe);
         const int pair_barrier = 1 + (warp & 1);
         int c = 0;  // tiles so far
-        bool ok = true;  // (after a wait that ran out nothing is waited for, but every barrier of the pair is still met)
+        bool ok = true;  // (after a wait that ran out nothing is waited for, but every barrier of the two warps is still met)
         while (walk.next()) {
-            const int r = walk.r0 + row;
-            const bool mine = row < walk.rows;
+            const int r = walk.r0 + rank * 64 + row;
+            const bool mine = rank * 64 + row < walk.rows;
             const int my_limit = mine ? walk.limit(r) : walk.rq.len;
-            const int first_limit = walk.limit(walk.r0);  // the least of the block's rows
-            const int load_end = min(walk.rq.len, (walk.kend + p.box_rows - 1) / p.box_rows * p.box_rows);
+            const int first_limit = walk.limit(walk.r0);  // the least of the unit's rows
             float ref = -INFINITY, sum = 0.f, rsum = 0.f;  // sums of this thread's keys: fp32 and rounded weights
             for (int j = walk.lo; j < walk.hi; ++j, ++c) {
                 ok = ok && wait_warp(b_sf + 8 * (c & 1), (c >> 1) & 1);
                 ptx::tc_fence_after_sync();
                 const int key0 = j * kLatKeys;
-                uint32_t sv[32];
-                ptx::tmem_ld_32x32b_x32(tmem + lane_off + 256 + 32 * (c & 1), sv);
+                uint32_t sv[64];
+                ptx::tmem_ld_32x32b_x64(tmem + lane_off + 256 + 64 * (c & 1), sv);
                 ptx::tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) ptx::reg_fence(sv[e]);
+                for (int e = 0; e < 64; ++e) ptx::reg_fence(sv[e]);
                 if (key0 + kLatKeys > first_limit) {
-                    const int seen = my_limit - key0 - 32 * half;
+                    const int seen = my_limit - key0 - 64 * half;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
+                    for (int e = 0; e < 64; ++e)
                         if (e >= seen) sv[e] = __float_as_uint(-INFINITY);
                 }
-                float top = __uint_as_float(sv[0]);
+                float top = __uint_as_float(sv[0]), top2 = __uint_as_float(sv[1]);
 #pragma unroll
-                for (int e = 1; e + 1 < 32; e += 2) top = ptx::fmax3(top, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                top = fmaxf(top, __uint_as_float(sv[31]));
+                for (int e = 2; e + 3 < 64; e += 4) {
+                    top = ptx::fmax3(top, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
+                    top2 = ptx::fmax3(top2, __uint_as_float(sv[e + 2]), __uint_as_float(sv[e + 3]));
+                }
+                top = ptx::fmax3(fmaxf(top, top2), __uint_as_float(sv[62]), __uint_as_float(sv[63]));
                 ctl->top[c & 1][half][row] = top;
                 ptx::named_barrier_sync(pair_barrier, 64);
                 top = fmaxf(top, ctl->top[c & 1][half ^ 1][row]) * p.scale_log2;
-                // U holds the products of the tiles before, and the weights' memory is free
-                if (c > 0) ok = ok && wait_warp(b_pv, (c - 1) & 1);
-                ptx::tc_fence_after_sync();
                 const bool moves = top > ref + kLatLag;  // (the same in both warps of the row)
                 if (__any_sync(0xffffffffu, moves)) {
+                    // U holds the products of the tiles before
+                    if (c > 0) ok = ok && wait_warp(b_pv + 8 * ((c - 1) & 1), ((c - 1) >> 1) & 1);
+                    ptx::tc_fence_after_sync();
                     float alpha = 1.f;
                     if (moves) {
                         if (ref != -INFINITY) alpha = ptx::ex2_approx(ref - top);
@@ -295,7 +433,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     sum *= alpha, rsum *= alpha;
                     if (j > walk.lo) {
                         const float2 av = make_float2(alpha, alpha);
-                        const int cols = p.C <= 64 ? 32 : p.C <= 128 ? 64 : p.C <= 256 ? 128 : 256;
+                        const int cols = p.C <= 128 ? 64 : p.C <= 256 ? 128 : p.C <= 384 ? 192 : 256;
 #pragma unroll 1
                         for (int x = 0; x < cols; x += 32) {
                             uint32_t ov[32];
@@ -316,41 +454,63 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 const float sub = (ref == -INFINITY ? 0.f : ref) - kLatShift;
                 const float2 fv = make_float2(p.scale_log2, p.scale_log2), nv = make_float2(-sub, -sub);
                 float2 acc = make_float2(0.f, 0.f), racc = make_float2(0.f, 0.f);
-                uint32_t pk[16];
+                uint32_t pk[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), fv, nv);
-                    const float2 w = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
-                    acc = __fadd2_rn(acc, w);
-                    pk[e] = pack16(w.x, w.y, BF16);
-                    racc = __fadd2_rn(racc, unpack16(pk[e], BF16));
+                for (int i = 0; i < 8; ++i) {
+#pragma unroll
+                    for (int e = 4 * i; e < 4 * i + 4; ++e) {
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), fv, nv);
+                        const float2 w = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+                        acc = __fadd2_rn(acc, w);
+                        pk[e] = pack16(w.x, w.y, BF16);
+                        racc = __fadd2_rn(racc, unpack16(pk[e], BF16));
+                    }
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + ((i ^ (lane & 7)) << 4)), "r"(pk[4 * i]), "r"(pk[4 * i + 1]),
+                                 "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3])
+                                 : "memory");
                 }
                 sum += acc.x + acc.y, rsum += racc.x + racc.y;
+                // Both lanes of a row take the weights of all its keys: the product's first half of channels reads lanes
+                // 0-63, the second lanes 64-127.  (Weights go through tensor memory because written to shared memory they would
+                // need a proxy fence.)  Their columns are free once U += P(c - 2) V is done, as it always is: S(c) was issued behind it.
+                if (c >= 2) ok = ok && wait_warp(b_pv + 8 * (c & 1), ((c >> 1) - 1) & 1);
+                const uint32_t p_addr = tmem + lane_off + 384 + 64 * (c & 1);
+                ptx::tmem_st_32x32b_x32(p_addr + 32 * half, pk);
+                ptx::named_barrier_sync(pair_barrier, 64);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + (((4 * half + i) ^ (row & 7)) << 4)),
-                                 "r"(pk[4 * i]), "r"(pk[4 * i + 1]), "r"(pk[4 * i + 2]), "r"(pk[4 * i + 3])
+                for (int i = 0; i < 8; ++i)
+                    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(pk[4 * i]), "=r"(pk[4 * i + 1]), "=r"(pk[4 * i + 2]), "=r"(pk[4 * i + 3])
+                                 : "r"(other + ((i ^ (lane & 7)) << 4))
                                  : "memory");
-                // rows behind the last key that was loaded may hold anything: as values they are zeros
-                // (S of this tile is done, so nothing else reads them)
-                if (key0 + kLatKeys > load_end) {
-                    const uint32_t tile = sbase + kLatOffK + (c & 1) * (kLatPieces * kLatPiece);
-                    const int from = max(0, load_end - key0);
-                    const int chunks = kLatKeys - from;  // rows
-                    for (int i = tid; i < chunks * 8 * kp; i += 128) {
-                        const int piece = i / (8 * chunks), at = i - piece * (8 * chunks);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + piece * kLatPiece + from * 128 + at * 16), "r"(0)
-                                     : "memory");
+                ptx::tmem_st_32x32b_x32(p_addr + 32 * (half ^ 1), pk);
+                ptx::tmem_wait_st();
+                // the peer's keys are there as values; rows behind the last key that was loaded may hold anything: as
+                // values they are zeros (S of this tile is done, so nothing else reads them)
+                ok = ok && wait_warp(b_vf + 8 * (c & 1), (c >> 1) & 1);
+                if (key0 + kLatKeys > walk.load_end) {
+                    const uint32_t stage = sbase + kLatOffK + (c & 1) * (kLatSlots * kLatPiece);
+                    for (int s = 0; s < kLatSlots; ++s) {
+                        const bool wide = p.C - 256 * (s >> 2) > 128;   // channels of the slot's block: 256 or 128
+                        const int from = max(0, walk.load_end - key0 - 64 * (wide ? (s & 3) >> 1 : s & 1));
+                        for (int i = from * 8 + tid; i < 64 * 8; i += 128)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(stage + s * kLatPiece + i * 16), "r"(0) : "memory");
                     }
+                    ptx::fence_proxy_async_smem();
                 }
-                ptx::fence_proxy_async_smem();
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(b_pf);
+                __syncwarp();
+                if (lane == 0) {
+                    if (key0 + kLatKeys > walk.load_end)
+                        arrive_remote_release(r_pf + 8 * (c & 1));
+                    else
+                        arrive_remote(r_pf + 8 * (c & 1));
+                }
             }
             // ---- O = U / sum, whole or as a part
             const bool any = walk.hi > walk.lo;
             if (any) {
-                ok = ok && wait_warp(b_pv, (c - 1) & 1);
+                ok = ok && wait_warp(b_pv + 8 * ((c - 1) & 1), ((c - 1) >> 1) & 1);
                 ptx::tc_fence_after_sync();
             }
             // the two halves' sums (the barrier behind the last exchange of maxima has been passed by both)
@@ -362,35 +522,62 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             const float inv = rsum != 0.f ? 1.f / rsum : 0.f;
             const float lse2 = sum != 0.f ? ref - kLatShift + log2f(sum) : -INFINITY;
             const int tok = walk.rq.q0 + r / p.H, head = r % p.H;
-            const long long part = static_cast<long long>(blockIdx.x) * 2 + (walk.at_start ? 0 : 1);
-            uint16_t* dst = p.o + static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh;
-            float* pdst = p.o_part + (part * kLatRows + row) * p.C;
+            const long long part = (static_cast<long long>(pair) * 2 + (walk.at_start ? 0 : 1)) * kLatRows + rank * 64 + row;
+            // Stores of a row per thread would touch 32 lines each; through the warp's exchange memory eight lanes write 128
+            // bytes of a row.
+            const long long at = !mine ? -1
+                                 : walk.whole ? static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh : part * p.C;
             if (any || walk.whole) {
-                for (int h = 0; h * 256 < p.C; ++h) {
-                    const int left = p.C - 256 * h, wide = left <= 64 ? 32 : left <= 128 ? 64 : 128;
+                for (int b = 0; b * 256 < p.C; ++b) {
+                    const int wide = p.C - 256 * b > 128 ? 128 : 64;
 #pragma unroll 1
                     for (int x = 0; x < wide; x += 32) {
                         uint32_t ov[32];
                         if (any) {
-                            ptx::tmem_ld_32x32b_x32(tmem + lane_off + 128 * h + x, ov);
+                            ptx::tmem_ld_32x32b_x32(tmem + lane_off + 128 * b + x, ov);
                             ptx::tmem_wait_ld();
                         }
-                        const int d0 = 256 * h + half * wide + x;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            float f[8];
+                        for (int e = 0; e < 32; ++e) {
+                            if (any) ptx::reg_fence(ov[e]); else ov[e] = 0;
+                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv);
+                        }
+                        const int d0 = 256 * b + half * wide + x;
+                        if (walk.whole) {  // 32 channels in 64 bytes, two passes to a box
+                            const int c0 = (x & 32) >> 3;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (any) ptx::reg_fence(ov[e + i]); else ov[e + i] = 0;
-                                f[i] = __uint_as_float(ov[e + i]) * inv;
+                            for (int e = 0; e < 4; ++e) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) w[i] = pack16(__uint_as_float(ov[8 * e + 2 * i]), __uint_as_float(ov[8 * e + 2 * i + 1]), BF16);
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + (((c0 + e) ^ (lane & 7)) << 4)), "r"(w[0]), "r"(w[1]),
+                                             "r"(w[2]), "r"(w[3])
+                                             : "memory");
                             }
-                            if (!mine || d0 + e >= p.C) continue;
-                            if (walk.whole) {
-                                *reinterpret_cast<uint4*>(dst + d0 + e) = make_uint4(
-                                    pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
-                            } else {
-                                *reinterpret_cast<float4*>(pdst + d0 + e) = make_float4(f[0], f[1], f[2], f[3]);
-                                *reinterpret_cast<float4*>(pdst + d0 + e + 4) = make_float4(f[4], f[5], f[6], f[7]);
+                            if (!(x & 32)) continue;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + ((e ^ (lane & 7)) << 4)), "r"(ov[4 * e]),
+                                             "r"(ov[4 * e + 1]), "r"(ov[4 * e + 2]), "r"(ov[4 * e + 3])
+                                             : "memory");
+                        }
+                        __syncwarp();
+                        const int ch = walk.whole ? d0 - 32 + (lane & 7) * 8 : d0 + (lane & 7) * 4;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int y = 4 * i + (lane >> 3);  // row of the box
+                            const long long to = __shfl_sync(0xffffffffu, at, y);
+                            uint4 v;
+                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                         : "r"(box + y * 128 + (((lane & 7) ^ (y & 7)) << 4))
+                                         : "memory");
+                            if (to >= 0 && ch < p.C) {
+                                if (walk.whole)
+                                    *reinterpret_cast<uint4*>(p.o + to + ch) = v;
+                                else
+                                    *reinterpret_cast<uint4*>(p.o_part + to + ch) = v;
                             }
                         }
                         __syncwarp();
@@ -399,222 +586,320 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             }
             if (any) {
                 ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(b_oe);
+                __syncwarp();
+                if (lane == 0) arrive_remote(r_oe);
             }
             if (mine && half == 0) {
                 if (walk.whole)
                     p.lse[static_cast<long long>(tok) * p.H + head] = lse2 * 0.69314718055994531f;
                 else
-                    p.stats[part * kLatRows + row] =
-                        make_float2(lse2, rsum != 0.f ? ref - kLatShift + log2f(rsum) : -INFINITY);
+                    p.stats[part] = make_float2(lse2, rsum != 0.f ? ref - kLatShift + log2f(rsum) : -INFINITY);
             }
         }
     } else if (warp == 4) {
-        // ========================================================== key tiles
-        const int boxes = kLatKeys / p.box_rows;   // of a tile
+        // ================================================ this CTA's keys
+        const uint32_t r_kf = in_first_cta(b_kf);
         int c = 0;
         bool ok = true;
         while (ok && walk.next()) {
-            const int* trow = p.table + static_cast<long long>(walk.b) * p.max_pages;
-            const int load_end = min(walk.rq.len, (walk.kend + p.box_rows - 1) / p.box_rows * p.box_rows);
-            auto page_of = [&](int j) {  // this lane's box of tile j: its page, -1 where it is not read
-                const int key = j * kLatKeys + lane * p.box_rows;
-                return j < walk.hi && lane < boxes && key < load_end ? ld_meta(trow + (key >> p.page_shift)) : -1;
-            };
-            int page = page_of(walk.lo), page1 = page_of(walk.lo + 1), page2 = page_of(walk.lo + 2);
-            for (int j = walk.lo; j < walk.hi; ++j, ++c) {
-                const int page3 = page_of(j + 3);
-                const int s = c & 1, key = j * kLatKeys + lane * p.box_rows;
-                const bool wanted = lane < boxes && key < load_end;
-                const bool there = wanted && static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
-                if (wanted && !there) report(kBadData);
-                const int n = __popc(__ballot_sync(0xffffffffu, there));
-                if (c >= kLatStages && !(ok = wait_warp(b_ke + 8 * s, ((c >> 1) - 1) & 1))) break;
-                if (lane == 0) {
-                    if (n > 0)
-                        ptx::mbar_arrive_expect_tx(b_kf + 8 * s, n * kp * p.box_rows * 128);
-                    else
-                        ptx::mbar_arrive(b_kf + 8 * s);
+            LatPages pages(p, walk, rank, lane);
+            for (int j = walk.lo; ok && j < walk.hi; ++j, ++c) {
+                const int s = c & 1, row = pages.take(j, lane);
+                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                const uint32_t dst = sbase + kLatOffK + s * (kLatSlots * kLatPiece) + lane * p.box_rows * 128;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int bar = 16 * s + 8 * h, pieces = max(0, min(4, kp - 4 * h));
+                    if (c >= kLatStages && !(ok = wait_warp(b_ke + bar, ((c >> 1) - 1) & 1))) break;
+                    if (lane == 0) arrive_remote_expect(r_kf + bar, n * pieces * p.box_rows * 128);
+                    __syncwarp();
+                    if (row >= 0)
+                        for (int i = 4 * h; i < 4 * h + pieces; ++i) tma_load_2d_pair(dst + i * kLatPiece, &tm, r_kf + bar, 64 * i, row);
+                    __syncwarp();
                 }
-                __syncwarp();
-                if (there) {
-                    const int at = (page << p.page_shift) + (key & ((1 << p.page_shift) - 1));
-                    const uint32_t dst = sbase + kLatOffK + s * (kLatPieces * kLatPiece) + lane * p.box_rows * 128;
-                    for (int i = 0; i < kp; ++i) tma_load_2d(dst + i * kLatPiece, &tm, b_kf + 8 * s, 64 * i, at);
-                }
-                __syncwarp();
-                page = page1, page1 = page2, page2 = page3;
             }
         }
-        // nothing may still be landing in this CTA's memory when it ends
-        for (int i = max(0, c - kLatStages); i < c; ++i) wait_warp(b_kf + 8 * (i & 1), (i >> 1) & 1);
-    } else if (warp == 5) {
-        // ================================================== tensor-core issuer
-        const uint32_t id_s = lat_instr(BF16, kLatKeys, false);
-        const uint64_t q_desc = lat_desc(sbase, 16), k_desc = lat_desc(sbase + kLatOffK, 16);
-        const uint64_t p_desc = lat_desc(sbase + kLatOffP, 16), v_desc = lat_desc(sbase + kLatOffK, kLatPiece);
-        constexpr uint64_t kPieceStep = kLatPiece / 16, kStageStep = kLatPieces * kPieceStep;
-        const int steps = (p.W + 15) >> 4;
-        auto issue_s = [&](int c) {
-            const uint64_t kd = k_desc + (c & 1) * kStageStep;
-            if (ptx::elect_one()) {
-                for (int i = 0; i < steps; ++i) {
-                    const uint64_t off = (i >> 2) * kPieceStep + 2 * (i & 3);
-                    mma_ws(tmem + 256 + 32 * (c & 1), q_desc + off, kd + off, id_s, i > 0);
-                }
-            }
+    } else if (warp == 6) {
+        // ============================== the peer's keys as values; channels from 512 on
+        const uint32_t r_kf = in_first_cta(b_kf);
+        auto load_tail = [&](int c, int row) {
+            const uint32_t bar = r_kf + 16 * (c & 1) + 8;
+            const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+            if (lane == 0) arrive_remote_expect(bar, n * p.box_rows * 128);
             __syncwarp();
-            ptx::tc_commit_elect(b_sf + 8 * (c & 1));
-        };
-        auto issue_pv = [&](int c, bool accumulate) {
-            const uint64_t vd = v_desc + (c & 1) * kStageStep;
-            if (ptx::elect_one()) {
-                for (int h = 0; h * 256 < p.C; ++h) {
-                    const int left = p.C - 256 * h;
-                    const uint32_t id = lat_instr(BF16, left <= 64 ? 64 : left <= 128 ? 128 : 256, true);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mma_ws(tmem + 128 * h, p_desc + 2 * i, vd + h * 4 * kPieceStep + 128 * i, id, accumulate || i > 0);
-                }
-            }
+            if (row >= 0) tma_load_2d_pair(sbase + kLatOffTail + lane * p.box_rows * 128, &tm, bar, 64 * kLatSlots, row);
             __syncwarp();
         };
-        int c = 0, parts = 0;
+        // The channels from 512 on go a tile ahead: of tile c + 1 as soon as S(c) is done.
+        LatWalk ahead(p, ctl, f0, f1);
+        int ca = 0, ja = 0;
+        bool more = tail;
+        int next_page = -1;
+        auto key_of = [&] { return ja * kLatKeys + rank * 64 + lane * p.box_rows; };
+        auto advance = [&] {  // to the next tile of the share, its page on its way
+            ++ja;
+            while (more && ja >= ahead.hi) {
+                more = ahead.next();
+                if (more) ja = ahead.lo;
+            }
+            next_page = -1;
+            if (more && lane * p.box_rows < 64 && key_of() < ahead.load_end)
+                next_page = ld_meta(p.table + static_cast<long long>(ahead.b) * p.max_pages + (key_of() >> p.page_shift));
+        };
+        auto next_row = [&] {
+            return static_cast<unsigned>(next_page) < static_cast<unsigned>(p.num_pages)
+                       ? (next_page << p.page_shift) + (key_of() & ((1 << p.page_shift) - 1)) : -1;
+        };
+        if (more) {
+            ahead.hi = 0;
+            advance();
+            if (more) {
+                load_tail(ca++, next_row());
+                advance();
+            }
+        }
+        int slots = 0;  // of the peer's keys
+        for (int b = 0; b * 256 < p.C; ++b) slots += p.C - 256 * b > 128 ? 2 : 1;
+        int c = 0;
         bool ok = true;
         while (ok && walk.next()) {
-            const int n = walk.hi - walk.lo;
-            if (n == 0) continue;
-            if (!(ok = wait_warp(b_qf, parts & 1) && wait_warp(b_kf + 8 * (c & 1), (c >> 1) & 1))) break;
-            ptx::tc_fence_after_sync();
-            issue_s(c);
-            if (n == 1) ptx::tc_commit_elect(b_qe);
-            for (int i = 0; i < n; ++i, ++c) {
-                if (i + 1 < n) {
-                    if (!(ok = wait_warp(b_kf + 8 * ((c + 1) & 1), ((c + 1) >> 1) & 1))) break;
-                    ptx::tc_fence_after_sync();
-                    issue_s(c + 1);  // (its columns were read before the weights of tile c - 1 were handed over)
-                    if (i + 2 == n) ptx::tc_commit_elect(b_qe);
+            LatPages pages(p, walk, rank ^ 1, lane);
+            for (int j = walk.lo; j < walk.hi; ++j, ++c) {
+                const int s = c & 1, row = pages.take(j, lane);
+                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                const uint32_t dst = sbase + kLatOffK + s * (kLatSlots * kLatPiece) + lane * p.box_rows * 128;
+                // S has passed the first four pieces, then all: as keys they are not needed any more
+                for (int b = 0; b < 2; ++b) {
+                    if (!(ok = wait_warp((b == 0 && kp > 4 ? b_sh : b_sf) + 8 * s, (c >> 1) & 1))) break;
+                    if (b == 0 && lane == 0) ptx::mbar_arrive_expect_tx(b_vf + 8 * s, n * slots * p.box_rows * 128);
+                    __syncwarp();
+                    if (row >= 0 && b * 256 < p.C) {
+                        const int wide = p.C - 256 * b > 128 ? 2 : 1;
+                        for (int i = 0; i < wide; ++i)
+                            tma_load_2d(dst + (4 * b + wide * (rank ^ 1) + i) * kLatPiece, &tm, b_vf + 8 * s, 64 * (4 * b + wide * rank + i), row);
+                    }
+                    __syncwarp();
                 }
-                if (!(ok = wait_warp(b_pf, c & 1))) break;
-                if (i == 0 && parts > 0 && !(ok = wait_warp(b_oe, (parts - 1) & 1))) break;
-                ptx::tc_fence_after_sync();
-                issue_pv(c, i > 0);
-                ptx::tc_commit_elect(b_ke + 8 * (c & 1));
-                ptx::tc_commit_elect(b_pv);
-                __syncwarp();
+                if (!ok) break;
+                if (more) {
+                    load_tail(ca++, next_row());
+                    advance();
+                }
             }
-            ++parts;
         }
-        ptx::tc_commit_elect(b_drain);
+        // nothing may still be landing in this CTA's memory when it ends (its keys were read by products that are done)
+        for (int i = max(0, c - 2); i < c; ++i) wait_warp(b_vf + 8 * (i & 1), (i >> 1) & 1);
+    } else if (warp == 5) {
+        // ================================================== tensor-core issuer
+        if (rank == 0) {
+            const uint32_t id_s = lat_instr(BF16, kLatKeys, false);
+            const uint64_t q_desc = lat_desc(sbase, 16), k_desc = lat_desc(sbase + kLatOffK, 16), t_desc = lat_desc(sbase + kLatOffTail, 16);
+            const uint64_t v_desc = lat_desc(sbase + kLatOffK, kLatPiece);
+            constexpr uint64_t kPieceStep = kLatPiece / 16, kStageStep = kLatSlots * kPieceStep;
+            // S goes through the share's tiles, U += P V after it, each over the parts on its own
+            LatWalk qk(p, ctl, f0, f1);
+            int cq = 0, cp = 0, jq = 0, jp = 0, part_q = 0, part_p = 0, half_q = 0;
+            auto next_part = [](LatWalk& w, int& j) {
+                while (w.next()) {
+                    j = w.lo;
+                    if (w.hi > w.lo) return true;
+                }
+                return false;
+            };
+            auto ready = [](uint32_t bar, int parity) { return __all_sync(0xffffffffu, test_cluster(bar, parity)); };
+            bool q_left = next_part(qk, jq), p_left = next_part(walk, jp);
+            uint64_t since = ptx::globaltimer();
+            int idle = 0;
+            while (p_left) {
+                bool did = false;
+                // S(cq), in halves as its keys arrive (its columns were read before the weights of tile cq - 2 were handed over)
+                if (q_left && cq <= cp + 1 && ready(b_kf + 16 * (cq & 1) + 8 * half_q, (cq >> 1) & 1) &&
+                    (half_q == 1 || jq != qk.lo || ready(b_qf, part_q & 1))) {
+                    ptx::tc_fence_after_sync();
+                    const uint64_t kd = k_desc + (cq & 1) * kStageStep;
+                    const int end = min(kp, 4 * half_q + 4);
+                    for (int i = 4 * half_q; i < end; ++i)
+                        mma_pair_k64(tmem + 256 + 64 * (cq & 1), q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, i > 0);
+                    if (half_q == 0) {
+                        if (kp > 4) commit_pair(b_sh + 8 * (cq & 1));
+                        half_q = 1;
+                    } else {
+                        if (tail) mma_pair_k64(tmem + 256 + 64 * (cq & 1), q_desc + kLatSlots * kPieceStep, t_desc, id_s, 1u);
+                        commit_pair(b_sf + 8 * (cq & 1));
+                        half_q = 0;
+                        ++cq;
+                        if (++jq == qk.hi) {
+                            commit_pair(b_qe);
+                            ++part_q;
+                            q_left = next_part(qk, jq);
+                        }
+                    }
+                    __syncwarp();
+                    did = true;
+                }
+                if (cp < cq && ready(b_pf + 8 * (cp & 1), (cp >> 1) & 1) && (jp != walk.lo || part_p == 0 || ready(b_oe, (part_p - 1) & 1))) {
+                    ptx::tc_fence_after_sync();
+                    const uint64_t vd = v_desc + (cp & 1) * kStageStep;
+                    const uint32_t more = jp > walk.lo;
+                    for (int b = 0; b < 2; ++b) {
+                        if (b * 256 < p.C) {
+                            const int wide = p.C - 256 * b > 128 ? 2 : 1;
+                            const uint32_t id = lat_instr(BF16, 128 * wide, true);
+                            const uint64_t vb = vd + 4 * b * kPieceStep;
+                            const uint32_t weights = tmem + 384 + 64 * (cp & 1);
+                            mma_pair_ts_k64(tmem + 128 * b, weights, vb, id, more);
+                            mma_pair_ts_k64(tmem + 128 * b, weights + 32, vb + wide * kPieceStep, id, 1u);
+                        }
+                        commit_pair(b_ke + 16 * (cp & 1) + 8 * b);
+                    }
+                    commit_pair(b_pv + 8 * (cp & 1));
+                    ++cp;
+                    if (++jp == walk.hi) {
+                        ++part_p;
+                        p_left = next_part(walk, jp);
+                    }
+                    __syncwarp();
+                    did = true;
+                }
+                if (did) {
+                    idle = 0;
+                    since = ptx::globaltimer();
+                } else if ((++idle & 1023) == 0 && __any_sync(0xffffffffu, ptx::globaltimer() - since > kTimeoutNs)) {
+                    report(kTimeout);
+                    break;
+                }
+            }
+            __syncwarp();
+            asm volatile(
+                "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(b_drain)
+                : "memory");
+            __syncwarp();
+            wait_warp(b_drain, 0);
+        }
         __syncwarp();
-        wait_warp(b_drain, 0);
     } else {
         // ============================================================ queries
-        const int t = tid - 192;
+        const uint32_t r_qf = in_first_cta(b_qf);
+        const int t = tid - 224;
         int parts = 0;
         while (walk.next()) {
             if (walk.hi == walk.lo) continue;
+            if (p.q_box && warp == 8) break;  // (one warp's boxes)
             if (parts > 0 && !wait_warp(b_qe, (parts - 1) & 1)) break;
-            const int ch = (t & 7) * 8;
-#pragma unroll 1
-            for (int row = t >> 3; row < kLatRows; row += 8) {
-                const int r = walk.r0 + row;
-                const bool mine = row < walk.rows;
-                const uint16_t* src = p.q + static_cast<long long>(walk.rq.q0 + (mine ? r / p.H : 0)) * p.q_st +
-                                      static_cast<long long>(mine ? r % p.H : 0) * p.q_sh + ch;
-                const uint32_t dst = sbase + row * 128 + (((t & 7) ^ (row & 7)) << 4);
-                for (int i = 0; i < kp; ++i) {
-                    const bool there = mine && 64 * i + ch < p.W;
-                    cp_async16(dst + i * kLatPiece, there ? src + 64 * i : p.q, there);
+            const int here = max(0, min(64, walk.rows - rank * 64));  // rows
+            if (p.q_box) {
+                // rows behind the last one are left as they are: no other row's result takes from them
+                const int boxes = (here + p.q_box - 1) / p.q_box;     // (whole boxes: H is a multiple of q_box)
+                if (lane == 0) arrive_remote_expect(r_qf, boxes * kp * p.q_box * 128);
+                __syncwarp();
+                for (int i = lane; i < boxes * kp; i += 32) {
+                    const int piece = i / boxes, box = i - piece * boxes, r = walk.r0 + rank * 64 + box * p.q_box;
+                    tma_load_3d_pair(sbase + piece * kLatPiece + box * p.q_box * 128, &tm_q, r_qf, 64 * piece, r % p.H, walk.rq.q0 + r / p.H);
                 }
+                __syncwarp();
+            } else {
+                const int ch = (t & 7) * 8;
+#pragma unroll 1
+                for (int row = t >> 3; row < 64; row += 8) {
+                    const int r = walk.r0 + rank * 64 + row;
+                    const bool mine = row < here;
+                    const uint16_t* src = p.q + static_cast<long long>(walk.rq.q0 + (mine ? r / p.H : 0)) * p.q_st +
+                                          static_cast<long long>(mine ? r % p.H : 0) * p.q_sh + ch;
+                    const uint32_t dst = sbase + row * 128 + (((t & 7) ^ (row & 7)) << 4);
+                    for (int i = 0; i < kp; ++i) {
+                        const bool there = mine && 64 * i + ch < p.W;
+                        cp_async16(dst + i * kLatPiece, there ? src + 64 * i : p.q, there);
+                    }
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                ptx::fence_proxy_async_smem();
+                arrive_remote_release(r_qf);
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(b_qf);
             ++parts;
         }
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
+    cluster_sync();  // neither CTA's memory is written or read by the other any more
     if (warp == 5) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, 512);
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
 }
 
-// The parts of the units that shares cut: a warp per row.  CTA (x, y): boundary between shares x and x + 1, member of
-// the group and rows.  O = sum_s w_s O_s / sum_s w_s with w_s the sum of a part's rounded weights (its O_s is divided
-// by that), LSE from the sums of the fp32 weights.
+// The parts of the units that shares cut.  CTA (x, y): boundary between shares x and x + 1, and eight rows x 128 channels, a
+// warp for each (a row's parts are read 8 at a time, so that a request of few tiles that many pairs share is joined
+// in a few round trips).  O = sum_s w_s O_s / sum_s w_s with w_s the sum of a part's rounded weights (its O_s is divided by
+// that), LSE from the sums of the fp32 weights.
 constexpr int kLatJoinThreads = 256;
+constexpr int kLatJoinRows = kLatJoinThreads / 32;
 template <bool BF16>
 __global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const LatentParams p) {
     dependents_may_start();
     wait_for_previous();
-    const int groups = static_cast<int>(gridDim.x) + 1, i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int pairs = static_cast<int>(gridDim.x) + 1, i = blockIdx.x + 1, lane = threadIdx.x & 31;
     const int4 unit = ld(p.shares + i);
-    const int share = ld(p.shares + groups).x;
+    const int share = ld(p.shares + pairs).x;
     const long long at = static_cast<long long>(i) * share;
     if (unit.x >= at || unit.y <= at || at - share > unit.x) return;  // not inside a unit, or not the first boundary inside
     // part of share i - 1 (its first unit or its last), then the first ones of the shares that begin inside
-    const int parts = 1 + static_cast<int>(min(static_cast<long long>(groups - i), (unit.y - at + share - 1) / share));
-    constexpr int kBlocks = kLatRows / (kLatJoinThreads / 32);
-    const int member = blockIdx.y / kBlocks;
-    const int row = (blockIdx.y - member * kBlocks) * (kLatJoinThreads / 32) + (threadIdx.x >> 5);
+    const int parts = 1 + static_cast<int>(min(static_cast<long long>(pairs - i), (unit.y - at + share - 1) / share));
+    const int slice = blockIdx.y / (kLatRows / kLatJoinRows);
+    const int row = (blockIdx.y - slice * (kLatRows / kLatJoinRows)) * kLatJoinRows + (threadIdx.x >> 5);
     const int head_slot = unit.x == at - share ? 0 : 1;
-    auto slot = [&](int j) {
-        return ((static_cast<long long>(i - 1 + j) * p.members + member) * 2 + (j == 0 ? head_slot : 0)) * kLatRows + row;
-    };
+    auto slot = [&](int j) { return (static_cast<long long>(i - 1 + j) * 2 + (j == 0 ? head_slot : 0)) * kLatRows + row; };
     bool bad = false;
     const LatRequest rq = lat_request(p, unit.z, bad);
-    const int r = (unit.w * p.members + member) * kLatRows + row;
+    const int r = unit.w * kLatRows + row;
     if (r >= rq.nq * p.H) return;
-    const int tok = rq.q0 + r / p.H, head = r % p.H;
-    uint16_t* dst = p.o + static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh;
-    for (int c0 = 0; c0 < p.C; c0 += 256) {
-        const int c = c0 + lane * 8;
-        float top = -INFINITY, rtop = -INFINITY, l = 0.f, rl = 0.f;
-        float o[8] = {};
-        for (int j0 = 0; j0 < parts; j0 += 32) {
-            float2 a = make_float2(-INFINITY, -INFINITY);
-            if (j0 + lane < parts) a = ld(p.stats + slot(j0 + lane));
-            float next = fmaxf(a.x, top), rnext = fmaxf(a.y, rtop);
+    const int tok = rq.q0 + r / p.H, head = r % p.H, c = 128 * slice + lane * 4;
+    float top = -INFINITY, rtop = -INFINITY, l = 0.f, rl = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < parts; j0 += 32) {
+        float2 a = make_float2(-INFINITY, -INFINITY);
+        if (j0 + lane < parts) a = ld(p.stats + slot(j0 + lane));
+        float next = fmaxf(a.x, top), rnext = fmaxf(a.y, rtop);
 #pragma unroll
-            for (int x = 16; x; x >>= 1) {
-                next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, x));
-                rnext = fmaxf(rnext, __shfl_xor_sync(0xffffffffu, rnext, x));
-            }
-            const float ref = next == -INFINITY ? 0.f : next, rref = rnext == -INFINITY ? 0.f : rnext;
-            const float old = ptx::ex2_approx(rtop - rref);
-            float sum = ptx::ex2_approx(a.x - ref);
-            const float w = ptx::ex2_approx(a.y - rref);
-            float rsum = w;
-#pragma unroll
-            for (int x = 16; x; x >>= 1) {
-                sum += __shfl_xor_sync(0xffffffffu, sum, x);
-                rsum += __shfl_xor_sync(0xffffffffu, rsum, x);
-            }
-            l = fmaf(l, ptx::ex2_approx(top - ref), sum);
-            rl = fmaf(rl, old, rsum);
-            top = next, rtop = rnext;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[e] *= old;
-            const int n = min(32, parts - j0);
-#pragma unroll 4
-            for (int j = 0; j < n; ++j) {
-                const float wj = __shfl_sync(0xffffffffu, w, j);
-                if (wj == 0.f || c >= p.C) continue;  // (a part without a key wrote no O)
-                const float4* src = reinterpret_cast<const float4*>(p.o_part + slot(j0 + j) * p.C + c);
-                const float4 u = ld(src), v = ld(src + 1);
-                o[0] = fmaf(u.x, wj, o[0]), o[1] = fmaf(u.y, wj, o[1]), o[2] = fmaf(u.z, wj, o[2]), o[3] = fmaf(u.w, wj, o[3]);
-                o[4] = fmaf(v.x, wj, o[4]), o[5] = fmaf(v.y, wj, o[5]), o[6] = fmaf(v.z, wj, o[6]), o[7] = fmaf(v.w, wj, o[7]);
-            }
+        for (int x = 16; x; x >>= 1) {
+            next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, x));
+            rnext = fmaxf(rnext, __shfl_xor_sync(0xffffffffu, rnext, x));
         }
-        const float inv = rl != 0.f ? 1.f / rl : 0.f;
-        if (c < p.C)
-            *reinterpret_cast<uint4*>(dst + c) = make_uint4(pack16(o[0] * inv, o[1] * inv, BF16), pack16(o[2] * inv, o[3] * inv, BF16),
-                                                            pack16(o[4] * inv, o[5] * inv, BF16), pack16(o[6] * inv, o[7] * inv, BF16));
-        if (c == 0) p.lse[static_cast<long long>(tok) * p.H + head] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        const float ref = next == -INFINITY ? 0.f : next, rref = rnext == -INFINITY ? 0.f : rnext;
+        const float old = ptx::ex2_approx(rtop - rref);
+        float sum = ptx::ex2_approx(a.x - ref);
+        const float w = ptx::ex2_approx(a.y - rref);
+        float rsum = w;
+#pragma unroll
+        for (int x = 16; x; x >>= 1) {
+            sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            rsum += __shfl_xor_sync(0xffffffffu, rsum, x);
+        }
+        l = fmaf(l, ptx::ex2_approx(top - ref), sum);
+        rl = fmaf(rl, old, rsum);
+        top = next, rtop = rnext;
+        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
+        const int n = min(32, parts - j0);
+        for (int j = 0; j < n; j += 8) {
+            float4 v[8];
+            float wj[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                wj[e] = j + e < n ? __shfl_sync(0xffffffffu, w, (j + e) & 31) : 0.f;
+                v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                // (a part without a key wrote no O)
+                if (wj[e] != 0.f && c < p.C) v[e] = ld(reinterpret_cast<const float4*>(p.o_part + slot(j0 + j + e) * p.C + c));
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                o.x = fmaf(v[e].x, wj[e], o.x), o.y = fmaf(v[e].y, wj[e], o.y), o.z = fmaf(v[e].z, wj[e], o.z), o.w = fmaf(v[e].w, wj[e], o.w);
+        }
     }
+    const float inv = rl != 0.f ? 1.f / rl : 0.f;
+    if (c < p.C)
+        *reinterpret_cast<uint2*>(p.o + static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh + c) =
+            make_uint2(pack16(o.x * inv, o.y * inv, BF16), pack16(o.z * inv, o.w * inv, BF16));
+    if (c == 0) p.lse[static_cast<long long>(tok) * p.H + head] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
 }
 
 }  // namespace paged
