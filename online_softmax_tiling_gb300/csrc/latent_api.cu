@@ -83,10 +83,12 @@ LatentPlan latent_plan(const fa_latent_paged_args& a) {
     return pl;
 }
 size_t round256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+size_t part_bytes(const fa_latent_paged_args& a, const LatentPlan& pl) {
+    return static_cast<size_t>(pg::lat_part(2ll * pl.pairs, 0, 0, 0, a.cache.value_dim)) * 16;
+}
 size_t latent_workspace(const fa_latent_paged_args& a, const LatentPlan& pl) {
     if (pl.pairs < 2) return 0;
-    const size_t rows = 2ull * pl.pairs * pg::kLatRows;
-    return round256(rows * a.cache.value_dim * 4) + round256(rows * 8) + (static_cast<size_t>(pl.pairs) + 1) * 16;
+    return part_bytes(a, pl) + round256(2ull * pl.pairs * pg::kLatRows * 8) + (static_cast<size_t>(pl.pairs) + 1) * 16;
 }
 
 int check_latent_paged(const fa_latent_paged_args& a) {
@@ -231,6 +233,7 @@ int fa_latent_paged_fwd(const fa_latent_paged_args* args) {
     pg::LatentParams p = {};
     p.q = static_cast<const uint16_t*>(a.q), p.o = static_cast<uint16_t*>(a.o), p.lse = a.lse;
     p.cu_q = a.cu_q, p.table = a.block_table, p.lens = a.lens;
+    p.cache = static_cast<const uint16_t*>(a.cache.rows);
     p.q_st = a.q_stride[0], p.q_sh = a.q_stride[1], p.o_st = a.o_stride[0], p.o_sh = a.o_stride[1];
     p.T = a.T, p.B = a.B, p.H = a.H, p.C = a.cache.value_dim, p.W = a.cache.value_dim + a.cache.rope_dim;
     p.max_q = a.max_q, p.max_pages = a.max_pages, p.num_pages = a.cache.num_pages, p.page_shift = shift_of(a.cache.page_size);
@@ -240,11 +243,10 @@ int fa_latent_paged_fwd(const fa_latent_paged_args* args) {
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     if (need > 0) {
         char* ws = static_cast<char*>(a.workspace);
-        const size_t rows = 2ull * pl.pairs * pg::kLatRows;
-        p.o_part = reinterpret_cast<float*>(ws);
-        ws += round256(rows * p.C * 4);
+        p.o_part = reinterpret_cast<float4*>(ws);
+        ws += part_bytes(a, pl);
         p.stats = reinterpret_cast<float2*>(ws);
-        p.shares = reinterpret_cast<int4*>(ws + round256(rows * 8));
+        p.shares = reinterpret_cast<int4*>(ws + round256(2ull * pl.pairs * pg::kLatRows * 8));
     } else {
         p.min_share = INT32_MAX;  // one pair: all of it
     }
@@ -260,9 +262,16 @@ int fa_latent_paged_fwd(const fa_latent_paged_args* args) {
     if (!ensure_smem(fn, pg::kLatSmem, device) || !launch(fn, 2ll * pl.pairs, 1, pg::kLatThreads, pg::kLatSmem, 2, a.stream, kargs))
         return FA_ERR_CUDA;
     if (need > 0) {
-        const void* join = bf16 ? reinterpret_cast<const void*>(&pg::latent_join_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_join_kernel<false>);
+        // units cut into eight parts and more: a CTA per job of the join
+        const int64_t units = a.B * ((static_cast<int64_t>(a.max_q) * a.H + pg::kLatRows - 1) / pg::kLatRows);
+        const bool split = 8 * units <= pl.pairs;
+        const int jobs = 8 * pg::lat_chunks(p.C);
+        const void* join = split ? (bf16 ? reinterpret_cast<const void*>(&pg::latent_join_kernel<true, true>)
+                                         : reinterpret_cast<const void*>(&pg::latent_join_kernel<false, true>))
+                                 : (bf16 ? reinterpret_cast<const void*>(&pg::latent_join_kernel<true, false>)
+                                         : reinterpret_cast<const void*>(&pg::latent_join_kernel<false, false>));
         void* jargs[] = {&p};
-        if (!launch(join, pl.pairs - 1, pg::kLatRows / pg::kLatJoinRows * ((p.C + 127) / 128), pg::kLatJoinThreads, 0, 1, a.stream, jargs))
+        if (!launch(join, pl.pairs - 1, split ? jobs : jobs / pg::kLatJoinWarps, 32 * pg::kLatJoinWarps, 0, 1, a.stream, jargs))
             return FA_ERR_CUDA;
     }
     return FA_OK;

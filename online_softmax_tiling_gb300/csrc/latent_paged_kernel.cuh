@@ -63,6 +63,7 @@ struct LatentParams {
     const int* cu_q;
     const int* table;
     const int* lens;
+    const uint16_t* cache;
     long long q_st, q_sh, o_st, o_sh;
     int T, B, H, C, W, max_q, max_pages, num_pages, page_shift;
     int min_share;    // tiles
@@ -70,17 +71,35 @@ struct LatentParams {
     int box_rows;
     int causal;
     float scale_log2;
-    float* o_part;    // [2 pairs][128][C]: the parts of a share's first and last unit
+    float4* o_part;   // the parts of a share's first and last unit: [2 pairs][CTA][warp][32 channels][quad][lane], as lat_part says
     float2* stats;    // [2 pairs][128]: log2 of the sums of the fp32 and of the rounded weights
     int4* shares;     // [pairs + 1]: first unit's begin, end, request, row block; behind the last: the share
 };
+
+// Rows and keys of request b, and its units: blocks of 128 rows times tiles of keys (at least one).
+struct LatRequest {
+    int q0, nq, len, blocks, tiles;
+};
+// 32-channel pieces of U that a softmax warp holds: columns of tensor memory over 32.
+__host__ __device__ constexpr int lat_chunks(int C) { return C <= 128 ? 2 : C <= 256 ? 4 : C <= 384 ? 6 : 8; }
+// A part in the workspace: a warp's quads of channels lie as its lanes hold them, so that they are written and read 512 bytes at
+// a time.
+__host__ __device__ constexpr long long lat_part(long long part, int rank, int warp, int chunk, int C) {
+    return (((part * 2 + rank) * 4 + warp) * lat_chunks(C) + chunk) * 8 * 32;
+}
+// Output channel of column 32 `chunk` of a warp with key half (here: channel half) `half`.
+__host__ __device__ constexpr int lat_channel(int chunk, int half, int C) {
+    const int block = chunk >> 2, wide = C - 256 * block > 128 ? 128 : 64;
+    return 256 * block + half * wide + 32 * (chunk & 3);
+}
 
 struct LatCtl {
     // signalled in the first CTA by both: queries, keys, weights, U read; in both by the tensor core, or by the CTA's own loads
     uint64_t q_full, k_full[4], p_full[2], o_empty;                            // k: by stage and half of its pieces
     uint64_t q_empty, k_empty[4], s_half[2], s_full[2], pv_done[2], v_full[2], drain;
     uint32_t tmem_base;
-    int start[4];                // request, row block, tile of the share's first unit; tiles of that unit
+    int start[3];                // request, row block, tile of the share's first unit
+    LatRequest first;            // that request
     float top[2][2][64];         // by tile parity, key half, row
 };
 static_assert(kLatOffCtl + sizeof(LatCtl) + 1024 <= 232448, "shared memory of a CTA");
@@ -194,10 +213,7 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
-// Rows and keys of request b, and its units: blocks of 128 rows times tiles of keys (at least one).
-struct LatRequest {
-    int q0, nq, len, blocks, tiles;
-};
+// Device data that cannot be leaves a request without rows or keys.
 __device__ __forceinline__ LatRequest lat_request(const LatentParams& p, int b, bool& bad) {
     LatRequest r;
     r.q0 = b, r.nq = 1;
@@ -224,10 +240,7 @@ struct LatWalk {
     bool whole, at_start;
 
     __device__ LatWalk(const LatentParams& p_, const LatCtl* ctl, int f0_, int f1_)
-        : p(p_), f0(f0_), f1(f1_), f(f0_), b(ctl->start[0]), block(ctl->start[1]), first(ctl->start[2]) {
-        bool bad = false;
-        if (f < f1) rq = lat_request(p, b, bad);
-    }
+        : p(p_), f0(f0_), f1(f1_), f(f0_), b(ctl->start[0]), block(ctl->start[1]), first(ctl->start[2]), rq(ctl->first) {}
     __device__ int limit(int r) const { return p.causal ? min(rq.len, rq.len - rq.nq + r / p.H + 1) : rq.len; }
     // the next part; false behind the last
     __device__ bool next() {
@@ -267,6 +280,14 @@ struct LatPages {
     __device__ int key(int j, int lane) const { return j * kLatKeys + half * 64 + lane * p.box_rows; }
     __device__ bool wanted(int j, int lane) const { return j < w.hi && lane * p.box_rows < 64 && key(j, lane) < w.load_end; }
     __device__ int at(int j, int lane) const { return wanted(j, lane) ? ld_meta(trow + (key(j, lane) >> p.page_shift)) : -1; }
+    // Has the lane's box of tile j + 2 brought to L2 (a page's rows lie together): one tile is all that fits in shared
+    // memory ahead of the one in work, and its load is to take no longer than from there.
+    __device__ void prefetch(int j, int lane) const {
+        if (static_cast<unsigned>(page2) >= static_cast<unsigned>(p.num_pages)) return;
+        const int place = key(j + 2, lane) & ((1 << p.page_shift) - 1);
+        const uint16_t* from = p.cache + (static_cast<long long>(page2) << p.page_shift) * p.W + static_cast<long long>(place) * p.W;
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(p.box_rows * p.W * 2) : "memory");
+    }
     // First row of the lane's box of tile j in the cache (-1: not read); moves on to tile j + 1.
     __device__ int take(int j, int lane) {
         const int ahead = at(j + 3, lane);
@@ -331,8 +352,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         const int per = (p.B + kLatThreads - 1) / kLatThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
         bool bad = false;
         int own = 0;
+        LatRequest r = {};
         for (int b = b0; b < b1; ++b) {
-            const LatRequest r = lat_request(p, b, bad);
+            r = lat_request(p, b, bad);
             own += r.blocks * r.tiles;
         }
         if (bad) report(kBadData);
@@ -354,11 +376,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         f1 = static_cast<int>(min(static_cast<long long>(f0) + share, static_cast<long long>(all)));
         if (f0 < f1 && run <= f0 && f0 < run + own) {
             for (int b = b0; b < b1; ++b) {
-                const LatRequest r = lat_request(p, b, bad);
+                if (per > 1) r = lat_request(p, b, bad);
                 const int n = r.blocks * r.tiles;
                 if (f0 < run + n) {
                     const int rel = f0 - run;
-                    ctl->start[0] = b, ctl->start[1] = rel / r.tiles, ctl->start[2] = rel % r.tiles, ctl->start[3] = r.tiles;
+                    ctl->start[0] = b, ctl->start[1] = rel / r.tiles, ctl->start[2] = rel % r.tiles, ctl->first = r;
                     break;
                 }
                 run += n;
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         ptx::tc_fence_after_sync();
         if (p.shares && rank == 0 && tid == 0) {
             int4 u = make_int4(f0, f0, 0, 0);
-            if (f0 < f1) u = make_int4(f0 - ctl->start[2], f0 - ctl->start[2] + ctl->start[3], ctl->start[0], ctl->start[1]);
+            if (f0 < f1) u = make_int4(f0 - ctl->start[2], f0 - ctl->start[2] + ctl->first.tiles, ctl->start[0], ctl->start[1]);
             p.shares[pair] = u;
             if (pair == 0) p.shares[pairs] = make_int4(share, 0, 0, 0);
         }
@@ -522,66 +544,64 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             const float inv = rsum != 0.f ? 1.f / rsum : 0.f;
             const float lse2 = sum != 0.f ? ref - kLatShift + log2f(sum) : -INFINITY;
             const int tok = walk.rq.q0 + r / p.H, head = r % p.H;
-            const long long part = (static_cast<long long>(pair) * 2 + (walk.at_start ? 0 : 1)) * kLatRows + rank * 64 + row;
-            // Stores of a row per thread would touch 32 lines each; through the warp's exchange memory eight lanes write 128
-            // bytes of a row.
-            const long long at = !mine ? -1
-                                 : walk.whole ? static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh : part * p.C;
-            if (any || walk.whole) {
-                for (int b = 0; b * 256 < p.C; ++b) {
-                    const int wide = p.C - 256 * b > 128 ? 128 : 64;
-#pragma unroll 1
-                    for (int x = 0; x < wide; x += 32) {
+            const long long part = static_cast<long long>(pair) * 2 + (walk.at_start ? 0 : 1);
+            auto u_chunk = [&](int x, uint32_t(&ov)[32]) {  // columns 32 x .. of U over the sum
+                if (any) {
+                    ptx::tmem_ld_32x32b_x32(tmem + lane_off + 32 * x, ov);
+                    ptx::tmem_wait_ld();
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    if (any) ptx::reg_fence(ov[e]); else ov[e] = 0;
+                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv);
+                }
+            };
+            if (walk.whole) {
+                // Stores of a row per thread would touch 32 lines each; through the warp's exchange memory eight lanes write
+                // 128 bytes of a row.
+                const long long at = mine ? static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh : -1;
+                for (int x = 0; x < lat_chunks(p.C); x += 2) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
                         uint32_t ov[32];
-                        if (any) {
-                            ptx::tmem_ld_32x32b_x32(tmem + lane_off + 128 * b + x, ov);
-                            ptx::tmem_wait_ld();
-                        }
+                        u_chunk(x + h, ov);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (any) ptx::reg_fence(ov[e]); else ov[e] = 0;
-                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv);
-                        }
-                        const int d0 = 256 * b + half * wide + x;
-                        if (walk.whole) {  // 32 channels in 64 bytes, two passes to a box
-                            const int c0 = (x & 32) >> 3;
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t w[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) w[i] = pack16(__uint_as_float(ov[8 * e + 2 * i]), __uint_as_float(ov[8 * e + 2 * i + 1]), BF16);
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + (((c0 + e) ^ (lane & 7)) << 4)), "r"(w[0]), "r"(w[1]),
-                                             "r"(w[2]), "r"(w[3])
-                                             : "memory");
-                            }
-                            if (!(x & 32)) continue;
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + ((e ^ (lane & 7)) << 4)), "r"(ov[4 * e]),
-                                             "r"(ov[4 * e + 1]), "r"(ov[4 * e + 2]), "r"(ov[4 * e + 3])
-                                             : "memory");
-                        }
-                        __syncwarp();
-                        const int ch = walk.whole ? d0 - 32 + (lane & 7) * 8 : d0 + (lane & 7) * 4;
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int y = 4 * i + (lane >> 3);  // row of the box
-                            const long long to = __shfl_sync(0xffffffffu, at, y);
-                            uint4 v;
-                            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                         : "r"(box + y * 128 + (((lane & 7) ^ (y & 7)) << 4))
+                            for (int i = 0; i < 4; ++i) w[i] = pack16(__uint_as_float(ov[8 * e + 2 * i]), __uint_as_float(ov[8 * e + 2 * i + 1]), BF16);
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(own + (((4 * h + e) ^ (lane & 7)) << 4)), "r"(w[0]),
+                                         "r"(w[1]), "r"(w[2]), "r"(w[3])
                                          : "memory");
-                            if (to >= 0 && ch < p.C) {
-                                if (walk.whole)
-                                    *reinterpret_cast<uint4*>(p.o + to + ch) = v;
-                                else
-                                    *reinterpret_cast<uint4*>(p.o_part + to + ch) = v;
-                            }
                         }
-                        __syncwarp();
                     }
+                    __syncwarp();
+                    const int ch = lat_channel(x, half, p.C) + (lane & 7) * 8;
+                    uint4 v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int y = 4 * i + (lane >> 3);  // row of the box
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                                     : "r"(box + y * 128 + (((lane & 7) ^ (y & 7)) << 4))
+                                     : "memory");
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const long long to = __shfl_sync(0xffffffffu, at, 4 * i + (lane >> 3));
+                        if (to >= 0 && ch < p.C) *reinterpret_cast<uint4*>(p.o + to + ch) = v[i];
+                    }
+                    __syncwarp();
+                }
+            } else if (any) {
+                for (int x = 0; x < lat_chunks(p.C); ++x) {
+                    uint32_t ov[32];
+                    u_chunk(x, ov);
+                    float4* dst = p.o_part + lat_part(part, rank, warp, x, p.C) + lane;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dst[32 * e] = make_float4(__uint_as_float(ov[4 * e]), __uint_as_float(ov[4 * e + 1]), __uint_as_float(ov[4 * e + 2]),
+                                                  __uint_as_float(ov[4 * e + 3]));
                 }
             }
             if (any) {
@@ -593,7 +613,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 if (walk.whole)
                     p.lse[static_cast<long long>(tok) * p.H + head] = lse2 * 0.69314718055994531f;
                 else
-                    p.stats[part] = make_float2(lse2, rsum != 0.f ? ref - kLatShift + log2f(rsum) : -INFINITY);
+                    p.stats[part * kLatRows + rank * 64 + row] = make_float2(lse2, rsum != 0.f ? ref - kLatShift + log2f(rsum) : -INFINITY);
             }
         }
     } else if (warp == 4) {
@@ -604,6 +624,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         while (ok && walk.next()) {
             LatPages pages(p, walk, rank, lane);
             for (int j = walk.lo; ok && j < walk.hi; ++j, ++c) {
+                pages.prefetch(j, lane);
                 const int s = c & 1, row = pages.take(j, lane);
                 const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
                 const uint32_t dst = sbase + kLatOffK + s * (kLatSlots * kLatPiece) + lane * p.box_rows * 128;
@@ -828,78 +849,105 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     }
 }
 
-// The parts of the units that shares cut.  CTA (x, y): boundary between shares x and x + 1, and eight rows x 128 channels, a
-// warp for each (a row's parts are read 8 at a time, so that a request of few tiles that many pairs share is joined
-// in a few round trips).  O = sum_s w_s O_s / sum_s w_s with w_s the sum of a part's rounded weights (its O_s is divided by
-// that), LSE from the sums of the fp32 weights.
-constexpr int kLatJoinThreads = 256;
-constexpr int kLatJoinRows = kLatJoinThreads / 32;
-template <bool BF16>
-__global__ void __launch_bounds__(kLatJoinThreads) latent_join_kernel(const LatentParams p) {
+// The parts of the units that shares cut.  A job is what a softmax warp of a unit held of 32 channels: its lanes' rows, from
+// each part.  CTA (x, y): boundary between shares x and x + 1, and eight jobs, a warp each; where few units are cut into
+// many parts (SPLIT) one job, whose parts the CTA's warps take in turn and join in shared memory.
+// O = sum_s w_s O_s / sum_s w_s with w_s the sum of a part's rounded weights (its O_s is divided by that), LSE from the
+// sums of the fp32 weights.
+constexpr int kLatJoinWarps = 8;
+template <bool BF16, bool SPLIT>
+__global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const LatentParams p) {
+    constexpr int STEP = SPLIT ? kLatJoinWarps : 1;
     dependents_may_start();
     wait_for_previous();
-    const int pairs = static_cast<int>(gridDim.x) + 1, i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int pairs = static_cast<int>(gridDim.x) + 1, i = blockIdx.x + 1, lane = threadIdx.x & 31, w0 = threadIdx.x >> 5;
     const int4 unit = ld(p.shares + i);
     const int share = ld(p.shares + pairs).x;
     const long long at = static_cast<long long>(i) * share;
     if (unit.x >= at || unit.y <= at || at - share > unit.x) return;  // not inside a unit, or not the first boundary inside
     // part of share i - 1 (its first unit or its last), then the first ones of the shares that begin inside
     const int parts = 1 + static_cast<int>(min(static_cast<long long>(pairs - i), (unit.y - at + share - 1) / share));
-    const int slice = blockIdx.y / (kLatRows / kLatJoinRows);
-    const int row = (blockIdx.y - slice * (kLatRows / kLatJoinRows)) * kLatJoinRows + (threadIdx.x >> 5);
-    const int head_slot = unit.x == at - share ? 0 : 1;
-    auto slot = [&](int j) { return (static_cast<long long>(i - 1 + j) * 2 + (j == 0 ? head_slot : 0)) * kLatRows + row; };
+    const int chunks = lat_chunks(p.C), job = SPLIT ? blockIdx.y : blockIdx.y * kLatJoinWarps + w0;
+    const int chunk = job % chunks, warp = job / chunks & 3, rank = job / (4 * chunks);
+    const int head_slot = unit.x == at - share ? 0 : 1, row = rank * 64 + (warp & 1) * 32 + lane;
+    auto part_of = [&](int j) { return static_cast<long long>(i - 1 + j) * 2 + (j == 0 ? head_slot : 0); };
     bool bad = false;
     const LatRequest rq = lat_request(p, unit.z, bad);
     const int r = unit.w * kLatRows + row;
-    if (r >= rq.nq * p.H) return;
-    const int tok = rq.q0 + r / p.H, head = r % p.H, c = 128 * slice + lane * 4;
+    const bool mine = r < rq.nq * p.H;
+    if (unit.w * kLatRows + rank * 64 + (warp & 1) * 32 >= rq.nq * p.H) return;  // (the whole CTA's, or a warp's own)
+    auto stats_of = [&](int j) {
+        return mine && j < parts ? ld(p.stats + part_of(j) * kLatRows + row) : make_float2(-INFINITY, -INFINITY);
+    };
     float top = -INFINITY, rtop = -INFINITY, l = 0.f, rl = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < parts; j0 += 32) {
-        float2 a = make_float2(-INFINITY, -INFINITY);
-        if (j0 + lane < parts) a = ld(p.stats + slot(j0 + lane));
-        float next = fmaxf(a.x, top), rnext = fmaxf(a.y, rtop);
+    const int first = SPLIT ? w0 : 0;
+#pragma unroll 8
+    for (int j = first; j < parts; j += STEP) {
+        const float2 a = stats_of(j);
+        top = fmaxf(top, a.x), rtop = fmaxf(rtop, a.y);
+    }
+    const float ref = top == -INFINITY ? 0.f : top, rref = rtop == -INFINITY ? 0.f : rtop;
+    float o[32] = {};
+    for (int j0 = first; j0 < parts; j0 += 2 * STEP) {
+        float4 v[2][8];
 #pragma unroll
-        for (int x = 16; x; x >>= 1) {
-            next = fmaxf(next, __shfl_xor_sync(0xffffffffu, next, x));
-            rnext = fmaxf(rnext, __shfl_xor_sync(0xffffffffu, rnext, x));
-        }
-        const float ref = next == -INFINITY ? 0.f : next, rref = rnext == -INFINITY ? 0.f : rnext;
-        const float old = ptx::ex2_approx(rtop - rref);
-        float sum = ptx::ex2_approx(a.x - ref);
-        const float w = ptx::ex2_approx(a.y - rref);
-        float rsum = w;
+        for (int j = 0; j < 2; ++j) {
+            const float4* src = p.o_part + lat_part(part_of(min(j0 + j * STEP, parts - 1)), rank, warp, chunk, p.C) + lane;
 #pragma unroll
-        for (int x = 16; x; x >>= 1) {
-            sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            rsum += __shfl_xor_sync(0xffffffffu, rsum, x);
+            for (int e = 0; e < 8; ++e) v[j][e] = ld(src + 32 * e);
         }
-        l = fmaf(l, ptx::ex2_approx(top - ref), sum);
-        rl = fmaf(rl, old, rsum);
-        top = next, rtop = rnext;
-        o.x *= old, o.y *= old, o.z *= old, o.w *= old;
-        const int n = min(32, parts - j0);
-        for (int j = 0; j < n; j += 8) {
-            float4 v[8];
-            float wj[8];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float2 a = stats_of(j0 + j * STEP);
+            const float w = ptx::ex2_approx(a.y - rref);
+            l += ptx::ex2_approx(a.x - ref), rl += w;
+            const bool use = w != 0.f;  // (a part without a key wrote no O)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                wj[e] = j + e < n ? __shfl_sync(0xffffffffu, w, (j + e) & 31) : 0.f;
-                v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                // (a part without a key wrote no O)
-                if (wj[e] != 0.f && c < p.C) v[e] = ld(reinterpret_cast<const float4*>(p.o_part + slot(j0 + j + e) * p.C + c));
+                o[4 * e] = use ? fmaf(v[j][e].x, w, o[4 * e]) : o[4 * e], o[4 * e + 1] = use ? fmaf(v[j][e].y, w, o[4 * e + 1]) : o[4 * e + 1];
+                o[4 * e + 2] = use ? fmaf(v[j][e].z, w, o[4 * e + 2]) : o[4 * e + 2], o[4 * e + 3] = use ? fmaf(v[j][e].w, w, o[4 * e + 3]) : o[4 * e + 3];
             }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                o.x = fmaf(v[e].x, wj[e], o.x), o.y = fmaf(v[e].y, wj[e], o.y), o.z = fmaf(v[e].z, wj[e], o.z), o.w = fmaf(v[e].w, wj[e], o.w);
         }
     }
-    const float inv = rl != 0.f ? 1.f / rl : 0.f;
-    if (c < p.C)
-        *reinterpret_cast<uint2*>(p.o + static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh + c) =
-            make_uint2(pack16(o.x * inv, o.y * inv, BF16), pack16(o.z * inv, o.w * inv, BF16));
-    if (c == 0) p.lse[static_cast<long long>(tok) * p.H + head] = l != 0.f ? (top + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const int ch = lat_channel(chunk, warp >> 1, p.C), tok = mine ? rq.q0 + r / p.H : 0, head = r % p.H;
+    uint16_t* dst = p.o + static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh + ch;
+    float lse2 = l != 0.f ? ref + log2f(l) : -INFINITY;
+    if constexpr (SPLIT) {
+        // warp w0 joins channels 4 w0 .. of all warps' results
+        __shared__ float4 part_o[kLatJoinWarps][8][32];
+        __shared__ float4 part_s[kLatJoinWarps][32];
+        part_s[w0][lane] = make_float4(top, rtop, l, rl);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) part_o[w0][e][lane] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        __syncthreads();
+        float4 s[kLatJoinWarps];
+        float all = -INFINITY, rall = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < kLatJoinWarps; ++k) s[k] = part_s[k][lane], all = fmaxf(all, s[k].x), rall = fmaxf(rall, s[k].y);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        l = rl = 0.f;
+#pragma unroll
+        for (int k = 0; k < kLatJoinWarps; ++k) {
+            const float w = s[k].y == -INFINITY ? 0.f : ptx::ex2_approx(s[k].y - rall);
+            l += s[k].x == -INFINITY ? 0.f : s[k].z * ptx::ex2_approx(s[k].x - all);
+            rl += s[k].w * w;
+            const float4 v = part_o[k][w0][lane];
+            sum.x = fmaf(v.x, w, sum.x), sum.y = fmaf(v.y, w, sum.y), sum.z = fmaf(v.z, w, sum.z), sum.w = fmaf(v.w, w, sum.w);
+        }
+        const float inv = rl != 0.f ? 1.f / rl : 0.f;
+        lse2 = l != 0.f ? all + log2f(l) : -INFINITY;
+        if (mine && ch + 4 * w0 < p.C)
+            *reinterpret_cast<uint2*>(dst + 4 * w0) = make_uint2(pack16(sum.x * inv, sum.y * inv, BF16), pack16(sum.z * inv, sum.w * inv, BF16));
+    } else if (mine) {
+        const float inv = rl != 0.f ? 1.f / rl : 0.f;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8)
+            if (ch + e < p.C)
+                *reinterpret_cast<uint4*>(dst + e) = make_uint4(pack16(o[e] * inv, o[e + 1] * inv, BF16), pack16(o[e + 2] * inv, o[e + 3] * inv, BF16),
+                                                                pack16(o[e + 4] * inv, o[e + 5] * inv, BF16), pack16(o[e + 6] * inv, o[e + 7] * inv, BF16));
+    }
+    if (mine && ch == 0 && (!SPLIT || w0 == 0))
+        p.lse[static_cast<long long>(tok) * p.H + head] = lse2 == -INFINITY ? lse2 : lse2 * 0.69314718055994531f;
 }
 
 }  // namespace paged
