@@ -66,15 +66,16 @@ struct AppendItem {
     int h, w;               // head; K (0) or V (1)
 };
 
-// A thread's rows of an item: 16-bit values; with keys turned the fp32 values (so that they are rounded
-// once, to e4m3), or, for more rows than the registers hold of these, none: they are read twice.
+// A thread's rows of an item, 16-bit values; where keys are turned also the channels that make pairs with them.  Turned
+// values are fp32 (so that a key is rounded once, to e4m3), and for more rows than the registers hold of these,
+// nothing is held: rows are read twice.
 template <int NL, bool ROT>
 struct AppendRows {
     uint4 v[NL];
 };
 template <int NL>
 struct AppendRows<NL, true> {
-    float f[NL <= 4 ? NL : 1][8];
+    uint4 v[NL <= 4 ? NL : 1], other[NL <= 4 ? NL : 1];
 };
 
 // What a team of TH threads does with one item: load() its rows into registers,
@@ -86,66 +87,98 @@ struct AppendTeam {
     const AppendParams& p;
     const int tid;
     const int* row_of;           // rows of the CTA's tokens
+    const int* pos_of;           // ROT: their rows of the table, -1 where they are not turned
     const int LR, rows, r0, c8;  // threads per row (8 channels each), rows per pass, this thread's place
     const bool on;
     float* red;                  // team's shared memory: a value per warp,
     uint4* bred;                 //   least, then largest codes of a thread's rows (fp16 pairs),
     int *blo, *bhi;              //   bounds of a page's older codes
 
-    __device__ AppendTeam(const AppendParams& p_, int tid_, const int* row_of_, float* red_, uint4* bred_, int* blo_, int* bhi_)
-        : p(p_), tid(tid_), row_of(row_of_), LR(p_.d >> 3), rows(TH / LR), r0(tid / LR), c8((tid - r0 * LR) * 8), on(r0 < rows),
+    __device__ AppendTeam(const AppendParams& p_, int tid_, const int* row_of_, const int* pos_of_, float* red_, uint4* bred_, int* blo_, int* bhi_)
+        : p(p_), tid(tid_), row_of(row_of_), pos_of(pos_of_), LR(p_.d >> 3), rows(TH / LR), r0(tid / LR), c8((tid - r0 * LR) * 8), on(r0 < rows),
           red(red_), bred(bred_), blo(blo_), bhi(bhi_) {}
 
     __device__ static void sync() {
         if constexpr (TH == 32) __syncwarp(); else __syncthreads();
     }
 
-    // Channels c8 .. c8 + 7 of the item's row r in fp32, keys turned.
-    __device__ void fetch(const AppendItem& m, int r, float (&f)[8]) const {
-        const int row = row_of[m.e + r];
-        const uint16_t* src = (m.w ? p.x[1] : p.x[0]) + m.h * (m.w ? p.sh[1] : p.sh[0]) + row * (m.w ? p.st[1] : p.st[0]);
-        const uint4 own = ld(reinterpret_cast<const uint4*>(src + c8));
+    // Whether the thread's channels of this item are turned, and where their partners are (in the thread's own piece
+    // where pairs are neighbours).
+    __device__ bool turned(const AppendItem& m) const { return m.w == 0 && c8 < 2 * p.turn.half; }
+    __device__ int partner() const { return c8 < p.turn.half ? c8 + p.turn.half : c8 - p.turn.half; }
+
+    // 16-bit values of the thread's k-th row (of the item's first where it has none) and their partners.
+    __device__ void fetch(const AppendItem& m, int k, uint4& v, uint4& other) const {
+        const int r = r0 + k * rows;
+        const uint16_t* x = (m.w ? p.x[1] : p.x[0]) + m.h * (m.w ? p.sh[1] : p.sh[0]) +
+                            row_of[m.e + (on && r < m.n ? r : 0)] * (m.w ? p.st[1] : p.st[0]);
+        v = ld(reinterpret_cast<const uint4*>(x + (on ? c8 : 0)));
+        if (turned(m) && !p.turn.interleaved) other = ld(reinterpret_cast<const uint4*>(x + partner()));
+    }
+
+    // Rows k0 .. k0 + N - 1 in fp32, keys turned.  The table's loads are unconditional (its first row for a row that is not
+    // turned), so that those of N rows are on their way at once.
+    template <int N>
+    __device__ void turn(const AppendItem& m, int k0, const uint4* v, const uint4* other, float (*f)[8]) const {
         const int half = p.turn.half;
-        const bool first = c8 < half, pairs_here = p.turn.interleaved != 0;
-        const float* turn = m.w == 0 && c8 < 2 * half ? rotary_row(p.turn, row) : nullptr;
-        uint4 other = own;
-        if (turn && !pairs_here) other = ld(reinterpret_cast<const uint4*>(src + (first ? c8 + half : c8 - half)));
-        const uint32_t a[4] = {own.x, own.y, own.z, own.w}, b[4] = {other.x, other.y, other.z, other.w};
-        if (turn && pairs_here) {
-            const float4 c = ld(reinterpret_cast<const float4*>(turn + c8 / 2)), s = ld(reinterpret_cast<const float4*>(turn + half + c8 / 2));
-            const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+        const bool pairs_here = p.turn.interleaved != 0, first = c8 < half, here = turned(m);
+        float4 cs[N][2], sn[N][2];
+        int at[N];
+        if (here) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int r = r0 + (k0 + k) * rows;
+                at[k] = pos_of[m.e + (on && r < m.n ? r : 0)];
+                const float* row = p.turn.rows + static_cast<long long>(max(at[k], 0)) * (2 * half);
+                const float4 *c = reinterpret_cast<const float4*>(row + (pairs_here ? c8 / 2 : first ? c8 : c8 - half)),
+                             *s = reinterpret_cast<const float4*>(row + half + (pairs_here ? c8 / 2 : first ? c8 : c8 - half));
+                cs[k][0] = ld(c), sn[k][0] = ld(s);
+                if (!pairs_here) cs[k][1] = ld(c + 1), sn[k][1] = ld(s + 1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t a[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 x = unpack16(a[i], BF16);
-                f[2 * i] = turn_first(x.x, x.y, cs[i], sn[i]);
-                f[2 * i + 1] = turn_second(x.x, x.y, cs[i], sn[i]);
+                f[k][2 * i] = x.x, f[k][2 * i + 1] = x.y;
             }
-        } else if (turn) {
-            float cs[8], sn[8];
-            load_floats8(turn + (first ? c8 : c8 - half), cs);
-            load_floats8(turn + (first ? c8 + half : c8), sn);
+            if (!here || at[k] < 0) continue;
+            if (pairs_here) {
+                const float c[4] = {cs[k][0].x, cs[k][0].y, cs[k][0].z, cs[k][0].w}, s[4] = {sn[k][0].x, sn[k][0].y, sn[k][0].z, sn[k][0].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = unpack16(a[i], BF16), y = unpack16(b[i], BF16);
-                f[2 * i] = first ? turn_first(x.x, y.x, cs[2 * i], sn[2 * i]) : turn_second(y.x, x.x, cs[2 * i], sn[2 * i]);
-                f[2 * i + 1] = first ? turn_first(x.y, y.y, cs[2 * i + 1], sn[2 * i + 1]) : turn_second(y.y, x.y, cs[2 * i + 1], sn[2 * i + 1]);
-            }
-        } else {
+                for (int i = 0; i < 4; ++i) {
+                    const float x = f[k][2 * i], y = f[k][2 * i + 1];
+                    f[k][2 * i] = turn_first(x, y, c[i], s[i]), f[k][2 * i + 1] = turn_second(x, y, c[i], s[i]);
+                }
+            } else {
+                const uint32_t b[4] = {other[k].x, other[k].y, other[k].z, other[k].w};
+                const float c[8] = {cs[k][0].x, cs[k][0].y, cs[k][0].z, cs[k][0].w, cs[k][1].x, cs[k][1].y, cs[k][1].z, cs[k][1].w};
+                const float s[8] = {sn[k][0].x, sn[k][0].y, sn[k][0].z, sn[k][0].w, sn[k][1].x, sn[k][1].y, sn[k][1].z, sn[k][1].w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 x = unpack16(a[i], BF16);
-                f[2 * i] = x.x, f[2 * i + 1] = x.y;
+                for (int i = 0; i < 4; ++i) {
+                    const float2 y = unpack16(b[i], BF16);
+                    const float x0 = f[k][2 * i], x1 = f[k][2 * i + 1];
+                    f[k][2 * i] = first ? turn_first(x0, y.x, c[2 * i], s[2 * i]) : turn_second(y.x, x0, c[2 * i], s[2 * i]);
+                    f[k][2 * i + 1] = first ? turn_first(x1, y.y, c[2 * i + 1], s[2 * i + 1]) : turn_second(y.y, x1, c[2 * i + 1], s[2 * i + 1]);
+                }
             }
         }
     }
 
-    // The k-th of this thread's rows in fp32.
-    __device__ void values(const AppendItem& m, const Rows& v, int k, float (&f)[8]) const {
+    // The k-th of this thread's rows in fp32 (`held`: all of them, turned).
+    __device__ void values(const AppendItem& m, const Rows& v, int k, const float (*held)[8], float (&f)[8]) const {
         if constexpr (kReadTwice) {
-            fetch(m, r0 + k * rows, f);
+            uint4 own, other = make_uint4(0, 0, 0, 0);
+            float one[1][8];
+            fetch(m, k, own, other);
+            turn<1>(m, k, &own, &other, one);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = one[0][i];
         } else if constexpr (ROT) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f[i] = v.f[k][i];
+            for (int i = 0; i < 8; ++i) f[i] = held[k][i];
         } else {
             const uint32_t u[4] = {v.v[k].x, v.v[k].y, v.v[k].z, v.v[k].w};
 #pragma unroll
@@ -156,16 +189,18 @@ struct AppendTeam {
         }
     }
 
-    __device__ void load(const AppendItem& m, Rows& held, float& old) const {
+    __device__ void load(const AppendItem& m, Rows& rows16, float& old) const {
         old = m.place == 0 ? 0.f : (m.w ? p.scale[1] : p.scale[0])[static_cast<long long>(m.page) * p.Hk + m.h];
-        if constexpr (ROT) {
-            if constexpr (!kReadTwice) {
+        if constexpr (kReadTwice) {
+        } else if constexpr (ROT) {
 #pragma unroll
-                for (int k = 0; k < NL; ++k)
-                    if (on && r0 + k * rows < m.n) fetch(m, r0 + k * rows, held.f[k]);
+            for (int k = 0; k < NL; ++k) {
+                // (a decode step's one-warp items have one row: the others are not read)
+                if constexpr (TH == 32) rows16.v[k] = rows16.other[k] = make_uint4(0, 0, 0, 0);
+                if (TH > 32 || k * rows < m.n) fetch(m, k, rows16.v[k], rows16.other[k]);
             }
         } else {
-            load16(m, held.v);
+            load16(m, rows16.v);
         }
     }
 
@@ -196,11 +231,17 @@ struct AppendTeam {
 
     __device__ void store(const AppendItem& m, const Rows& v, float old) const {
         float amax = 0.f;
+        float held[ROT && !kReadTwice ? NL : 1][8];
+        if constexpr (ROT && !kReadTwice) {
+#pragma unroll
+            for (int k = 0; k < NL; k += 2)
+                if (TH > 32 || k * rows < m.n) turn<2>(m, k, v.v + k, v.other + k, held + k);
+        }
 #pragma unroll
         for (int k = 0; k < NL; ++k) {
-            if (ROT && !(on && r0 + k * rows < m.n)) continue;  // (else rows of zeros)
+            if (ROT && !(on && r0 + k * rows < m.n)) continue;  // (else they are zeros)
             float f[8];
-            values(m, v, k, f);
+            values(m, v, k, held, f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (fabsf(f[i]) < INFINITY) amax = fmaxf(amax, fabsf(f[i]));  // an infinity or NaN does not count
@@ -231,7 +272,7 @@ struct AppendTeam {
             const int r = r0 + k * rows;
             if (!on || r >= m.n) continue;
             float f[8];
-            values(m, v, k, f);
+            values(m, v, k, held, f);
             uint32_t q[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = e4m3x2(f[2 * i] * inv, f[2 * i + 1] * inv);
@@ -319,6 +360,7 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_ap
     __shared__ int n_short, n_long;
     __shared__ int2 short_runs[kAppendMaxChunk], long_runs[kAppendMaxChunk];  // first token | length << 8, slot
     __shared__ int row_of[kAppendEntries];      // rows of the tokens
+    __shared__ int pos_of[ROT ? kAppendEntries : 1];
     __shared__ float red[kWarps];
     __shared__ uint4 bred[BOUNDS ? 2 * kAppendThreads : 1];
     __shared__ int blo[BOUNDS ? kWarps : 1][256], bhi[BOUNDS ? kWarps : 1][256];
@@ -340,13 +382,18 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_ap
     // rows t0 .. t0 + 255: the chunk and what runs that begin in it may reach
     const int t = t0 + tid;
     int slot = t < p.T ? ld_meta(p.slots + t) : -1;
+    int edge = -1, position = -1;
+    if (lane == 0 && t > 0 && t - 1 < p.T) edge = ld_meta(p.slots + t - 1);
+    if constexpr (ROT) position = t < p.T ? ld_meta(p.turn.positions + t) : -1;
     int before = __shfl_up_sync(0xffffffffu, slot, 1);
-    if (lane == 0) before = (t > 0 && t - 1 < p.T) ? ld_meta(p.slots + t - 1) : -1;
+    if (lane == 0) before = edge;
+    if constexpr (ROT) position = rotary_row(p.turn, position);
     bool same = slot >= 0 && before >= 0 && (slot >> p.page_shift) == (before >> p.page_shift);
     bool go_on = same && slot == before + 1;
     const uint32_t new_run = __ballot_sync(0xffffffffu, !go_on);
     if (lane == 0) breaks[warp] = new_run;
     row_of[tid] = t;
+    if constexpr (ROT) pos_of[tid] = position;
     // Tokens are numbered from the chunk's start.  Mostly that is their row, and a token goes on
     // from the row above; where one stands behind rows left out, or a run may pass the end of
     // the window over such rows, they are counted out.
@@ -380,6 +427,9 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_ap
         __syncthreads();
         const int rank = rank_of_row(), tokens = count();
         if (slot >= 0) slot_of[rank] = slot, row_of[rank] = t;
+        if constexpr (ROT) {
+            if (slot >= 0) pos_of[rank] = position;
+        }
         if (tid < kAppendEntries / 32 - kWarps) breaks[kWarps + tid] = 0;
         __syncthreads();
         slot = -1, before = -1;
@@ -415,7 +465,10 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_ap
                 if (lane == 0) stored[warp] = has;
                 __syncthreads();
                 const int at = rank_of_row(), all = count();
-                if (s >= 0 && at < left) slot_of[limit + at] = s, row_of[limit + at] = u + tid;
+                if (s >= 0 && at < left) {
+                    slot_of[limit + at] = s, row_of[limit + at] = u + tid;
+                    if constexpr (ROT) pos_of[limit + at] = rotary_position(p.turn, u + tid);
+                }
                 __syncthreads();
                 const int i = limit + tid;
                 const bool goes_on = tid < min(all, left) && slot_of[i] == last + 1 + tid && row_of[i] - row_of[i - 1] <= kAppendGap;
@@ -459,9 +512,9 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_ap
         return AppendItem{r.x & 255, r.x >> 8, r.y >> p.page_shift, r.y & (P - 1), pair >> 1, pair & 1};
     };
     if (n_long > 0) {
-        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS, ROT> team(p, tid, row_of, red, bred, blo[0], bhi[0]);
+        const AppendTeam<kAppendThreads, NL, BF16, BOUNDS, ROT> team(p, tid, row_of, pos_of, red, bred, blo[0], bhi[0]);
         const int items = n_long * pairs;
-        if constexpr (NL <= 4 && !ROT) {  // the next item is read while this one is stored
+        if constexpr (NL <= 4) {  // the next item is read while this one is stored
             AppendRows<NL, ROT> v, next;
             float old, next_old = 0.f;
             AppendItem m = item(long_runs, 0);
@@ -488,7 +541,7 @@ __global__ void __launch_bounds__(kAppendThreads, NL == 4 && !ROT ? 4 : 2) kv_ap
     }
     if (n_short > 0) {
         const int w = BOUNDS ? warp : 0;
-        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS, ROT> team(p, lane, row_of, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
+        const AppendTeam<32, kAppendShortRows, BF16, BOUNDS, ROT> team(p, lane, row_of, pos_of, red, bred + (BOUNDS ? 64 * warp : 0), blo[w], bhi[w]);
         for (int i = warp; i < n_short * pairs; i += kWarps) {
             const AppendItem m = item(short_runs, i);
             AppendRows<kAppendShortRows, ROT> v;

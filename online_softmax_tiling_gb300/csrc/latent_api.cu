@@ -150,20 +150,7 @@ int fa_rotary_embed(const fa_rotary* rotary, const fa_rotary_part* q, const fa_r
     if (st == FA_OK && k) st = check_part(k, T);
     if (st != FA_OK) return st;
     if (T == 0) return FA_OK;
-    pg::RotaryWork w = rotary_work(*rotary, q, k, T, d);
-    const int heads = w.part[0].heads + w.part[1].heads;
-    // Items of four heads read the table a quarter as often; of one, where there are too few items to fill the SMs.
-    const int64_t width = w.cols + w.tail, one = static_cast<int64_t>(T) * heads * width;
-    const bool single = one < 4ll * 2048 * sm_count();
-    w.groups = single ? heads : (heads + pg::kRotaryHeads - 1) / pg::kRotaryHeads;
-    if (static_cast<int64_t>(T) * w.groups * width > INT32_MAX) return FA_ERR_INVALID_ARG;
-    const bool bf16 = dtype == FA_BF16;
-    const void* fn = single ? (bf16 ? reinterpret_cast<const void*>(&pg::rotary_kernel<1, true>) : reinterpret_cast<const void*>(&pg::rotary_kernel<1, false>))
-                            : (bf16 ? reinterpret_cast<const void*>(&pg::rotary_kernel<pg::kRotaryHeads, true>)
-                                    : reinterpret_cast<const void*>(&pg::rotary_kernel<pg::kRotaryHeads, false>));
-    void* args[] = {&w};
-    const int64_t ctas = (static_cast<int64_t>(T) * w.groups * width + pg::kRotaryThreads - 1) / pg::kRotaryThreads;
-    return launch(fn, ctas, 1, pg::kRotaryThreads, 0, 1, stream, args) ? FA_OK : FA_ERR_CUDA;
+    return launch_rotary(rotary_work(*rotary, q, k, T, d), dtype == FA_BF16, stream);
 }
 
 int fa_latent_cache_append(const fa_latent_cache* cache, const void* latent, long long latent_stride, const void* rope,

@@ -53,7 +53,8 @@ __global__ void __launch_bounds__(kRotaryThreads) latent_append_kernel(const Lat
     }
     const int c0 = p.r.interleaved ? at * 16 : at * 8, c1 = p.r.interleaved ? c0 + 8 : c0 + p.r.half;
     uint4 u = ld(reinterpret_cast<const uint4*>(src + c0)), v = ld(reinterpret_cast<const uint4*>(src + c1));
-    if (const float* row = rotary_row(p.r, token)) {
+    if (const int row_at = rotary_position(p.r, token); row_at >= 0) {
+        const float* row = p.r.rows + static_cast<long long>(row_at) * p.R;
         float c[8], s[8];
         load_floats8(row + at * 8, c);
         load_floats8(row + p.r.half + at * 8, s);

@@ -281,8 +281,15 @@ int append(const fa_kv_cache* cache, const void* k, const void* v, const int* sl
             p.q.groups = q->heads;
             const int64_t items = static_cast<int64_t>(T) * q->heads * (p.q.cols + p.q.tail);
             if (items > INT32_MAX) return FA_ERR_INVALID_ARG;
-            // an item per thread; the grid's rows end at 65535, what is beyond goes round
-            rows = std::min<int64_t>(65535, rows + (items + columns * pg::kAppendThreads - 1) / (columns * pg::kAppendThreads));
+            if (items > 1024ll * sm_count()) {
+                // Many: a launch of their own, at the occupancy that turning alone has (22 thousand tokens of 32 heads, d 128:
+                // 61 us of it, behind this kernel's registers 180).
+                const int st = launch_rotary(p.q, bf16, stream);
+                if (st != FA_OK) return st;
+                p.q.T = 0;
+            } else {  // an item per thread; the grid's rows end at 65535, what is beyond goes round
+                rows = std::min<int64_t>(65535, rows + (items + columns * pg::kAppendThreads - 1) / (columns * pg::kAppendThreads));
+            }
         }
     }
     void* args[] = {&p};

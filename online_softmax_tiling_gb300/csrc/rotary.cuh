@@ -20,6 +20,12 @@ struct RotaryTable {
     int num_positions, half; // half = h, a multiple of 8
     int interleaved, inverse;
 };
+// The table's row for a position (-1: not turned), a token's row.
+__device__ __forceinline__ int rotary_row(const RotaryTable& r, int position) {
+    if (position >= r.num_positions) report(kBadData);
+    return position < r.num_positions ? max(position, -1) : -1;
+}
+__device__ __forceinline__ int rotary_position(const RotaryTable& r, int token) { return rotary_row(r, ld_meta(r.positions + token)); }
 // Some heads of every token; y may be x.
 struct RotaryPart {
     const uint16_t* x;
@@ -31,16 +37,11 @@ struct RotaryWork {
     RotaryTable r;
     RotaryPart part[2];
     int T;
-    int cols, tail;  // items of 8 pairs per head; 8-channel pieces behind them that are copied (0 in place)
+    int cols, tail;  // items of 8 pairs per head; of 16 channels behind them that are copied (0 in place)
+    int d;
     int groups;      // of heads
 };
 
-// The token's table row, or null where it is not turned.
-__device__ __forceinline__ const float* rotary_row(const RotaryTable& r, int token) {
-    const int at = ld_meta(r.positions + token);
-    if (at >= r.num_positions) report(kBadData);
-    return at >= 0 && at < r.num_positions ? r.rows + static_cast<long long>(at) * (2 * r.half) : nullptr;
-}
 __device__ __forceinline__ float turn_first(float a, float b, float c, float s) { return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)); }
 __device__ __forceinline__ float turn_second(float a, float b, float c, float s) { return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)); }
 
@@ -75,8 +76,9 @@ __device__ __forceinline__ void rotary_item(const RotaryWork& w, unsigned item) 
     const int all = w.part[0].heads + w.part[1].heads;
     const bool turned = col < w.cols;
     // channels of the item's first and second piece
-    const int c0 = !turned ? 2 * w.r.half + (col - w.cols) * 8 : w.r.interleaved ? col * 16 : col * 8;
-    const int c1 = w.r.interleaved ? c0 + 8 : c0 + w.r.half;
+    const int c0 = !turned ? 2 * w.r.half + (col - w.cols) * 16 : w.r.interleaved ? col * 16 : col * 8;
+    const int c1 = !turned || w.r.interleaved ? c0 + 8 : c0 + w.r.half;
+    const bool second_piece = turned || c1 < w.d;
     uint4 u[U], v[U];
     uint16_t* dst[U];
 #pragma unroll
@@ -92,12 +94,13 @@ __device__ __forceinline__ void rotary_item(const RotaryWork& w, unsigned item) 
             dst[i] = (second ? w.part[1].y : w.part[0].y) + token * (second ? w.part[1].yt : w.part[0].yt) +
                      h * (second ? w.part[1].yh : w.part[0].yh);
             u[i] = ld(reinterpret_cast<const uint4*>(src + c0));
-            if (turned) v[i] = ld(reinterpret_cast<const uint4*>(src + c1));
+            if (second_piece) v[i] = ld(reinterpret_cast<const uint4*>(src + c1));
         }
     }
-    const float* row = turned ? rotary_row(w.r, token) : nullptr;
+    const int at = turned ? rotary_position(w.r, token) : -1;
     float c[8], s[8];
-    if (row) {
+    if (at >= 0) {
+        const float* row = w.r.rows + static_cast<long long>(at) * (2 * w.r.half);
         load_floats8(row + col * 8, c);
         load_floats8(row + w.r.half + col * 8, s);
         if (w.r.inverse) {
@@ -108,9 +111,9 @@ __device__ __forceinline__ void rotary_item(const RotaryWork& w, unsigned item) 
 #pragma unroll
     for (int i = 0; i < U; ++i) {
         if (!dst[i]) continue;
-        if (row) turn16(u[i], v[i], c, s, w.r.interleaved != 0, BF16);
+        if (at >= 0) turn16(u[i], v[i], c, s, w.r.interleaved != 0, BF16);
         *reinterpret_cast<uint4*>(dst[i] + c0) = u[i];
-        if (turned) *reinterpret_cast<uint4*>(dst[i] + c1) = v[i];
+        if (second_piece) *reinterpret_cast<uint4*>(dst[i] + c1) = v[i];
     }
 }
 

@@ -39,8 +39,25 @@ pg::RotaryWork rotary_work(const fa_rotary& r, const fa_rotary_part* q, const fa
     }
     w.T = T;
     w.cols = r.dim / 16;
-    w.tail = in_place ? 0 : (d - r.dim) / 8;
+    w.tail = in_place ? 0 : (d - r.dim + 15) / 16;
+    w.d = d;
     return w;
+}
+
+// The launch that turns them.  Items of four heads read the table a quarter as often; of one, where there are too few items
+// to fill the SMs.
+[[maybe_unused]] int launch_rotary(pg::RotaryWork w, bool bf16, void* stream) {
+    const int heads = w.part[0].heads + w.part[1].heads;
+    const int64_t width = w.cols + w.tail, one = static_cast<int64_t>(w.T) * heads * width;
+    const bool single = one < 4ll * 2048 * sm_count();
+    w.groups = single ? heads : (heads + pg::kRotaryHeads - 1) / pg::kRotaryHeads;
+    const int64_t items = static_cast<int64_t>(w.T) * w.groups * width;
+    if (items > INT32_MAX) return FA_ERR_INVALID_ARG;
+    const void* fn = single ? (bf16 ? reinterpret_cast<const void*>(&pg::rotary_kernel<1, true>) : reinterpret_cast<const void*>(&pg::rotary_kernel<1, false>))
+                            : (bf16 ? reinterpret_cast<const void*>(&pg::rotary_kernel<pg::kRotaryHeads, true>)
+                                    : reinterpret_cast<const void*>(&pg::rotary_kernel<pg::kRotaryHeads, false>));
+    void* args[] = {&w};
+    return launch(fn, (items + pg::kRotaryThreads - 1) / pg::kRotaryThreads, 1, pg::kRotaryThreads, 0, 1, stream, args) ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
