@@ -19,7 +19,7 @@ DEPENDS = SOURCES + [os.path.join(CSRC, f) for f in ("fa_fwd_kernel.cuh", "fa_fw
                                                      "kv_append.cuh", "kv_page_select.cuh", "paged_fwd_kernel.cuh",
                                                      "paged_prompt_kernel.cuh", "paged_prompt_wide_kernel.cuh",
                                                      "rotary.cuh", "rotary_host.h", "host_common.h", "latent_append.cuh",
-                                                     "latent_paged_kernel.cuh", "latent_fwd_kernel.cuh", "sm103_ptx.cuh")] + [
+                                                     "latent_paged_kernel.cuh", "latent_fwd_kernel.cuh", "pair_ptx.cuh", "sm103_ptx.cuh")] + [
     os.path.join(ROOT, "include", f) for f in ("fa.h", "fa_ceilings.h", "fa_naive.h", "fa_paged.h", "fa_rotary.h", "fa_latent.h")]
 LIBRARY = os.path.join(HERE, "libfa_gb300.so")
 BINDING = os.path.join(HERE, "_paged_binding" + sysconfig.get_config_var("EXT_SUFFIX"))

@@ -277,9 +277,13 @@ int fa_latent_fwd(const fa_latent_args* args) {
     p.o = static_cast<uint16_t*>(a.o), p.lse = a.lse, p.cu_q = a.cu_q, p.cu_k = a.cu_k;
     p.o_st = a.o_stride[0], p.o_sh = a.o_stride[1];
     p.T = a.T, p.Tk = a.Tk, p.B = a.B, p.H = a.H, p.Dn = a.Dn, p.Dv = a.Dv, p.max_q = a.max_q;
-    p.pieces = (a.Dn + 63) / 64 + 1, p.wide_v = a.Dv > 64;
-    p.q_blocks = (a.max_q + 255) / 256;
-    p.units = a.B * a.H * p.q_blocks;
+    p.pieces = (a.Dn + 63) / 64 + 1, p.half_v = (a.Dv + 31) / 32 * 16;
+    p.q_blocks = (a.max_q + pg::kLfRows - 1) / pg::kLfRows;
+    // Blocks of all requests, at most: where that is well below one for every request and block of the longest, the kernel
+    // counts them (a prompt among many short ones).
+    const int64_t blocks = static_cast<int64_t>(a.B) * p.q_blocks, most = a.T / pg::kLfRows + static_cast<int64_t>(a.B);
+    p.compact = a.B <= pg::kLfMaxB && 2 * most <= blocks;
+    const int64_t units = a.H * (p.compact ? most : blocks);
     p.causal = a.causal != 0;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     // (request, head) pairs whose keys and values fill about half of L2
@@ -288,14 +292,14 @@ int fa_latent_fwd(const fa_latent_args* args) {
     CUtensorMap tq, tk, ts, tv;
     const int keys = std::max(a.Tk, 1);  // (no key at all: nothing is read)
     if (!encode_rows(&tq, a.q, bf16, a.Dn + a.R, a.T, a.H, a.q_stride[0], a.q_stride[1], 128) ||
-        !encode_rows(&tk, a.k, bf16, a.Dn, keys, a.H, a.k_stride[0], a.k_stride[1], 128) ||
-        !encode_rows(&ts, a.k_rope, bf16, a.R, keys, 1, a.k_rope_stride, a.k_rope_stride, 128) ||
-        !encode_rows(&tv, a.v, bf16, a.Dv, keys, a.H, a.v_stride[0], a.v_stride[1], 64))
+        !encode_rows(&tk, a.k, bf16, a.Dn, keys, a.H, a.k_stride[0], a.k_stride[1], 64) ||
+        !encode_rows(&ts, a.k_rope, bf16, a.R, keys, 1, a.k_rope_stride, a.k_rope_stride, 64) ||
+        !encode_rows(&tv, a.v, bf16, a.Dv, keys, a.H, a.v_stride[0], a.v_stride[1], 128))
         return FA_ERR_CUDA;
     const void* fn = bf16 ? reinterpret_cast<const void*>(&pg::latent_fwd_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_fwd_kernel<false>);
     void* kargs[] = {&tq, &tk, &ts, &tv, &p};
     if (!ensure_smem(fn, pg::kLfSmem, device) ||
-        !launch(fn, std::min(p.units, sm_count()), 1, pg::kLfThreads, pg::kLfSmem, 1, a.stream, kargs))
+        !launch(fn, 2 * units, 1, pg::kLfThreads, pg::kLfSmem, 2, a.stream, kargs))
         return FA_ERR_CUDA;
     return FA_OK;
 }

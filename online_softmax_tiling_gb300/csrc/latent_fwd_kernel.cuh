@@ -6,31 +6,41 @@
 // 2 (Dn + R + Dv) operations per visible pair: bound by the tensor cores.  The shared channels are one more
 // 64-channel piece of the first product's depth, read from the one copy there is (never laid out per head).
 //
-// Mapping: that of the fused forward kernel.  A persistent CTA per SM walks units of 256 query rows of one
-// (request, head), two tiles A and B of 128: softmax of A in warps 0-3 and of B in warps 4-7 (a thread per row), loader
-// warp 8, tensor-core issuer warp 9 in the order PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1), each PV in two halves of
-// 64 keys.  TMEM: S_A 0, S_B 128 (16-bit weights over the first 64 columns), U_A 256, U_B 384.
-// With a depth of 192 the queries take 96 KB and a key tile 48: two of them and two value tiles would not fit beside
-// the queries, so keys and values share one ring of eight 16 KB slots, each with barriers of its own: a slot
-// holds 64 channels of 128 keys, or 64 keys of all value channels (the half that a PV step reads), and is free as soon as
-// its last product is done.
+// Mapping.  A unit is 512 query rows of one (request, head), two tiles A and B of 256, on a pair of CTAs: tcgen05.mma of both
+// (cta_group::2, M = 256), each CTA with 128 rows of a tile and half of every B operand: 64 keys of a key tile of 128 for
+// S = Q K^T, half of the value channels (of all keys) for U += P V.  With a depth of 192 the queries take 96 KB; key
+// and value halves are 40 KB a tile, so three tiles fit beside them (one CTA alone: one and a half), and per product
+// shared memory is read 96 bytes a cycle instead of 128, which left nothing for the loads (75 cycles a step instead of 64).
+//   * warps 0-3 / 4-7: softmax of the CTA's rows of tile A / B, a thread per row; weights go to tensor memory;
+//   * warp 8: loads (TMA) and the next unit;
+//   * warp 9 (of the first CTA): products in the order PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1), each PV in two
+//     halves of 64 keys: while one tile's weights are computed, the tensor cores work for the other.
+// TMEM: S_A 0, S_B 128 (16-bit weights over the first 64 columns), U_A 256, U_B 384.
+// Units are handed out by the launch itself: a pair that is done takes the next cluster of the grid that has not begun
+// (clusterlaunchcontrol), asked for one unit ahead, so that its queries and keys are on their way before the last products of this one.
+// (Dealt out in turn, the CTA with the most work had a quarter more than the average.)  They go through heads in groups
+// whose keys and values stay in L2, within a group longest first.
 // Requests lie behind one another, so a tile may hold the next request's keys: masked as keys; as values they
 // are overwritten with zeros (weight 0 times infinity or NaN would reach this request).
-// Units go through heads in groups whose keys and values stay in L2, within a group longest first.
 #pragma once
 
 #include <type_traits>
 
-#include "paged_common.cuh"
+#include "pair_ptx.cuh"
 
 namespace fa {
 namespace paged {
 
 constexpr int kLfThreads = 320;
-constexpr int kLfSlot = 128 * 128;   // 16 KB
-constexpr int kLfSlots = 8;
+constexpr int kLfRows = 512;         // of a unit
+constexpr int kLfQPiece = 128 * 128; // 128 rows x 64 channels
+constexpr int kLfKPiece = 64 * 128;  // 64 keys x 64 channels
+constexpr int kLfVTile = 128 * 128;  // 128 keys x up to 64 channels
 constexpr int kLfMaxPieces = 3;      // 64-channel pieces of a query or key
-constexpr int kLfOffCtl = 2 * kLfMaxPieces * kLfSlot + kLfSlots * kLfSlot;
+constexpr int kLfStages = 3;
+constexpr int kLfStage = kLfMaxPieces * kLfKPiece + kLfVTile;
+constexpr int kLfOffK = 2 * kLfMaxPieces * kLfQPiece;
+constexpr int kLfOffCtl = kLfOffK + kLfStages * kLfStage;
 
 struct LatentFwdParams {
     uint16_t* o;
@@ -40,16 +50,23 @@ struct LatentFwdParams {
     long long o_st, o_sh;
     int T, Tk, B, H, Dn, Dv, max_q;
     int pieces;        // of a key: those of its own channels, then the shared one
-    int wide_v;        // Dv > 64
-    int q_blocks;      // of 256 rows, of the longest request
+    int half_v;        // value channels of a CTA: a multiple of 16, at most 64
+    int q_blocks;      // of 512 rows, of the longest request
     int group;         // (request, head) pairs gone through together
-    int units;
+    int compact;       // most requests are far shorter than the longest: units by the blocks that there are
     int causal;
     float scale_log2;
 };
+constexpr int kLfMaxB = 2048;   // requests whose blocks are counted (compact)
 struct LfCtl {
-    uint64_t q_full, q_empty, full[kLfSlots], empty[kLfSlots], s_full[2], p_half[2], p_full[2], o_half[2], o_ready[2], drain;
+    // signalled in the first CTA by both
+    uint64_t q_full, k_full[kLfStages], p_half[2], p_full[2], unit_empty[2];
+    // in both by the tensor core, by the launch control, or by the CTA's own loads
+    uint64_t q_empty, k_empty[kLfStages], v_empty[kLfStages], s_full[2], o_half[2], o_ready[2], unit_full[2], v_full[kLfStages], drain;
+    alignas(16) uint4 unit[2];   // answers of the launch control
     uint32_t tmem_base;
+    int warp_sum[kLfThreads / 32];
+    int before[kLfMaxB + 1];     // compact: blocks before each request
 };
 constexpr int kLfSmem = kLfOffCtl + static_cast<int>(sizeof(LfCtl)) + 1024;
 static_assert(kLfSmem <= 232448, "shared memory of a CTA");
@@ -62,29 +79,56 @@ struct LfUnit {
     __device__ int n(int x) const { return x ? nb : na; }
 };
 
-__device__ __forceinline__ LfUnit lf_unit(const LatentFwdParams& p, int u, bool& bad) {
+// Unit u: heads in groups, in a group the last block of every (request, head), then the last but one (a request that has
+// fewer has none); compact: head by head the blocks of all requests, each request's from the last.
+__device__ __forceinline__ LfUnit lf_unit(const LatentFwdParams& p, const LfCtl* ctl, int u, bool& bad) {
     LfUnit w;
-    const int heads = p.B * p.H, per = p.group * p.q_blocks, g = u / per, rest = u - g * per;
-    const int here = min(p.group, heads - g * p.group), back = rest / here, bh = g * p.group + rest - back * here;
-    const int b = bh / p.H;
-    w.head = bh - b * p.H;
+    int b, back;
+    if (p.compact) {
+        const int all = max(ctl->before[p.B], 1), k = u % all;
+        w.head = u / all;
+        b = owner_of(ctl->before, p.B, k);
+        back = w.head < p.H ? k - ctl->before[b] : p.q_blocks;  // (behind the last unit)
+    } else {
+        const int heads = p.B * p.H, per = p.group * p.q_blocks, g = u / per, rest = u - g * per;
+        const int here = min(p.group, heads - g * p.group), bh = g * p.group + rest % here;
+        back = rest / here;
+        b = bh / p.H;
+        w.head = bh - b * p.H;
+    }
     w.q0 = ld_meta(p.cu_q + b), w.k0 = ld_meta(p.cu_k + b);
     w.nq = ld_meta(p.cu_q + b + 1) - w.q0, w.nk = ld_meta(p.cu_k + b + 1) - w.k0;
     if (w.q0 < 0 || w.nq < 0 || w.nq > p.max_q || w.q0 > p.T - w.nq || w.k0 < 0 || w.nk < 0 || w.k0 > p.Tk - w.nk)
         bad = true, w.nq = 0;
-    w.row0 = ((w.nq + 255) / 256 - 1 - back) * 256;  // (the last block, with the most keys, first; negative: none)
+    w.row0 = ((w.nq + kLfRows - 1) / kLfRows - 1 - back) * kLfRows;  // (the last block, with the most keys, first; negative: none)
     auto tiles_of = [&](int i0) {
-        const int last = min(i0 + 127, w.nq - 1), limit = p.causal ? min(w.nk, last + 1 + w.nk - w.nq) : w.nk;
+        const int last = min(i0 + 255, w.nq - 1), limit = p.causal ? min(w.nk, last + 1 + w.nk - w.nq) : w.nk;
         return w.row0 < 0 || i0 >= w.nq ? 0 : (max(limit, 0) + 127) / 128;
     };
-    w.na = tiles_of(w.row0), w.nb = tiles_of(w.row0 + 128);
+    w.na = tiles_of(w.row0), w.nb = tiles_of(w.row0 + 256);
     w.tiles = max(w.na, w.nb);
     return w;
 }
-// Units of a CTA: c, then 2 G - 1 - c, 2 G + c, ...
-__device__ __forceinline__ int lf_unit_id(int r) {
-    const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
-    return r * G + ((r & 1) ? G - 1 - c : c);
+
+// Asks for the next cluster of the grid: 16 bytes at `answer` of both CTAs, signalled on `bar` of both.
+__device__ __forceinline__ void ask_unit(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.multicast::cluster::all.b128 [%0], [%1];" ::"r"(answer),
+                 "r"(bar)
+                 : "memory");
+}
+// The unit of an answer, -1 where there is none any more.
+__device__ __forceinline__ int answered_unit(uint32_t answer) {
+    uint32_t yes, x;
+    asm volatile(
+        "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 r, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, r;\n\t}"
+        : "=r"(yes), "=r"(x)
+        : "r"(answer)
+        : "memory");
+    return yes ? static_cast<int>(x >> 1) : -1;
 }
 
 template <bool BF16>
@@ -97,26 +141,34 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     const uint32_t sbase = ptx::smem_addr(smem);
     LfCtl* ctl = reinterpret_cast<LfCtl*>(smem + kLfOffCtl);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int KP = p.pieces, VP = p.wide_v ? 2 : 1, per_tile = KP + VP;
-    const uint32_t ring = sbase + 2 * kLfMaxPieces * kLfSlot;
+    const int rank = static_cast<int>(cluster_rank());
+    const int KP = p.pieces;
 
     const uint32_t b_q = ptx::smem_addr(&ctl->q_full), b_qe = ptx::smem_addr(&ctl->q_empty);
-    const uint32_t b_full = ptx::smem_addr(&ctl->full[0]), b_empty = ptx::smem_addr(&ctl->empty[0]);
+    const uint32_t b_kf = ptx::smem_addr(&ctl->k_full[0]), b_ke = ptx::smem_addr(&ctl->k_empty[0]);
+    const uint32_t b_vf = ptx::smem_addr(&ctl->v_full[0]), b_ve = ptx::smem_addr(&ctl->v_empty[0]);
     const uint32_t b_sf = ptx::smem_addr(&ctl->s_full[0]), b_ph = ptx::smem_addr(&ctl->p_half[0]), b_pf = ptx::smem_addr(&ctl->p_full[0]);
     const uint32_t b_oh = ptx::smem_addr(&ctl->o_half[0]), b_or = ptx::smem_addr(&ctl->o_ready[0]), b_drain = ptx::smem_addr(&ctl->drain);
+    const uint32_t b_uf = ptx::smem_addr(&ctl->unit_full[0]), b_ue = ptx::smem_addr(&ctl->unit_empty[0]);
+    const uint32_t answers = ptx::smem_addr(&ctl->unit[0]);
+    constexpr int kReaders = 2 * 9 + 1;  // warps that take a unit from an answer: softmax and loader of both, the issuer
     if (tid == 0) {
-        ptx::mbar_init(b_q, 1);
+        ptx::mbar_init(b_q, 2);
         ptx::mbar_init(b_qe, 1);
-        for (int s = 0; s < kLfSlots; ++s) {
-            ptx::mbar_init(b_full + 8 * s, 1);
-            ptx::mbar_init(b_empty + 8 * s, 1);
+        for (int s = 0; s < kLfStages; ++s) {
+            ptx::mbar_init(b_kf + 8 * s, 2);
+            ptx::mbar_init(b_ke + 8 * s, 1);
+            ptx::mbar_init(b_vf + 8 * s, 1);
+            ptx::mbar_init(b_ve + 8 * s, 1);
         }
         for (int x = 0; x < 2; ++x) {
             ptx::mbar_init(b_sf + 8 * x, 1);
-            ptx::mbar_init(b_ph + 8 * x, 128);
-            ptx::mbar_init(b_pf + 8 * x, 128);
+            ptx::mbar_init(b_ph + 8 * x, 8);
+            ptx::mbar_init(b_pf + 8 * x, 8);
             ptx::mbar_init(b_oh + 8 * x, 1);
             ptx::mbar_init(b_or + 8 * x, 1);
+            ptx::mbar_init(b_uf + 8 * x, 1);
+            ptx::mbar_init(b_ue + 8 * x, kReaders);
         }
         ptx::mbar_init(b_drain, 1);
         ptx::fence_mbar_init();
@@ -125,139 +177,176 @@ __global__ void __launch_bounds__(kLfThreads, 1)
         ptx::prefetch_tensormap(&tm_s);
         ptx::prefetch_tensormap(&tm_v);
     }
-    if (warp == 9) {
-        ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), 512);
-        ptx::tmem_relinquish();
-    }
+    if (warp == 9) tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base));
     ptx::tc_fence_before_sync();
     __syncthreads();
+    cluster_sync();  // barriers and tensor memory of both CTAs are there
     ptx::tc_fence_after_sync();
     const uint32_t tmem = ctl->tmem_base;
     dependents_may_start();
     wait_for_previous();
+    if (p.compact) {
+        const int per = (p.B + kLfThreads - 1) / kLfThreads, b0 = min(tid * per, p.B), b1 = min(b0 + per, p.B);
+        auto blocks_of = [&](int b) {
+            const int q0 = ld_meta(p.cu_q + b), nq = ld_meta(p.cu_q + b + 1) - q0;
+            return nq < 0 || nq > p.max_q || q0 < 0 || q0 > p.T - nq ? 1 : (nq + kLfRows - 1) / kLfRows;  // (bad marks: a unit to report them)
+        };
+        int own = 0;
+        for (int b = b0; b < b1; ++b) own += blocks_of(b);
+        int incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) ctl->warp_sum[warp] = incl;
+        __syncthreads();
+        int run = incl - own;
+        for (int i = 0; i < warp; ++i) run += ctl->warp_sum[i];
+        for (int b = b0; b < b1; ++b) {
+            ctl->before[b] = run;
+            run += blocks_of(b);
+        }
+        if (b0 < b1 && b1 == p.B) ctl->before[p.B] = run;
+        __syncthreads();
+    }
 
-    // Pieces in the ring, numbered from the unit's first: K(0), V(0), K(1), V(1), ...  With slots for 8 of 5 per tile V(j)
-    // comes a whole tile ahead, K(j + 1) while S_B(j) and PV_A(j) run.
-    auto k_piece = [&](int j) { return j * per_tile; };
-    auto v_piece = [&](int j) { return j * per_tile + KP; };
+    // The unit behind a role's i-th (the first is the pair's own); -1: none, or the wait ran out.
+    const uint32_t r_ue = in_first_cta(b_ue);
+    auto unit_after = [&](int i) {
+        const int s = i & 1;
+        if (!wait_pair(b_uf + 8 * s, (i >> 1) & 1)) return -1;
+        const int u = answered_unit(answers + 16 * s);
+        ptx::fence_proxy_async_smem();  // (read before the launch control writes there again)
+        __syncwarp();
+        if (lane == 0) arrive_remote(r_ue + 8 * s);
+        return u;
+    };
+    const int first_unit = static_cast<int>(blockIdx.x >> 1);
 
     if (warp == 8) {
         // =============================================================== loader
-        int n = 0;      // pieces so far
-        int units = 0;  // whose queries were loaded
+        const uint32_t r_q = in_first_cta(b_q), r_kf = in_first_cta(b_kf);
+        int s = 0, wrap = 0;  // stage and times round of the next key tile
+        int units = 0;        // whose queries were loaded
         bool ok = true;
-        auto slot_free = [&](int i) { return i < kLfSlots || wait_warp(b_empty + 8 * (i % kLfSlots), (i / kLfSlots - 1) & 1); };
-        for (int r = 0; ok; ++r) {
-            const int u = lf_unit_id(r);
-            if (u >= p.units) break;
-            bool bad = false;
-            const LfUnit w = lf_unit(p, u, bad);
-            if (w.tiles == 0) continue;
-            if (units > 0 && !(ok = wait_warp(b_qe, (units - 1) & 1))) break;
+        int u = first_unit;
+        for (int i = 0; u >= 0; ++i) {
+            // the unit after this one: the answer's place is free once all have read the one before last
+            if (rank == 0 && i >= 2 && !(ok = wait_pair(b_ue + 8 * (i & 1), ((i >> 1) - 1) & 1))) break;
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(b_q, (w.n(1) > 0 ? 2 : 1) * KP * kLfSlot);
-                for (int x = 0; x < (w.n(1) > 0 ? 2 : 1); ++x)
-                    for (int i = 0; i < KP; ++i)
-                        ptx::tma_load_4d(sbase + (x * kLfMaxPieces + i) * kLfSlot, &tm_q, b_q, i + 1 < KP ? 64 * i : p.Dn,
-                                         w.q0 + w.row0 + 128 * x, w.head, 0);
+                ptx::mbar_arrive_expect_tx(b_uf + 8 * (i & 1), 16);
+                if (rank == 0) ask_unit(answers + 16 * (i & 1), b_uf + 8 * (i & 1));
             }
-            ++units;
-            for (int j = 0; ok && j < w.tiles; ++j) {
-                const int key = w.k0 + j * 128;
-                for (int i = 0; i < per_tile; ++i, ++n) {
-                    if (!(ok = slot_free(n))) break;
-                    const uint32_t bar = b_full + 8 * (n % kLfSlots), dst = ring + (n % kLfSlots) * kLfSlot;
+            __syncwarp();
+            bool bad = false;
+            const LfUnit w = lf_unit(p, ctl, u, bad);
+            if (w.tiles > 0) {
+                if (units > 0 && !(ok = wait_warp(b_qe, (units - 1) & 1))) break;
+                const int tiles_q = w.nb > 0 ? 2 : 1;
+                if (lane == 0) {
+                    arrive_remote_expect(r_q, tiles_q * KP * kLfQPiece);
+                    for (int x = 0; x < tiles_q; ++x)
+                        for (int d = 0; d < KP; ++d)
+                            tma_load_4d_pair(sbase + (x * kLfMaxPieces + d) * kLfQPiece, &tm_q, r_q, d + 1 < KP ? 64 * d : p.Dn,
+                                             w.q0 + w.row0 + 256 * x + 128 * rank, w.head, 0);
+                }
+                ++units;
+                for (int j = 0; j < w.tiles; ++j) {
+                    const uint32_t stage = sbase + kLfOffK + s * kLfStage;
+                    if (wrap > 0 && !(ok = wait_warp(b_ke + 8 * s, (wrap - 1) & 1))) break;
                     if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(bar, kLfSlot);
-                        if (i + 1 < KP) {
-                            ptx::tma_load_4d(dst, &tm_k, bar, 64 * i, key, w.head, 0);
-                        } else if (i < KP) {
-                            ptx::tma_load_4d(dst, &tm_s, bar, 0, key, 0, 0);
-                        } else {
-                            // two boxes of 64 keys x 64 channels: both channel groups of a half, or both halves
-                            const int h = i - KP;
-                            ptx::tma_load_4d(dst, &tm_v, bar, 0, key + 64 * h, w.head, 0);
-                            ptx::tma_load_4d(dst + kLfSlot / 2, &tm_v, bar, VP == 2 ? 64 : 0, key + (VP == 2 ? 64 * h : 64), w.head, 0);
-                        }
+                        arrive_remote_expect(r_kf + 8 * s, KP * kLfKPiece);
+                        const int key = w.k0 + 128 * j + 64 * rank;
+                        for (int d = 0; d + 1 < KP; ++d) tma_load_4d_pair(stage + d * kLfKPiece, &tm_k, r_kf + 8 * s, 64 * d, key, w.head, 0);
+                        tma_load_4d_pair(stage + (KP - 1) * kLfKPiece, &tm_s, r_kf + 8 * s, 0, key, 0, 0);
                     }
                     __syncwarp();
+                    if (wrap > 0 && !(ok = wait_warp(b_ve + 8 * s, (wrap - 1) & 1))) break;
+                    if (lane == 0) {
+                        ptx::mbar_arrive_expect_tx(b_vf + 8 * s, kLfVTile);
+                        ptx::tma_load_4d(stage + kLfMaxPieces * kLfKPiece, &tm_v, b_vf + 8 * s, p.half_v * rank, w.k0 + 128 * j, w.head, 0);
+                    }
+                    __syncwarp();
+                    if (++s == kLfStages) s = 0, ++wrap;
                 }
+                if (!ok) break;
             }
+            u = unit_after(i);
         }
-        // nothing may still be landing in this CTA's memory when it ends
-        if (units > 0) wait_warp(b_q, (units - 1) & 1);
-        for (int i = max(0, n - kLfSlots); i < n; ++i) wait_warp(b_full + 8 * (i % kLfSlots), (i / kLfSlots) & 1);
+        // nothing may still be landing in this CTA's memory when it ends (queries and keys were read by products that are done)
+        for (int n = 0; n < kLfStages; ++n) {
+            if (--s < 0) s = kLfStages - 1, --wrap;
+            if (wrap >= 0) wait_warp(b_vf + 8 * s, wrap & 1);
+        }
     } else if (warp == 9) {
         // ====================================================== tensor-core issuer
-        const uint32_t types = BF16 ? (1u << 7) | (1u << 10) : 0u;
-        const uint32_t idesc_s = pr_instr(128, 128, false) | types, idesc_pv = pr_instr(128, 64 * VP, true) | types;
-        constexpr uint64_t kStep = kLfSlot / 16;
-        const uint64_t q_desc = pr_desc(sbase, 16, 1024), k_desc = pr_desc(ring, 16, 1024), v_desc = pr_desc(ring, kLfSlot / 2, 1024);
-        int base = 0;        // pieces of the units before
-        uint32_t done[2] = {0, 0};  // key tiles of tile A, B so far
-        int units = 0;
-        bool ok = true;
-        auto full = [&](int i) { return wait_warp(b_full + 8 * (i % kLfSlots), (i / kLfSlots) & 1); };
-        // S_x of the key tile whose first piece is i; the first product with it waits for its pieces, the last frees them
-        auto issue_s = [&](int x, int i, bool first, bool last) {
-            for (int d = 0; d < KP; ++d) {
-                const int at = i + d;
-                if (first) {
-                    if (!full(at)) return false;
-                    ptx::tc_fence_after_sync();
-                }
-                ptx::mma_ss_k64(tmem + x * 128, q_desc + (x * kLfMaxPieces + d) * kStep, k_desc + (at % kLfSlots) * kStep, idesc_s, d > 0);
-                if (last) ptx::tc_commit_elect(b_empty + 8 * (at % kLfSlots));
-            }
-            ptx::tc_commit_elect(b_sf + 8 * x);
-            return true;
-        };
-        auto issue_pv = [&](int x, int i, bool first, bool last, bool accumulate) {
+        if (rank == 0) {
+            const uint32_t types = BF16 ? (1u << 7) | (1u << 10) : 0u;
+            const uint32_t idesc_s = pr_instr(256, 128, false) | types, idesc_pv = pr_instr(256, 2 * p.half_v, true) | types;
+            const uint64_t q_desc = pr_desc(sbase, 16, 1024), k_desc = pr_desc(sbase + kLfOffK, 16, 1024);
+            const uint64_t v_desc = pr_desc(sbase + kLfOffK + kLfMaxPieces * kLfKPiece, 16, 1024);
+            int sk = 0, wk = 0, sv = 0;  // stage (and times round) of the next key tile; stage of the next value tile
+            uint32_t done[2] = {0, 0};   // key tiles of tile A, B so far
+            int units = 0;
+            bool ok = true;
+            auto issue_s = [&](int x, int s, bool last) {
+                for (int d = 0; d < KP; ++d)
+                    mma_pair_k64(tmem + x * 128, q_desc + (x * kLfMaxPieces + d) * (kLfQPiece / 16), k_desc + s * (kLfStage / 16) + d * (kLfKPiece / 16),
+                                 idesc_s, d > 0);
+                commit_pair(b_sf + 8 * x);
+                if (last) commit_pair(b_ke + 8 * s);
+            };
+            auto issue_pv = [&](int x, bool last, bool accumulate) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int at = VP == 2 ? i + h : i;
-                if (first && (h == 0 || VP == 2) && !full(at)) return false;
-                if (!wait_warp((h ? b_pf : b_ph) + 8 * x, done[x] & 1)) return false;
-                ptx::tc_fence_after_sync();
-                ptx::mma_ts_k64(tmem + 256 + x * 128, tmem + x * 128 + 32 * h,
-                                v_desc + (at % kLfSlots) * kStep + (VP == 1 && h ? kStep / 2 : 0), idesc_pv, accumulate || h > 0);
-                ptx::tc_commit_elect((h ? b_or : b_oh) + 8 * x);
-                if (last && (h == 1 || VP == 2)) ptx::tc_commit_elect(b_empty + 8 * (at % kLfSlots));
-            }
-            ++done[x];
-            return true;
-        };
-        for (int r = 0; ok; ++r) {
-            const int u = lf_unit_id(r);
-            if (u >= p.units) break;
-            bool bad = false;
-            const LfUnit w = lf_unit(p, u, bad);
-            if (w.tiles == 0) continue;
-            if (!(ok = wait_warp(b_q, units & 1))) break;
-            ++units;
-            ptx::tc_fence_after_sync();
-            // (S_x overwrites columns that were read before the last weights of the unit before were handed over)
-            for (int x = 0; ok && x < 2; ++x)
-                if (w.n(x) > 0) ok = issue_s(x, base, x == 0 || w.n(0) == 0, x == 1 || w.n(1) == 0);
-            if (w.tiles == 1) ptx::tc_commit_elect(b_qe);
-            for (int j = 0; ok && j < w.tiles; ++j) {
-                const int kn = base + k_piece(j + 1), vn = base + v_piece(j);
-                for (int x = 0; ok && x < 2; ++x) {
-                    const bool other_v = w.n(x ^ 1) > j, other_k = w.n(x ^ 1) > j + 1;
-                    if (j < w.n(x)) ok = issue_pv(x, vn, x == 0 || !other_v, x == 1 || !other_v, j > 0);
-                    if (ok && j + 1 < w.n(x)) {
-                        ok = issue_s(x, kn, x == 0 || !other_k, x == 1 || !other_k);
-                        if (j + 2 == w.tiles && (x == 1 || !other_k)) ptx::tc_commit_elect(b_qe);
-                    }
-                    __syncwarp();
+                for (int h = 0; h < 2; ++h) {
+                    if (!wait_pair((h ? b_pf : b_ph) + 8 * x, done[x] & 1)) return false;
+                    ptx::tc_fence_after_sync();
+                    mma_pair_ts_k64(tmem + 256 + x * 128, tmem + x * 128 + 32 * h, v_desc + sv * (kLfStage / 16) + h * 512, idesc_pv, accumulate || h > 0);
+                    commit_pair((h ? b_or : b_oh) + 8 * x);
                 }
+                if (last) commit_pair(b_ve + 8 * sv);
+                ++done[x];
+                return true;
+            };
+            int u = first_unit;
+            for (int i = 0; ok && u >= 0; ++i) {
+                bool bad = false;
+                const LfUnit w = lf_unit(p, ctl, u, bad);
+                if (w.tiles > 0) {
+                    if (!(ok = wait_pair(b_q, units & 1) && wait_pair(b_kf + 8 * sk, wk & 1))) break;
+                    ++units;
+                    ptx::tc_fence_after_sync();
+                    // (S_x overwrites columns that were read before the last weights of the unit before were handed over)
+                    if (w.na > 0) issue_s(0, sk, w.nb == 0);
+                    if (w.nb > 0) issue_s(1, sk, true);
+                    if (w.tiles == 1) commit_pair(b_qe);
+                    if (++sk == kLfStages) sk = 0, ++wk;
+                    for (int j = 0; ok && j < w.tiles; ++j) {
+                        bool k_ready = false;
+                        for (int x = 0; ok && x < 2; ++x) {
+                            if (j < w.n(x)) ok = issue_pv(x, x == 1 || w.nb <= j, j > 0);
+                            if (ok && j + 1 < w.n(x)) {
+                                if (!k_ready && !(ok = wait_pair(b_kf + 8 * sk, wk & 1))) break;
+                                k_ready = true;
+                                ptx::tc_fence_after_sync();
+                                const bool last = x == 1 || w.nb <= j + 1;
+                                issue_s(x, sk, last);
+                                if (j + 2 == w.tiles && last) commit_pair(b_qe);
+                            }
+                            __syncwarp();
+                        }
+                        if (++sv == kLfStages) sv = 0;
+                        if (j + 1 < w.tiles && ++sk == kLfStages) sk = 0, ++wk;
+                    }
+                }
+                if (ok) u = unit_after(i);
             }
-            base += w.tiles * per_tile;
+            // nothing of the pair may still run on the tensor cores when it ends
+            commit_pair_here(b_drain);
+            __syncwarp();
+            wait_warp(b_drain, 0);
         }
-        // nothing of this CTA may still run on the tensor core when it ends
-        ptx::tc_commit_elect(b_drain);
-        __syncwarp();
-        wait_warp(b_drain, 0);
     } else {
         // ================================================= softmax of tile x
         const int x = warp >> 2, t = tid & 127;
@@ -265,19 +354,19 @@ __global__ void __launch_bounds__(kLfThreads, 1)
         const uint32_t s_addr = tmem + lane_off + x * 128, u_addr = tmem + lane_off + 256 + x * 128;
         const float c2 = p.scale_log2;
         const float2 c2v = make_float2(c2, c2);
+        const uint32_t r_ph = in_first_cta(b_ph + 8 * x), r_pf = in_first_cta(b_pf + 8 * x);
         constexpr float kLimit = BF16 ? 4294967296.f : 32768.f;  // keeps every weight inside the 16-bit type
-        uint32_t n = 0;   // key tiles of this query tile so far
-        int base = 0;     // pieces of the units before
+        uint32_t n = 0;          // key tiles of this query tile so far
+        int s0 = 0, w0 = 0;      // stage (and times round) of the unit's first key tile
         bool ok = true;
-        for (int r = 0; ok; ++r) {
-            const int u = lf_unit_id(r);
-            if (u >= p.units) break;
+        int u = first_unit;
+        for (int i = 0; ok && u >= 0; ++i) {
             bool bad = false;
-            const LfUnit w = lf_unit(p, u, bad);
+            const LfUnit w = lf_unit(p, ctl, u, bad);
             if (bad && tid == 0) report(kBadData);
-            if (w.row0 < 0) continue;
-            const int first_row = w.row0 + 128 * x, row = first_row + t, T = w.n(x), offset = w.nk - w.nq;
-            const bool mine = row < w.nq;
+            const int first_row = w.row0 + 256 * x + 128 * rank, row = first_row + t, T = w.row0 < 0 ? 0 : w.n(x), offset = w.nk - w.nq;
+            int sv = s0, wv = w0;  // of the key tile in work
+            const bool mine = w.row0 >= 0 && row < w.nq;
             float ref = -INFINITY;                    // reference of the raw scores
             float sum = 0.f, rsum = 0.f;              // of the fp32 and of the rounded weights
             for (int j = 0; j < T; ++j, ++n) {
@@ -331,7 +420,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                 auto rescale = [&](float alpha) {
                     const float2 av = make_float2(alpha, alpha);
 #pragma unroll 1
-                    for (int c = 0; c < 64 * VP; c += 16) {
+                    for (int c = 0; c < 2 * p.half_v; c += 16) {
                         uint32_t ov[16];
                         ptx::tmem_ld_32x32b_x16(u_addr + c, ov);
                         ptx::tmem_wait_ld();
@@ -346,23 +435,24 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     }
                     ptx::tmem_wait_st();
                 };
-                // values of keys behind the request's last: zeros (by tile A's warps where A sees the tile)
-                if (key0 + 128 > w.nk && (x == 0 || w.n(0) <= j)) {
-                    const int from = w.nk - key0, vn = base + v_piece(j);
-                    for (int i = 0; i < VP; ++i) {
-                        const int at = vn + i;
-                        if (!(ok = ok && wait_warp(b_full + 8 * (at % kLfSlots), (at / kLfSlots) & 1))) break;
-                        // 1024 16-byte pieces: of 64 keys, twice (channel groups of half i, or both halves)
-                        for (int c = t; c < 1024; c += 128) {
-                            const int key = ((c >> 3) & 63) + 64 * (VP == 2 ? i : c >> 9);
-                            if (key >= from)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(ring + (at % kLfSlots) * kLfSlot + c * 16), "r"(0)
-                                             : "memory");
-                        }
-                    }
-                    if (!ok) break;
+                // this CTA's half of the values is there; those of keys behind the request's last are zeros (written by tile
+                // A's warps where A sees the tile)
+                if (!(ok = wait_warp(b_vf + 8 * sv, wv & 1))) break;
+                const bool zeroed = key0 + 128 > w.nk && (x == 0 || w.na <= j);
+                if (zeroed) {
+                    const uint32_t tile = sbase + kLfOffK + sv * kLfStage + kLfMaxPieces * kLfKPiece;
+                    for (int c = (w.nk - key0) * 8 + t; c < 1024; c += 128)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * 16), "r"(0) : "memory");
                     ptx::fence_proxy_async_smem();
                 }
+                auto hand_over = [&](uint32_t bar) {
+                    ptx::tmem_wait_st();
+                    ptx::tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (zeroed) arrive_remote_release(bar); else arrive_remote(bar);
+                    }
+                };
                 uint32_t pk[32];
                 float2 s = make_float2(0.f, 0.f), rs = make_float2(0.f, 0.f);
                 bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
@@ -388,9 +478,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     weigh(sv, N32{}, ref == -INFINITY ? 0.f : -ref * c2, pk, s, rs);
                 }
                 ptx::tmem_st_32x32b_x32(s_addr, pk);
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(b_ph + 8 * x);
+                hand_over(r_ph);
                 sum += s.x + s.y, rsum += rs.x + rs.y;
                 s = rs = make_float2(0.f, 0.f);
                 {
@@ -419,10 +507,9 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     }
                 }
                 ptx::tmem_st_32x32b_x32(s_addr + 32, pk);
-                ptx::tmem_wait_st();
-                ptx::tc_fence_before_sync();
-                ptx::mbar_arrive(b_pf + 8 * x);
+                hand_over(r_pf);
                 sum += s.x + s.y, rsum += rs.x + rs.y;
+                if (++sv == kLfStages) sv = 0, ++wv;
             }
             // ---- O = U / sum
             if (ok && T > 0) ok = wait_warp(b_or + 8 * x, (n - 1) & 1);
@@ -432,7 +519,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             const long long tok = w.q0 + row;
             uint16_t* dst = p.o + tok * p.o_st + static_cast<long long>(w.head) * p.o_sh;
 #pragma unroll 1
-            for (int c = 0; c < 64 * VP; c += 32) {
+            for (int c = 0; c < 2 * p.half_v; c += 32) {
                 uint32_t ov[32];
                 if (T > 0) {
                     ptx::tmem_ld_32x32b_x32(u_addr + c, ov);
@@ -456,14 +543,17 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             if (mine)
                 p.lse[tok * p.H + w.head] = sum != 0.f ? (ref * c2 + log2f(sum)) * 0.69314718055994531f : -INFINITY;
             ptx::tc_fence_before_sync();  // (U is overwritten behind this thread's next weights)
-            base += w.tiles * per_tile;
+            w0 += (s0 + w.tiles) / kLfStages;
+            s0 = (s0 + w.tiles) % kLfStages;
+            u = unit_after(i);
         }
     }
     ptx::tc_fence_before_sync();
     __syncthreads();
+    cluster_sync();  // neither CTA's memory is written or read by the other any more
     if (warp == 9) {
         ptx::tc_fence_after_sync();
-        ptx::tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem);
     }
 }
 

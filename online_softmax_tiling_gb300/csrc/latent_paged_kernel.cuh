@@ -39,7 +39,7 @@
 // pairs as run at once, whatever the lengths.  Parts of a unit go through a workspace and are joined by a second launch.
 #pragma once
 
-#include "paged_common.cuh"
+#include "pair_ptx.cuh"
 
 namespace fa {
 namespace paged {
@@ -115,102 +115,6 @@ __device__ __forceinline__ uint32_t lat_instr(bool bf16, int n, bool b_mn_major)
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-}
-
-// ---- a pair of CTAs
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-// The shared address `a` in the first CTA of the cluster.
-__device__ __forceinline__ uint32_t in_first_cta(uint32_t a) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(a));
-    return r;
-}
-// An arrival in either CTA.  What it orders is tensor memory (behind the tcgen05 fences) and the execution of what waits for
-// it; a release to the cluster would first wait for all of the SM's memory traffic, the next tile's loads too (1.3 us).
-__device__ __forceinline__ void arrive_remote(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// The same behind writes to shared memory that the tensor cores of the pair are to read.
-__device__ __forceinline__ void arrive_remote_release(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ void arrive_remote_expect(uint32_t bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-// Whether the phase is complete, with what both CTAs did before it visible (does not wait).
-__device__ __forceinline__ bool test_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-// A TMA load into this CTA that signals a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
-        : "memory");
-}
-// D (tmem of both) (+)= A (smem, 64 rows of each) B (smem, half of the columns of each)^T over four steps of 16 along
-// K, 32 bytes of swizzled rows each.  One elected lane of the (converged) warp issues.
-__device__ __forceinline__ void mma_pair_k64(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred e, p0, p1;\n\t.reg .b64 x, y;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p0, %4, 0;\n\t"
-        "setp.eq.b32 p1, %4, %4;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p0;\n\t"
-        "add.s64 x, %1, 2;\n\tadd.s64 y, %2, 2;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t"
-        "add.s64 x, %1, 4;\n\tadd.s64 y, %2, 4;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t"
-        "add.s64 x, %1, 6;\n\tadd.s64 y, %2, 6;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// The same with A in tensor memory (16 elements in 8 columns), B's steps 16 rows of 128 bytes.
-__device__ __forceinline__ void mma_pair_ts_k64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred e, p0, p1;\n\t.reg .b32 x;\n\t.reg .b64 y;\n\t"
-        "elect.sync _|e, 0xffffffff;\n\t"
-        "setp.ne.b32 p0, %4, 0;\n\t"
-        "setp.eq.b32 p1, %4, %4;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p0;\n\t"
-        "add.u32 x, %1, 8;\n\tadd.s64 y, %2, 128;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [x], y, %3, p1;\n\t"
-        "add.u32 x, %1, 16;\n\tadd.s64 y, %2, 256;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [x], y, %3, p1;\n\t"
-        "add.u32 x, %1, 24;\n\tadd.s64 y, %2, 384;\n\t"
-        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [x], y, %3, p1;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrives on `bar` in both CTAs when what the elected lane issued before is done.
-__device__ __forceinline__ void commit_pair(uint32_t bar) {
-    asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
-        "h"(static_cast<unsigned short>(3))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1, int32_t c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
 }
 
 // Device data that cannot be leaves a request without rows or keys.
@@ -338,8 +242,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         if (p.q_box) ptx::prefetch_tensormap(&tm_q);
     }
     if (warp == 5) {
-        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(ptx::smem_addr(&ctl->tmem_base)), "r"(512) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base));
     }
     dependents_may_start();
     wait_for_previous();
@@ -791,10 +694,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 }
             }
             __syncwarp();
-            asm volatile(
-                "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(b_drain)
-                : "memory");
+            commit_pair_here(b_drain);
             __syncwarp();
             wait_warp(b_drain, 0);
         }
@@ -845,7 +745,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     cluster_sync();  // neither CTA's memory is written or read by the other any more
     if (warp == 5) {
         ptx::tc_fence_after_sync();
-        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        tmem_dealloc_pair(tmem);
     }
 }
 
