@@ -292,8 +292,8 @@ int fa_latent_fwd(const fa_latent_args* args) {
     CUtensorMap tq, tk, ts, tv;
     const int keys = std::max(a.Tk, 1);  // (no key at all: nothing is read)
     if (!encode_rows(&tq, a.q, bf16, a.Dn + a.R, a.T, a.H, a.q_stride[0], a.q_stride[1], 128) ||
-        !encode_rows(&tk, a.k, bf16, a.Dn, keys, a.H, a.k_stride[0], a.k_stride[1], 64) ||
-        !encode_rows(&ts, a.k_rope, bf16, a.R, keys, 1, a.k_rope_stride, a.k_rope_stride, 64) ||
+        !encode_rows(&tk, a.k, bf16, a.Dn, keys, a.H, a.k_stride[0], a.k_stride[1], 32) ||
+        !encode_rows(&ts, a.k_rope, bf16, a.R, keys, 1, a.k_rope_stride, a.k_rope_stride, 32) ||
         !encode_rows(&tv, a.v, bf16, a.Dv, keys, a.H, a.v_stride[0], a.v_stride[1], 128))
         return FA_ERR_CUDA;
     const void* fn = bf16 ? reinterpret_cast<const void*>(&pg::latent_fwd_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_fwd_kernel<false>);

@@ -13,9 +13,12 @@
 // shared memory is read 96 bytes a cycle instead of 128, which left nothing for the loads (75 cycles a step instead of 64).
 //   * warps 0-3 / 4-7: softmax of the CTA's rows of tile A / B, a thread per row; weights go to tensor memory;
 //   * warp 8: loads (TMA) and the next unit;
-//   * warp 9 (of the first CTA): products in the order PV_A(j), S_A(j + 1), PV_B(j), S_B(j + 1), each PV in two
-//     halves of 64 keys: while one tile's weights are computed, the tensor cores work for the other.
-// TMEM: S_A 0, S_B 128 (16-bit weights over the first 64 columns), U_A 256, U_B 384.
+//   * warp 9 (of the first CTA): products in the order PV_A(k), S_A(k + 2), PV_B(k), S_B(k + 2) for steps k of 64 keys.
+// The way from a step's scores over its weights to the next scores (weights 1,000 cycles, the signals between two CTAs
+// 300 to 450 each, the products themselves) is longer than what the tensor cores have to do for the other tile
+// meanwhile.  So S is held twice, for steps of 64 keys: S(k + 1) is there before the weights of step k are done.  (Steps
+// of 128 keys and one S: 4,400 cycles per 128 keys, of which the tensor cores worked 2,560.)
+// TMEM: S_A 0 and 64, S_B 128 and 192 (16-bit weights over the first 32 columns of each), U_A 256, U_B 384.
 // Units are handed out by the launch itself: a pair that is done takes the next cluster of the grid that has not begun
 // (clusterlaunchcontrol), asked for one unit ahead, so that its queries and keys are on their way before the last products of this one.
 // (Dealt out in turn, the CTA with the most work had a quarter more than the average.)  They go through heads in groups
@@ -31,7 +34,7 @@
 namespace fa {
 namespace paged {
 
-constexpr int kLfThreads = 320;
+constexpr int kLfThreads = 352;
 constexpr int kLfRows = 512;         // of a unit
 constexpr int kLfQPiece = 128 * 128; // 128 rows x 64 channels
 constexpr int kLfKPiece = 64 * 128;  // 64 keys x 64 channels
@@ -60,9 +63,9 @@ struct LatentFwdParams {
 constexpr int kLfMaxB = 2048;   // requests whose blocks are counted (compact)
 struct LfCtl {
     // signalled in the first CTA by both
-    uint64_t q_full, k_full[kLfStages], p_half[2], p_full[2], unit_empty[2];
+    uint64_t q_full, k_full[kLfStages], v_full[kLfStages], p_full[4], unit_empty[2];   // p: by tile and step parity
     // in both by the tensor core, by the launch control, or by the CTA's own loads
-    uint64_t q_empty, k_empty[kLfStages], v_empty[kLfStages], s_full[2], o_half[2], o_ready[2], unit_full[2], v_full[kLfStages], drain;
+    uint64_t q_empty, k_empty[kLfStages], v_empty[kLfStages], s_full[4], o_ready[4], unit_full[2], v_last[kLfStages], drain[2];
     alignas(16) uint4 unit[2];   // answers of the launch control
     uint32_t tmem_base;
     int warp_sum[kLfThreads / 32];
@@ -74,8 +77,8 @@ static_assert(kLfSmem <= 232448, "shared memory of a CTA");
 struct LfUnit {
     int q0, nq, k0, nk, head;
     int row0;      // first row of the unit in its request
-    int na, nb;    // key tiles that tile A, B sees
-    int tiles;     // the larger
+    int na, nb;    // steps of 64 keys that tile A, B sees
+    int steps, tiles;  // the larger; in key tiles of 128
     __device__ int n(int x) const { return x ? nb : na; }
 };
 
@@ -101,12 +104,12 @@ __device__ __forceinline__ LfUnit lf_unit(const LatentFwdParams& p, const LfCtl*
     if (w.q0 < 0 || w.nq < 0 || w.nq > p.max_q || w.q0 > p.T - w.nq || w.k0 < 0 || w.nk < 0 || w.k0 > p.Tk - w.nk)
         bad = true, w.nq = 0;
     w.row0 = ((w.nq + kLfRows - 1) / kLfRows - 1 - back) * kLfRows;  // (the last block, with the most keys, first; negative: none)
-    auto tiles_of = [&](int i0) {
+    auto steps_of = [&](int i0) {
         const int last = min(i0 + 255, w.nq - 1), limit = p.causal ? min(w.nk, last + 1 + w.nk - w.nq) : w.nk;
-        return w.row0 < 0 || i0 >= w.nq ? 0 : (max(limit, 0) + 127) / 128;
+        return w.row0 < 0 || i0 >= w.nq ? 0 : (max(limit, 0) + 63) / 64;
     };
-    w.na = tiles_of(w.row0), w.nb = tiles_of(w.row0 + 256);
-    w.tiles = max(w.na, w.nb);
+    w.na = steps_of(w.row0), w.nb = steps_of(w.row0 + 256);
+    w.steps = max(w.na, w.nb), w.tiles = (w.steps + 1) / 2;
     return w;
 }
 
@@ -147,30 +150,31 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     const uint32_t b_q = ptx::smem_addr(&ctl->q_full), b_qe = ptx::smem_addr(&ctl->q_empty);
     const uint32_t b_kf = ptx::smem_addr(&ctl->k_full[0]), b_ke = ptx::smem_addr(&ctl->k_empty[0]);
     const uint32_t b_vf = ptx::smem_addr(&ctl->v_full[0]), b_ve = ptx::smem_addr(&ctl->v_empty[0]);
-    const uint32_t b_sf = ptx::smem_addr(&ctl->s_full[0]), b_ph = ptx::smem_addr(&ctl->p_half[0]), b_pf = ptx::smem_addr(&ctl->p_full[0]);
-    const uint32_t b_oh = ptx::smem_addr(&ctl->o_half[0]), b_or = ptx::smem_addr(&ctl->o_ready[0]), b_drain = ptx::smem_addr(&ctl->drain);
+    const uint32_t b_sf = ptx::smem_addr(&ctl->s_full[0]), b_pf = ptx::smem_addr(&ctl->p_full[0]);
+    const uint32_t b_vl = ptx::smem_addr(&ctl->v_last[0]), b_or = ptx::smem_addr(&ctl->o_ready[0]), b_drain = ptx::smem_addr(&ctl->drain[0]);
     const uint32_t b_uf = ptx::smem_addr(&ctl->unit_full[0]), b_ue = ptx::smem_addr(&ctl->unit_empty[0]);
     const uint32_t answers = ptx::smem_addr(&ctl->unit[0]);
-    constexpr int kReaders = 2 * 9 + 1;  // warps that take a unit from an answer: softmax and loader of both, the issuer
+    constexpr int kReaders = 2 * 9 + 2;  // warps that take a unit from an answer: softmax and loader of both, the issuers
     if (tid == 0) {
         ptx::mbar_init(b_q, 2);
-        ptx::mbar_init(b_qe, 1);
+        ptx::mbar_init(b_qe, 2);
         for (int s = 0; s < kLfStages; ++s) {
             ptx::mbar_init(b_kf + 8 * s, 2);
-            ptx::mbar_init(b_ke + 8 * s, 1);
-            ptx::mbar_init(b_vf + 8 * s, 1);
-            ptx::mbar_init(b_ve + 8 * s, 1);
+            ptx::mbar_init(b_ke + 8 * s, 2);
+            ptx::mbar_init(b_vf + 8 * s, 2);
+            ptx::mbar_init(b_ve + 8 * s, 2);
+            ptx::mbar_init(b_vl + 8 * s, 1);
         }
         for (int x = 0; x < 2; ++x) {
-            ptx::mbar_init(b_sf + 8 * x, 1);
-            ptx::mbar_init(b_ph + 8 * x, 8);
-            ptx::mbar_init(b_pf + 8 * x, 8);
-            ptx::mbar_init(b_oh + 8 * x, 1);
-            ptx::mbar_init(b_or + 8 * x, 1);
+            for (int k = 2 * x; k < 2 * x + 2; ++k) {
+                ptx::mbar_init(b_sf + 8 * k, 1);
+                ptx::mbar_init(b_pf + 8 * k, 8);
+                ptx::mbar_init(b_or + 8 * k, 1);
+            }
             ptx::mbar_init(b_uf + 8 * x, 1);
+            ptx::mbar_init(b_drain + 8 * x, 1);
             ptx::mbar_init(b_ue + 8 * x, kReaders);
         }
-        ptx::mbar_init(b_drain, 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tm_q);
         ptx::prefetch_tensormap(&tm_k);
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
 
     if (warp == 8) {
         // =============================================================== loader
-        const uint32_t r_q = in_first_cta(b_q), r_kf = in_first_cta(b_kf);
+        const uint32_t r_q = in_first_cta(b_q), r_kf = in_first_cta(b_kf), r_vf = in_first_cta(b_vf);
         int s = 0, wrap = 0;  // stage and times round of the next key tile
         int units = 0;        // whose queries were loaded
         bool ok = true;
@@ -241,7 +245,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             __syncwarp();
             bool bad = false;
             const LfUnit w = lf_unit(p, ctl, u, bad);
-            if (w.tiles > 0) {
+            if (w.steps > 0) {
                 if (units > 0 && !(ok = wait_warp(b_qe, (units - 1) & 1))) break;
                 const int tiles_q = w.nb > 0 ? 2 : 1;
                 if (lane == 0) {
@@ -257,15 +261,25 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     if (wrap > 0 && !(ok = wait_warp(b_ke + 8 * s, (wrap - 1) & 1))) break;
                     if (lane == 0) {
                         arrive_remote_expect(r_kf + 8 * s, KP * kLfKPiece);
-                        const int key = w.k0 + 128 * j + 64 * rank;
-                        for (int d = 0; d + 1 < KP; ++d) tma_load_4d_pair(stage + d * kLfKPiece, &tm_k, r_kf + 8 * s, 64 * d, key, w.head, 0);
-                        tma_load_4d_pair(stage + (KP - 1) * kLfKPiece, &tm_s, r_kf + 8 * s, 0, key, 0, 0);
+                        for (int h = 0; h < 2; ++h) {  // its half of each step's keys
+                            const int key = w.k0 + 128 * j + 64 * h + 32 * rank;
+                            const uint32_t to = stage + h * (kLfKPiece / 2);
+                            for (int d = 0; d + 1 < KP; ++d) tma_load_4d_pair(to + d * kLfKPiece, &tm_k, r_kf + 8 * s, 64 * d, key, w.head, 0);
+                            tma_load_4d_pair(to + (KP - 1) * kLfKPiece, &tm_s, r_kf + 8 * s, 0, key, 0, 0);
+                        }
                     }
                     __syncwarp();
                     if (wrap > 0 && !(ok = wait_warp(b_ve + 8 * s, (wrap - 1) & 1))) break;
+                    const uint32_t to = stage + kLfMaxPieces * kLfKPiece;
                     if (lane == 0) {
-                        ptx::mbar_arrive_expect_tx(b_vf + 8 * s, kLfVTile);
-                        ptx::tma_load_4d(stage + kLfMaxPieces * kLfKPiece, &tm_v, b_vf + 8 * s, p.half_v * rank, w.k0 + 128 * j, w.head, 0);
+                        if (128 * (j + 1) > w.nk) {  // the softmax warps wait for it themselves, and hand it over with their weights
+                            ptx::mbar_arrive_expect_tx(b_vl + 8 * s, kLfVTile);
+                            ptx::tma_load_4d(to, &tm_v, b_vl + 8 * s, p.half_v * rank, w.k0 + 128 * j, w.head, 0);
+                            arrive_remote(r_vf + 8 * s);
+                        } else {
+                            arrive_remote_expect(r_vf + 8 * s, kLfVTile);
+                            tma_load_4d_pair(to, &tm_v, r_vf + 8 * s, p.half_v * rank, w.k0 + 128 * j, w.head, 0);
+                        }
                     }
                     __syncwarp();
                     if (++s == kLfStages) s = 0, ++wrap;
@@ -274,245 +288,200 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             }
             u = unit_after(i);
         }
-        // nothing may still be landing in this CTA's memory when it ends (queries and keys were read by products that are done)
-        for (int n = 0; n < kLfStages; ++n) {
-            if (--s < 0) s = kLfStages - 1, --wrap;
-            if (wrap >= 0) wait_warp(b_vf + 8 * s, wrap & 1);
-        }
-    } else if (warp == 9) {
-        // ====================================================== tensor-core issuer
+        // (everything that was loaded was read by products, or waited for, before the pair ends)
+    } else if (warp == 9 || warp == 10) {
+        // ============================================ tensor-core issuer of tile x
         if (rank == 0) {
+            const int x = warp - 9;
             const uint32_t types = BF16 ? (1u << 7) | (1u << 10) : 0u;
-            const uint32_t idesc_s = pr_instr(256, 128, false) | types, idesc_pv = pr_instr(256, 2 * p.half_v, true) | types;
-            const uint64_t q_desc = pr_desc(sbase, 16, 1024), k_desc = pr_desc(sbase + kLfOffK, 16, 1024);
-            const uint64_t v_desc = pr_desc(sbase + kLfOffK + kLfMaxPieces * kLfKPiece, 16, 1024);
-            int sk = 0, wk = 0, sv = 0;  // stage (and times round) of the next key tile; stage of the next value tile
-            uint32_t done[2] = {0, 0};   // key tiles of tile A, B so far
+            const uint32_t idesc_s = pr_instr(256, 64, false) | types, idesc_pv = pr_instr(256, 2 * p.half_v, true) | types;
+            const uint64_t qd = pr_desc(sbase + x * kLfMaxPieces * kLfQPiece, 16, 1024);
+            const uint64_t k_desc = pr_desc(sbase + kLfOffK, 16, 1024), v_desc = pr_desc(sbase + kLfOffK + kLfMaxPieces * kLfKPiece, 16, 1024);
+            const uint32_t s_cols = tmem + x * 128, u_cols = tmem + 256 + x * 128, bars = 16 * x;
+            // of the key tile that S is at, and of the value tile: stage, parity, descriptor
+            int sk = 0, sv = 0;
+            uint32_t wk = 0, wv = 0, n = 0;   // n: steps so far
+            uint64_t kd = k_desc, vd = v_desc;
             int units = 0;
             bool ok = true;
-            auto issue_s = [&](int x, int s, bool last) {
-                for (int d = 0; d < KP; ++d)
-                    mma_pair_k64(tmem + x * 128, q_desc + (x * kLfMaxPieces + d) * (kLfQPiece / 16), k_desc + s * (kLfStage / 16) + d * (kLfKPiece / 16),
-                                 idesc_s, d > 0);
-                commit_pair(b_sf + 8 * x);
-                if (last) commit_pair(b_ke + 8 * s);
-            };
-            auto issue_pv = [&](int x, bool last, bool accumulate) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!wait_pair((h ? b_pf : b_ph) + 8 * x, done[x] & 1)) return false;
+            // S of the unit's step s.  Key and value tiles are passed on by both issuers, by the one whose tile does
+            // not see them too.
+            auto issue_s = [&](int s, int mine, int steps) {
+                if (!(s & 1) && !wait_pair_lean(b_kf + 8 * sk, wk)) return false;
+                if (s < mine) {
                     ptx::tc_fence_after_sync();
-                    mma_pair_ts_k64(tmem + 256 + x * 128, tmem + x * 128 + 32 * h, v_desc + sv * (kLfStage / 16) + h * 512, idesc_pv, accumulate || h > 0);
-                    commit_pair((h ? b_or : b_oh) + 8 * x);
+                    const uint32_t odd = (n + s) & 1;
+                    const uint64_t b = kd + (s & 1) * (kLfKPiece / 32);
+                    if (KP == 3) {
+                        mma_pair_k192(s_cols + 64 * odd, qd, b, idesc_s);
+                    } else {
+                        for (int c = 0; c < KP; ++c) mma_pair_k64(s_cols + 64 * odd, qd + c * (kLfQPiece / 16), b + c * (kLfKPiece / 16), idesc_s, c > 0);
+                    }
+                    commit_pair(b_sf + bars + 8 * odd);
                 }
-                if (last) commit_pair(b_ve + 8 * sv);
-                ++done[x];
+                if ((s & 1) || s + 1 == steps) {
+                    commit_pair(b_ke + 8 * sk);
+                    kd += kLfStage / 16;
+                    if (++sk == kLfStages) sk = 0, wk ^= 1, kd = k_desc;
+                }
+                if (s + 1 == steps) commit_pair(b_qe);
                 return true;
             };
             int u = first_unit;
             for (int i = 0; ok && u >= 0; ++i) {
                 bool bad = false;
                 const LfUnit w = lf_unit(p, ctl, u, bad);
-                if (w.tiles > 0) {
-                    if (!(ok = wait_pair(b_q, units & 1) && wait_pair(b_kf + 8 * sk, wk & 1))) break;
+                const int mine = w.n(x), steps = w.steps;
+                if (steps > 0) {
+                    if (!(ok = wait_pair_lean(b_q, units & 1))) break;
                     ++units;
                     ptx::tc_fence_after_sync();
-                    // (S_x overwrites columns that were read before the last weights of the unit before were handed over)
-                    if (w.na > 0) issue_s(0, sk, w.nb == 0);
-                    if (w.nb > 0) issue_s(1, sk, true);
-                    if (w.tiles == 1) commit_pair(b_qe);
-                    if (++sk == kLfStages) sk = 0, ++wk;
-                    for (int j = 0; ok && j < w.tiles; ++j) {
-                        bool k_ready = false;
-                        for (int x = 0; ok && x < 2; ++x) {
-                            if (j < w.n(x)) ok = issue_pv(x, x == 1 || w.nb <= j, j > 0);
-                            if (ok && j + 1 < w.n(x)) {
-                                if (!k_ready && !(ok = wait_pair(b_kf + 8 * sk, wk & 1))) break;
-                                k_ready = true;
-                                ptx::tc_fence_after_sync();
-                                const bool last = x == 1 || w.nb <= j + 1;
-                                issue_s(x, sk, last);
-                                if (j + 2 == w.tiles && last) commit_pair(b_qe);
-                            }
-                            __syncwarp();
+                    // (S overwrites columns that were read, and weights whose product was issued, before)
+                    for (int s = 0; ok && s < min(2, steps); ++s) ok = issue_s(s, mine, steps);
+                    for (int k = 0; ok && k < steps; ++k) {
+                        if (!(k & 1) && !(ok = wait_pair_lean(b_vf + 8 * sv, wv))) break;
+                        if (k < mine) {
+                            const uint32_t odd = (n + k) & 1;
+                            if (!(ok = wait_pair_lean(b_pf + bars + 8 * odd, ((n + k) >> 1) & 1))) break;
+                            ptx::tc_fence_after_sync();
+                            mma_pair_ts_k64(u_cols, s_cols + 64 * odd, vd + (k & 1) * (64 * 128 / 16), idesc_pv, k > 0);
+                            commit_pair(b_or + bars + 8 * odd);
                         }
-                        if (++sv == kLfStages) sv = 0;
-                        if (j + 1 < w.tiles && ++sk == kLfStages) sk = 0, ++wk;
+                        if ((k & 1) || k + 1 == steps) {
+                            commit_pair(b_ve + 8 * sv);
+                            vd += kLfStage / 16;
+                            if (++sv == kLfStages) sv = 0, wv ^= 1, vd = v_desc;
+                        }
+                        if (k + 2 < steps) ok = issue_s(k + 2, mine, steps);
                     }
+                    n += mine;
                 }
                 if (ok) u = unit_after(i);
             }
-            // nothing of the pair may still run on the tensor cores when it ends
-            commit_pair_here(b_drain);
             __syncwarp();
-            wait_warp(b_drain, 0);
+            // nothing of the pair may still run on the tensor cores when it ends
+            commit_pair_here(b_drain + 8 * x);
+            __syncwarp();
+            wait_warp(b_drain + 8 * x, 0);
         }
-    } else {
+    } else if (warp < 8) {
         // ================================================= softmax of tile x
         const int x = warp >> 2, t = tid & 127;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr = tmem + lane_off + x * 128, u_addr = tmem + lane_off + 256 + x * 128;
+        const uint32_t u_addr = tmem + lane_off + 256 + x * 128;
         const float c2 = p.scale_log2;
         const float2 c2v = make_float2(c2, c2);
-        const uint32_t r_ph = in_first_cta(b_ph + 8 * x), r_pf = in_first_cta(b_pf + 8 * x);
         constexpr float kLimit = BF16 ? 4294967296.f : 32768.f;  // keeps every weight inside the 16-bit type
-        uint32_t n = 0;          // key tiles of this query tile so far
-        int s0 = 0, w0 = 0;      // stage (and times round) of the unit's first key tile
+        uint32_t n = 0;          // steps of this query tile so far
+        int s0 = 0;              // stage of the unit's first key tile
+        uint32_t last_phase = 0; // bit s: parity of the next tile in stage s with keys behind its request's last
         bool ok = true;
         int u = first_unit;
         for (int i = 0; ok && u >= 0; ++i) {
             bool bad = false;
             const LfUnit w = lf_unit(p, ctl, u, bad);
             if (bad && tid == 0) report(kBadData);
-            const int first_row = w.row0 + 256 * x + 128 * rank, row = first_row + t, T = w.row0 < 0 ? 0 : w.n(x), offset = w.nk - w.nq;
-            int sv = s0, wv = w0;  // of the key tile in work
+            const int first_row = w.row0 + 256 * x + 128 * rank, row = first_row + t, T = w.n(x), offset = w.nk - w.nq;
             const bool mine = w.row0 >= 0 && row < w.nq;
             float ref = -INFINITY;                    // reference of the raw scores
             float sum = 0.f, rsum = 0.f;              // of the fp32 and of the rounded weights
-            for (int j = 0; j < T; ++j, ++n) {
-                if (!(ok = wait_warp(b_sf + 8 * x, n & 1))) break;
+            for (int k = 0; k < T; ++k, ++n) {
+                const uint32_t at = 16 * x + 8 * (n & 1), s_addr = tmem + lane_off + x * 128 + 64 * (n & 1);
+                if (!(ok = wait_warp(b_sf + at, (n >> 1) & 1))) break;
                 ptx::tc_fence_after_sync();
-                // (taken here so that a later wait on this tile's phase is unambiguous)
-                if (j > 0 && !(ok = wait_warp(b_oh + 8 * x, (n - 1) & 1))) break;
-                const int key0 = j * 128;
-                const bool masked = key0 + 128 > w.nk || (p.causal && key0 + 127 > first_row + offset);
+                const int key0 = 64 * k;
+                const bool masked = key0 + 64 > w.nk || (p.causal && key0 + 63 > first_row + offset);
                 const int seen = (p.causal ? min(w.nk, row + offset + 1) : w.nk) - key0;
-                auto load = [&](auto& sv, int c) {  // scores [32 c, ...), masked
-                    constexpr int N = sizeof(sv) / 4;
-                    if constexpr (N == 64)
-                        ptx::tmem_ld_32x32b_x64(s_addr + 32 * c, sv);
-                    else
-                        ptx::tmem_ld_32x32b_x32(s_addr + 32 * c, sv);
+                auto load = [&](uint32_t(&sv)[64]) {
+                    ptx::tmem_ld_32x32b_x64(s_addr, sv);
                     ptx::tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < N; ++e) ptx::reg_fence(sv[e]);
+                    for (int e = 0; e < 64; ++e) ptx::reg_fence(sv[e]);
                     if (masked) {
 #pragma unroll
-                        for (int e = 0; e < N; ++e)
-                            if (32 * c + e >= seen) sv[e] = __float_as_uint(-INFINITY);
+                        for (int e = 0; e < 64; ++e)
+                            if (e >= seen) sv[e] = __float_as_uint(-INFINITY);
                     }
                 };
-                // weights 2^(c2 x + nr) of 2 N scores, their sum and the sum of the rounded ones
-                auto weigh = [&](const uint32_t* sv, auto count, float nr, uint32_t* pk, float2& s, float2& rs) {
+                uint32_t sv[64], pk[32];
+                float2 s, rs;
+                // weights 2^(c2 (x - ref)), their sum and the sum of the rounded ones
+                auto weigh = [&] {
+                    const float nr = ref == -INFINITY ? 0.f : -ref * c2;
                     const float2 nv = make_float2(nr, nr);
+                    float2 a[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, b[2] = {a[0], a[0]};
 #pragma unroll
-                    for (int e = 0; e < decltype(count)::value; ++e) {
+                    for (int e = 0; e < 32; ++e) {
                         const float2 y = __ffma2_rn(make_float2(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), c2v, nv);
                         const float2 wt = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
-                        s = __fadd2_rn(s, wt);
+                        a[e & 1] = __fadd2_rn(a[e & 1], wt);
                         pk[e] = pack16(wt.x, wt.y, BF16);
-                        rs = __fadd2_rn(rs, unpack16(pk[e], BF16));
+                        b[e & 1] = __fadd2_rn(b[e & 1], unpack16(pk[e], BF16));
                     }
+                    s = __fadd2_rn(a[0], a[1]), rs = __fadd2_rn(b[0], b[1]);
                 };
-                using N32 = std::integral_constant<int, 32>;
-                using N16 = std::integral_constant<int, 16>;
-                auto top_of = [&](int c0, int c1) {
-                    float top = -INFINITY;
-#pragma unroll 1
-                    for (int c = c0; c < c1; ++c) {
-                        uint32_t sv[32];
-                        load(sv, c);
-#pragma unroll
-                        for (int e = 0; e < 32; e += 2) top = ptx::fmax3(top, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
-                    }
-                    return top;
-                };
-                auto rescale = [&](float alpha) {
-                    const float2 av = make_float2(alpha, alpha);
-#pragma unroll 1
-                    for (int c = 0; c < 2 * p.half_v; c += 16) {
-                        uint32_t ov[16];
-                        ptx::tmem_ld_32x32b_x16(u_addr + c, ov);
-                        ptx::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            ptx::reg_fence(ov[e]);
-                            ptx::reg_fence(ov[e + 1]);
-                            const float2 y = __fmul2_rn(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])), av);
-                            ov[e] = __float_as_uint(y.x), ov[e + 1] = __float_as_uint(y.y);
-                        }
-                        ptx::tmem_st_32x32b_x16(u_addr + c, ov);
-                    }
-                    ptx::tmem_wait_st();
-                };
-                // this CTA's half of the values is there; those of keys behind the request's last are zeros (written by tile
-                // A's warps where A sees the tile)
-                if (!(ok = wait_warp(b_vf + 8 * sv, wv & 1))) break;
-                const bool zeroed = key0 + 128 > w.nk && (x == 0 || w.na <= j);
-                if (zeroed) {
-                    const uint32_t tile = sbase + kLfOffK + sv * kLfStage + kLfMaxPieces * kLfKPiece;
-                    for (int c = (w.nk - key0) * 8 + t; c < 1024; c += 128)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * 16), "r"(0) : "memory");
-                    ptx::fence_proxy_async_smem();
-                }
-                auto hand_over = [&](uint32_t bar) {
-                    ptx::tmem_wait_st();
-                    ptx::tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (zeroed) arrive_remote_release(bar); else arrive_remote(bar);
-                    }
-                };
-                uint32_t pk[32];
-                float2 s = make_float2(0.f, 0.f), rs = make_float2(0.f, 0.f);
+                load(sv);
                 bool moved = __any_sync(0xffffffffu, ref == -INFINITY);
                 if (!moved) {
-                    uint32_t sv[64];
-                    load(sv, 0);
-                    weigh(sv, N32{}, -ref * c2, pk, s, rs);
+                    weigh();
+                    // (all weights are positive: their sum bounds each)
                     moved = __any_sync(0xffffffffu, s.x + s.y > kLimit);
                 }
                 if (moved) {
-                    // the tile's maximum; U holds the tiles before (S(j) was issued behind them)
-                    const float top = top_of(0, 4);
+                    // The step's maximum becomes the reference; U, which holds the steps before once the last product is done, is
+                    // rescaled.
+                    load(sv);
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 64; e += 2) top = ptx::fmax3(top, __uint_as_float(sv[e]), __uint_as_float(sv[e + 1]));
                     float alpha = 1.f;
                     if (top > ref) {
                         if (ref != -INFINITY) alpha = ptx::ex2_approx((ref - top) * c2);
                         ref = top;
                     }
-                    if (j > 0) rescale(alpha);
+                    weigh();
+                    if (k > 0) {
+                        if (!(ok = wait_warp(b_or + 16 * x + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1))) break;
+                        ptx::tc_fence_after_sync();
+                        const float2 av = make_float2(alpha, alpha);
+#pragma unroll 1
+                        for (int c = 0; c < 2 * p.half_v; c += 16) {
+                            uint32_t ov[16];
+                            ptx::tmem_ld_32x32b_x16(u_addr + c, ov);
+                            ptx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; e += 2) {
+                                ptx::reg_fence(ov[e]);
+                                ptx::reg_fence(ov[e + 1]);
+                                const float2 y = __fmul2_rn(make_float2(__uint_as_float(ov[e]), __uint_as_float(ov[e + 1])), av);
+                                ov[e] = __float_as_uint(y.x), ov[e + 1] = __float_as_uint(y.y);
+                            }
+                            ptx::tmem_st_32x32b_x16(u_addr + c, ov);
+                        }
+                    }
                     sum *= alpha, rsum *= alpha;
-                    s = rs = make_float2(0.f, 0.f);
-                    uint32_t sv[64];
-                    load(sv, 0);
-                    weigh(sv, N32{}, ref == -INFINITY ? 0.f : -ref * c2, pk, s, rs);
                 }
                 ptx::tmem_st_32x32b_x32(s_addr, pk);
-                hand_over(r_ph);
                 sum += s.x + s.y, rsum += rs.x + rs.y;
-                s = rs = make_float2(0.f, 0.f);
-                {
-                    uint32_t sv[64];
-                    load(sv, 2);
-                    weigh(sv, N32{}, ref == -INFINITY ? 0.f : -ref * c2, pk, s, rs);
+                // values of keys behind the request's last: zeros (by tile A's warps where A sees the step)
+                const bool zeroed = 128 * (k / 2 + 1) > w.nk && (x == 0 || w.na <= k);
+                if (zeroed) {
+                    const int st = (s0 + k / 2) % kLfStages;
+                    if (!(ok = wait_warp(b_vl + 8 * st, (last_phase >> st) & 1))) break;
+                    const uint32_t tile = sbase + kLfOffK + st * kLfStage + kLfMaxPieces * kLfKPiece;
+                    for (int c = max(w.nk, key0) * 8 + t; c < (key0 + 64) * 8; c += 128)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (c - 1024 * (k / 2)) * 16), "r"(0) : "memory");
+                    ptx::fence_proxy_async_smem();
                 }
-                if (__any_sync(0xffffffffu, s.x + s.y > kLimit)) {
-                    // the first half's weights are under way: U takes them in first
-                    const float top = top_of(2, 4);
-                    float alpha = 1.f;
-                    if (top > ref) {
-                        if (ref != -INFINITY) alpha = ptx::ex2_approx((ref - top) * c2);
-                        ref = top;
-                    }
-                    if (!(ok = wait_warp(b_oh + 8 * x, n & 1))) break;
-                    ptx::tc_fence_after_sync();
-                    rescale(alpha);
-                    sum *= alpha, rsum *= alpha;
-                    s = rs = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int c = 2; c < 4; ++c) {
-                        uint32_t sv[32];
-                        load(sv, c);
-                        weigh(sv, N16{}, ref == -INFINITY ? 0.f : -ref * c2, pk + 16 * (c - 2), s, rs);
-                    }
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) {
+                    if (zeroed) arrive_remote_release(in_first_cta(b_pf + at)); else arrive_remote(in_first_cta(b_pf + at));
                 }
-                ptx::tmem_st_32x32b_x32(s_addr + 32, pk);
-                hand_over(r_pf);
-                sum += s.x + s.y, rsum += rs.x + rs.y;
-                if (++sv == kLfStages) sv = 0, ++wv;
             }
             // ---- O = U / sum
-            if (ok && T > 0) ok = wait_warp(b_or + 8 * x, (n - 1) & 1);
+            if (ok && T > 0) ok = wait_warp(b_or + 16 * x + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
             if (!ok) break;
             ptx::tc_fence_after_sync();
             const float inv = rsum != 0.f ? 1.f / rsum : 0.f;
@@ -534,7 +503,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     if (!mine || c + e >= p.Dv) continue;
                     float f[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(ov[e + i]) * inv;
+                    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(ov[e + k]) * inv;
                     *reinterpret_cast<uint4*>(dst + c + e) =
                         make_uint4(pack16(f[0], f[1], BF16), pack16(f[2], f[3], BF16), pack16(f[4], f[5], BF16), pack16(f[6], f[7], BF16));
                 }
@@ -543,7 +512,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             if (mine)
                 p.lse[tok * p.H + w.head] = sum != 0.f ? (ref * c2 + log2f(sum)) * 0.69314718055994531f : -INFINITY;
             ptx::tc_fence_before_sync();  // (U is overwritten behind this thread's next weights)
-            w0 += (s0 + w.tiles) / kLfStages;
+            if (w.tiles > 0 && 128 * w.tiles > w.nk) last_phase ^= 1u << (s0 + w.tiles - 1) % kLfStages;  // (a unit's last tile alone can be one)
             s0 = (s0 + w.tiles) % kLfStages;
             u = unit_after(i);
         }

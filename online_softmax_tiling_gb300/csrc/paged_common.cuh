@@ -137,6 +137,11 @@ __host__ __device__ constexpr uint32_t pr_instr(int m, int n, bool b_mn_major) {
            ((static_cast<uint32_t>(m) >> 4) << 24);
 }
 
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int32_t c0, int32_t c1) {
     asm volatile(

@@ -81,11 +81,6 @@ __device__ __forceinline__ uint4 ldg_codes(const uint8_t* a) {
     return v;
 }
 
-template <int N>
-__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // 16 codes to fp16, stored at two 16-byte chunks of a swizzled row.
 __device__ __forceinline__ void pr_widen16(uint32_t dst0, uint32_t dst1, const uint4& v) {
     const uint32_t c[4] = {v.x, v.y, v.z, v.w};

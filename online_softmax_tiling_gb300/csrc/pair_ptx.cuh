@@ -69,6 +69,23 @@ __device__ __forceinline__ void mma_pair_k64(uint32_t d, uint64_t a, uint64_t b,
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+// The same over twelve steps: three pieces of 64 channels, A's 16 KB apart, B's 8 KB.
+__device__ __forceinline__ void mma_pair_k192(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p0, p1;\n\t.reg .b64 x, y;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p0, %3, %3;\n\t"
+        "setp.eq.b32 p1, %3, %3;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p0;\n\t"
+#define FA_STEP(A, B) "add.s64 x, %1, " #A ";\n\tadd.s64 y, %2, " #B ";\n\t@e tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p1;\n\t"
+        FA_STEP(2, 2) FA_STEP(4, 4) FA_STEP(6, 6)
+        FA_STEP(1024, 512) FA_STEP(1026, 514) FA_STEP(1028, 516) FA_STEP(1030, 518)
+        FA_STEP(2048, 1024) FA_STEP(2050, 1026) FA_STEP(2052, 1028) FA_STEP(2054, 1030)
+#undef FA_STEP
+        "}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc)
+        : "memory");
+}
 // The same with A in tensor memory (16 elements in 8 columns), B's steps 16 rows of 128 bytes.
 __device__ __forceinline__ void mma_pair_ts_k64(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
     asm volatile(
@@ -123,6 +140,33 @@ __device__ __forceinline__ bool wait_pair(uint32_t bar, uint32_t parity) {
         }
     }
     return __all_sync(0xffffffffu, ok);
+}
+
+// The same for the issuer of products, whose every instruction between a barrier and the product behind it is time that the
+// tensor cores may stand still: the time is looked at once in 4096 tries.
+__device__ __forceinline__ bool wait_pair_lean(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    uint64_t t0 = 0;
+    for (;;) {
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .b32 n;\n\tmov.u32 n, 0;\n\t"
+            "AGAIN:\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "@p bra DONE;\n\t"
+            "add.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 4096;\n\t"
+            "@q bra AGAIN;\n\t"
+            "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (__all_sync(0xffffffffu, ok)) return true;
+        const uint64_t now = ptx::globaltimer();
+        if (t0 == 0) t0 = now;
+        if (__any_sync(0xffffffffu, now - t0 > kTimeoutNs)) {
+            report(kTimeout);
+            return false;
+        }
+    }
 }
 
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t holder) {
