@@ -25,7 +25,8 @@
 //     the two warps of a row exchange its maximum and their weights through shared memory;
 //   * warp 4: TMA of the CTA's keys, pages looked up three tiles ahead, in two halves of four pieces with barriers of
 //     their own: S begins with the first half while the second is on its way, and U += P V frees them one by one;
-//   * warp 5 (of the first CTA): tcgen05.mma, S(j + 1) and U += P(j) V(j) in whichever order they become ready;
+//   * warps 5 and 9 (of the first CTA): tcgen05.mma, S and U += P V, each as its operands are ready (one warp for both left the
+//     tensor cores waiting for the instructions between a barrier and the next product);
 //   * warp 6: TMA of the peer's keys as values, half by half behind S, and of channels from 512 on;
 //   * warps 7-8: queries, for the next unit as soon as the last S of this one is done: TMA boxes of gcd(H, 64) heads, or
 //     where these are below eight cp.async.
@@ -45,7 +46,7 @@ namespace fa {
 namespace paged {
 
 constexpr int kLatRows = 128, kLatKeys = 128; // of a unit and a tile; half of each per CTA
-constexpr int kLatThreads = 288;
+constexpr int kLatThreads = 320;
 constexpr int kLatPieces = 9;                 // 64-channel pieces of a row: W <= 576
 constexpr int kLatPiece = 64 * 128;           // 64 rows x 64 16-bit channels, 128-byte swizzle
 constexpr int kLatStages = 2, kLatSlots = 8;  // pieces of a stage
@@ -96,7 +97,7 @@ __host__ __device__ constexpr int lat_channel(int chunk, int half, int C) {
 struct LatCtl {
     // signalled in the first CTA by both: queries, keys, weights, U read; in both by the tensor core, or by the CTA's own loads
     uint64_t q_full, k_full[4], p_full[2], o_empty;                            // k: by stage and half of its pieces
-    uint64_t q_empty, k_empty[4], s_half[2], s_full[2], pv_done[2], v_full[2], drain;
+    uint64_t q_empty, k_empty[4], s_half[2], s_full[2], pv_done[2], v_full[2], drain[2];
     uint32_t tmem_base;
     int start[3];                // request, row block, tile of the share's first unit
     LatRequest first;            // that request
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     const uint32_t b_kf = ptx::smem_addr(&ctl->k_full[0]), b_ke = ptx::smem_addr(&ctl->k_empty[0]);
     const uint32_t b_sh = ptx::smem_addr(&ctl->s_half[0]), b_sf = ptx::smem_addr(&ctl->s_full[0]), b_vf = ptx::smem_addr(&ctl->v_full[0]);
     const uint32_t b_pf = ptx::smem_addr(&ctl->p_full[0]), b_pv = ptx::smem_addr(&ctl->pv_done[0]), b_oe = ptx::smem_addr(&ctl->o_empty);
-    const uint32_t b_drain = ptx::smem_addr(&ctl->drain);
+    const uint32_t b_drain = ptx::smem_addr(&ctl->drain[0]);
     if (tid == 0) {
         ptx::mbar_init(b_qf, 2 * (p.q_box ? 1 : 64));
         ptx::mbar_init(b_qe, 1);
@@ -237,6 +238,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
         ptx::mbar_init(b_oe, 2 * 4);
         ptx::mbar_init(b_drain, 1);
+        ptx::mbar_init(b_drain + 8, 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tm);
         if (p.q_box) ptx::prefetch_tensormap(&tm_q);
@@ -397,7 +399,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 sum += acc.x + acc.y, rsum += racc.x + racc.y;
                 // Both lanes of a row take the weights of all its keys: the product's first half of channels reads lanes
                 // 0-63, the second lanes 64-127.  (Weights go through tensor memory because written to shared memory they would
-                // need a proxy fence.)  Their columns are free once U += P(c - 2) V is done, as it always is: S(c) was issued behind it.
+                // need a proxy fence.)  Their columns are free once U += P(c - 2) V is done, as it always is: tile c's keys lie where its were.
                 if (c >= 2) ok = ok && wait_warp(b_pv + 8 * (c & 1), ((c >> 1) - 1) & 1);
                 const uint32_t p_addr = tmem + lane_off + 384 + 64 * (c & 1);
                 ptx::tmem_st_32x32b_x32(p_addr + 32 * half, pk);
@@ -614,89 +616,73 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         // nothing may still be landing in this CTA's memory when it ends (its keys were read by products that are done)
         for (int i = max(0, c - 2); i < c; ++i) wait_warp(b_vf + 8 * (i & 1), (i >> 1) & 1);
     } else if (warp == 5) {
-        // ================================================== tensor-core issuer
+        // ============================================== tensor-core issuer of S
         if (rank == 0) {
             const uint32_t id_s = lat_instr(BF16, kLatKeys, false);
             const uint64_t q_desc = lat_desc(sbase, 16), k_desc = lat_desc(sbase + kLatOffK, 16), t_desc = lat_desc(sbase + kLatOffTail, 16);
-            const uint64_t v_desc = lat_desc(sbase + kLatOffK, kLatPiece);
             constexpr uint64_t kPieceStep = kLatPiece / 16, kStageStep = kLatSlots * kPieceStep;
-            // S goes through the share's tiles, U += P V after it, each over the parts on its own
-            LatWalk qk(p, ctl, f0, f1);
-            int cq = 0, cp = 0, jq = 0, jp = 0, part_q = 0, part_p = 0, half_q = 0;
-            auto next_part = [](LatWalk& w, int& j) {
-                while (w.next()) {
-                    j = w.lo;
-                    if (w.hi > w.lo) return true;
-                }
-                return false;
-            };
-            auto ready = [](uint32_t bar, int parity) { return __all_sync(0xffffffffu, test_cluster(bar, parity)); };
-            bool q_left = next_part(qk, jq), p_left = next_part(walk, jp);
-            uint64_t since = ptx::globaltimer();
-            int idle = 0;
-            while (p_left) {
-                bool did = false;
-                // S(cq), in halves as its keys arrive (its columns were read before the weights of tile cq - 2 were handed over)
-                if (q_left && cq <= cp + 1 && ready(b_kf + 16 * (cq & 1) + 8 * half_q, (cq >> 1) & 1) &&
-                    (half_q == 1 || jq != qk.lo || ready(b_qf, part_q & 1))) {
+            int c = 0, parts = 0;
+            bool ok = true;
+            while (ok && walk.next()) {
+                if (walk.hi == walk.lo) continue;
+                if (!(ok = wait_pair_lean(b_qf, parts & 1))) break;
+                ++parts;
+                for (int j = walk.lo; j < walk.hi; ++j, ++c) {
+                    const uint32_t d = tmem + 256 + 64 * (c & 1);
+                    const uint64_t kd = k_desc + (c & 1) * kStageStep;
+                    // the scores of tile c - 2 were read before its weights were handed over; then in halves as the keys arrive
+                    if (c >= 2 && !(ok = wait_pair_lean(b_pf + 8 * (c & 1), ((c >> 1) - 1) & 1))) break;
+                    if (!(ok = wait_pair_lean(b_kf + 16 * (c & 1), (c >> 1) & 1))) break;
                     ptx::tc_fence_after_sync();
-                    const uint64_t kd = k_desc + (cq & 1) * kStageStep;
-                    const int end = min(kp, 4 * half_q + 4);
-                    for (int i = 4 * half_q; i < end; ++i)
-                        mma_pair_k64(tmem + 256 + 64 * (cq & 1), q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, i > 0);
-                    if (half_q == 0) {
-                        if (kp > 4) commit_pair(b_sh + 8 * (cq & 1));
-                        half_q = 1;
-                    } else {
-                        if (tail) mma_pair_k64(tmem + 256 + 64 * (cq & 1), q_desc + kLatSlots * kPieceStep, t_desc, id_s, 1u);
-                        commit_pair(b_sf + 8 * (cq & 1));
-                        half_q = 0;
-                        ++cq;
-                        if (++jq == qk.hi) {
-                            commit_pair(b_qe);
-                            ++part_q;
-                            q_left = next_part(qk, jq);
-                        }
-                    }
-                    __syncwarp();
-                    did = true;
-                }
-                if (cp < cq && ready(b_pf + 8 * (cp & 1), (cp >> 1) & 1) && (jp != walk.lo || part_p == 0 || ready(b_oe, (part_p - 1) & 1))) {
+                    for (int i = 0; i < min(kp, 4); ++i) mma_pair_k64(d, q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, i > 0);
+                    if (kp > 4) commit_pair(b_sh + 8 * (c & 1));
+                    if (!(ok = wait_pair_lean(b_kf + 16 * (c & 1) + 8, (c >> 1) & 1))) break;
                     ptx::tc_fence_after_sync();
-                    const uint64_t vd = v_desc + (cp & 1) * kStageStep;
-                    const uint32_t more = jp > walk.lo;
-                    for (int b = 0; b < 2; ++b) {
-                        if (b * 256 < p.C) {
-                            const int wide = p.C - 256 * b > 128 ? 2 : 1;
-                            const uint32_t id = lat_instr(BF16, 128 * wide, true);
-                            const uint64_t vb = vd + 4 * b * kPieceStep;
-                            const uint32_t weights = tmem + 384 + 64 * (cp & 1);
-                            mma_pair_ts_k64(tmem + 128 * b, weights, vb, id, more);
-                            mma_pair_ts_k64(tmem + 128 * b, weights + 32, vb + wide * kPieceStep, id, 1u);
-                        }
-                        commit_pair(b_ke + 16 * (cp & 1) + 8 * b);
-                    }
-                    commit_pair(b_pv + 8 * (cp & 1));
-                    ++cp;
-                    if (++jp == walk.hi) {
-                        ++part_p;
-                        p_left = next_part(walk, jp);
-                    }
-                    __syncwarp();
-                    did = true;
-                }
-                if (did) {
-                    idle = 0;
-                    since = ptx::globaltimer();
-                } else if ((++idle & 1023) == 0 && __any_sync(0xffffffffu, ptx::globaltimer() - since > kTimeoutNs)) {
-                    report(kTimeout);
-                    break;
+                    for (int i = 4; i < min(kp, kLatSlots); ++i) mma_pair_k64(d, q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, 1u);
+                    if (tail) mma_pair_k64(d, q_desc + kLatSlots * kPieceStep, t_desc, id_s, 1u);
+                    commit_pair(b_sf + 8 * (c & 1));
+                    if (j + 1 == walk.hi) commit_pair(b_qe);
                 }
             }
             __syncwarp();
             commit_pair_here(b_drain);
             __syncwarp();
             wait_warp(b_drain, 0);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ====================================== tensor-core issuer of U += P V
+        if (rank == 0) {
+            const uint64_t v_desc = lat_desc(sbase + kLatOffK, kLatPiece);
+            constexpr uint64_t kPieceStep = kLatPiece / 16, kStageStep = kLatSlots * kPieceStep;
+            int c = 0, parts = 0;
+            bool ok = true;
+            while (ok && walk.next()) {
+                if (walk.hi == walk.lo) continue;
+                for (int j = walk.lo; j < walk.hi; ++j, ++c) {
+                    if (j == walk.lo && parts > 0 && !(ok = wait_pair_lean(b_oe, (parts - 1) & 1))) break;
+                    if (!(ok = wait_pair_lean(b_pf + 8 * (c & 1), (c >> 1) & 1))) break;
+                    ptx::tc_fence_after_sync();
+                    const uint64_t vd = v_desc + (c & 1) * kStageStep;
+                    const uint32_t weights = tmem + 384 + 64 * (c & 1);
+                    for (int b = 0; b < 2; ++b) {
+                        if (b * 256 < p.C) {
+                            const int wide = p.C - 256 * b > 128 ? 2 : 1;
+                            const uint32_t id = lat_instr(BF16, 128 * wide, true);
+                            const uint64_t vb = vd + 4 * b * kPieceStep;
+                            mma_pair_ts_k64(tmem + 128 * b, weights, vb, id, j > walk.lo);
+                            mma_pair_ts_k64(tmem + 128 * b, weights + 32, vb + wide * kPieceStep, id, 1u);
+                        }
+                        commit_pair(b_ke + 16 * (c & 1) + 8 * b);
+                    }
+                    commit_pair(b_pv + 8 * (c & 1));
+                }
+                ++parts;
+            }
+            __syncwarp();
+            commit_pair_here(b_drain + 8);
+            __syncwarp();
+            wait_warp(b_drain + 8, 0);
         }
         __syncwarp();
     } else {
