@@ -226,8 +226,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         ptx::mbar_init(b_qf, 2 * (p.q_box ? 1 : 64));
         ptx::mbar_init(b_qe, 1);
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(b_kf + 16 * s, 2);
-            ptx::mbar_init(b_kf + 16 * s + 8, tail ? 4 : 2);
+            ptx::mbar_init(b_kf + 16 * s, tail ? 4 : 2);
+            ptx::mbar_init(b_kf + 16 * s + 8, 2);
             ptx::mbar_init(b_ke + 16 * s, 1);
             ptx::mbar_init(b_ke + 16 * s + 8, 1);
             ptx::mbar_init(b_sh + 8 * s, 1);
@@ -549,14 +549,14 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         // ============================== the peer's keys as values; channels from 512 on
         const uint32_t r_kf = in_first_cta(b_kf);
         auto load_tail = [&](int c, int row) {
-            const uint32_t bar = r_kf + 16 * (c & 1) + 8;
+            const uint32_t bar = r_kf + 16 * (c & 1);
             const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
             if (lane == 0) arrive_remote_expect(bar, n * p.box_rows * 128);
             __syncwarp();
             if (row >= 0) tma_load_2d_pair(sbase + kLatOffTail + lane * p.box_rows * 128, &tm, bar, 64 * kLatSlots, row);
             __syncwarp();
         };
-        // The channels from 512 on go a tile ahead: of tile c + 1 as soon as S(c) is done.
+        // The channels from 512 on go a tile ahead: of tile c + 1 as soon as S(c), which takes them first, is half done.
         LatWalk ahead(p, ctl, f0, f1);
         int ca = 0, ja = 0;
         bool more = tail;
@@ -605,12 +605,12 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                             tma_load_2d(dst + (4 * b + wide * (rank ^ 1) + i) * kLatPiece, &tm, b_vf + 8 * s, 64 * (4 * b + wide * rank + i), row);
                     }
                     __syncwarp();
+                    if (b == 0 && more) {
+                        load_tail(ca++, next_row());
+                        advance();
+                    }
                 }
                 if (!ok) break;
-                if (more) {
-                    load_tail(ca++, next_row());
-                    advance();
-                }
             }
         }
         // nothing may still be landing in this CTA's memory when it ends (its keys were read by products that are done)
@@ -634,12 +634,12 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     if (c >= 2 && !(ok = wait_pair_lean(b_pf + 8 * (c & 1), ((c >> 1) - 1) & 1))) break;
                     if (!(ok = wait_pair_lean(b_kf + 16 * (c & 1), (c >> 1) & 1))) break;
                     ptx::tc_fence_after_sync();
-                    for (int i = 0; i < min(kp, 4); ++i) mma_pair_k64(d, q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, i > 0);
+                    if (tail) mma_pair_k64(d, q_desc + kLatSlots * kPieceStep, t_desc, id_s, 0u);
+                    for (int i = 0; i < min(kp, 4); ++i) mma_pair_k64(d, q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, tail || i > 0);
                     if (kp > 4) commit_pair(b_sh + 8 * (c & 1));
                     if (!(ok = wait_pair_lean(b_kf + 16 * (c & 1) + 8, (c >> 1) & 1))) break;
                     ptx::tc_fence_after_sync();
                     for (int i = 4; i < min(kp, kLatSlots); ++i) mma_pair_k64(d, q_desc + i * kPieceStep, kd + i * kPieceStep, id_s, 1u);
-                    if (tail) mma_pair_k64(d, q_desc + kLatSlots * kPieceStep, t_desc, id_s, 1u);
                     commit_pair(b_sf + 8 * (c & 1));
                     if (j + 1 == walk.hi) commit_pair(b_qe);
                 }
