@@ -95,9 +95,11 @@ __host__ __device__ constexpr int lat_channel(int chunk, int half, int C) {
 }
 
 struct LatCtl {
-    // signalled in the first CTA by both: queries, keys, weights, U read; in both by the tensor core, or by the CTA's own loads
-    uint64_t q_full, k_full[4], p_full[2], o_empty;                            // k: by stage and half of its pieces
-    uint64_t q_empty, k_empty[4], s_half[2], s_full[2], pv_done[2], v_full[2], drain[2];
+    // signalled in the first CTA by both: queries, keys, values, weights, U read; in both by the tensor core; by a CTA's own loads.
+    // k: by stage and half of its pieces; k_empty of the second half says that U += P V of the tile is done
+    uint64_t q_full, k_full[4], v_full[2], p_full[2], o_empty;
+    uint64_t q_empty, k_empty[4], s_half[2], s_full[2], drain[2];
+    uint64_t v_last[2];          // values of a tile with keys that were not loaded
     uint32_t tmem_base;
     int start[3];                // request, row block, tile of the share's first unit
     LatRequest first;            // that request
@@ -184,21 +186,28 @@ struct LatPages {
     }
     __device__ int key(int j, int lane) const { return j * kLatKeys + half * 64 + lane * p.box_rows; }
     __device__ bool wanted(int j, int lane) const { return j < w.hi && lane * p.box_rows < 64 && key(j, lane) < w.load_end; }
+    // bytes of a piece of tile j that both halves load
+    __device__ int both(int j) const { return min(kLatKeys, (w.load_end - j * kLatKeys + p.box_rows - 1) & -p.box_rows) * 128; }
     __device__ int at(int j, int lane) const { return wanted(j, lane) ? ld_meta(trow + (key(j, lane) >> p.page_shift)) : -1; }
     // Has the lane's box of tile j + 2 brought to L2 (a page's rows lie together): one tile is all that fits in shared
     // memory ahead of the one in work, and its load is to take no longer than from there.
     __device__ void prefetch(int j, int lane) const {
-        if (static_cast<unsigned>(page2) >= static_cast<unsigned>(p.num_pages)) return;
+        const bool there = static_cast<unsigned>(page2) < static_cast<unsigned>(p.num_pages);
         const int place = key(j + 2, lane) & ((1 << p.page_shift) - 1);
-        const uint16_t* from = p.cache + (static_cast<long long>(page2) << p.page_shift) * p.W + static_cast<long long>(place) * p.W;
-        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(p.box_rows * p.W * 2) : "memory");
+        const unsigned boxes = __ballot_sync(0xffffffffu, there);
+        const long long row = (static_cast<long long>(page2) << p.page_shift) + place;
+        for (unsigned left = boxes; left; left &= left - 1) {
+            const char* from = reinterpret_cast<const char*>(p.cache + __shfl_sync(0xffffffffu, row, __ffs(left) - 1) * p.W);
+            for (int i = lane * 128; i < p.box_rows * p.W * 2; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+        }
     }
-    // First row of the lane's box of tile j in the cache (-1: not read); moves on to tile j + 1.
+    // First row of the lane's box of tile j in the cache, one before the cache (where TMA reads zeros) if the table names no page
+    // of it; moves on to tile j + 1.
     __device__ int take(int j, int lane) {
         const int ahead = at(j + 3, lane);
         const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
         if (wanted(j, lane) && !there) report(kBadData);
-        const int row = there ? (page << p.page_shift) + (key(j, lane) & ((1 << p.page_shift) - 1)) : -1;
+        const int row = there ? (page << p.page_shift) + (key(j, lane) & ((1 << p.page_shift) - 1)) : -p.box_rows;
         page = page1, page1 = page2, page2 = ahead;
         return row;
     }
@@ -220,19 +229,19 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     const uint32_t b_qf = ptx::smem_addr(&ctl->q_full), b_qe = ptx::smem_addr(&ctl->q_empty);
     const uint32_t b_kf = ptx::smem_addr(&ctl->k_full[0]), b_ke = ptx::smem_addr(&ctl->k_empty[0]);
     const uint32_t b_sh = ptx::smem_addr(&ctl->s_half[0]), b_sf = ptx::smem_addr(&ctl->s_full[0]), b_vf = ptx::smem_addr(&ctl->v_full[0]);
-    const uint32_t b_pf = ptx::smem_addr(&ctl->p_full[0]), b_pv = ptx::smem_addr(&ctl->pv_done[0]), b_oe = ptx::smem_addr(&ctl->o_empty);
+    const uint32_t b_pf = ptx::smem_addr(&ctl->p_full[0]), b_pv = ptx::smem_addr(&ctl->k_empty[1]), b_vl = ptx::smem_addr(&ctl->v_last[0]), b_oe = ptx::smem_addr(&ctl->o_empty);
     const uint32_t b_drain = ptx::smem_addr(&ctl->drain[0]);
     if (tid == 0) {
         ptx::mbar_init(b_qf, 2 * (p.q_box ? 1 : 64));
         ptx::mbar_init(b_qe, 1);
         for (int s = 0; s < 2; ++s) {
-            ptx::mbar_init(b_kf + 16 * s, tail ? 4 : 2);
-            ptx::mbar_init(b_kf + 16 * s + 8, 2);
+            ptx::mbar_init(b_kf + 16 * s, 1);  // (the first CTA's expectation covers both CTAs' loads)
+            ptx::mbar_init(b_kf + 16 * s + 8, 1);
             ptx::mbar_init(b_ke + 16 * s, 1);
             ptx::mbar_init(b_ke + 16 * s + 8, 1);
             ptx::mbar_init(b_sh + 8 * s, 1);
             ptx::mbar_init(b_sf + 8 * s, 1);
-            ptx::mbar_init(b_pv + 8 * s, 1);
+            ptx::mbar_init(b_vl + 8 * s, 1);
             ptx::mbar_init(b_pf + 8 * s, 2 * 4);  // (a warp may be a tile ahead of another)
             ptx::mbar_init(b_vf + 8 * s, 1);
         }
@@ -314,7 +323,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         const uint32_t box = sbase + kLatOffP + warp * 4096, own = box + lane * 128, other = sbase + kLatOffP + (warp ^ 2) * 4096 + lane * 128;
         const uint32_t r_pf = in_first_cta(b_pf), r_oe = in_first_cta(b_oe);
         const int pair_barrier = 1 + (warp & 1);
-        int c = 0;  // tiles so far
+        int c = 0, last_phase = 0;  // tiles so far; phases of v_last
         bool ok = true;  // (after a wait that ran out nothing is waited for, but every barrier of the two warps is still met)
         while (walk.next()) {
             const int r = walk.r0 + rank * 64 + row;
@@ -350,7 +359,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 const bool moves = top > ref + kLatLag;  // (the same in both warps of the row)
                 if (__any_sync(0xffffffffu, moves)) {
                     // U holds the products of the tiles before
-                    if (c > 0) ok = ok && wait_warp(b_pv + 8 * ((c - 1) & 1), ((c - 1) >> 1) & 1);
+                    if (c > 0) ok = ok && wait_warp(b_pv + 16 * ((c - 1) & 1), ((c - 1) >> 1) & 1);
                     ptx::tc_fence_after_sync();
                     float alpha = 1.f;
                     if (moves) {
@@ -399,8 +408,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 sum += acc.x + acc.y, rsum += racc.x + racc.y;
                 // Both lanes of a row take the weights of all its keys: the product's first half of channels reads lanes
                 // 0-63, the second lanes 64-127.  (Weights go through tensor memory because written to shared memory they would
-                // need a proxy fence.)  Their columns are free once U += P(c - 2) V is done, as it always is: tile c's keys lie where its were.
-                if (c >= 2) ok = ok && wait_warp(b_pv + 8 * (c & 1), ((c >> 1) - 1) & 1);
+                // need a proxy fence.)  Their columns are free: U += P(c - 2) V is done, this tile's keys lie where its were.
                 const uint32_t p_addr = tmem + lane_off + 384 + 64 * (c & 1);
                 ptx::tmem_st_32x32b_x32(p_addr + 32 * half, pk);
                 ptx::named_barrier_sync(pair_barrier, 64);
@@ -412,10 +420,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                                  : "memory");
                 ptx::tmem_st_32x32b_x32(p_addr + 32 * (half ^ 1), pk);
                 ptx::tmem_wait_st();
-                // the peer's keys are there as values; rows behind the last key that was loaded may hold anything: as
-                // values they are zeros (S of this tile is done, so nothing else reads them)
-                ok = ok && wait_warp(b_vf + 8 * (c & 1), (c >> 1) & 1);
+                // Rows behind the last key that was loaded may hold anything: as values they are zeros, written once the peer's
+                // keys are there (S of this tile is done, so nothing else reads them).
                 if (key0 + kLatKeys > walk.load_end) {
+                    ok = ok && wait_warp(b_vl + 8 * (c & 1), last_phase >> (c & 1) & 1);
+                    last_phase ^= 1 << (c & 1);
                     const uint32_t stage = sbase + kLatOffK + (c & 1) * (kLatSlots * kLatPiece);
                     for (int s = 0; s < kLatSlots; ++s) {
                         const bool wide = p.C - 256 * (s >> 2) > 128;   // channels of the slot's block: 256 or 128
@@ -437,7 +446,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             // ---- O = U / sum, whole or as a part
             const bool any = walk.hi > walk.lo;
             if (any) {
-                ok = ok && wait_warp(b_pv + 8 * ((c - 1) & 1), ((c - 1) >> 1) & 1);
+                ok = ok && wait_warp(b_pv + 16 * ((c - 1) & 1), ((c - 1) >> 1) & 1);
                 ptx::tc_fence_after_sync();
             }
             // the two halves' sums (the barrier behind the last exchange of maxima has been passed by both)
@@ -530,16 +539,17 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             LatPages pages(p, walk, rank, lane);
             for (int j = walk.lo; ok && j < walk.hi; ++j, ++c) {
                 pages.prefetch(j, lane);
-                const int s = c & 1, row = pages.take(j, lane);
-                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                const int s = c & 1, bytes = pages.both(j);
+                const bool load = pages.wanted(j, lane);
+                const int row = pages.take(j, lane);
                 const uint32_t dst = sbase + kLatOffK + s * (kLatSlots * kLatPiece) + lane * p.box_rows * 128;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int bar = 16 * s + 8 * h, pieces = max(0, min(4, kp - 4 * h));
                     if (c >= kLatStages && !(ok = wait_warp(b_ke + bar, ((c >> 1) - 1) & 1))) break;
-                    if (lane == 0) arrive_remote_expect(r_kf + bar, n * pieces * p.box_rows * 128);
+                    if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(b_kf + bar, bytes * (pieces + (h == 0 && tail ? 1 : 0)));
                     __syncwarp();
-                    if (row >= 0)
+                    if (load)
                         for (int i = 4 * h; i < 4 * h + pieces; ++i) tma_load_2d_pair(dst + i * kLatPiece, &tm, r_kf + bar, 64 * i, row);
                     __syncwarp();
                 }
@@ -547,13 +557,9 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         }
     } else if (warp == 6) {
         // ============================== the peer's keys as values; channels from 512 on
-        const uint32_t r_kf = in_first_cta(b_kf);
+        const uint32_t r_kf = in_first_cta(b_kf), r_vf = in_first_cta(b_vf);
         auto load_tail = [&](int c, int row) {
-            const uint32_t bar = r_kf + 16 * (c & 1);
-            const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
-            if (lane == 0) arrive_remote_expect(bar, n * p.box_rows * 128);
-            __syncwarp();
-            if (row >= 0) tma_load_2d_pair(sbase + kLatOffTail + lane * p.box_rows * 128, &tm, bar, 64 * kLatSlots, row);
+            if (row != INT32_MIN) tma_load_2d_pair(sbase + kLatOffTail + lane * p.box_rows * 128, &tm, r_kf + 16 * (c & 1), 64 * kLatSlots, row);
             __syncwarp();
         };
         // The channels from 512 on go a tile ahead: of tile c + 1 as soon as S(c), which takes them first, is half done.
@@ -561,6 +567,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         int ca = 0, ja = 0;
         bool more = tail;
         int next_page = -1;
+        bool next_wanted = false;
         auto key_of = [&] { return ja * kLatKeys + rank * 64 + lane * p.box_rows; };
         auto advance = [&] {  // to the next tile of the share, its page on its way
             ++ja;
@@ -568,13 +575,14 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 more = ahead.next();
                 if (more) ja = ahead.lo;
             }
-            next_page = -1;
-            if (more && lane * p.box_rows < 64 && key_of() < ahead.load_end)
+            next_wanted = more && lane * p.box_rows < 64 && key_of() < ahead.load_end;
+            if (next_wanted)
                 next_page = ld_meta(p.table + static_cast<long long>(ahead.b) * p.max_pages + (key_of() >> p.page_shift));
         };
         auto next_row = [&] {
+            if (!next_wanted) return INT32_MIN;
             return static_cast<unsigned>(next_page) < static_cast<unsigned>(p.num_pages)
-                       ? (next_page << p.page_shift) + (key_of() & ((1 << p.page_shift) - 1)) : -1;
+                       ? (next_page << p.page_shift) + (key_of() & ((1 << p.page_shift) - 1)) : -p.box_rows;
         };
         if (more) {
             ahead.hi = 0;
@@ -591,18 +599,22 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         while (ok && walk.next()) {
             LatPages pages(p, walk, rank ^ 1, lane);
             for (int j = walk.lo; j < walk.hi; ++j, ++c) {
-                const int s = c & 1, row = pages.take(j, lane);
-                const int n = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                const int s = c & 1;
+                const bool load = pages.wanted(j, lane), last = (j + 1) * kLatKeys > walk.load_end;
+                const int here = __popc(__ballot_sync(0xffffffffu, load)) * p.box_rows * 128, both = pages.both(j), row = pages.take(j, lane);
                 const uint32_t dst = sbase + kLatOffK + s * (kLatSlots * kLatPiece) + lane * p.box_rows * 128;
                 // S has passed the first four pieces, then all: as keys they are not needed any more
                 for (int b = 0; b < 2; ++b) {
                     if (!(ok = wait_warp((b == 0 && kp > 4 ? b_sh : b_sf) + 8 * s, (c >> 1) & 1))) break;
-                    if (b == 0 && lane == 0) ptx::mbar_arrive_expect_tx(b_vf + 8 * s, n * slots * p.box_rows * 128);
+                    if (b == 0 && lane == 0) {
+                        if (last) ptx::mbar_arrive_expect_tx(b_vl + 8 * s, here * slots);
+                        else if (rank == 0) ptx::mbar_arrive_expect_tx(b_vf + 8 * s, both * slots);
+                    }
                     __syncwarp();
-                    if (row >= 0 && b * 256 < p.C) {
+                    if (load && b * 256 < p.C) {
                         const int wide = p.C - 256 * b > 128 ? 2 : 1;
                         for (int i = 0; i < wide; ++i)
-                            tma_load_2d(dst + (4 * b + wide * (rank ^ 1) + i) * kLatPiece, &tm, b_vf + 8 * s, 64 * (4 * b + wide * rank + i), row);
+                            tma_load_2d_pair(dst + (4 * b + wide * (rank ^ 1) + i) * kLatPiece, &tm, last ? b_vl + 8 * s : r_vf + 8 * s, 64 * (4 * b + wide * rank + i), row);
                     }
                     __syncwarp();
                     if (b == 0 && more) {
@@ -613,8 +625,8 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 if (!ok) break;
             }
         }
-        // nothing may still be landing in this CTA's memory when it ends (its keys were read by products that are done)
-        for (int i = max(0, c - 2); i < c; ++i) wait_warp(b_vf + 8 * (i & 1), (i >> 1) & 1);
+        // nothing may still be landing in this CTA's memory when it ends
+        for (int i = max(0, c - 2); i < c; ++i) wait_warp(b_pv + 16 * (i & 1), (i >> 1) & 1);
     } else if (warp == 5) {
         // ============================================== tensor-core issuer of S
         if (rank == 0) {
@@ -655,12 +667,16 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         if (rank == 0) {
             const uint64_t v_desc = lat_desc(sbase + kLatOffK, kLatPiece);
             constexpr uint64_t kPieceStep = kLatPiece / 16, kStageStep = kLatSlots * kPieceStep;
-            int c = 0, parts = 0;
+            int c = 0, parts = 0, v_phase = 0;
             bool ok = true;
             while (ok && walk.next()) {
                 if (walk.hi == walk.lo) continue;
                 for (int j = walk.lo; j < walk.hi; ++j, ++c) {
                     if (j == walk.lo && parts > 0 && !(ok = wait_pair_lean(b_oe, (parts - 1) & 1))) break;
+                    if ((j + 1) * kLatKeys <= walk.load_end) {
+                        if (!(ok = wait_pair_lean(b_vf + 8 * (c & 1), v_phase >> (c & 1) & 1))) break;
+                        v_phase ^= 1 << (c & 1);
+                    }
                     if (!(ok = wait_pair_lean(b_pf + 8 * (c & 1), (c >> 1) & 1))) break;
                     ptx::tc_fence_after_sync();
                     const uint64_t vd = v_desc + (c & 1) * kStageStep;
@@ -675,7 +691,6 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                         }
                         commit_pair(b_ke + 16 * (c & 1) + 8 * b);
                     }
-                    commit_pair(b_pv + 8 * (c & 1));
                 }
                 ++parts;
             }
