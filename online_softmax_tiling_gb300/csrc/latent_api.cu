@@ -43,6 +43,20 @@ bool encode_cache(CUtensorMap* map, const fa_latent_cache& c, bool bf16, int box
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same in boxes of four 64-channel pieces, piece after piece (W a multiple of 64).
+bool encode_cache_pieces(CUtensorMap* map, const fa_latent_cache& c, bool bf16, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t W = static_cast<cuuint64_t>(c.value_dim + c.rope_dim);
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(c.num_pages) * c.page_size, W / 64};
+    const cuuint64_t strides[2] = {W * 2, 128};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 4};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, c.rows, dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Queries [T, H, W] in boxes of 64 channels x `box` heads of one token.
 bool encode_queries(CUtensorMap* map, const fa_latent_paged_args& a, bool bf16, int box_heads) {
     EncodeTiledFn fn = encode_fn();
@@ -237,15 +251,18 @@ int fa_latent_paged_fwd(const fa_latent_paged_args* args) {
     } else {
         p.min_share = INT32_MAX;  // one pair: all of it
     }
-    CUtensorMap tm, tm_q = {};
+    CUtensorMap tm, tm_k = {}, tm_q = {};
     if (!encode_cache(&tm, a.cache, bf16, p.box_rows)) return FA_ERR_CUDA;
+    // four pieces of keys in one load, where a page has a CTA's 64 keys and pieces end with the row
+    p.box_pieces = p.box_rows == 64 && p.W % 64 == 0 ? 4 : 1;
+    if (p.box_pieces > 1 && !encode_cache_pieces(&tm_k, a.cache, bf16, p.box_rows)) return FA_ERR_CUDA;
     // boxes of queries: as many heads as divide both H and a CTA's 64 rows, a whole swizzle pattern (eight rows) at least
     int box = 64;
     while (a.H % box != 0) box /= 2;
     p.q_box = box >= 8 ? box : 0;
     if (p.q_box && !encode_queries(&tm_q, a, bf16, p.q_box)) return FA_ERR_CUDA;
     const void* fn = bf16 ? reinterpret_cast<const void*>(&pg::latent_paged_kernel<true>) : reinterpret_cast<const void*>(&pg::latent_paged_kernel<false>);
-    void* kargs[] = {&tm, &tm_q, &p};
+    void* kargs[] = {&tm, &tm_k, &tm_q, &p};
     if (!ensure_smem(fn, pg::kLatSmem, device) || !launch(fn, 2ll * pl.pairs, 1, pg::kLatThreads, pg::kLatSmem, 2, a.stream, kargs))
         return FA_ERR_CUDA;
     if (need > 0) {

@@ -70,6 +70,7 @@ struct LatentParams {
     int min_share;    // tiles
     int q_box;        // heads of a box of queries (0: read by cp.async)
     int box_rows;
+    int box_pieces;   // of a load of keys: 4 or 1
     int causal;
     float scale_log2;
     float4* o_part;   // the parts of a share's first and last unit: [2 pairs][CTA][warp][32 channels][quad][lane], as lat_part says
@@ -116,6 +117,8 @@ __device__ __forceinline__ uint32_t lat_instr(bool bf16, int n, bool b_mn_major)
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) | ((b_mn_major ? 1u : 0u) << 16) |
            ((static_cast<uint32_t>(n) >> 3) << 17) | ((128u >> 4) << 24);
 }
+// A line on its way to L2, whoever writes it meanwhile.
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
@@ -189,16 +192,14 @@ struct LatPages {
     // bytes of a piece of tile j that both halves load
     __device__ int both(int j) const { return min(kLatKeys, (w.load_end - j * kLatKeys + p.box_rows - 1) & -p.box_rows) * 128; }
     __device__ int at(int j, int lane) const { return wanted(j, lane) ? ld_meta(trow + (key(j, lane) >> p.page_shift)) : -1; }
-    // Has the lane's box of tile j + 2 brought to L2 (a page's rows lie together): one tile is all that fits in shared
-    // memory ahead of the one in work, and its load is to take no longer than from there.
-    __device__ void prefetch(int j, int lane) const {
-        const bool there = static_cast<unsigned>(page2) < static_cast<unsigned>(p.num_pages);
-        const int place = key(j + 2, lane) & ((1 << p.page_shift) - 1);
-        const unsigned boxes = __ballot_sync(0xffffffffu, there);
-        const long long row = (static_cast<long long>(page2) << p.page_shift) + place;
-        for (unsigned left = boxes; left; left &= left - 1) {
+    // Has the boxes of tile j + n, whose pages the lanes have in `of`, brought to L2 (a page's rows lie together): one tile is all
+    // that fits in shared memory ahead of the one in work, and its load is to take no longer than from there.
+    __device__ void prefetch(int j, int n, int of, int lane) const {
+        const int place = key(j + n, lane) & ((1 << p.page_shift) - 1);
+        const long long row = (static_cast<long long>(of) << p.page_shift) + place;
+        for (unsigned left = __ballot_sync(0xffffffffu, static_cast<unsigned>(of) < static_cast<unsigned>(p.num_pages)); left; left &= left - 1) {
             const char* from = reinterpret_cast<const char*>(p.cache + __shfl_sync(0xffffffffu, row, __ffs(left) - 1) * p.W);
-            for (int i = lane * 128; i < p.box_rows * p.W * 2; i += 32 * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(from + i));
+            for (int i = lane * 128; i < p.box_rows * p.W * 2; i += 32 * 128) prefetch_l2(from + i);
         }
     }
     // First row of the lane's box of tile j in the cache, one before the cache (where TMA reads zeros) if the table names no page
@@ -215,7 +216,7 @@ struct LatPages {
 
 template <bool BF16>
 __global__ void __launch_bounds__(kLatThreads, 1)
-    latent_paged_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_q, const LatentParams p) {
+    latent_paged_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_q, const LatentParams p) {
     extern __shared__ __align__(16) uint8_t lat_raw[];
     const uint32_t raw = ptx::smem_addr(lat_raw);
     uint8_t* smem = lat_raw + (((raw + 1023u) & ~1023u) - raw);
@@ -250,12 +251,20 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         ptx::mbar_init(b_drain + 8, 1);
         ptx::fence_mbar_init();
         ptx::prefetch_tensormap(&tm);
+        if (p.box_pieces > 1) ptx::prefetch_tensormap(&tm_k);
         if (p.q_box) ptx::prefetch_tensormap(&tm_q);
     }
     if (warp == 5) {
         tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base));
     }
     dependents_may_start();
+    // lengths and the table on their way to L2, as far as a line per thread goes
+    {
+        const long long i = (static_cast<long long>(blockIdx.x) * kLatThreads + tid) * 32;
+        if (i < p.B) prefetch_l2(p.lens + i);
+        if (p.cu_q && i <= p.B) prefetch_l2(p.cu_q + i);
+        if (i < static_cast<long long>(p.B) * p.max_pages) prefetch_l2(p.table + i);
+    }
     wait_for_previous();
 
     // ---- this pair's share [f0, f1) of all tiles, in order of request, row block, tile
@@ -537,20 +546,39 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         bool ok = true;
         while (ok && walk.next()) {
             LatPages pages(p, walk, rank, lane);
+            if (c > 0 && walk.hi > walk.lo) {
+                // the next unit's queries are loaded when the last S of this one is done, which is to be from L2
+                for (int i = lane; i < 64 && rank * 64 + i < walk.rows; i += 32) {
+                    const int r = walk.r0 + rank * 64 + i;
+                    const char* from = reinterpret_cast<const char*>(p.q + static_cast<long long>(walk.rq.q0 + r / p.H) * p.q_st + static_cast<long long>(r % p.H) * p.q_sh);
+                    for (int x = 0; x < p.W * 2; x += 128) prefetch_l2(from + x);
+                }
+                __syncwarp();
+            }
             for (int j = walk.lo; ok && j < walk.hi; ++j, ++c) {
-                pages.prefetch(j, lane);
+                // The share's first two tiles and queries come first of all from memory, what is to be in L2 after them.
+                if (c == 2) {
+                    if (!(ok = wait_warp(kp > 4 ? b_sh : b_sf, 0))) break;
+                    pages.prefetch(j, 0, pages.page, lane);
+                    pages.prefetch(j, 1, pages.page1, lane);
+                }
+                if (c >= 2) pages.prefetch(j, 2, pages.page2, lane);
                 const int s = c & 1, bytes = pages.both(j);
                 const bool load = pages.wanted(j, lane);
                 const int row = pages.take(j, lane);
                 const uint32_t dst = sbase + kLatOffK + s * (kLatSlots * kLatPiece) + lane * p.box_rows * 128;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int bar = 16 * s + 8 * h, pieces = max(0, min(4, kp - 4 * h));
+                    const int bar = 16 * s + 8 * h, pieces = kp > 4 * h ? max(p.box_pieces, min(4, kp - 4 * h)) : 0;
                     if (c >= kLatStages && !(ok = wait_warp(b_ke + bar, ((c >> 1) - 1) & 1))) break;
                     if (rank == 0 && lane == 0) ptx::mbar_arrive_expect_tx(b_kf + bar, bytes * (pieces + (h == 0 && tail ? 1 : 0)));
                     __syncwarp();
-                    if (load)
-                        for (int i = 4 * h; i < 4 * h + pieces; ++i) tma_load_2d_pair(dst + i * kLatPiece, &tm, r_kf + bar, 64 * i, row);
+                    if (load && pieces > 0) {
+                        if (p.box_pieces > 1)
+                            tma_load_3d_pair(dst + 4 * h * kLatPiece, &tm_k, r_kf + bar, 0, row, 4 * h);
+                        else
+                            for (int i = 4 * h; i < 4 * h + pieces; ++i) tma_load_2d_pair(dst + i * kLatPiece, &tm, r_kf + bar, 64 * i, row);
+                    }
                     __syncwarp();
                 }
             }
