@@ -639,3 +639,51 @@ def test_two_graphs_share_a_workspace():
     _ok()
     for o, l in outs:
         c.check(o, l)
+
+
+def test_expanded_a_long_request_among_many_short_ones():
+    """Requests far shorter than the longest, fewer and more of them than one CTA counts."""
+    torch = _torch()
+    rng = np.random.default_rng(130)
+    for B, H in ((300, 3), (2100, 1)):
+        news = rng.integers(0, 4, B)
+        news[B // 3] = 1500
+        c = Ragged(news, news + rng.integers(0, 40, B) * (news > 0), H, 64, 32, 64, "bf16", 131)
+        out, lse = c.call(check=True)
+        c.check(out, lse)
+        for _ in range(3):
+            again = c.call()
+            assert torch.equal(_bits(again[0]), _bits(out)) and torch.equal(again[1], lse)
+    _ok()
+
+
+def test_same_bits_while_the_memory_is_busy():
+    """Loads that come late or early change nothing."""
+    torch, fa = _torch(), _fa()
+    c = Case([5000, 129, 64, 8000, 1, 3000], [1] * 6, 128, 512, 64, 64, "bf16", 132)
+    d = (c.q.cuda(), c.cache.cuda(), _i32(c.table), _i32(c.lens), c.C, _i32(c.cu), 1)
+    r = Ragged([700, 1, 900], [800, 60, 900], 8, 128, 64, 128, "fp16", 133)
+    ragged = r.args()
+    out, lse = fa.latent_paged_attention_forward(*d, scale=c.scale, check=True)
+    c.check(out, lse)
+    wide, wide_lse = fa.latent_attention_forward(*ragged, 900, 900, check=True)
+    r.check(wide, wide_lse)
+    side, x, y = torch.cuda.Stream(), torch.zeros(1 << 28, dtype=torch.uint8, device="cuda"), torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(20):
+        with torch.cuda.stream(side):
+            y.copy_(x)
+        o, l = fa.latent_paged_attention_forward(*d, scale=c.scale)
+        w, m = fa.latent_attention_forward(*ragged, 900, 900)
+        assert torch.equal(_bits(o), _bits(out)) and torch.equal(l, lse), i
+        assert torch.equal(_bits(w), _bits(wide)) and torch.equal(m, wide_lse), i
+    _ok()
+
+
+@pytest.mark.parametrize("C,R", [(64, 0), (128, 0), (128, 64), (192, 64), (320, 64), (384, 128), (448, 128), (512, 0), (504, 72), (16, 560)])
+def test_absorbed_widths(C, R):
+    """Every number of 64-channel pieces, whole ones and cut ones, in pages of one box and of several."""
+    for P in (16, 128):
+        c = Case([300, 64, 5], [1, 2, 1], 24, C, R, P, "bf16", 134 + C)
+        out, lse = c.call(check=True)
+        c.check(out, lse)
