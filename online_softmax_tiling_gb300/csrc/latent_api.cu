@@ -102,7 +102,7 @@ size_t part_bytes(const fa_latent_paged_args& a, const LatentPlan& pl) {
 }
 size_t latent_workspace(const fa_latent_paged_args& a, const LatentPlan& pl) {
     if (pl.pairs < 2) return 0;
-    return part_bytes(a, pl) + round256(2ull * pl.pairs * pg::kLatRows * 8) + (static_cast<size_t>(pl.pairs) + 1) * 16;
+    return part_bytes(a, pl) + round256(2ull * pl.pairs * pg::kLatRows * 8) + static_cast<size_t>(pl.pairs) * 32;
 }
 
 int check_latent_paged(const fa_latent_paged_args& a) {

@@ -75,7 +75,7 @@ struct LatentParams {
     float scale_log2;
     float4* o_part;   // the parts of a share's first and last unit: [2 pairs][CTA][warp][32 channels][quad][lane], as lat_part says
     float2* stats;    // [2 pairs][128]: log2 of the sums of the fp32 and of the rounded weights
-    int4* shares;     // [pairs + 1]: first unit's begin, end, request, row block; behind the last: the share
+    int4* shares;     // [pairs][2]: the first unit's begin, end and row block, and the share; its request's first row and rows
 };
 
 // Rows and keys of request b, and its units: blocks of 128 rows times tiles of keys (at least one).
@@ -165,7 +165,7 @@ struct LatWalk {
         r0 = block * kLatRows;
         rows = min(kLatRows, rq.nq * p.H - r0);
         const int kend = max(0, limit(r0 + rows - 1)), kt = (kend + kLatKeys - 1) / kLatKeys;
-        load_end = min(rq.len, (kend + p.box_rows - 1) / p.box_rows * p.box_rows);
+        load_end = min(rq.len, (kend + p.box_rows - 1) & -p.box_rows);
         lo = min(first, kt), hi = min(first + n, kt);
         whole = first == 0 && n == rq.tiles;
         at_start = f == f0;
@@ -257,6 +257,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
     if (warp == 5) {
         tmem_alloc_pair(ptx::smem_addr(&ctl->tmem_base));
     }
+    ptx::tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // barriers and tensor memory of both CTAs are there
+    ptx::tc_fence_after_sync();
     dependents_may_start();
     // lengths and the table on their way to L2, as far as a line per thread goes
     {
@@ -290,6 +294,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
         if (lane == 31) before[warp] = incl;
         __syncthreads();
         int run = incl - own, all = 0;
+#pragma unroll
         for (int w = 0; w < kLatThreads / 32; ++w) {
             if (w < warp) run += before[w];
             all += before[w];
@@ -310,15 +315,11 @@ __global__ void __launch_bounds__(kLatThreads, 1)
             }
         }
         ptx::fence_proxy_async_smem();  // (what was read and written here is the queries' memory)
-        ptx::tc_fence_before_sync();
         __syncthreads();
-        cluster_sync();  // barriers and tensor memory of both CTAs are there
-        ptx::tc_fence_after_sync();
         if (p.shares && rank == 0 && tid == 0) {
-            int4 u = make_int4(f0, f0, 0, 0);
-            if (f0 < f1) u = make_int4(f0 - ctl->start[2], f0 - ctl->start[2] + ctl->first.tiles, ctl->start[0], ctl->start[1]);
-            p.shares[pair] = u;
-            if (pair == 0) p.shares[pairs] = make_int4(share, 0, 0, 0);
+            const int begin = f0 - (f0 < f1 ? ctl->start[2] : 0);
+            p.shares[2 * pair] = make_int4(begin, f0 < f1 ? begin + ctl->first.tiles : begin, ctl->start[1], share);
+            p.shares[2 * pair + 1] = make_int4(ctl->first.q0, ctl->first.nq, 0, 0);
         }
     }
     const uint32_t tmem = ctl->tmem_base;
@@ -790,8 +791,8 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const L
     dependents_may_start();
     wait_for_previous();
     const int pairs = static_cast<int>(gridDim.x) + 1, i = blockIdx.x + 1, lane = threadIdx.x & 31, w0 = threadIdx.x >> 5;
-    const int4 unit = ld(p.shares + i);
-    const int share = ld(p.shares + pairs).x;
+    const int4 unit = ld(p.shares + 2 * i), request = ld(p.shares + 2 * i + 1);
+    const int share = unit.w;
     const long long at = static_cast<long long>(i) * share;
     if (unit.x >= at || unit.y <= at || at - share > unit.x) return;  // not inside a unit, or not the first boundary inside
     // part of share i - 1 (its first unit or its last), then the first ones of the shares that begin inside
@@ -800,11 +801,20 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const L
     const int chunk = job % chunks, warp = job / chunks & 3, rank = job / (4 * chunks);
     const int head_slot = unit.x == at - share ? 0 : 1, row = rank * 64 + (warp & 1) * 32 + lane;
     auto part_of = [&](int j) { return static_cast<long long>(i - 1 + j) * 2 + (j == 0 ? head_slot : 0); };
-    bool bad = false;
-    const LatRequest rq = lat_request(p, unit.z, bad);
-    const int r = unit.w * kLatRows + row;
-    const bool mine = r < rq.nq * p.H;
-    if (unit.w * kLatRows + rank * 64 + (warp & 1) * 32 >= rq.nq * p.H) return;  // (the whole CTA's, or a warp's own)
+    const int r = unit.z * kLatRows + row, q0 = request.x, rows = request.y * p.H;
+    const bool mine = r < rows;
+    if (unit.z * kLatRows + rank * 64 + (warp & 1) * 32 >= rows) return;  // (the whole CTA's, or a warp's own)
+    // Two parts of O at a time, the first two on their way while the statistics are read.
+    float4 v[2][8];
+    auto load = [&](int j0) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float4* src = p.o_part + lat_part(part_of(min(j0 + j * STEP, parts - 1)), rank, warp, chunk, p.C) + lane;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[j][e] = ld(src + 32 * e);
+        }
+    };
+    load(SPLIT ? w0 : 0);
     auto stats_of = [&](int j) {
         return mine && j < parts ? ld(p.stats + part_of(j) * kLatRows + row) : make_float2(-INFINITY, -INFINITY);
     };
@@ -818,13 +828,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const L
     const float ref = top == -INFINITY ? 0.f : top, rref = rtop == -INFINITY ? 0.f : rtop;
     float o[32] = {};
     for (int j0 = first; j0 < parts; j0 += 2 * STEP) {
-        float4 v[2][8];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float4* src = p.o_part + lat_part(part_of(min(j0 + j * STEP, parts - 1)), rank, warp, chunk, p.C) + lane;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) v[j][e] = ld(src + 32 * e);
-        }
+        if (j0 > first) load(j0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float2 a = stats_of(j0 + j * STEP);
@@ -838,7 +842,7 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const L
             }
         }
     }
-    const int ch = lat_channel(chunk, warp >> 1, p.C), tok = mine ? rq.q0 + r / p.H : 0, head = r % p.H;
+    const int ch = lat_channel(chunk, warp >> 1, p.C), tok = mine ? q0 + r / p.H : 0, head = r % p.H;
     uint16_t* dst = p.o + static_cast<long long>(tok) * p.o_st + static_cast<long long>(head) * p.o_sh + ch;
     float lse2 = l != 0.f ? ref + log2f(l) : -INFINITY;
     if constexpr (SPLIT) {
