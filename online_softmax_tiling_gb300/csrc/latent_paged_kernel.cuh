@@ -517,7 +517,7 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                     }
                     __syncwarp();
                 }
-            } else if (any) {
+            } else if (any && rank * 64 + (warp & 1) * 32 < walk.rows) {  // (an SM stores 32 bytes per cycle: 2 us for all 128 KB)
                 for (int x = 0; x < lat_chunks(p.C); ++x) {
                     uint32_t ov[32];
                     u_chunk(x, ov);
