@@ -36,32 +36,28 @@ __global__ void __launch_bounds__(kRotaryThreads) latent_append_kernel(const Lat
     const unsigned copied = p.C >> 3, width = copied + (p.r.rows ? p.R >> 4 : p.R >> 3);
     const unsigned item = blockIdx.x * static_cast<unsigned>(kRotaryThreads) + threadIdx.x, token = item / width, col = item - token * width;
     if (token >= static_cast<unsigned>(p.T)) return;
-    const int slot = ld_meta(p.slots + token);
+    // (the slot is needed for the store alone: it is read beside the row's piece, not before it)
+    const int slot = ld_meta(p.slots + token), at = static_cast<int>(col - copied);
+    const bool turned = at >= 0 && p.r.rows;
+    const uint16_t* src = at < 0 ? p.latent + token * p.latent_st : p.rope + token * p.rope_st;
+    const int c0 = at < 0 ? col * 8 : !turned ? at * 8 : p.r.interleaved ? at * 16 : at * 8;
+    const int c1 = turned ? p.r.interleaved ? c0 + 8 : c0 + p.r.half : c0;
+    uint4 u = ld(reinterpret_cast<const uint4*>(src + c0)), v = u;
+    if (turned) {
+        v = ld(reinterpret_cast<const uint4*>(src + c1));
+        if (const int row_at = slot < 0 ? -1 : rotary_position(p.r, token); row_at >= 0) {
+            const float* row = p.r.rows + static_cast<long long>(row_at) * p.R;
+            float c[8], s[8];
+            load_floats8(row + at * 8, c);
+            load_floats8(row + p.r.half + at * 8, s);
+            turn16(u, v, c, s, p.r.interleaved != 0, BF16);
+        }
+    }
     if (slot >= p.num_slots) report(kBadData);
     if (slot < 0 || slot >= p.num_slots) return;
-    uint16_t* dst = p.cache + static_cast<long long>(slot) * (p.C + p.R);
-    if (col < copied) {
-        *reinterpret_cast<uint4*>(dst + col * 8) = ld(reinterpret_cast<const uint4*>(p.latent + token * p.latent_st + col * 8));
-        return;
-    }
-    const int at = col - copied;
-    const uint16_t* src = p.rope + token * p.rope_st;
-    dst += p.C;
-    if (!p.r.rows) {
-        *reinterpret_cast<uint4*>(dst + at * 8) = ld(reinterpret_cast<const uint4*>(src + at * 8));
-        return;
-    }
-    const int c0 = p.r.interleaved ? at * 16 : at * 8, c1 = p.r.interleaved ? c0 + 8 : c0 + p.r.half;
-    uint4 u = ld(reinterpret_cast<const uint4*>(src + c0)), v = ld(reinterpret_cast<const uint4*>(src + c1));
-    if (const int row_at = rotary_position(p.r, token); row_at >= 0) {
-        const float* row = p.r.rows + static_cast<long long>(row_at) * p.R;
-        float c[8], s[8];
-        load_floats8(row + at * 8, c);
-        load_floats8(row + p.r.half + at * 8, s);
-        turn16(u, v, c, s, p.r.interleaved != 0, BF16);
-    }
+    uint16_t* dst = p.cache + static_cast<long long>(slot) * (p.C + p.R) + (at < 0 ? 0 : p.C);
     *reinterpret_cast<uint4*>(dst + c0) = u;
-    *reinterpret_cast<uint4*>(dst + c1) = v;
+    if (turned) *reinterpret_cast<uint4*>(dst + c1) = v;
 }
 
 }  // namespace paged

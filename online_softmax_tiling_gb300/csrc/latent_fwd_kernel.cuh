@@ -13,11 +13,15 @@
 // shared memory is read 96 bytes a cycle instead of 128, which left nothing for the loads (75 cycles a step instead of 64).
 //   * warps 0-3 / 4-7: softmax of the CTA's rows of tile A / B, a thread per row; weights go to tensor memory;
 //   * warp 8: loads (TMA) and the next unit;
-//   * warp 9 (of the first CTA): products in the order PV_A(k), S_A(k + 2), PV_B(k), S_B(k + 2) for steps k of 64 keys.
+//   * warps 9 and 10 (of the first CTA): products of tile A / B, in the order PV(k), S(k + 2) for steps k of 64 keys.  (One warp for
+//     both left the tensor cores idle between a wait and the products behind it: 384 us for what takes 344 with two.)
 // The way from a step's scores over its weights to the next scores (weights 1,000 cycles, the signals between two CTAs
 // 300 to 450 each, the products themselves) is longer than what the tensor cores have to do for the other tile
 // meanwhile.  So S is held twice, for steps of 64 keys: S(k + 1) is there before the weights of step k are done.  (Steps
-// of 128 keys and one S: 4,400 cycles per 128 keys, of which the tensor cores worked 2,560.)
+// of 128 keys and one S: 4,400 cycles per 128 keys, of which the tensor cores worked 2,560.)  A step takes 1,900 cycles, of which the
+// tensor cores work 1,550; the same where tile A, which sees 256 keys less, is done and B goes on alone, which is what the
+// rest is lost to: 32 heads, pieces of 4000 and 2516 queries against up to 4000 keys 330 us, 1.32 PFLOP/s; 8192 queries of
+// 32 heads 246 us, 1.39 PFLOP/s.
 // TMEM: S_A 0 and 64, S_B 128 and 192 (16-bit weights over the first 32 columns of each), U_A 256, U_B 384.
 // Units are handed out by the launch itself: a pair that is done takes the next cluster of the grid that has not begun
 // (clusterlaunchcontrol), asked for one unit ahead, so that its queries and keys are on their way before the last products of this one.
