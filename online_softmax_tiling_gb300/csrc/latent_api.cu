@@ -193,10 +193,11 @@ int fa_latent_cache_append(const fa_latent_cache* cache, const void* latent, lon
     p.T = T, p.C = C, p.R = R, p.num_slots = cache->num_pages * cache->page_size;
     if (rotary) p.r = rotary_table(*rotary);
     int64_t q_ctas = 0;
+    bool single = true;
     if (q) {
         p.q = rotary_work(*rotary, q, nullptr, T, R);
-        p.q.groups = q->heads;
-        const int64_t items = static_cast<int64_t>(T) * q->heads * (p.q.cols + p.q.tail);
+        single = set_groups(p.q) == 1;
+        const int64_t items = static_cast<int64_t>(T) * p.q.groups * (p.q.cols + p.q.tail);
         if (items > INT32_MAX) return FA_ERR_INVALID_ARG;
         q_ctas = (items + pg::kRotaryThreads - 1) / pg::kRotaryThreads;
     }
@@ -204,8 +205,10 @@ int fa_latent_cache_append(const fa_latent_cache* cache, const void* latent, lon
     const int64_t ctas = (items + pg::kRotaryThreads - 1) / pg::kRotaryThreads;
     if (items > INT32_MAX || ctas + q_ctas > INT32_MAX) return FA_ERR_INVALID_ARG;
     p.latent_ctas = static_cast<int>(ctas);
-    const void* fn = dtype == FA_BF16 ? reinterpret_cast<const void*>(&pg::latent_append_kernel<true>)
-                                      : reinterpret_cast<const void*>(&pg::latent_append_kernel<false>);
+    const bool bf16 = dtype == FA_BF16;
+    const void* fn = single ? (bf16 ? reinterpret_cast<const void*>(&pg::latent_append_kernel<1, true>) : reinterpret_cast<const void*>(&pg::latent_append_kernel<1, false>))
+                            : (bf16 ? reinterpret_cast<const void*>(&pg::latent_append_kernel<pg::kRotaryHeads, true>)
+                                    : reinterpret_cast<const void*>(&pg::latent_append_kernel<pg::kRotaryHeads, false>));
     void* args[] = {&p};
     return launch(fn, ctas + q_ctas, 1, pg::kRotaryThreads, 0, 1, stream, args) ? FA_OK : FA_ERR_CUDA;
 }

@@ -23,13 +23,13 @@ struct LatentAppendParams {
     int latent_ctas;
 };
 
-template <bool BF16>
+template <int U, bool BF16>
 __global__ void __launch_bounds__(kRotaryThreads) latent_append_kernel(const LatentAppendParams p) {
     dependents_may_start();
     wait_for_previous();
     if (static_cast<int>(blockIdx.x) >= p.latent_ctas) {
         const unsigned item = (blockIdx.x - p.latent_ctas) * static_cast<unsigned>(kRotaryThreads) + threadIdx.x;
-        if (item < static_cast<unsigned>(p.q.T) * static_cast<unsigned>(p.q.groups * (p.q.cols + p.q.tail))) rotary_item<1, BF16>(p.q, item);
+        if (item < static_cast<unsigned>(p.q.T) * static_cast<unsigned>(p.q.groups * (p.q.cols + p.q.tail))) rotary_item<U, BF16>(p.q, item);
         return;
     }
     // pieces of a row: C / 8 copied, then R / 16 turned (two of 8 channels each) or R / 8 copied

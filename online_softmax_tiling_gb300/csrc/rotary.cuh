@@ -67,12 +67,12 @@ __device__ __forceinline__ void turn16(uint4& u, uint4& v, const float (&c)[8], 
     }
 }
 
-// Item `item` of T x groups x (cols + tail): U heads of one token.
+// Item `item` of T x groups x (cols + tail): U heads of one token, `groups` apart, so that a warp reads neighbouring heads at a time.
 template <int U, bool BF16>
 __device__ __forceinline__ void rotary_item(const RotaryWork& w, unsigned item) {
     const unsigned width = w.cols + w.tail;
     const unsigned rest = item / width, token = rest / w.groups;
-    const int col = item - rest * width, h0 = static_cast<int>(rest - token * w.groups) * U;
+    const int col = item - rest * width, h0 = static_cast<int>(rest - token * w.groups);
     const int all = w.part[0].heads + w.part[1].heads;
     const bool turned = col < w.cols;
     // channels of the item's first and second piece
@@ -83,7 +83,7 @@ __device__ __forceinline__ void rotary_item(const RotaryWork& w, unsigned item) 
     uint16_t* dst[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        const int head = h0 + i;
+        const int head = h0 + i * w.groups;
         dst[i] = nullptr;
         if (head < all) {
             const bool second = head >= w.part[0].heads;
@@ -118,7 +118,7 @@ __device__ __forceinline__ void rotary_item(const RotaryWork& w, unsigned item) 
 }
 
 constexpr int kRotaryThreads = 256;
-constexpr int kRotaryHeads = 4;  // heads of an item where there are items enough
+constexpr int kRotaryHeads = 2;  // heads of an item where there are items enough
 
 template <int U, bool BF16>
 __global__ void __launch_bounds__(kRotaryThreads) rotary_kernel(const RotaryWork w) {
