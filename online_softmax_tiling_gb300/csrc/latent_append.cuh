@@ -2,8 +2,9 @@
 // latent cache [pages, P, C + R], and the queries' R channels turned beside it.
 //
 // What bounds it: HBM for prompts (4 (C + R) bytes per token, 4 H R for the queries), one launch and two
-// dependent reads (slot and position, then the row) for a decode step.  CTAs of the first grid row
-// block take 8-channel pieces of the cache's rows, the others the queries.
+// dependent reads (position, then the table's row) for a decode step.  The first CTAs take 8-channel
+// pieces of the cache's rows, a piece a thread, the others the queries.  18 thousand tokens with 16 heads' queries: 26 us, 4.7 TB/s,
+// of which some 4 us are start and end; 16384 with 128 heads 91.5, 6.3 TB/s; 64 tokens with 128 heads 2.3 us in a graph.
 #pragma once
 
 #include "rotary.cuh"

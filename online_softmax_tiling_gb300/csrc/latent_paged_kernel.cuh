@@ -38,6 +38,14 @@
 //
 // Sharing out.  All (request, 128 rows, tile) of a call, in that order, are dealt out in equal shares to as many
 // pairs as run at once, whatever the lengths.  Parts of a unit go through a workspace and are joined by a second launch.
+//
+// What bounds it.  A tile passes through load (1.1 us), S (1.3, with the other stage's U += P V between its halves), softmax
+// (0.8) and U += P V (0.5 and the signals), 4 us in all, and two are under way: 2.0 us a tile, where HBM would take 1.7
+// and the tensor cores work 1.15.  64 requests of 5000 to 16384 keys, 128 heads: 178 us, 4.5 TB/s and 1.07 PFLOP/s (16 heads: 170);
+// 8 us of it pass before the first product, 12 in the join.  One request of 4096 keys, 32 heads: 13.4 us, latency: lengths,
+// queries and keys, two tiles, parts, the join's start and its reads.
+// Tried: tiles of 64 keys in four stages 186 us (loads of 4 KB: TMA brings an SM 36 bytes a cycle so, 47 in 8 KB, 55 in 32 KB,
+// and a tile needs its keys twice); eight softmax warps 191; a second warp for each kind of load 185; table entries 32 at a time 182.
 #pragma once
 
 #include "pair_ptx.cuh"
