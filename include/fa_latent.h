@@ -32,7 +32,7 @@ typedef struct fa_latent_cache {
 
 /*
  * fa_latent_cache_append - rows of T tokens written into their slots (negative: not stored; beyond the cache:
- * reported and not stored; the same slot twice in a call: one of the rows).
+ * reported and not stored; a slot that a call names twice may hold parts of both rows).
  * latent [T, C], rope [T, R] 16-bit, channels contiguous, token strides in elements (positive multiples of 8), 16-byte aligned.
  * rotary NULL: the R channels are stored as they are.  Else dim must be R, and they are turned (inverse is not taken);
  * q, if given, is [T, heads, R], turned in the same launch.  rope may be NULL where R = 0.
@@ -45,7 +45,7 @@ int fa_latent_cache_append(const fa_latent_cache* cache, const void* latent, lon
  * fa_latent_paged_fwd - absorbed form: O = softmax(scale q c^T) c[:, :C] and the natural log-sum-exp of each
  * request's new queries over its cached rows c.  q [T, H, C + R], o [T, H, C], lse [T, H]; strides, cu_q, lens,
  * block_table, causal, scale, T = 0 and rows that are no request's: as in fa_paged_fwd.
- * dtype is the cache's type too.  Made for few new tokens per request (a unit of work is 64 heads x tokens); whole prompts
+ * dtype is the cache's type too.  Made for few new tokens per request (a unit of work is 128 heads x tokens); whole prompts
  * take any length, but cost less in the expanded form.
  * The softmax runs in 32 bits; its weights enter the second product in the 16-bit type, scaled so that fp16 keeps 11 bits
  * down to 2^-20 of a row's largest.
