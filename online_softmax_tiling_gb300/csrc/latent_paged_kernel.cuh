@@ -40,11 +40,11 @@
 // pairs as run at once, whatever the lengths.  Parts of a unit go through a workspace and are joined by a second launch.
 //
 // What bounds it.  A tile passes through load (1.1 us), S (1.3, with the other stage's U += P V between its halves), softmax
-// (0.8) and U += P V (0.5 and the signals), 4 us in all, and two are under way: 2.0 us a tile, where HBM would take 1.7
-// and the tensor cores work 1.15.  64 requests of 5000 to 16384 keys, 128 heads: 178 us, 4.5 TB/s and 1.07 PFLOP/s (16 heads: 170);
+// (0.8) and U += P V (0.5 and the signals), and two are under way: 1.9 us a tile, where HBM would take 1.7
+// and the tensor cores work 1.15.  64 requests of 5000 to 16384 keys, 128 heads: 165 us, 4.9 TB/s and 1.15 PFLOP/s (16 heads: 158);
 // 8 us of it pass before the first product, 12 in the join.  One request of 4096 keys, 32 heads: 13.4 us, latency: lengths,
 // queries and keys, two tiles, parts, the join's start and its reads.
-// Tried: tiles of 64 keys in four stages 186 us (loads of 4 KB: TMA brings an SM 36 bytes a cycle so, 47 in 8 KB, 55 in 32 KB,
+// Tried (against 178, before what prefetch() says): tiles of 64 keys in four stages 186 us (loads of 4 KB: TMA brings an SM 36 bytes a cycle so, 47 in 8 KB, 55 in 32 KB,
 // and a tile needs its keys twice); eight softmax warps 191; a second warp for each kind of load 185; table entries 32 at a time 182.
 #pragma once
 
@@ -200,14 +200,18 @@ struct LatPages {
     // bytes of a piece of tile j that both halves load
     __device__ int both(int j) const { return min(kLatKeys, (w.load_end - j * kLatKeys + p.box_rows - 1) & -p.box_rows) * 128; }
     __device__ int at(int j, int lane) const { return wanted(j, lane) ? ld_meta(trow + (key(j, lane) >> p.page_shift)) : -1; }
-    // Has the boxes of tile j + n, whose pages the lanes have in `of`, brought to L2 (a page's rows lie together): one tile is all
-    // that fits in shared memory ahead of the one in work, and its load is to take no longer than from there.
-    __device__ void prefetch(int j, int n, int of, int lane) const {
-        const int place = key(j + n, lane) & ((1 << p.page_shift) - 1);
-        const long long row = (static_cast<long long>(of) << p.page_shift) + place;
-        for (unsigned left = __ballot_sync(0xffffffffu, static_cast<unsigned>(of) < static_cast<unsigned>(p.num_pages)); left; left &= left - 1) {
-            const char* from = reinterpret_cast<const char*>(p.cache + __shfl_sync(0xffffffffu, row, __ffs(left) - 1) * p.W);
-            for (int i = lane * 128; i < p.box_rows * p.W * 2; i += 32 * 128) prefetch_l2(from + i);
+    // Has the boxes of tile j brought to L2 (a page's rows lie together) while the tile's place in shared memory is still
+    // taken.  A tile earlier it costs more than it brings, as tiles that are waited for queue behind it (64 requests, 128 heads: 165 us;
+    // one tile ahead 167, two 177, three 193, nothing 200).  By lines where a half is one box, else a box a lane (ragged batch
+    // 165 and 167 us; 64 requests in pages of 16 114 and 106).
+    __device__ void prefetch(int j, int lane) const {
+        const uint16_t* from = p.cache + ((static_cast<long long>(page) << p.page_shift) + (key(j, lane) & ((1 << p.page_shift) - 1))) * p.W;
+        const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(p.num_pages);
+        if (p.box_rows < 64) {
+            if (there) asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"(p.box_rows * p.W * 2) : "memory");
+        } else if (__shfl_sync(0xffffffffu, there, 0)) {
+            const char* at = reinterpret_cast<const char*>(__shfl_sync(0xffffffffu, reinterpret_cast<long long>(from), 0));
+            for (int i = lane * 128; i < 64 * p.W * 2; i += 32 * 128) prefetch_l2(at + i);
         }
     }
     // First row of the lane's box of tile j in the cache, one before the cache (where TMA reads zeros) if the table names no page
@@ -565,13 +569,10 @@ __global__ void __launch_bounds__(kLatThreads, 1)
                 __syncwarp();
             }
             for (int j = walk.lo; ok && j < walk.hi; ++j, ++c) {
-                // The share's first two tiles and queries come first of all from memory, what is to be in L2 after them.
-                if (c == 2) {
-                    if (!(ok = wait_warp(kp > 4 ? b_sh : b_sf, 0))) break;
-                    pages.prefetch(j, 0, pages.page, lane);
-                    pages.prefetch(j, 1, pages.page1, lane);
-                }
-                if (c >= 2) pages.prefetch(j, 2, pages.page2, lane);
+                // A long share's first two tiles and queries come first of all from memory (71 tiles a pair: 166 us, 168 without
+                // this wait; 5 tiles: 29 and 27, so a short one does not wait).
+                if (c == kLatStages && f1 - f0 > 16 && !(ok = wait_warp(kp > 4 ? b_sh : b_sf, 0))) break;
+                if (c >= kLatStages) pages.prefetch(j, lane);
                 const int s = c & 1, bytes = pages.both(j);
                 const bool load = pages.wanted(j, lane);
                 const int row = pages.take(j, lane);
