@@ -28,7 +28,8 @@
 // (Dealt out in turn, the CTA with the most work had a quarter more than the average.)  They go through heads in groups
 // whose keys and values stay in L2, within a group longest first.
 // Requests lie behind one another, so a tile may hold the next request's keys: masked as keys; as values they
-// are overwritten with zeros (weight 0 times infinity or NaN would reach this request).
+// are overwritten with zeros (weight 0 times infinity or NaN would reach this request).  The warps of one query tile do that for
+// both, and both tiles' issuers wait for them: the weights of the other tile say nothing of these values.
 #pragma once
 
 #include <type_traits>
@@ -68,6 +69,7 @@ constexpr int kLfMaxB = 2048;   // requests whose blocks are counted (compact)
 struct LfCtl {
     // signalled in the first CTA by both
     uint64_t q_full, k_full[kLfStages], v_full[kLfStages], p_full[4], unit_empty[2];   // p: by tile and step parity
+    uint64_t v_ready[kLfStages];   // values of a tile with keys behind its request's last are there, zeros written
     // in both by the tensor core, by the launch control, or by the CTA's own loads
     uint64_t q_empty, k_empty[kLfStages], v_empty[kLfStages], s_full[4], o_ready[4], unit_full[2], v_last[kLfStages], drain[2];
     alignas(16) uint4 unit[2];   // answers of the launch control
@@ -84,6 +86,8 @@ struct LfUnit {
     int na, nb;    // steps of 64 keys that tile A, B sees
     int steps, tiles;  // the larger; in key tiles of 128
     __device__ int n(int x) const { return x ? nb : na; }
+    // whether step k is the first of a key tile with keys behind the request's last (the last tile alone can be one)
+    __device__ bool ends_at(int k) const { return k == 2 * (tiles - 1) && 128 * tiles > nk; }
 };
 
 // Unit u: heads in groups, in a group the last block of every (request, head), then the last but one (a request that has
@@ -156,6 +160,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
     const uint32_t b_vf = ptx::smem_addr(&ctl->v_full[0]), b_ve = ptx::smem_addr(&ctl->v_empty[0]);
     const uint32_t b_sf = ptx::smem_addr(&ctl->s_full[0]), b_pf = ptx::smem_addr(&ctl->p_full[0]);
     const uint32_t b_vl = ptx::smem_addr(&ctl->v_last[0]), b_or = ptx::smem_addr(&ctl->o_ready[0]), b_drain = ptx::smem_addr(&ctl->drain[0]);
+    const uint32_t b_vr = ptx::smem_addr(&ctl->v_ready[0]);
     const uint32_t b_uf = ptx::smem_addr(&ctl->unit_full[0]), b_ue = ptx::smem_addr(&ctl->unit_empty[0]);
     const uint32_t answers = ptx::smem_addr(&ctl->unit[0]);
     constexpr int kReaders = 2 * 9 + 2;  // warps that take a unit from an answer: softmax and loader of both, the issuers
@@ -168,6 +173,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             ptx::mbar_init(b_vf + 8 * s, 2);
             ptx::mbar_init(b_ve + 8 * s, 2);
             ptx::mbar_init(b_vl + 8 * s, 1);
+            ptx::mbar_init(b_vr + 8 * s, 8);
         }
         for (int x = 0; x < 2; ++x) {
             for (int k = 2 * x; k < 2 * x + 2; ++k) {
@@ -276,7 +282,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     if (wrap > 0 && !(ok = wait_warp(b_ve + 8 * s, (wrap - 1) & 1))) break;
                     const uint32_t to = stage + kLfMaxPieces * kLfKPiece;
                     if (lane == 0) {
-                        if (128 * (j + 1) > w.nk) {  // the softmax warps wait for it themselves, and hand it over with their weights
+                        if (128 * (j + 1) > w.nk) {  // softmax warps wait for it and write zeros into it: v_ready says that it is there
                             ptx::mbar_arrive_expect_tx(b_vl + 8 * s, kLfVTile);
                             ptx::tma_load_4d(to, &tm_v, b_vl + 8 * s, p.half_v * rank, w.k0 + 128 * j, w.head, 0);
                             arrive_remote(r_vf + 8 * s);
@@ -306,6 +312,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             int sk = 0, sv = 0;
             uint32_t wk = 0, wv = 0, n = 0;   // n: steps so far
             uint64_t kd = k_desc, vd = v_desc;
+            uint32_t ready_phase = 0;  // bit s: parity of the next tile in stage s that v_ready speaks of
             int units = 0;
             bool ok = true;
             // S of the unit's step s.  Key and value tiles are passed on by both issuers, by the one whose tile does
@@ -343,7 +350,13 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                     // (S overwrites columns that were read, and weights whose product was issued, before)
                     for (int s = 0; ok && s < min(2, steps); ++s) ok = issue_s(s, mine, steps);
                     for (int k = 0; ok && k < steps; ++k) {
-                        if (!(k & 1) && !(ok = wait_pair_lean(b_vf + 8 * sv, wv))) break;
+                        if (!(k & 1)) {
+                            if (!(ok = wait_pair_lean(b_vf + 8 * sv, wv))) break;
+                            if (w.ends_at(k)) {
+                                if (!(ok = wait_pair_lean(b_vr + 8 * sv, (ready_phase >> sv) & 1))) break;
+                                ready_phase ^= 1u << sv;
+                            }
+                        }
                         if (k < mine) {
                             const uint32_t odd = (n + k) & 1;
                             if (!(ok = wait_pair_lean(b_pf + bars + 8 * odd, ((n + k) >> 1) & 1))) break;
@@ -467,22 +480,21 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                 }
                 ptx::tmem_st_32x32b_x32(s_addr, pk);
                 sum += s.x + s.y, rsum += rs.x + rs.y;
-                // values of keys behind the request's last: zeros (by tile A's warps where A sees the step)
-                const bool zeroed = 128 * (k / 2 + 1) > w.nk && (x == 0 || w.na <= k);
-                if (zeroed) {
+                // Values of keys behind the request's last: zeros, for both query tiles, by A's warps where A sees the step.
+                if (w.ends_at(k) && x == (w.na > k ? 0 : 1)) {
                     const int st = (s0 + k / 2) % kLfStages;
                     if (!(ok = wait_warp(b_vl + 8 * st, (last_phase >> st) & 1))) break;
                     const uint32_t tile = sbase + kLfOffK + st * kLfStage + kLfMaxPieces * kLfKPiece;
-                    for (int c = max(w.nk, key0) * 8 + t; c < (key0 + 64) * 8; c += 128)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + (c - 1024 * (k / 2)) * 16), "r"(0) : "memory");
+                    for (int c = (w.nk - key0) * 8 + t; c < 128 * 8; c += 128)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(tile + c * 16), "r"(0) : "memory");
                     ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive_remote_release(in_first_cta(b_vr + 8 * st));
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) {
-                    if (zeroed) arrive_remote_release(in_first_cta(b_pf + at)); else arrive_remote(in_first_cta(b_pf + at));
-                }
+                if (lane == 0) arrive_remote(in_first_cta(b_pf + at));
             }
             // ---- O = U / sum
             if (ok && T > 0) ok = wait_warp(b_or + 16 * x + 8 * ((n - 1) & 1), ((n - 1) >> 1) & 1);
@@ -516,7 +528,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
             if (mine)
                 p.lse[tok * p.H + w.head] = sum != 0.f ? (ref * c2 + log2f(sum)) * 0.69314718055994531f : -INFINITY;
             ptx::tc_fence_before_sync();  // (U is overwritten behind this thread's next weights)
-            if (w.tiles > 0 && 128 * w.tiles > w.nk) last_phase ^= 1u << (s0 + w.tiles - 1) % kLfStages;  // (a unit's last tile alone can be one)
+            if (w.tiles > 0 && 128 * w.tiles > w.nk) last_phase ^= 1u << (s0 + w.tiles - 1) % kLfStages;
             s0 = (s0 + w.tiles) % kLfStages;
             u = unit_after(i);
         }

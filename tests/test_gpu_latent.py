@@ -687,3 +687,25 @@ def test_absorbed_widths(C, R):
         c = Case([300, 64, 5], [1, 2, 1], 24, C, R, P, "bf16", 134 + C)
         out, lse = c.call(check=True)
         c.check(out, lse)
+
+
+@pytest.mark.parametrize("news,keys", [([260, 9], [300, 40]), ([300, 80], [360, 80]), ([300, 1], [500, 1]), ([700, 64], [801, 100]), ([513, 30], [513, 100])])
+@pytest.mark.parametrize("causal", [True, False])
+def test_expanded_second_query_tile_beside_broken_values(news, keys, causal):
+    """Requests of more than 256 rows, which two query tiles share, in front of one full of NaN and infinities: both tiles
+    wait for a last tile's values and for the zeros behind them, also where loads come late."""
+    torch, fa = _torch(), _fa()
+    c = Ragged(news, keys, 5, 128, 64, 128, "bf16", 140)
+    clean, clean_lse = c.call(causal=causal, check=True)
+    c.check(clean, clean_lse, causal)
+    a, n = c.cu_k[1], c.cu_q[1]
+    c.kv[a::2], c.kv[a + 1::2], c.shared[a:] = math.nan, math.inf, math.nan
+    broken = c.args()
+    side, x, y = torch.cuda.Stream(), torch.zeros(1 << 28, dtype=torch.uint8, device="cuda"), torch.zeros(1 << 28, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for i in range(20):
+        with torch.cuda.stream(side):
+            y.copy_(x)
+        out, lse = fa.latent_attention_forward(*broken, max(news), max(keys), causal=causal)
+        assert torch.equal(_bits(out[:n]), _bits(clean[:n])) and torch.equal(lse[:n], clean_lse[:n]), i
+    _ok()
