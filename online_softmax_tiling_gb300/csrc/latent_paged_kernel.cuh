@@ -871,7 +871,8 @@ __global__ void __launch_bounds__(32 * kLatJoinWarps) latent_join_kernel(const L
 #pragma unroll
         for (int k = 0; k < kLatJoinWarps; ++k) {
             const float w = s[k].y == -INFINITY ? 0.f : ptx::ex2_approx(s[k].y - rall);
-            l += s[k].x == -INFINITY ? 0.f : s[k].z * ptx::ex2_approx(s[k].x - all);
+            // (by the sum, not by the maximum, which passes over NaN)
+            l += s[k].z == 0.f ? 0.f : s[k].z * ptx::ex2_approx(s[k].x - all);
             rl += s[k].w * w;
             const float4 v = part_o[k][w0][lane];
             sum.x = fmaf(v.x, w, sum.x), sum.y = fmaf(v.y, w, sum.y), sum.z = fmaf(v.z, w, sum.z), sum.w = fmaf(v.w, w, sum.w);

@@ -709,3 +709,25 @@ def test_expanded_second_query_tile_beside_broken_values(news, keys, causal):
         out, lse = fa.latent_attention_forward(*broken, max(news), max(keys), causal=causal)
         assert torch.equal(_bits(out[:n]), _bits(clean[:n])) and torch.equal(lse[:n], clean_lse[:n]), i
     _ok()
+
+
+@pytest.mark.parametrize("lens,H", [([4096], 32), ([70001], 5), ([900], 128), ([3000] * 11, 32), ([2000, 1500, 300], 128)])
+def test_absorbed_nan_through_the_join(lens, H):
+    """A NaN in a query or in a cached row is a NaN in O and in the LSE, however many parts a request was cut into."""
+    torch = _torch()
+    c = Case(lens, [1] * len(lens), H, 128, 64, 64, "bf16", 142)
+    clean, clean_lse = c.call(check=True)
+    b, keep = len(lens) - 1, c.q.clone()
+    c.q[b, H - 2, 5], c.q[0, 0, 150] = math.nan, math.nan
+    out, lse = c.call(check=True)
+    hit = torch.zeros(len(lens), H, dtype=torch.bool, device="cuda")
+    hit[b, H - 2] = hit[0, 0] = True
+    assert out[hit].isnan().all() and lse[hit].isnan().all()
+    assert torch.equal(_bits(out[~hit]), _bits(clean[~hit])) and torch.equal(lse[~hit], clean_lse[~hit])
+    for key, channel in ((0, 3), (lens[b] // 2, 180), (lens[b] - 1, 127)):
+        c.q, was = keep, c.cache.clone()
+        c.cache[c.table[b, key // c.P], key % c.P, channel] = math.nan
+        out, lse = c.call(check=True)
+        assert out[b].isnan().all() and lse[b].isnan().all(), (key, channel)
+        assert torch.equal(_bits(out[:b]), _bits(clean[:b])) and torch.equal(lse[:b], clean_lse[:b])
+        c.cache = was
