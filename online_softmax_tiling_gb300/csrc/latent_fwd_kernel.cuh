@@ -231,9 +231,9 @@ __global__ void __launch_bounds__(kLfThreads, 1)
         const int s = i & 1;
         if (!wait_pair(b_uf + 8 * s, (i >> 1) & 1)) return -1;
         const int u = answered_unit(answers + 16 * s);
-        ptx::fence_proxy_async_smem();  // (read before the launch control writes there again)
+        ptx::fence_proxy_async_smem();  // (read before the launch control, asked by the first CTA, writes there again)
         __syncwarp();
-        if (lane == 0) arrive_remote(r_ue + 8 * s);
+        if (lane == 0) arrive_remote_release(r_ue + 8 * s);
         return u;
     };
     const int first_unit = static_cast<int>(blockIdx.x >> 1);

@@ -24,7 +24,8 @@ __device__ __forceinline__ uint32_t in_first_cta(uint32_t a) {
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-// The same behind writes to shared memory that the tensor cores of the pair are to read.
+// The same behind writes to shared memory that the tensor cores of the pair are to read, or reads of what is written there
+// next at the other CTA's request.
 __device__ __forceinline__ void arrive_remote_release(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
