@@ -85,6 +85,7 @@ size_t fa_latent_paged_workspace_size(const fa_latent_paged_args* args);
  *     cu_k[b] .. cu_k[b + 1] - 1 of k, k_rope and v, its new tokens' own last.  max_k: about the longest request's keys (a
  *     hint for the order of work; any value >= 1 gives the same results).
  *   causal: query i of nq sees keys j <= i + nk - nq.  A query that sees no key gets O = 0 and LSE = -inf.
+ * Softmax and its weights as in fa_latent_paged_fwd.
  * Keys of one request never reach another, whatever they hold; a NaN or infinity in a value that only the causal mask
  * hides may reach its own request's queries.  Rows of o and lse that are no request's are left as they were.
  * A request with marks that cannot be is reported and has no output.

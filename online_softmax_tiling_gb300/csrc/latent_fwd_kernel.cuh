@@ -389,6 +389,9 @@ __global__ void __launch_bounds__(kLfThreads, 1)
         const float c2 = p.scale_log2;
         const float2 c2v = make_float2(c2, c2);
         constexpr float kLimit = BF16 ? 4294967296.f : 32768.f;  // keeps every weight inside the 16-bit type
+        // Weights in fp16 are 2^7 times as large: they keep 11 bits down to 2^-21 of the reference, and only below 2^-32 of it are
+        // they lost (100,000 keys of 2^-25 would be 0.3% of a row; as many of 2^-32 are 2^-15).
+        constexpr float kShift = BF16 ? 0.f : 7.f;
         uint32_t n = 0;          // steps of this query tile so far
         int s0 = 0;              // stage of the unit's first key tile
         uint32_t last_phase = 0; // bit s: parity of the next tile in stage s with keys behind its request's last
@@ -422,9 +425,9 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                 };
                 uint32_t sv[64], pk[32];
                 float2 s, rs;
-                // weights 2^(c2 (x - ref)), their sum and the sum of the rounded ones
+                // weights 2^(c2 (x - ref) + kShift), their sum and the sum of the rounded ones
                 auto weigh = [&] {
-                    const float nr = ref == -INFINITY ? 0.f : -ref * c2;
+                    const float nr = ref == -INFINITY ? 0.f : fmaf(-ref, c2, kShift);
                     const float2 nv = make_float2(nr, nr);
                     float2 a[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)}, b[2] = {a[0], a[0]};
 #pragma unroll
@@ -526,7 +529,7 @@ __global__ void __launch_bounds__(kLfThreads, 1)
                 __syncwarp();
             }
             if (mine)
-                p.lse[tok * p.H + w.head] = sum != 0.f ? (ref * c2 + log2f(sum)) * 0.69314718055994531f : -INFINITY;
+                p.lse[tok * p.H + w.head] = sum != 0.f ? (ref * c2 + (log2f(sum) - kShift)) * 0.69314718055994531f : -INFINITY;
             ptx::tc_fence_before_sync();  // (U is overwritten behind this thread's next weights)
             if (w.tiles > 0 && 128 * w.tiles > w.nk) last_phase ^= 1u << (s0 + w.tiles - 1) % kLfStages;
             s0 = (s0 + w.tiles) % kLfStages;

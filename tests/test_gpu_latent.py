@@ -731,3 +731,25 @@ def test_absorbed_nan_through_the_join(lens, H):
         assert out[b].isnan().all() and lse[b].isnan().all(), (key, channel)
         assert torch.equal(_bits(out[:b]), _bits(clean[:b])) and torch.equal(lse[:b], clean_lse[:b])
         c.cache = was
+
+
+@pytest.mark.parametrize("first", [0, 70, 3999])
+def test_expanded_small_weights_in_fp16(first):
+    """Many keys of 2^-25 to 2^-26 of the largest weight: together they are the output, whether the largest comes first or last.
+    The weights enter the product times 2^7: below the type's normal range each is off by 2^-25 2^-7 of the largest at most, so
+    what lref.tolerances says of such weights holds with a 2^-7th of the largest value."""
+    torch = _torch()
+    n, rows = 4000, 300
+    c = Ragged([rows], [n], 2, 64, 32, 64, "fp16", 144)
+    rng = np.random.default_rng(145)
+    c.q[:], c.shared[:], c.kv[:] = 0, 0, 0
+    c.q[..., 0], c.scale = 1, 1.0
+    c.kv[..., 0] = torch.from_numpy(20 - math.log(2) * rng.uniform(25.1, 25.9, (n, 2))).half()
+    c.kv[..., 64:] = torch.from_numpy(rng.uniform(8, 16, (n, 2, 64))).half()
+    c.kv[first, :, 0], c.kv[first, :, 64:] = 20, 0
+    out, lse = c.call(causal=False, scale=1.0, check=True)
+    O, L, A, S = c.want(False)
+    to, tl = lref.tolerances(O, L, A, S, 96, n, 16 * 2.0 ** -7, torch.float16)
+    assert (O > 5e-4).all() and (to < 0.1 * O).all()
+    assert (np.abs(_f64(out) - O) <= to).all(), np.abs(_f64(out) / O - 1).max()
+    assert (np.abs(_f64(lse) - L) <= tl).all()
