@@ -56,7 +56,8 @@ int fa_rotary_embed(const fa_rotary* rotary, const fa_rotary_part* q, const fa_r
 /*
  * fa_kv_cache_append_rotary - fa_kv_cache_append of keys that are turned first (in fp32: a
  * value is rounded once, to e4m3), and, unless q is NULL, queries [T, heads, cache->d] turned as fa_rotary_embed
- * does, in the same launch.  inverse is not taken (FA_ERR_INVALID_ARG).
+ * does: in the same launch, or where there are many in one of their own behind it (a call that returns an error has turned
+ * none of them).  inverse is not taken (FA_ERR_INVALID_ARG).
  */
 int fa_kv_cache_append_rotary(const fa_kv_cache* cache, const void* k, const void* v, const int* slots, int T,
                               const long long* k_stride, const long long* v_stride, const fa_rotary* rotary,

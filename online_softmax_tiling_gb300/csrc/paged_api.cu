@@ -272,6 +272,7 @@ int append(const fa_kv_cache* cache, const void* k, const void* v, const int* sl
     const int64_t columns = (static_cast<int64_t>(T) + p.chunk - 1) / p.chunk;
     p.pair_rows = (2 * p.Hk + p.pairs - 1) / p.pairs;
     int64_t rows = p.pair_rows;
+    pg::RotaryWork queries = {};
     const void* fn = rotary ? append_kernel<true>(cache->page_size, p.d, bf16, p.bounds != nullptr)
                             : append_kernel<false>(cache->page_size, p.d, bf16, p.bounds != nullptr);
     if (rotary) {
@@ -282,10 +283,9 @@ int append(const fa_kv_cache* cache, const void* k, const void* v, const int* sl
             const int64_t items = static_cast<int64_t>(T) * q->heads * (p.q.cols + p.q.tail);
             if (items > INT32_MAX) return FA_ERR_INVALID_ARG;
             if (items > 1024ll * sm_count()) {
-                // Many: a launch of their own, at the occupancy that turning alone has (22 thousand tokens of 32 heads, d 128:
-                // 61 us of it, behind this kernel's registers 180).
-                const int st = launch_rotary(p.q, bf16, stream);
-                if (st != FA_OK) return st;
+                // Many: a launch of their own, at the occupancy that turning alone has (24.6 thousand tokens of 32 heads, d 128:
+                // 61 us of it, behind this kernel's registers 180).  It comes last, so that a call that fails has turned no query in place.
+                queries = p.q;
                 p.q.T = 0;
             } else {  // an item per thread; the grid's rows end at 65535, what is beyond goes round
                 rows = std::min<int64_t>(65535, rows + (items + columns * pg::kAppendThreads - 1) / (columns * pg::kAppendThreads));
@@ -294,7 +294,7 @@ int append(const fa_kv_cache* cache, const void* k, const void* v, const int* sl
     }
     void* args[] = {&p};
     if (!launch(fn, columns, static_cast<int>(rows), pg::kAppendThreads, 0, 1, stream, args)) return FA_ERR_CUDA;
-    return FA_OK;
+    return queries.T > 0 ? launch_rotary(queries, bf16, stream) : FA_OK;
 }
 
 }  // namespace

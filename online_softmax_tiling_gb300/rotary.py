@@ -8,7 +8,8 @@ re-exports the functions here.
     q, k = rotary_embed(q, k, positions, table)
     q = kv_cache_append_rotary(q, k, v, positions, table, slots, k_cache, v_cache, k_scale, v_scale)
 
-The second call turns and returns, the third replaces it and kv_cache_append by one launch.  What
+The second call turns and returns, the third replaces it and kv_cache_append (by one launch for a decode step, by two
+where there are many queries).  What
 paged.py says of streams, graphs and bad device data holds here too.
 """
 from __future__ import annotations
@@ -108,8 +109,8 @@ def rotary_embed(q, k, positions, table, interleaved: bool = False, inverse: boo
 def kv_cache_append_rotary(q, k, v, positions, table, slots, k_cache, v_cache, k_scale, v_scale, k_bounds=None,
                            interleaved: bool = False, q_out=None, stream=None, check: bool = False):
     """kv_cache_append of keys turned on their way (a key is rounded once, to the cache's 8 bits), and the
-    queries [T, Hq, d] turned as rotary_embed does, in the same launch.  Returns the turned queries (q_out if given, which may be q; None
-    for q None)."""
+    queries [T, Hq, d] turned as rotary_embed does, in the same launch or, where there are many, in one of their own behind
+    it.  Returns the turned queries (q_out if given, which may be q; None for q None)."""
     if stream is not None:
         with _there(k, stream):
             return kv_cache_append_rotary(q, k, v, positions, table, slots, k_cache, v_cache, k_scale, v_scale, k_bounds,

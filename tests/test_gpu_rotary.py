@@ -320,3 +320,24 @@ def test_step_turned_and_stored_then_read():
         want = ref.attend(cache, q, tb, lens, r["cu"], d ** -0.5, True)
         v_top = max(np.abs(cache.request(tb[b], int(lens[b]), "v")).max() for b in range(B))
         ref.check(got[0], got[1], want, d, int(lens.max()), v_top, torch.bfloat16, rows=slice(0, int(r["cu"][-1])))
+
+
+@pytest.mark.parametrize("dtype,inter", [("bf16", False), ("fp16", True)])
+def test_append_rotary_many_queries(dtype, inter):
+    """Queries enough (1024 items per SM) for a launch of their own: into new memory, and in place beside the keys and values."""
+    torch, fa = _torch(), _fa()
+    Hk, G, P, d, dim = 8, 4, 64, 64, 48
+    for in_place in (False, True):
+        cache, qkv, slots, pos, tab = _append_case(Hk, G, P, d, dim, dtype, [900, 400], [5, 0], 51, inter)
+        before = qkv.clone()
+        q, k, v = qkv[:, :Hk * G], qkv[:, Hk * G:Hk * G + Hk], qkv[:, Hk * G + Hk:]
+        want = _want(q, pos, tab, inter, False, dtype)
+        g = cache.cuda()
+        got = fa.kv_cache_append_rotary(q, k, v, _i32(pos), torch.from_numpy(tab).cuda(), _i32(slots), *g[:4], k_bounds=g[4],
+                                        interleaved=inter, q_out=q if in_place else None, check=True)
+        cache.append(lref.turn(_f32(k), pos, tab, inter).astype(np.float64), _f32(v).astype(np.float64), slots, True)
+        _check_cache(g, cache, True)
+        assert torch.equal(_bits(got), _bits(want)) and (got is q) == in_place
+        assert torch.equal(_bits(qkv[:, Hk * G:]), _bits(before[:, Hk * G:]))
+        assert in_place or torch.equal(_bits(qkv), _bits(before))
+    _ok()
