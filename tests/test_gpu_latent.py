@@ -753,3 +753,35 @@ def test_expanded_small_weights_in_fp16(first):
     assert (O > 5e-4).all() and (to < 0.1 * O).all()
     assert (np.abs(_f64(out) - O) <= to).all(), np.abs(_f64(out) / O - 1).max()
     assert (np.abs(_f64(lse) - L) <= tl).all()
+
+
+@pytest.mark.parametrize("dtype,inter", [("bf16", True), ("fp16", False)])
+def test_latent_append_of_many_queries(dtype, inter):
+    """Items enough (1.25 million) for two heads each, of an odd count; queries into views and in place."""
+    torch, fa = _torch(), _fa()
+    T, H, C, R, P = 2420, 129, 64, 64, 64
+    rng = np.random.default_rng(146)
+    slots = rng.permutation((-(-T // P) + 1) * P)[:T]
+    slots[rng.random(T) < 0.05] = -1
+    pos = np.where(rng.random(T) < 0.05, -1, rng.integers(0, 500, T))
+    tab = lref.table(500, R)
+    kv, q = _rand((T, C + R), dtype, 147).cuda(), _rand((T, H, C + R), dtype, 148).cuda()
+    cache = _rand((-(-T // P) + 1, P, C + R), dtype, 149).cuda()
+    want, on = cache.view(-1, C + R).clone(), slots >= 0
+    k = torch.from_numpy(lref.turn(kv[:, None, C:].float().cpu().numpy(), pos, tab, inter)[:, 0]).to(_dt(dtype)).cuda()
+    want[slots[on]] = torch.cat([kv[:, :C], k], dim=1)[torch.from_numpy(on).cuda()]
+    wq = q.clone()
+    wq[..., C:] = torch.from_numpy(lref.turn(q[..., C:].float().cpu().numpy(), pos, tab, inter)).to(_dt(dtype)).cuda()
+    kw = dict(positions=_i32(pos), table=torch.from_numpy(tab).cuda(), interleaved=inter, check=True)
+    out = fa.latent_cache_append(kv[:, :C], kv[:, C:], _i32(slots), cache, q_rope=q[..., C:], **kw)
+    assert torch.equal(_bits(cache.view(-1, C + R)), _bits(want)) and torch.equal(_bits(out), _bits(wq[..., C:]))
+    fa.latent_cache_append(kv[:, :C], kv[:, C:], _i32(slots), cache, q_rope=q[..., C:], q_out=q[..., C:], **kw)
+    assert torch.equal(_bits(cache.view(-1, C + R)), _bits(want)) and torch.equal(_bits(q), _bits(wq))
+
+
+@pytest.mark.parametrize("C,R,P", [(512, 64, 64), (64, 0, 128), (256, 32, 16)])
+def test_absorbed_long_shares(C, R, P):
+    """Shares of more than 16 tiles (ten requests of 17 thousand keys: 18 to each of 76 pairs)."""
+    c = Case([17000 + 31 * i for i in range(10)], [1] * 10, 4, C, R, P, "bf16", 150)
+    out, lse = c.call(check=True)
+    c.check(out, lse)
