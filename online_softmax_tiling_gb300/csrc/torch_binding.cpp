@@ -342,7 +342,8 @@ fa_rotary_part part_of(const at::Tensor& x, const char* name, PyObject* out, con
         const at::Tensor& o = tensor(out, out_name);
         ys = rows16(o, out_name, type, dev);
         if (o.sizes() != x.sizes()) refuse(PyExc_ValueError, out_name, "must have the shape of its input");
-        if (o.data_ptr() == x.data_ptr() && o.strides() != x.strides() && x.numel() > 0)
+        // (strides that are used: those of dimensions of one element may differ)
+        if (o.data_ptr() == x.data_ptr() && (xs.s[0] != ys.s[0] || xs.s[1] != ys.s[1]) && x.numel() > 0)
             refuse(PyExc_ValueError, out_name, "must be its input or not overlap it");
         made = o;
     }

@@ -341,3 +341,16 @@ def test_append_rotary_many_queries(dtype, inter):
         assert torch.equal(_bits(qkv[:, Hk * G:]), _bits(before[:, Hk * G:]))
         assert in_place or torch.equal(_bits(qkv), _bits(before))
     _ok()
+
+
+def test_in_place_through_a_view_with_other_unused_strides():
+    """One token's queries within a joint projection and a view of the same memory: the token stride is never used."""
+    torch, fa = _torch(), _fa()
+    tab, pos = lref.table(9, 32), np.array([7])
+    qkv = _rand((1, 12, 32), "bf16", 52).cuda()
+    q, want = qkv[:, :4], qkv.clone()
+    want[:, :4] = _want(q, pos, tab, False, False, "bf16")
+    view = q.as_strided((1, 4, 32), (4 * 32, 32, 1))
+    assert view.stride() != q.stride() and view.data_ptr() == q.data_ptr()
+    got, _ = fa.rotary_embed(q, None, _i32(pos), torch.from_numpy(tab).cuda(), q_out=view, check=True)
+    assert got is view and torch.equal(_bits(qkv), _bits(want))
