@@ -37,7 +37,7 @@ typedef struct fa_rotary {
 } fa_rotary;
 
 /* x, y: [T, heads, d] 16-bit, d contiguous, {token, head} strides in elements, positive multiples of 8,
- * 16-byte aligned.  y is x with the same strides (in place), or does not overlap it. */
+ * 16-byte aligned.  y is x with the same strides (in place; FA_ERR_INVALID_ARG with others), or does not overlap it. */
 typedef struct fa_rotary_part {
     const void* x;
     void* y;

@@ -19,6 +19,9 @@ int check_rotary(const fa_rotary* r, int d, int T) {
 int check_part(const fa_rotary_part* p, int T) {
     if ((T > 0 && (!p->x || !p->y)) || p->heads < 1) return FA_ERR_INVALID_ARG;
     if (bad_strides(p->x_stride) || bad_strides(p->y_stride) || misaligned(p->x, 16) || misaligned(p->y, 16)) return FA_ERR_MISALIGNED;
+    // in place with other strides, one token or head would be written where another is read
+    if (T > 0 && p->x == p->y && ((T > 1 && p->x_stride[0] != p->y_stride[0]) || (p->heads > 1 && p->x_stride[1] != p->y_stride[1])))
+        return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 pg::RotaryTable rotary_table(const fa_rotary& r) {

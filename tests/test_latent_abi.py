@@ -76,6 +76,14 @@ def test_part_refusals(lib, kw, want):  # noqa: F811
     assert lib.fa_latent_cache_append(P(l), A, 576, A, 576, A, 5, P(rot), P(q), 1, None) == want
 
 
+@pytest.mark.parametrize("x,y,T,heads,want", [([512, 128], [512, 64], 5, 4, BAD), ([512, 128], [1024, 128], 5, 4, BAD),
+                                              ([512, 128], [1024, 128], 5, 1, BAD), ([512, 128], [512, 64], 1, 4, BAD)])
+def test_in_place_with_other_strides(lib, x, y, T, heads, want):  # noqa: F811
+    q = _part(y=A + 0x1000, x_stride=x, y_stride=y, heads=heads)
+    assert _embed(lib, q=q, T=T) == want and _embed(lib, k=q, T=T) == want
+    assert _embed(lib, q=_part(y=A + 0x1000, x_stride=x, y_stride=y, heads=heads), T=0) == 0   # nothing is written
+
+
 def test_rotary_call_refusals(lib):  # noqa: F811
     assert lib.fa_rotary_embed(None, P(_part()), None, 5, 128, 1, None) == BAD
     assert lib.fa_rotary_embed(P(_rot()), None, None, 5, 128, 1, None) == BAD
