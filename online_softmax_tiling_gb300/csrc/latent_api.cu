@@ -310,8 +310,9 @@ int fa_latent_fwd(const fa_latent_args* args) {
     // (request, head) pairs in groups of equal size whose keys and values come to about 96 MB (of 129 MB of L2).  Fewer and
     // larger groups leave the pairs of CTAs more even work at the end: 32 heads, pieces of 4000 and 2516 queries 328 us with
     // groups of 96 MB, 344 with 48, 349 without (197 MB).
-    const int64_t all = static_cast<int64_t>(a.B) * a.H, bytes = all * std::max(a.max_k, 1) * (a.Dn + a.Dv) * 2;
-    const int64_t groups = std::max<int64_t>(1, std::min<int64_t>(all, (bytes + (48ll << 20)) / (96ll << 20)));
+    const int64_t all = static_cast<int64_t>(a.B) * a.H;
+    const double bytes = 2.0 * all * std::max(a.max_k, 1) * (a.Dn + a.Dv);  // (max_k is any hint: beyond 64 bits)
+    const int64_t groups = static_cast<int64_t>(std::max(1.0, std::min<double>(all, std::floor(bytes / (96 << 20) + 0.5))));
     p.group = static_cast<int>(std::min<int64_t>((all + groups - 1) / groups, INT32_MAX / p.q_blocks));
     CUtensorMap tq, tk, ts, tv;
     const int keys = std::max(a.Tk, 1);  // (no key at all: nothing is read)

@@ -97,7 +97,8 @@ def rotary_embed(q, k, positions, table, interleaved: bool = False, inverse: boo
     d contiguous and a multiple of 8 (views of a joint projection are fine); positions [T] int32, rows of table
     [num_positions, dim] float32 (rotary_table); dim a multiple of 16.  interleaved: pairs (2 i, 2 i + 1) instead of (i, i + dim / 2).  A
     negative position leaves its token as it is; so does one beyond the table, which fa_check_device_status
-    reports.  inverse turns back: the gradient with respect to q and k, given that of the outputs.  q_out, k_out: q and k
+    reports.  inverse turns back: the gradient with respect to q and k, given that of the outputs (as everywhere in this
+    package nothing is recorded for autograd, whatever q and k require: a backward pass makes that call itself).  q_out, k_out: q and k
     themselves (in place), or tensors that do not overlap them; new ones unless given.
     """
     if stream is not None:
