@@ -68,7 +68,7 @@ struct AppendItem {
 
 // A thread's rows of an item, 16-bit values; where keys are turned also the channels that make pairs with them.  Turned
 // values are fp32 (so that a key is rounded once, to e4m3), and for more rows than the registers hold of these,
-// nothing is held: rows are read twice.  22 thousand tokens of 8 heads, d 128, half of the channels turned: 60 us for keys
+// nothing is held: rows are read twice.  24.6 thousand tokens of 8 heads, d 128, half of the channels turned: 60 us for keys
 // and values (39 unturned: the table's reads, and registers for two CTAs per SM; bounded to three CTAs they spill and it takes
 // longer), and 95 for pages of 128 with d 256, which are read twice.
 template <int NL, bool ROT>

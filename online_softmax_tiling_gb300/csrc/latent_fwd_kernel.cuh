@@ -20,8 +20,10 @@
 // meanwhile.  So S is held twice, for steps of 64 keys: S(k + 1) is there before the weights of step k are done.  (Steps
 // of 128 keys and one S: 4,400 cycles per 128 keys, of which the tensor cores worked 2,560.)  A step takes 1,900 cycles, of which the
 // tensor cores work 1,550; the same where tile A, which sees 256 keys less, is done and B goes on alone, which is what the
-// rest is lost to: 32 heads, pieces of 4000 and 2516 queries on up to 6000 keys 330 us, 1.32 PFLOP/s; 8192 queries of
-// 16 heads 246 us, 1.39 PFLOP/s.
+// rest is lost to: 32 heads, pieces of 4000 and 2516 queries on up to 6000 keys 331 us in a graph, 1.32 PFLOP/s (350 from a cold
+// L2); 8192 queries of 16 heads 245 us, 1.40 PFLOP/s.
+// Weights are rounded to the operands' 16-bit type, as both operands of a product are of one; O is divided by the sum of the
+// rounded ones, the LSE takes the fp32 sum.
 // TMEM: S_A 0 and 64, S_B 128 and 192 (16-bit weights over the first 32 columns of each), U_A 256, U_B 384.
 // Units are handed out by the launch itself: a pair that is done takes the next cluster of the grid that has not begun
 // (clusterlaunchcontrol), asked for one unit ahead, so that its queries and keys are on their way before the last products of this one.

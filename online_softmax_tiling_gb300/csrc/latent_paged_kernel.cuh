@@ -41,7 +41,8 @@
 //
 // What bounds it.  A tile passes through load (1.1 us), S (1.3, with the other stage's U += P V between its halves), softmax
 // (0.8) and U += P V (0.5 and the signals), and two are under way: 1.9 us a tile, where HBM would take 1.7
-// and the tensor cores work 1.15.  64 requests of 5000 to 16384 keys, 128 heads: 165 us, 4.9 TB/s and 1.15 PFLOP/s (16 heads: 158);
+// and the tensor cores work 1.15.  64 requests of 5000 to 16384 keys, 128 heads, in a graph: 166 us, 4.9 TB/s and 1.15 PFLOP/s (16 heads: 158), from a
+// cold L2 177 us, 4.5 TB/s;
 // 8 us of it pass before the first product, 12 in the join.  One request of 4096 keys, 32 heads: 13.4 us, latency: lengths,
 // queries and keys, two tiles, parts, the join's start and its reads.
 // Tried (against 178, before what prefetch() says): tiles of 64 keys in four stages 186 us (loads of 4 KB: TMA brings an SM 36 bytes a cycle so, 47 in 8 KB, 55 in 32 KB,
